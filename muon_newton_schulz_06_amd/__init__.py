@@ -499,4 +499,8 @@ def profile_read(kind) -> dict:
 
 from .optim import Muon  # noqa: E402  (torch.optim front end)
 
+from . import layers  # noqa: E402  (embedding, RMS norm, gated FFN)
+from .layers import *  # noqa: E402,F401,F403
+
 __all__.append("Muon")
+__all__ += ["layers", *layers.__all__]

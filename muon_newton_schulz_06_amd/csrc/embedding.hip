@@ -1,0 +1,486 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens.
+//
+// Lookup: out[t] = scale·W[id_t], one 16-byte chunk per lane; HBM-bound.
+//
+// Gradient: dW[v] = scale·Σ_{t: id_t = v} dy[t] without float atomics (their
+// order, and so the last bits, would change from run to run):
+//   1. a stable radix sort of (id, t) by id;
+//   2. pieces: the sorted list is cut every kEmbedPiece positions; a piece
+//      that lies wholly inside one run of equal ids is summed to an fp32 row
+//      in the workspace, so that no run is summed by one lane group alone;
+//   3. one lane group per run: the rows before its first whole piece, the
+//      pieces' sums, the rows after the last one, in that order; the same
+//      launch writes the zero rows of the ids that do not occur.
+// Ids outside [0, vocab) sort to the end as the key `vocab` and are skipped.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "layers.hpp"
+
+namespace muon {
+namespace {
+
+__device__ __forceinline__ int64_t load_id(const void* ids, int id64, int64_t t) {
+  return id64 ? ((const int64_t*)ids)[t] : (int64_t)((const int32_t*)ids)[t];
+}
+
+// ----- lookup ----------------------------------------------------------------
+// A group of `lanes` lanes (a power of two) serves one token; it takes up to
+// four chunks per lane and slice of the row (blockIdx.y).
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void embedding_kernel(const EmbedLaunch L, int lanes, int shift) {
+  constexpr int V = LType<T>::kVec;
+  const int g = threadIdx.x >> shift, l = threadIdx.x & (lanes - 1);
+  const int64_t t = (int64_t)blockIdx.x * (256 >> shift) + g;
+  if (t >= L.tokens) return;
+  const int64_t id = load_id(L.ids, L.id64, t);
+  const bool ok = id >= 0 && id < L.vocab;
+  constexpr int E = 16 / V;  // bytes per element
+  const char* src = (const char*)L.weight + (ok ? id : 0) * L.ldw * E;
+  char* dst = (char*)L.out + t * L.ldo * E;
+  const int64_t c0 = (int64_t)blockIdx.y * lanes * 4 + l;
+  lu32x4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t e = (c0 + i * lanes) * V;
+    if (e < L.dim && ok) v[i] = l_load<T, VEC>(src, e, L.dim);
+    else v[i] = lu32x4{0u, 0u, 0u, 0u};
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t e = (c0 + i * lanes) * V;
+    if (e < L.dim) {
+      float f[V];
+      l_widen<T>(v[i], f);
+      if (ok) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) f[k] *= L.scale;
+      }
+      l_store<T, VEC>(dst, e, L.dim, l_narrow<T>(f));
+    }
+  }
+}
+
+// ----- sort ------------------------------------------------------------------
+__device__ __forceinline__ uint32_t sort_key(const EmbedGradLaunch& L, int64_t t) {
+  const int64_t id = load_id(L.ids, L.id64, t);
+  return id >= 0 && id < L.vocab ? (uint32_t)id : (uint32_t)L.vocab;
+}
+
+// Lanes of the wave with the same digit, among the active ones of `in`.
+template <int BITS>
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t in) {
+  uint64_t m = in;
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
+    const bool bit = (d >> b) & 1u;
+    const uint64_t set = __ballot(bit);
+    m &= bit ? set : ~set;
+  }
+  return m;
+}
+
+// One stable counting pass over a workgroup's items, held in registers in
+// wave order: wave w's items are consecutive, ITEMS rounds of 64 lanes.
+// cnt[digit·WAVES + wave] must be zero on entry and holds the wave's digit
+// counts afterwards; rank[i] is the item's rank among its wave's equal digits.
+template <int BITS, int ITEMS, int WAVES>
+__device__ __forceinline__ void rank_items(const uint32_t (&key)[ITEMS], const bool (&have)[ITEMS],
+                                           int sh, uint32_t* cnt, int wave, int lane,
+                                           uint32_t (&rank)[ITEMS]) {
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t d = (key[i] >> sh) & ((1u << BITS) - 1u);
+    const uint64_t in = __ballot(have[i]);
+    const uint64_t m = same_digit<BITS>(d, in);
+    uint32_t* c = cnt + d * WAVES + wave;
+    const uint32_t before = have[i] ? *c : 0u;
+    rank[i] = before + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
+    // the last lane of each digit stores the new count; the LDS serves a
+    // wave's accesses in order, so the next round reads it
+    if (have[i] && (m >> lane) == 1ull) *c = rank[i] + 1u;
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Exclusive scan of n counts in shared memory by the whole workgroup (n a
+// multiple of the thread count).
+template <int NT>
+__device__ __forceinline__ void scan_counts(uint32_t* cnt, int n, uint32_t* wsum) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = n / NT;
+  uint32_t s = 0;
+  for (int i = 0; i < per; ++i) s += cnt[tid * per + i];
+  uint32_t inc = s;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t v = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 63) wsum[wave] = inc;
+  __syncthreads();
+  uint32_t base = 0;
+  for (int w = 0; w < wave; ++w) base += wsum[w];
+  uint32_t run = base + inc - s;
+  for (int i = 0; i < per; ++i) {
+    const uint32_t c = cnt[tid * per + i];
+    cnt[tid * per + i] = run;
+    run += c;
+  }
+  __syncthreads();
+}
+
+// The whole sort of up to kEmbedSmallSort tokens in one workgroup: keys live
+// in registers, each pass permutes them through shared memory.  9-bit digits,
+// so a vocabulary of up to 2^18 − 1 takes two passes.
+template <int ITEMS>
+__global__ __launch_bounds__(1024) void embed_sort_small(const EmbedGradLaunch L, int passes) {
+  constexpr int BITS = 9, WAVES = 16, BINS = 1 << BITS;
+  __shared__ uint32_t cnt[BINS * WAVES];
+  __shared__ uint32_t skey[ITEMS * 1024];
+  __shared__ uint16_t sidx[ITEMS * 1024];
+  __shared__ uint32_t wsum[WAVES];
+  static_assert(ITEMS * 1024 <= 65536, "token positions are kept in 16 bits");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int n = (int)L.tokens;
+  uint32_t key[ITEMS], idx[ITEMS], rank[ITEMS];
+  bool have[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int p = wave * (ITEMS * 64) + i * 64 + lane;
+    have[i] = p < n;
+    key[i] = have[i] ? sort_key(L, p) : 0u;
+    idx[i] = p;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const int sh = pass * BITS;
+    for (int i = tid; i < BINS * WAVES; i += 1024) cnt[i] = 0u;
+    __syncthreads();
+    rank_items<BITS, ITEMS, WAVES>(key, have, sh, cnt, wave, lane, rank);
+    __syncthreads();
+    scan_counts<1024>(cnt, BINS * WAVES, wsum);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (have[i]) {
+        const uint32_t to = cnt[((key[i] >> sh) & (BINS - 1u)) * WAVES + wave] + rank[i];
+        skey[to] = key[i];
+        sidx[to] = (uint16_t)idx[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int p = wave * (ITEMS * 64) + i * 64 + lane;
+      if (have[i]) {
+        key[i] = skey[p];
+        idx[i] = sidx[p];
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int p = wave * (ITEMS * 64) + i * 64 + lane;
+    if (have[i]) {
+      L.key[0][p] = key[i];
+      L.idx[0][p] = idx[i];
+    }
+  }
+}
+
+// Sort in device memory, one 8-bit digit per pass: counts per workgroup, one
+// scan over (digit, workgroup), stable scatter.
+constexpr int kSortItems = kEmbedSortBlock / 256;
+constexpr int kSortBins = 1 << kEmbedSortBits;
+
+__device__ __forceinline__ void load_items(const EmbedGradLaunch& L, int pass, uint32_t (&key)[kSortItems],
+                                           uint32_t (&idx)[kSortItems], bool (&have)[kSortItems]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t b0 = (int64_t)blockIdx.x * kEmbedSortBlock + wave * (kSortItems * 64) + lane;
+  const int from = (pass + 1) & 1;
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    const int64_t p = b0 + i * 64;
+    have[i] = p < L.tokens;
+    key[i] = idx[i] = 0u;
+    if (have[i]) {
+      key[i] = pass == 0 ? sort_key(L, p) : L.key[from][p];
+      idx[i] = pass == 0 ? (uint32_t)p : L.idx[from][p];
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void embed_sort_count(const EmbedGradLaunch L, int pass) {
+  __shared__ uint32_t cnt[kSortBins * 4];
+  uint32_t key[kSortItems], idx[kSortItems], rank[kSortItems];
+  bool have[kSortItems];
+  for (int i = threadIdx.x; i < kSortBins * 4; i += 256) cnt[i] = 0u;
+  load_items(L, pass, key, idx, have);
+  __syncthreads();
+  rank_items<kEmbedSortBits, kSortItems, 4>(key, have, pass * kEmbedSortBits, cnt, threadIdx.x >> 6,
+                                            threadIdx.x & 63, rank);
+  __syncthreads();
+  const int d = threadIdx.x;
+  L.counts[(int64_t)d * gridDim.x + blockIdx.x] = cnt[4 * d] + cnt[4 * d + 1] + cnt[4 * d + 2] + cnt[4 * d + 3];
+}
+
+__global__ __launch_bounds__(1024) void embed_sort_scan(uint32_t* counts, int64_t n) {
+  __shared__ uint32_t wsum[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t per = (n + 1023) / 1024, lo = min(n, tid * per), hi = min(n, lo + per);
+  uint32_t s = 0;
+  for (int64_t i = lo; i < hi; ++i) s += counts[i];
+  uint32_t inc = s;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t v = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 63) wsum[wave] = inc;
+  __syncthreads();
+  uint32_t run = inc - s;
+  for (int w = 0; w < wave; ++w) run += wsum[w];
+  for (int64_t i = lo; i < hi; ++i) {
+    const uint32_t c = counts[i];
+    counts[i] = run;
+    run += c;
+  }
+}
+
+__global__ __launch_bounds__(256) void embed_sort_scatter(const EmbedGradLaunch L, int pass) {
+  __shared__ uint32_t cnt[kSortBins * 4];
+  uint32_t key[kSortItems], idx[kSortItems], rank[kSortItems];
+  bool have[kSortItems];
+  for (int i = threadIdx.x; i < kSortBins * 4; i += 256) cnt[i] = 0u;
+  load_items(L, pass, key, idx, have);
+  __syncthreads();
+  const int sh = pass * kEmbedSortBits, wave = threadIdx.x >> 6;
+  rank_items<kEmbedSortBits, kSortItems, 4>(key, have, sh, cnt, wave, threadIdx.x & 63, rank);
+  __syncthreads();
+  const int d = threadIdx.x;
+  uint32_t run = L.counts[(int64_t)d * gridDim.x + blockIdx.x];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t c = cnt[4 * d + w];
+    cnt[4 * d + w] = run;
+    run += c;
+  }
+  __syncthreads();
+  const int to = pass & 1;
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    if (have[i]) {
+      const uint32_t p = cnt[((key[i] >> sh) & (kSortBins - 1u)) * 4 + wave] + rank[i];
+      L.key[to][p] = key[i];
+      L.idx[to][p] = idx[i];
+    }
+  }
+}
+
+// ----- segmented sums --------------------------------------------------------
+// Sums of whole pieces inside one run.  One lane group per (piece, slice).
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void embed_pieces(const EmbedGradLaunch L, const uint32_t* key,
+                                                    const uint32_t* idx, int lanes, int shift) {
+  constexpr int V = LType<T>::kVec, E = 16 / V;
+  const int g = threadIdx.x >> shift, l = threadIdx.x & (lanes - 1);
+  const int64_t c = (int64_t)blockIdx.x * (256 >> shift) + g;
+  const int64_t p0 = c * kEmbedPiece;
+  if (p0 + kEmbedPiece > L.tokens) return;
+  const uint32_t k = key[p0];
+  if (k != key[p0 + kEmbedPiece - 1] || k >= (uint32_t)L.vocab) return;
+  const int64_t e = ((int64_t)blockIdx.y * lanes + l) * V;
+  if (e >= L.dim) return;
+  float acc[V] = {};
+#pragma unroll 8
+  for (int j = 0; j < kEmbedPiece; ++j) {
+    const char* row = (const char*)L.dy + (int64_t)idx[p0 + j] * L.ldy * E;
+    float f[V];
+    l_widen<T>(l_load<T, VEC>(row, e, L.dim), f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += f[i];
+  }
+  float* out = L.pieces + c * L.dim + e;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (VEC || e + i < L.dim) out[i] = acc[i];
+}
+
+// Stores V values of a dweight row (adding to it when accumulating).
+template <typename TW, bool VECW, int V>
+__device__ __forceinline__ void put_dw(const EmbedGradLaunch& L, int64_t v, int64_t e, const float (&f)[V]) {
+  constexpr int VW = LType<TW>::kVec, EW = 16 / VW;
+  char* row = (char*)L.dw + v * L.ldw * EW;
+  if constexpr (VECW && V % VW == 0) {
+#pragma unroll
+    for (int h = 0; h < V; h += VW) {
+      if (e + h >= L.dim) break;  // the row is whole chunks of dweight's type, not always of dy's
+      float o[VW];
+      if (L.accumulate) l_widen<TW>(l_load<TW, true>(row, e + h, L.dim), o);
+      else {
+#pragma unroll
+        for (int i = 0; i < VW; ++i) o[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < VW; ++i) o[i] = fmaf(L.scale, f[h + i], o[i]);
+      l_store<TW, true>(row, e + h, L.dim, l_narrow<TW>(o));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e + i < L.dim) {
+        const float old = L.accumulate ? LType<TW>::get(row, e + i) : 0.f;
+        LType<TW>::put(row, e + i, fmaf(L.scale, f[i], old));
+      }
+  }
+}
+
+// blockIdx.x < runBlocks: lane groups look at one sorted position each and
+// sum the run that starts there.  The other workgroups write zero rows: 64
+// ids each, present ones found by binary search in the sorted keys.
+template <typename T, bool VEC, typename TW, bool VECW>
+__global__ __launch_bounds__(256) void embed_rows(const EmbedGradLaunch L, const uint32_t* key,
+                                                  const uint32_t* idx, int lanes, int shift,
+                                                  int64_t runBlocks) {
+  constexpr int V = LType<T>::kVec, E = 16 / V;
+  if (blockIdx.x < runBlocks) {
+    const int g = threadIdx.x >> shift, l = threadIdx.x & (lanes - 1);
+    const int64_t s = (int64_t)blockIdx.x * (256 >> shift) + g;
+    if (s >= L.tokens) return;
+    const uint32_t k = key[s];
+    if (k >= (uint32_t)L.vocab || (s > 0 && key[s - 1] == k)) return;
+    const int64_t e = ((int64_t)blockIdx.y * lanes + l) * V;
+    if (e >= L.dim) return;
+    float acc[V] = {};
+    auto add_row = [&](int64_t p) {
+      const char* row = (const char*)L.dy + (int64_t)idx[p] * L.ldy * E;
+      float f[V];
+      l_widen<T>(l_load<T, VEC>(row, e, L.dim), f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += f[i];
+    };
+    int64_t p = s;
+    // rows up to the first piece boundary
+    const int64_t b = (s + kEmbedPiece - 1) / kEmbedPiece * kEmbedPiece;
+    for (; p < b && p < L.tokens && key[p] == k; ++p) add_row(p);
+    if (p == b) {
+      while (p + kEmbedPiece <= L.tokens && key[p + kEmbedPiece - 1] == k) {
+        const float* pc = L.pieces + (p / kEmbedPiece) * L.dim + e;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (VEC || e + i < L.dim) acc[i] += pc[i];
+        p += kEmbedPiece;
+      }
+      for (; p < L.tokens && key[p] == k; ++p) add_row(p);
+    }
+    put_dw<TW, VECW, V>(L, k, e, acc);
+    return;
+  }
+  // zero rows
+  __shared__ uint64_t present;
+  const int64_t v0 = ((int64_t)blockIdx.x - runBlocks) * 64;
+  if (threadIdx.x < 64) {
+    const int64_t v = v0 + threadIdx.x;
+    int64_t lo = 0, hi = L.tokens;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if ((int64_t)key[mid] < v) lo = mid + 1;
+      else hi = mid;
+    }
+    const bool here = v < L.vocab && lo < L.tokens && (int64_t)key[lo] == v;
+    const uint64_t m = __ballot(here);
+    if (threadIdx.x == 0) present = m;
+  }
+  __syncthreads();
+  const uint64_t m = present;
+  constexpr int VW = LType<TW>::kVec, EW = 16 / VW;
+  const int64_t rows = min((int64_t)64, L.vocab - v0);
+  for (int64_t r = threadIdx.x >> 6; r < rows; r += 4) {
+    if ((m >> r) & 1ull) continue;
+    char* row = (char*)L.dw + (v0 + r) * L.ldw * EW;
+    for (int64_t e = ((int64_t)blockIdx.y * 64 + (threadIdx.x & 63)) * VW; e < L.dim;
+         e += (int64_t)gridDim.y * 64 * VW)
+      l_store<TW, VECW>(row, e, L.dim, lu32x4{0u, 0u, 0u, 0u});
+  }
+}
+
+// Lanes of a group: the chunks of a row, at most a wave's.
+int group_shift(int64_t chunks) {
+  int s = 3;
+  while (s < 6 && (1 << s) < chunks) ++s;
+  return s;
+}
+
+template <typename T, bool VEC, typename TW, bool VECW>
+hipError_t rows_launch(const EmbedGradLaunch& L, hipStream_t st) {
+  constexpr int V = LType<T>::kVec;
+  const int64_t chunks = (L.dim + V - 1) / V;
+  const int sh = group_shift(chunks), lanes = 1 << sh, per = 256 >> sh;
+  const int64_t slices = (chunks + lanes - 1) / lanes;
+  const int64_t np = L.tokens / kEmbedPiece;
+  // the device-memory sort ends in the buffer its last pass wrote
+  const uint32_t *key = L.key[0], *idx = L.idx[0];
+  if (np > 0) {
+    hipLaunchKernelGGL((embed_pieces<T, VEC>), dim3((np + per - 1) / per, slices), dim3(256), 0, st, L,
+                       key, idx, lanes, sh);
+  }
+  const int64_t runBlocks = (L.tokens + per - 1) / per;
+  const int64_t zeroBlocks = L.accumulate ? 0 : (L.vocab + 63) / 64;
+  if (runBlocks + zeroBlocks > 0)
+    hipLaunchKernelGGL((embed_rows<T, VEC, TW, VECW>), dim3(runBlocks + zeroBlocks, slices), dim3(256), 0,
+                       st, L, key, idx, lanes, sh, runBlocks);
+  return hipGetLastError();
+}
+
+template <typename T, bool VEC>
+hipError_t rows_dw(const EmbedGradLaunch& L, hipStream_t st) {
+  if (L.dwBf16)
+    return L.vecw ? rows_launch<T, VEC, Bf16, true>(L, st) : rows_launch<T, VEC, Bf16, false>(L, st);
+  return L.vecw ? rows_launch<T, VEC, float, true>(L, st) : rows_launch<T, VEC, float, false>(L, st);
+}
+
+}  // namespace
+
+hipError_t launch_embedding(const EmbedLaunch& L, hipStream_t st) {
+  const int V = L.bf16 ? 8 : 4;
+  const int64_t chunks = (L.dim + V - 1) / V;
+  const int sh = group_shift(chunks), lanes = 1 << sh, per = 256 >> sh;
+  const dim3 grid((L.tokens + per - 1) / per, (chunks + 4 * lanes - 1) / (4 * lanes));
+  if (L.bf16) {
+    if (L.vec) hipLaunchKernelGGL((embedding_kernel<Bf16, true>), grid, dim3(256), 0, st, L, lanes, sh);
+    else hipLaunchKernelGGL((embedding_kernel<Bf16, false>), grid, dim3(256), 0, st, L, lanes, sh);
+  } else {
+    if (L.vec) hipLaunchKernelGGL((embedding_kernel<float, true>), grid, dim3(256), 0, st, L, lanes, sh);
+    else hipLaunchKernelGGL((embedding_kernel<float, false>), grid, dim3(256), 0, st, L, lanes, sh);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_embedding_grad(const EmbedGradLaunch& L0, hipStream_t st) {
+  EmbedGradLaunch L = L0;
+  int bits = 1;  // of the largest key, vocab
+  while ((L.vocab >> bits) != 0) ++bits;
+  if (L.tokens > 0 && L.tokens <= kEmbedSmallSort) {
+    const int passes = (bits + 8) / 9;
+    if (L.tokens <= 1024) hipLaunchKernelGGL(embed_sort_small<1>, dim3(1), dim3(1024), 0, st, L, passes);
+    else if (L.tokens <= 4096) hipLaunchKernelGGL(embed_sort_small<4>, dim3(1), dim3(1024), 0, st, L, passes);
+    else hipLaunchKernelGGL(embed_sort_small<16>, dim3(1), dim3(1024), 0, st, L, passes);
+  } else if (L.tokens > 0) {
+    const int passes = (bits + kEmbedSortBits - 1) / kEmbedSortBits;
+    const int blocks = (int)((L.tokens + kEmbedSortBlock - 1) / kEmbedSortBlock);
+    for (int p = 0; p < passes; ++p) {
+      hipLaunchKernelGGL(embed_sort_count, dim3(blocks), dim3(256), 0, st, L, p);
+      hipLaunchKernelGGL(embed_sort_scan, dim3(1), dim3(1024), 0, st, L.counts, (int64_t)blocks * kSortBins);
+      hipLaunchKernelGGL(embed_sort_scatter, dim3(blocks), dim3(256), 0, st, L, p);
+    }
+    if ((passes & 1) == 0) {  // pass p writes buffer p & 1: the last one ended in buffer 1
+      std::swap(L.key[0], L.key[1]);
+      std::swap(L.idx[0], L.idx[1]);
+    }
+  }
+  if (L.dyBf16) return L.vec ? rows_dw<Bf16, true>(L, st) : rows_dw<Bf16, false>(L, st);
+  return L.vec ? rows_dw<float, true>(L, st) : rows_dw<float, false>(L, st);
+}
+
+}  // namespace muon

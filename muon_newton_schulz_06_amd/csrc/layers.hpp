@@ -1,0 +1,243 @@
+// Launch descriptors and device helpers of the layer operators (embedding,
+// RMS norm, gated feed-forward block).  Descriptors are passed by value.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace muon {
+
+// ----- embedding -------------------------------------------------------------
+struct EmbedLaunch {
+  const void* ids;
+  int32_t id64;
+  int32_t bf16;
+  int64_t tokens, vocab, dim;
+  const void* weight;
+  int64_t ldw;
+  void* out;
+  int64_t ldo;
+  float scale;
+  int32_t vec;  // 16-byte aligned rows of whole 16-byte chunks
+};
+hipError_t launch_embedding(const EmbedLaunch& L, hipStream_t st);
+
+// Positions per piece of a long run of equal ids.
+constexpr int kEmbedPiece = 32;
+// Tokens sorted by one workgroup in shared memory.
+constexpr int64_t kEmbedSmallSort = 16384;
+// Tokens per workgroup and digit bits of the sort in device memory.
+constexpr int kEmbedSortBlock = 4096;
+constexpr int kEmbedSortBits = 8;
+
+struct EmbedGradLaunch {
+  const void* ids;
+  int32_t id64;
+  int32_t dyBf16, dwBf16, accumulate;
+  int64_t tokens, vocab, dim;
+  const void* dy;
+  int64_t ldy;
+  void* dw;
+  int64_t ldw;
+  float scale;
+  int32_t vec;       // dy rows are whole aligned 16-byte chunks
+  int32_t vecw;      // so are dweight's
+  uint32_t* key[2];  // sorted ids (vocab: none), ping-pong
+  uint32_t* idx[2];  // their token positions
+  uint32_t* counts;  // digit counts of the device-memory sort
+  float* pieces;     // sums of whole pieces of long runs, dim floats each
+};
+hipError_t launch_embedding_grad(const EmbedGradLaunch& L, hipStream_t st);
+
+// ----- RMS norm --------------------------------------------------------------
+struct NormFwdLaunch {
+  const void* x;
+  const void* res;
+  const void* w;
+  void* y;
+  void* sum;
+  float* rstd;
+  int64_t ldx, ldr, ldy, lds;
+  int64_t tokens, dim;
+  float eps;
+  int32_t bf16, wBf16, vec;
+};
+hipError_t launch_rms_norm(const NormFwdLaunch& L, hipStream_t st);
+
+struct NormGradLaunch {
+  const void* dy;
+  const void* s;
+  const void* w;
+  const void* dsum;
+  const float* rstd;
+  void* dx;
+  void* dw;
+  float* part;  // blocks × dim partial sums of dweight
+  int64_t ldy, lds, ldd, ldx;
+  int64_t tokens, dim;
+  int32_t blocks;
+  int32_t bf16, wBf16, vec, accumulate;
+};
+// Workgroups (and rows of partial sums) of the backward pass.
+int rms_norm_grad_blocks(int64_t tokens, int64_t dim);
+hipError_t launch_rms_norm_grad(const NormGradLaunch& L, hipStream_t st);
+
+// ----- gated feed-forward block ----------------------------------------------
+// C = A·Bᵀ over one or two ranges of k.  An operand is k-contiguous (element
+// (row, k) at p[row·ld + k]) or row-contiguous (p[k·ld + row]); which one is a
+// property of the launch.
+enum FfnEpi : int32_t {
+  FFN_GLU = 0,    // B holds w_gate and w_up: h = act(g)·u, optional a, b
+  FFN_BACK = 1,   // dh → dg = dh·a, du = dh·b
+  FFN_STORE = 2,  // C ← acc (+ C)
+};
+
+struct FfnProb {
+  const void* A[2];  // per k range
+  const void* B[2];  // per k range (FFN_GLU: w_gate, w_up over the one range)
+  int64_t lda, ldb[2];
+  int32_t M, N;
+  int32_t K[2];
+  void* C;
+  int64_t ldc;
+};
+
+struct FfnLaunch {
+  FfnProb prob[3];
+  int32_t tiles[4];  // first tile of each problem, and the total
+  int32_t nprob;
+  int32_t act;
+  int32_t outBf16, accumulate;
+  // FFN_GLU: a, b (rows of 2·ldh: a then b; null: not wanted), C is h;
+  // FFN_BACK: reads them, C is dg, du (rows of 2·ldh)
+  void* ab;
+  int64_t ldh;  // hidden rounded up to 8: row length of h and of each half
+};
+hipError_t launch_ffn_tile32(int epi, bool aRowContig, bool bRowContig, bool bf16,
+                             const FfnLaunch& L, hipStream_t st);
+
+// ----- device helpers --------------------------------------------------------
+typedef float lf32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t lu32x4 __attribute__((ext_vector_type(4)));
+
+struct Bf16 {
+  uint16_t v;
+};
+
+__device__ __forceinline__ float l_bf16_f32(uint32_t h) { return __uint_as_float(h << 16); }
+
+// Round to nearest even; NaN stays NaN.
+__device__ __forceinline__ uint32_t l_f32_bf16(float f) {
+  uint32_t u = __float_as_uint(f);
+  if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;
+  u += 0x7fffu + ((u >> 16) & 1u);
+  return u >> 16;
+}
+
+template <typename T> struct LType;
+template <> struct LType<float> {
+  static constexpr int kVec = 4;  // elements of a 16-byte chunk
+  static __device__ __forceinline__ float get(const void* p, int64_t e) { return ((const float*)p)[e]; }
+  static __device__ __forceinline__ void put(void* p, int64_t e, float v) { ((float*)p)[e] = v; }
+};
+template <> struct LType<Bf16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float get(const void* p, int64_t e) {
+    return l_bf16_f32(((const uint16_t*)p)[e]);
+  }
+  static __device__ __forceinline__ void put(void* p, int64_t e, float v) {
+    ((uint16_t*)p)[e] = (uint16_t)l_f32_bf16(v);
+  }
+};
+
+// A raw 16-byte chunk widened to fp32.
+template <typename T> __device__ __forceinline__ void l_widen(lu32x4 c, float (&v)[LType<T>::kVec]) {
+  if constexpr (LType<T>::kVec == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(c[i] << 16);
+      v[2 * i + 1] = __uint_as_float(c[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(c[i]);
+  }
+}
+
+template <typename T> __device__ __forceinline__ lu32x4 l_narrow(const float (&v)[LType<T>::kVec]) {
+  lu32x4 c;
+  if constexpr (LType<T>::kVec == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = l_f32_bf16(v[2 * i]) | (l_f32_bf16(v[2 * i + 1]) << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(v[i]);
+  }
+  return c;
+}
+
+// Elements [e, e + kVec) of a row of n elements as a chunk: one 16-byte
+// access when VEC, else one access per element that exists (others 0).
+template <typename T, bool VEC>
+__device__ __forceinline__ lu32x4 l_load(const void* row, int64_t e, int64_t n) {
+  if constexpr (VEC) {
+    return *(const lu32x4*)((const char*)row + e * (16 / LType<T>::kVec));
+  } else {
+    lu32x4 c = {0u, 0u, 0u, 0u};
+    if constexpr (LType<T>::kVec == 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (e + i < n) c[i / 2] |= (uint32_t)((const uint16_t*)row)[e + i] << (16 * (i & 1));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e + i < n) c[i] = ((const uint32_t*)row)[e + i];
+    }
+    return c;
+  }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void l_store(void* row, int64_t e, int64_t n, lu32x4 c) {
+  if constexpr (VEC) {
+    *(lu32x4*)((char*)row + e * (16 / LType<T>::kVec)) = c;
+  } else if constexpr (LType<T>::kVec == 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e + i < n) ((uint16_t*)row)[e + i] = (uint16_t)(c[i / 2] >> (16 * (i & 1)));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e + i < n) ((uint32_t*)row)[e + i] = c[i];
+  }
+}
+
+__device__ __forceinline__ float l_wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// 16-bit float with 6 exponent bits (bias 31) and 9 mantissa bits, rounded to
+// nearest even: the fp32 exponent field less 96.  Magnitudes below 2^-30
+// become zero, those of 2^32 and more infinity; NaN stays NaN.
+__device__ __forceinline__ uint32_t l_pack_e6m9(float f) {
+  const uint32_t u = __float_as_uint(f);
+  const uint32_t m = u & 0x7fffffffu;
+  uint32_t r;
+  if (m > 0x7f800000u) {
+    r = 0x7fffu;
+  } else {
+    const uint32_t rounded = m + 0x1fffu + ((m >> 14) & 1u);
+    r = rounded < (97u << 23) ? 0u : min((rounded - (96u << 23)) >> 14, 0x7e00u);
+  }
+  return r | ((u >> 16) & 0x8000u);
+}
+__device__ __forceinline__ float l_unpack_e6m9(uint32_t c) {
+  const uint32_t r = c & 0x7fffu;
+  uint32_t m = r < 0x200u ? 0u : (r << 14) + (96u << 23);
+  if (r >= 0x7e00u) m |= 0x7f800000u;
+  return __uint_as_float(m | ((c & 0x8000u) << 16));
+}
+
+}  // namespace muon

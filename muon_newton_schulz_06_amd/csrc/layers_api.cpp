@@ -1,0 +1,613 @@
+// C ABI of the layer operators (include/muon_layers.h): argument checks,
+// workspace layout and launches on the caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdlib>
+#include <string>
+#include <vector>
+
+#include "../../include/muon_layers.h"
+#include "launch.hpp"
+#include "layers.hpp"
+
+namespace muon {
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int64_t kMaxVocab = int64_t(1) << 24;
+constexpr int64_t kMaxWidth = int64_t(1) << 20;
+constexpr int64_t kMaxLd = int64_t(1) << 32;
+
+// Collects a call's argument errors and address ranges; the first error is
+// kept.  Everything here runs before any HIP call.
+struct Args {
+  struct Range {
+    uintptr_t lo, hi;
+    const char* name;
+    int64_t ld;
+    bool written;
+  };
+  muon_status_t status = MUON_OK;
+  std::string msg;
+  std::vector<Range> ranges;
+
+  bool ok() const { return status == MUON_OK; }
+  void fail(muon_status_t s, const std::string& m) {
+    if (ok()) {
+      status = s;
+      msg = m;
+    }
+  }
+  void size(const char* name, int64_t v, int64_t lo, int64_t hi) {
+    if (v < lo) fail(MUON_ERR_INVALID_ARG, std::string(name) + " below " + std::to_string(lo));
+    else if (v > hi) fail(MUON_ERR_UNSUPPORTED, std::string(name) + " above " + std::to_string(hi));
+  }
+  void dtype(const char* name, int32_t d) {
+    if (d != MUON_DTYPE_F32 && d != MUON_DTYPE_BF16)
+      fail(MUON_ERR_INVALID_ARG, std::string("unknown ") + name);
+  }
+  // rows × cols of esz-byte elements; a matrix without rows may be NULL
+  void matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t esz,
+              bool written) {
+    if (!ok() || rows == 0) return;
+    if (!p) return fail(MUON_ERR_INVALID_ARG, std::string(name) + " is NULL");
+    if ((uintptr_t)p % esz) return fail(MUON_ERR_INVALID_ARG, std::string(name) + " is not aligned to its type");
+    if (ld < cols) return fail(MUON_ERR_INVALID_ARG, std::string(name) + ": row stride below the row length");
+    if (ld > kMaxLd) return fail(MUON_ERR_UNSUPPORTED, std::string(name) + ": row stride above 2^32");
+    const uintptr_t lo = (uintptr_t)p;
+    ranges.push_back({lo, lo + (uintptr_t)(((rows - 1) * ld + cols) * (int64_t)esz), name, ld, written});
+  }
+  void buffer(const char* name, const void* p, size_t have, size_t need, bool written) {
+    if (!ok() || need == 0) return;
+    if (!p) return fail(MUON_ERR_WORKSPACE, std::string(name) + " is NULL");
+    if ((uintptr_t)p & 255) return fail(MUON_ERR_WORKSPACE, std::string(name) + " not 256-byte aligned");
+    if (have < need)
+      return fail(MUON_ERR_WORKSPACE, std::string(name) + " too small: need " + std::to_string(need) +
+                                          " bytes, got " + std::to_string(have));
+    const uintptr_t lo = (uintptr_t)p;
+    ranges.push_back({lo, lo + need, name, 0, written});
+  }
+  // Written ranges overlap nothing, but for the pairs `same` allows (an
+  // output that is the same matrix as an input).
+  template <typename F>
+  void aliases(F&& same) {
+    for (size_t i = 0; ok() && i < ranges.size(); ++i)
+      for (size_t j = 0; ok() && j < ranges.size(); ++j) {
+        const Range &a = ranges[i], &b = ranges[j];
+        if (i == j || !a.written || !(a.lo < b.hi && b.lo < a.hi)) continue;
+        if (!b.written && a.lo == b.lo && a.hi == b.hi && a.ld == b.ld && same(a.name, b.name)) continue;
+        fail(MUON_ERR_ALIAS, std::string(a.name) + " overlaps " + b.name);
+      }
+  }
+  void aliases() {
+    aliases([](const char*, const char*) { return false; });
+  }
+  muon_status_t report() const {
+    if (!ok()) set_last_error(msg);
+    return status;
+  }
+};
+
+muon_status_t check_device() {
+  int n = 0;
+  if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
+    set_last_error("no HIP device visible");
+    return MUON_ERR_NO_DEVICE;
+  }
+  return MUON_OK;
+}
+
+// Status of a launch; with MUON_DEBUG_SYNC=1 (and no capture) it waits for
+// the stream, so that a failing kernel is named.
+muon_status_t launched(const char* what, hipError_t e, hipStream_t st) {
+  if (e == hipSuccess) {
+    const char* dbg = std::getenv("MUON_DEBUG_SYNC");
+    if (dbg && dbg[0] == '1') {
+      hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+      if (hipStreamIsCapturing(st, &cs) == hipSuccess && cs == hipStreamCaptureStatusNone) {
+        e = hipStreamSynchronize(st);
+        if (e == hipSuccess) e = hipGetLastError();
+      }
+    }
+  }
+  if (e == hipSuccess) return MUON_OK;
+  set_last_error(std::string(what) + ": " + hipGetErrorString(e));
+  return MUON_ERR_HIP;
+}
+
+// No exception leaves an entry point.
+template <typename F>
+muon_status_t guarded(F&& f) {
+  try {
+    set_last_error("");
+    return f();
+  } catch (const std::exception& e) {
+    try {
+      set_last_error(e.what());
+    } catch (...) {
+    }
+    return MUON_ERR_INVALID_ARG;
+  } catch (...) {
+    return MUON_ERR_INVALID_ARG;
+  }
+}
+
+size_t esize(int32_t dtype) { return dtype == MUON_DTYPE_BF16 ? 2 : 4; }
+
+// Rows of whole 16-byte chunks at 16-byte aligned addresses.
+bool whole_chunks(const void* p, int64_t ld, int64_t cols, size_t esz) {
+  const int64_t v = 16 / (int64_t)esz;
+  return ((uintptr_t)p & 15) == 0 && ld % v == 0 && cols % v == 0;
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// ----- embedding gradient's workspace ----------------------------------------
+struct EmbedLayout {
+  size_t key[2], idx[2], counts, pieces, total;
+};
+EmbedLayout embed_layout(int64_t tokens, int64_t dim) {
+  EmbedLayout l{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += align256(n);
+    return o;
+  };
+  const bool small = tokens <= kEmbedSmallSort;
+  for (int i = 0; i < 2; ++i) {
+    const size_t n = i && small ? 0 : (size_t)tokens * 4;
+    l.key[i] = take(n);
+    l.idx[i] = take(n);
+  }
+  const int64_t blocks = (tokens + kEmbedSortBlock - 1) / kEmbedSortBlock;
+  l.counts = take(small ? 0 : (size_t)(blocks << kEmbedSortBits) * 4);
+  l.pieces = take((size_t)(tokens / kEmbedPiece) * dim * 4);
+  l.total = at;
+  return l;
+}
+
+// ----- gated feed-forward block ----------------------------------------------
+struct FfnLayout {
+  int64_t ldh;                  // hidden rounded up to 8
+  size_t ab, savedH, saved;     // in `saved`
+  size_t h, fwd;                // workspace of the forward pass
+  size_t dgu, bwd;              // workspace of the backward pass
+};
+FfnLayout ffn_layout(const muon_ffn_t& f) {
+  FfnLayout l{};
+  const size_t e = esize(f.dtype);
+  l.ldh = (f.hidden + 7) / 8 * 8;
+  const size_t rows = (size_t)f.tokens * l.ldh * e;
+  l.ab = 0;
+  l.savedH = align256(2 * rows);
+  l.saved = l.savedH + align256(rows);
+  l.h = 0;
+  l.fwd = align256(rows);
+  l.dgu = 0;
+  l.bwd = align256(2 * rows);
+  return l;
+}
+
+void ffn_sizes(Args& a, const muon_ffn_t* f) {
+  if (!f) return a.fail(MUON_ERR_INVALID_ARG, "ffn is NULL");
+  a.size("tokens", f->tokens, 0, kMaxTokens);
+  a.size("model", f->model, 1, kMaxWidth);
+  a.size("hidden", f->hidden, 1, kMaxWidth);
+  a.dtype("dtype", f->dtype);
+}
+
+void ffn_weights(Args& a, const muon_ffn_t& f) {
+  const size_t e = esize(f.dtype);
+  a.matrix("w_gate", f.w_gate, f.hidden, f.model, f.ld_gate, e, false);
+  a.matrix("w_up", f.w_up, f.hidden, f.model, f.ld_up, e, false);
+  a.matrix("w_down", f.w_down, f.model, f.hidden, f.ld_down, e, false);
+}
+
+constexpr int64_t kFfnTile = 128;
+int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+// Sets prob q's tile range (tile edges tm × tn).
+void set_tiles(FfnLaunch& L, int q, int64_t tm, int64_t tn) {
+  L.tiles[q + 1] = L.tiles[q] + (int32_t)(tiles_of(L.prob[q].M, tm) * tiles_of(L.prob[q].N, tn));
+  L.nprob = q + 1;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+muon_status_t muon_embedding(const void* ids, int32_t id_bytes, int64_t tokens, const void* weight,
+                             int64_t ld_weight, int64_t vocab, int64_t dim, float scale, void* out,
+                             int64_t ld_out, muon_dtype_t dtype, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    a.size("tokens", tokens, 0, kMaxTokens);
+    a.size("vocab", vocab, 1, kMaxVocab);
+    a.size("dim", dim, 1, kMaxWidth);
+    a.dtype("dtype", dtype);
+    if (id_bytes != 4 && id_bytes != 8) a.fail(MUON_ERR_INVALID_ARG, "id_bytes must be 4 or 8");
+    if (!std::isfinite(scale)) a.fail(MUON_ERR_INVALID_ARG, "scale not finite");
+    if (a.ok()) {
+      const size_t e = esize(dtype);
+      a.matrix("ids", ids, tokens > 0, tokens, tokens, id_bytes, false);
+      a.matrix("weight", weight, tokens > 0 ? vocab : 0, dim, ld_weight, e, false);
+      a.matrix("out", out, tokens, dim, ld_out, e, true);
+    }
+    a.aliases();
+    if (!a.ok()) return a.report();
+    if (tokens == 0) return MUON_OK;
+    const muon_status_t s = check_device();
+    if (s != MUON_OK) return s;
+    const size_t e = esize(dtype);
+    EmbedLaunch L{ids, id_bytes == 8, dtype == MUON_DTYPE_BF16, tokens, vocab, dim, weight, ld_weight,
+                  out, ld_out, scale,
+                  whole_chunks(weight, ld_weight, dim, e) && whole_chunks(out, ld_out, dim, e)};
+    return launched("embedding", launch_embedding(L, (hipStream_t)stream), (hipStream_t)stream);
+  });
+}
+
+muon_status_t muon_embedding_grad_workspace_size(int64_t tokens, int64_t vocab, int64_t dim,
+                                                 size_t* bytes) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    a.size("tokens", tokens, 0, kMaxTokens);
+    a.size("vocab", vocab, 1, kMaxVocab);
+    a.size("dim", dim, 1, kMaxWidth);
+    if (!bytes) a.fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+    if (!a.ok()) return a.report();
+    *bytes = embed_layout(tokens, dim).total;
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_embedding_grad(const void* dy, int64_t ld_dy, const void* ids, int32_t id_bytes,
+                                  int64_t tokens, int64_t vocab, int64_t dim, float scale,
+                                  void* dweight, int64_t ld_dweight, muon_dtype_t dtype,
+                                  muon_dtype_t dweight_dtype, int32_t accumulate, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    a.size("tokens", tokens, 0, kMaxTokens);
+    a.size("vocab", vocab, 1, kMaxVocab);
+    a.size("dim", dim, 1, kMaxWidth);
+    a.dtype("dtype", dtype);
+    a.dtype("dweight_dtype", dweight_dtype);
+    if (id_bytes != 4 && id_bytes != 8) a.fail(MUON_ERR_INVALID_ARG, "id_bytes must be 4 or 8");
+    if (!std::isfinite(scale)) a.fail(MUON_ERR_INVALID_ARG, "scale not finite");
+    EmbedLayout lay{};
+    if (a.ok()) {
+      lay = embed_layout(tokens, dim);
+      a.matrix("ids", ids, tokens > 0, tokens, tokens, id_bytes, false);
+      a.matrix("dy", dy, tokens, dim, ld_dy, esize(dtype), false);
+      a.matrix("dweight", dweight, vocab, dim, ld_dweight, esize(dweight_dtype), true);
+      a.buffer("workspace", workspace, workspace_bytes, lay.total, true);
+    }
+    a.aliases();
+    if (!a.ok()) return a.report();
+    if (tokens == 0 && accumulate) return MUON_OK;
+    const muon_status_t s = check_device();
+    if (s != MUON_OK) return s;
+    char* ws = (char*)workspace;
+    EmbedGradLaunch L{};
+    L.ids = ids;
+    L.id64 = id_bytes == 8;
+    L.dyBf16 = dtype == MUON_DTYPE_BF16;
+    L.dwBf16 = dweight_dtype == MUON_DTYPE_BF16;
+    L.accumulate = accumulate != 0;
+    L.tokens = tokens;
+    L.vocab = vocab;
+    L.dim = dim;
+    L.dy = dy;
+    L.ldy = ld_dy;
+    L.dw = dweight;
+    L.ldw = ld_dweight;
+    L.scale = scale;
+    L.vec = whole_chunks(dy, ld_dy, dim, esize(dtype));
+    L.vecw = whole_chunks(dweight, ld_dweight, dim, esize(dweight_dtype));
+    for (int i = 0; i < 2; ++i) {
+      L.key[i] = (uint32_t*)(ws + lay.key[i]);
+      L.idx[i] = (uint32_t*)(ws + lay.idx[i]);
+    }
+    L.counts = (uint32_t*)(ws + lay.counts);
+    L.pieces = (float*)(ws + lay.pieces);
+    return launched("embedding gradient", launch_embedding_grad(L, (hipStream_t)stream), (hipStream_t)stream);
+  });
+}
+
+muon_status_t muon_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                            const void* weight, muon_dtype_t weight_dtype, float eps, void* y,
+                            int64_t ld_y, void* sum, int64_t ld_sum, float* rstd, int64_t tokens,
+                            int64_t dim, muon_dtype_t dtype, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    a.size("tokens", tokens, 0, kMaxTokens);
+    a.size("dim", dim, 1, kMaxWidth);
+    a.dtype("dtype", dtype);
+    a.dtype("weight_dtype", weight_dtype);
+    if (!std::isfinite(eps) || eps < 0) a.fail(MUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (sum && !residual && tokens > 0) a.fail(MUON_ERR_INVALID_ARG, "sum without residual");
+    const size_t e = esize(dtype);
+    if (a.ok()) {
+      a.matrix("x", x, tokens, dim, ld_x, e, false);
+      if (residual) a.matrix("residual", residual, tokens, dim, ld_residual, e, false);
+      a.matrix("weight", weight, tokens > 0, dim, dim, esize(weight_dtype), false);
+      a.matrix("y", y, tokens, dim, ld_y, e, true);
+      if (sum) a.matrix("sum", sum, tokens, dim, ld_sum, e, true);
+      if (rstd) a.matrix("rstd", rstd, tokens > 0, tokens, tokens, 4, true);
+    }
+    a.aliases([](const char* out, const char* in) {
+      return (out[0] == 'y' || out[0] == 's') && (in[0] == 'x' || std::string(in) == "residual");
+    });
+    if (!a.ok()) return a.report();
+    if (tokens == 0) return MUON_OK;
+    const muon_status_t s = check_device();
+    if (s != MUON_OK) return s;
+    NormFwdLaunch L{x, residual, weight, y, sum, rstd, ld_x, ld_residual, ld_y, ld_sum, tokens, dim, eps,
+                    dtype == MUON_DTYPE_BF16, weight_dtype == MUON_DTYPE_BF16,
+                    whole_chunks(x, ld_x, dim, e) && whole_chunks(y, ld_y, dim, e) &&
+                        (!residual || whole_chunks(residual, ld_residual, dim, e)) &&
+                        (!sum || whole_chunks(sum, ld_sum, dim, e))};
+    return launched("rms norm", launch_rms_norm(L, (hipStream_t)stream), (hipStream_t)stream);
+  });
+}
+
+muon_status_t muon_rms_norm_grad_workspace_size(int64_t tokens, int64_t dim, size_t* bytes) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    a.size("tokens", tokens, 0, kMaxTokens);
+    a.size("dim", dim, 1, kMaxWidth);
+    if (!bytes) a.fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+    if (!a.ok()) return a.report();
+    *bytes = tokens == 0 ? 0 : align256((size_t)rms_norm_grad_blocks(tokens, dim) * dim * 4);
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_rms_norm_grad(const void* dy, int64_t ld_dy, const void* s, int64_t ld_s,
+                                 const void* weight, muon_dtype_t weight_dtype, const float* rstd,
+                                 const void* dsum, int64_t ld_dsum, void* dx, int64_t ld_dx,
+                                 void* dweight, int32_t accumulate, int64_t tokens, int64_t dim,
+                                 muon_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    a.size("tokens", tokens, 0, kMaxTokens);
+    a.size("dim", dim, 1, kMaxWidth);
+    a.dtype("dtype", dtype);
+    a.dtype("weight_dtype", weight_dtype);
+    const size_t e = esize(dtype);
+    size_t need = 0;
+    if (a.ok()) {
+      if (dweight && tokens > 0) need = align256((size_t)rms_norm_grad_blocks(tokens, dim) * dim * 4);
+      a.matrix("dy", dy, tokens, dim, ld_dy, e, false);
+      a.matrix("s", s, tokens, dim, ld_s, e, false);
+      a.matrix("weight", weight, tokens > 0, dim, dim, esize(weight_dtype), false);
+      a.matrix("rstd", rstd, tokens > 0, tokens, tokens, 4, false);
+      if (dsum) a.matrix("dsum", dsum, tokens, dim, ld_dsum, e, false);
+      a.matrix("dx", dx, tokens, dim, ld_dx, e, true);
+      if (dweight) a.matrix("dweight", dweight, 1, dim, dim, esize(weight_dtype), true);
+      a.buffer("workspace", workspace, workspace_bytes, need, true);
+    }
+    a.aliases([](const char* out, const char* in) {
+      return std::string(out) == "dx" && (std::string(in) == "dy" || std::string(in) == "dsum");
+    });
+    if (!a.ok()) return a.report();
+    if (tokens == 0 && (!dweight || accumulate)) return MUON_OK;
+    const muon_status_t st = check_device();
+    if (st != MUON_OK) return st;
+    NormGradLaunch L{};
+    L.dy = dy;
+    L.s = s;
+    L.w = weight;
+    L.dsum = dsum;
+    L.rstd = rstd;
+    L.dx = dx;
+    L.dw = dweight;
+    L.part = (float*)workspace;
+    L.ldy = ld_dy;
+    L.lds = ld_s;
+    L.ldd = ld_dsum;
+    L.ldx = ld_dx;
+    L.tokens = tokens;
+    L.dim = dim;
+    L.blocks = tokens > 0 ? rms_norm_grad_blocks(tokens, dim) : 0;
+    L.bf16 = dtype == MUON_DTYPE_BF16;
+    L.wBf16 = weight_dtype == MUON_DTYPE_BF16;
+    L.vec = whole_chunks(dy, ld_dy, dim, e) && whole_chunks(s, ld_s, dim, e) && whole_chunks(dx, ld_dx, dim, e) &&
+            (!dsum || whole_chunks(dsum, ld_dsum, dim, e));
+    L.accumulate = accumulate != 0;
+    return launched("rms norm gradient", launch_rms_norm_grad(L, (hipStream_t)stream), (hipStream_t)stream);
+  });
+}
+
+muon_status_t muon_gated_ffn_saved_size(const muon_ffn_t* ffn, size_t* bytes) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    ffn_sizes(a, ffn);
+    if (!bytes) a.fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+    if (!a.ok()) return a.report();
+    *bytes = ffn_layout(*ffn).saved;
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_gated_ffn_workspace_size(const muon_ffn_t* ffn, int32_t grad, size_t* bytes) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    ffn_sizes(a, ffn);
+    if (!bytes) a.fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+    if (!a.ok()) return a.report();
+    const FfnLayout l = ffn_layout(*ffn);
+    *bytes = grad ? l.bwd : l.fwd;
+    return MUON_OK;
+  });
+}
+
+muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x, void* y,
+                             int64_t ld_y, void* saved, size_t saved_bytes, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    ffn_sizes(a, ffn);
+    FfnLayout l{};
+    if (a.ok()) {
+      if (ffn->activation < MUON_ACT_SILU || ffn->activation > MUON_ACT_GELU_TANH)
+        a.fail(MUON_ERR_INVALID_ARG, "unknown activation");
+      l = ffn_layout(*ffn);
+      const size_t e = esize(ffn->dtype);
+      ffn_weights(a, *ffn);
+      a.matrix("x", x, ffn->tokens, ffn->model, ld_x, e, false);
+      a.matrix("y", y, ffn->tokens, ffn->model, ld_y, e, true);
+      if (saved) a.buffer("saved", saved, saved_bytes, l.saved, true);
+      a.buffer("workspace", workspace, workspace_bytes, l.fwd, true);
+    }
+    a.aliases();
+    if (!a.ok()) return a.report();
+    if (ffn->tokens == 0) return MUON_OK;
+    muon_status_t s = check_device();
+    if (s != MUON_OK) return s;
+    const hipStream_t st = (hipStream_t)stream;
+    const bool bf16 = ffn->dtype == MUON_DTYPE_BF16;
+    void* h = saved ? (char*)saved + l.savedH : (char*)workspace + l.h;
+    FfnLaunch L{};
+    L.act = ffn->activation;
+    L.ldh = l.ldh;
+    L.ab = saved ? (char*)saved + l.ab : nullptr;
+    L.outBf16 = bf16;
+    FfnProb& p = L.prob[0];
+    p.A[0] = x;
+    p.lda = ld_x;
+    p.B[0] = ffn->w_gate;
+    p.B[1] = ffn->w_up;
+    p.ldb[0] = ffn->ld_gate;
+    p.ldb[1] = ffn->ld_up;
+    p.M = (int32_t)ffn->tokens;
+    p.N = (int32_t)ffn->hidden;
+    p.K[0] = (int32_t)ffn->model;
+    p.C = h;
+    p.ldc = l.ldh;
+    set_tiles(L, 0, kFfnTile, kFfnTile / 2);
+    s = launched("gated projections", launch_ffn_tile32(FFN_GLU, false, false, bf16, L, st), st);
+    if (s != MUON_OK) return s;
+    FfnLaunch D{};
+    D.outBf16 = bf16;
+    FfnProb& d = D.prob[0];
+    d.A[0] = h;
+    d.lda = l.ldh;
+    d.B[0] = ffn->w_down;
+    d.ldb[0] = ffn->ld_down;
+    d.M = (int32_t)ffn->tokens;
+    d.N = (int32_t)ffn->model;
+    d.K[0] = (int32_t)ffn->hidden;
+    d.C = y;
+    d.ldc = ld_y;
+    set_tiles(D, 0, kFfnTile, kFfnTile);
+    return launched("down projection", launch_ffn_tile32(FFN_STORE, false, false, bf16, D, st), st);
+  });
+}
+
+muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t ld_x,
+                                  const void* dy, int64_t ld_dy, const void* saved,
+                                  size_t saved_bytes, const muon_ffn_grads_t* grads,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    Args a;
+    ffn_sizes(a, ffn);
+    if (!grads) a.fail(MUON_ERR_INVALID_ARG, "grads is NULL");
+    FfnLayout l{};
+    bool wantW = false;
+    if (a.ok()) {
+      l = ffn_layout(*ffn);
+      const size_t e = esize(ffn->dtype);
+      wantW = grads->dw_gate || grads->dw_up || grads->dw_down;
+      if (wantW) a.dtype("grad_dtype", grads->grad_dtype);
+      const size_t eg = esize(grads->grad_dtype);
+      ffn_weights(a, *ffn);
+      a.matrix("x", x, ffn->tokens, ffn->model, ld_x, e, false);
+      a.matrix("dy", dy, ffn->tokens, ffn->model, ld_dy, e, false);
+      a.buffer("saved", saved, saved_bytes, l.saved, false);
+      if (grads->dx) a.matrix("dx", grads->dx, ffn->tokens, ffn->model, grads->ld_dx, e, true);
+      if (wantW) {
+        a.matrix("dw_gate", grads->dw_gate, ffn->hidden, ffn->model, grads->ld_gate, eg, true);
+        a.matrix("dw_up", grads->dw_up, ffn->hidden, ffn->model, grads->ld_up, eg, true);
+        a.matrix("dw_down", grads->dw_down, ffn->model, ffn->hidden, grads->ld_down, eg, true);
+      }
+      a.buffer("workspace", workspace, workspace_bytes, l.bwd, true);
+    }
+    a.aliases();
+    if (!a.ok()) return a.report();
+    if (!wantW && (!grads->dx || ffn->tokens == 0)) return MUON_OK;
+    if (ffn->tokens == 0 && grads->accumulate) return MUON_OK;
+    muon_status_t s = check_device();
+    if (s != MUON_OK) return s;
+    const hipStream_t st = (hipStream_t)stream;
+    const bool bf16 = ffn->dtype == MUON_DTYPE_BF16;
+    const size_t e = esize(ffn->dtype);
+    const char* sv = (const char*)saved;
+    char* dgu = (char*)workspace + l.dgu;
+    const int32_t T = (int32_t)ffn->tokens, D = (int32_t)ffn->model, F = (int32_t)ffn->hidden;
+    if (T > 0) {
+      FfnLaunch L{};
+      L.ldh = l.ldh;
+      L.ab = (void*)(sv + l.ab);
+      FfnProb& p = L.prob[0];
+      p.A[0] = dy;
+      p.lda = ld_dy;
+      p.B[0] = ffn->w_down;
+      p.ldb[0] = ffn->ld_down;
+      p.M = T;
+      p.N = F;
+      p.K[0] = D;
+      p.C = dgu;
+      p.ldc = 2 * l.ldh;
+      set_tiles(L, 0, kFfnTile, kFfnTile);
+      s = launched("gradient of the gated product", launch_ffn_tile32(FFN_BACK, false, true, bf16, L, st), st);
+      if (s != MUON_OK) return s;
+    }
+    if (T > 0 && grads->dx) {
+      FfnLaunch L{};
+      L.outBf16 = bf16;
+      FfnProb& p = L.prob[0];
+      p.A[0] = dgu;
+      p.A[1] = dgu + l.ldh * e;
+      p.lda = 2 * l.ldh;
+      p.B[0] = ffn->w_gate;
+      p.B[1] = ffn->w_up;
+      p.ldb[0] = ffn->ld_gate;
+      p.ldb[1] = ffn->ld_up;
+      p.M = T;
+      p.N = D;
+      p.K[0] = p.K[1] = F;
+      p.C = grads->dx;
+      p.ldc = grads->ld_dx;
+      set_tiles(L, 0, kFfnTile, kFfnTile);
+      s = launched("gradient of the input", launch_ffn_tile32(FFN_STORE, false, true, bf16, L, st), st);
+      if (s != MUON_OK) return s;
+    }
+    if (!wantW) return MUON_OK;
+    FfnLaunch L{};
+    L.outBf16 = grads->grad_dtype == MUON_DTYPE_BF16;
+    L.accumulate = grads->accumulate != 0;
+    for (int q = 0; q < 3; ++q) {
+      FfnProb& p = L.prob[q];
+      p.A[0] = q < 2 ? (const void*)(dgu + q * l.ldh * e) : dy;
+      p.lda = q < 2 ? 2 * l.ldh : ld_dy;
+      p.B[0] = q < 2 ? x : (const void*)(sv + l.savedH);
+      p.ldb[0] = q < 2 ? ld_x : l.ldh;
+      p.M = q < 2 ? F : D;
+      p.N = q < 2 ? D : F;
+      p.K[0] = T;
+      p.C = q == 0 ? grads->dw_gate : q == 1 ? grads->dw_up : grads->dw_down;
+      p.ldc = q == 0 ? grads->ld_gate : q == 1 ? grads->ld_up : grads->ld_down;
+      set_tiles(L, q, kFfnTile, kFfnTile);
+    }
+    return launched("gradients of the weights", launch_ffn_tile32(FFN_STORE, true, true, bf16, L, st), st);
+  });
+}
+
+}  // extern "C"
