@@ -148,8 +148,10 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of `saved`, and of the workspaces of muon_gated_ffn (grad = 0) and
- * muon_gated_ffn_grad (grad = 1).  The weights' addresses and strides and
- * ffn->activation are not read; the sizes cover any alignment. */
+ * muon_gated_ffn_grad (grad = 1).  ffn->activation is not read.  For bf16 the
+ * workspace has room for aligned copies of x and dy, and of each weight whose
+ * address, stride and row length do not give 16-byte aligned rows of whole
+ * 16-byte chunks; `saved` does not depend on that. */
 muon_status_t muon_gated_ffn_saved_size(const muon_ffn_t* ffn, size_t* bytes);
 muon_status_t muon_gated_ffn_workspace_size(const muon_ffn_t* ffn, int32_t grad, size_t* bytes);
 

@@ -1,0 +1,312 @@
+// Products of the gated feed-forward block on bf16 MFMA.
+//
+// C[i][j] = Σ_k A[i][k]·B[j][k] on TILE×TILE tiles (TILE 256: eight waves of
+// 128×64; TILE 128: four waves of 64×64), k in steps of 32, with the 256-tile
+// kernel's scheme of gemm.hpp: operands go straight from global memory into
+// a 4-slot LDS ring (three k-tiles in flight), one barrier per k-tile with
+// explicit vmcnt waits, fragments of the next quarter read while the MFMAs of
+// the current one run.  What differs from it:
+//  * an operand is k-contiguous (LDS rows of 32 k, read with 16-byte reads) or
+//    row-contiguous (LDS panel of 32 k-rows, read with transposing reads):
+//    the weights are used both ways and nothing is ever transposed in memory;
+//  * no padded operands: the loads are buffer loads whose lanes point past the
+//    buffer (and so deliver zeros) outside rows and k.  The k loop always runs
+//    a multiple of four k-tiles, the surplus ones zero;
+//  * FFN_GLU: a tile is TILE rows × TILE/2 columns of both projections.  Of a
+//    wave's 64 B rows 32 are w_gate's and 32 w_up's, so g and u of one element
+//    meet in one lane and the activation runs on fp32 registers.
+// Operands need 16-byte aligned rows of whole 16-byte chunks; the host copies
+// others once.
+#pragma once
+
+#include "ffn_epi.hpp"
+#include "gemm.hpp"
+
+namespace muon {
+
+typedef __bf16 fbf16x8 __attribute__((ext_vector_type(8)));
+typedef int32_t fi32x4 __attribute__((ext_vector_type(4)));
+
+// Buffer resource over [p, p + 2 GiB).
+__device__ __forceinline__ fi32x4 f_buffer(uint64_t p) {
+  fi32x4 r;
+  r[0] = (int32_t)(uint32_t)p;
+  r[1] = (int32_t)(uint32_t)(p >> 32);
+  r[2] = (int32_t)0x80000000u;
+  r[3] = 0x00020000;
+  return r;
+}
+constexpr uint32_t kFfnNowhere = 0x80000000u;  // outside every such buffer: reads as zero
+
+// One 16-byte buffer→LDS load per lane: lane l writes lds_base + 16·l.
+__device__ __forceinline__ void f_dma16(uint32_t lds_base, uint32_t off, fi32x4 rsrc) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds_base), "v"(off), "s"(rsrc)
+               : "memory", "m0");
+}
+
+// Four accumulators of one row → columns [j, j + 4) of C.
+__device__ __forceinline__ void f_store4(void* C, int64_t ldc, int64_t i, int64_t j, int64_t n, bool bf16,
+                                         bool accumulate, bool vec, const floatx4& c) {
+  const int64_t e = i * ldc + j;
+  if (bf16) {
+    uint16_t* o = (uint16_t*)C + e;
+    if (vec && j + 4 <= n) {
+      float v[4] = {c[0], c[1], c[2], c[3]};
+      if (accumulate) {
+        const uint2 u = *(const uint2*)o;
+        v[0] += __uint_as_float(u.x << 16);
+        v[1] += __uint_as_float(u.x & 0xffff0000u);
+        v[2] += __uint_as_float(u.y << 16);
+        v[3] += __uint_as_float(u.y & 0xffff0000u);
+      }
+      *(uint2*)o = make_uint2(l_f32_bf16(v[0]) | (l_f32_bf16(v[1]) << 16),
+                              l_f32_bf16(v[2]) | (l_f32_bf16(v[3]) << 16));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (j + r < n) o[r] = (uint16_t)l_f32_bf16(c[r] + (accumulate ? l_bf16_f32(o[r]) : 0.f));
+    }
+  } else {
+    float* o = (float*)C + e;
+    if (vec && j + 4 <= n) {
+      lf32x4 v = {c[0], c[1], c[2], c[3]};
+      if (accumulate) v += *(const lf32x4*)o;
+      *(lf32x4*)o = v;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (j + r < n) o[r] = c[r] + (accumulate ? o[r] : 0.f);
+    }
+  }
+}
+
+template <int TILE, int EPI, bool AROW, bool BROW>
+__global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
+  constexpr int NW = TILE / 32, WN = TILE / 64, WTM = TILE / 2, FM = WTM / 16, FN = 4;
+  constexpr int KB = 32;                              // k per k-tile
+  constexpr int kHalf = TILE * KB * 2, kSlot = 2 * kHalf;  // bytes of an operand's tile, of a slot
+  constexpr int NQ = FM / 2;                          // quarters (pairs of block rows) per k-tile
+  __shared__ __attribute__((aligned(1024))) char lds[4 * kSlot];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int lc = lane & 15, lg = lane >> 4;
+
+  // problem, tile and k split of this workgroup
+  const int b = xcd_window_remap(blockIdx.x, gridDim.x, kXcdShift);
+  int q = 0;
+  while (q + 1 < L.nprob && b >= L.tiles[q + 1]) ++q;
+  const FfnProb& P = L.prob[q];
+  constexpr int TN = EPI == FFN_GLU ? TILE / 2 : TILE;
+  const int tilesM = (P.M + TILE - 1) / TILE, tilesN = (P.N + TN - 1) / TN;
+  int t = b - L.tiles[q];
+  const int split = t / (tilesM * tilesN);
+  t -= split * (tilesM * tilesN);
+  // bands of four tile rows, column by column inside a band
+  const int band = t / (kBand * tilesN), r0 = band * kBand, bh = min(kBand, tilesM - r0);
+  const int tb = t - r0 * tilesN, tj = tb / bh, ti = r0 + tb - tj * bh;
+  const int64_t i0 = (int64_t)ti * TILE, j0 = (int64_t)tj * TN;
+
+  const int KT0 = (P.K[0] + KB - 1) / KB;
+  const int KT = KT0 + (P.K[1] + KB - 1) / KB;
+  const int per = L.splitTiles;  // k-tiles per split, a multiple of four
+  const int kt0 = split * per;
+  const int n = min(per, (KT - kt0 + 3) & ~3);
+
+  // Each lane's place in the loads (two per operand and k-tile): byte offset
+  // from the operand's tile start, the k it holds, and whether its row (or
+  // its chunk of a row-contiguous operand) exists.
+  uint32_t offA[2], offB[2];
+  int kA[2], kB[2];
+  auto place = [&](bool rowc, int64_t ld, int64_t first, int64_t extent, int p, uint32_t& off, int& k) {
+    if (rowc) {
+      constexpr int CH = TILE / 8, RPI = 64 / CH;  // chunks of a k-row, k-rows per load
+      const int r = wave * (KB / NW) + p * RPI + lane / CH;
+      const int c = (lane % CH) ^ tswz(r);
+      k = r;
+      off = first + c * 8 < extent ? (uint32_t)(r * ld * 2 + c * 16) : kFfnNowhere;
+    } else {
+      const int r = wave * 32 + p * 16 + (lane >> 2);
+      const int c = (lane & 3) ^ swz4(r);
+      k = c * 8;
+      off = first + r < extent ? (uint32_t)(r * ld * 2 + c * 16) : kFfnNowhere;
+    }
+  };
+  const int bsel = EPI == FFN_GLU ? (wave & 1) : 0;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    place(AROW, P.lda, i0, AROW ? P.extA : P.M, p, offA[p], kA[p]);
+    if constexpr (EPI == FFN_GLU) {
+      // rows 64·c + 0..31 of the tile are w_gate's rows 32·c.., the next 32 w_up's
+      const int r = wave * 32 + p * 16 + (lane >> 2), c = (lane & 3) ^ swz4(r);
+      const int f = (r >> 6) * 32 + (r & 31);
+      kB[p] = c * 8;
+      offB[p] = j0 + f < P.N ? (uint32_t)(f * P.ldb[bsel] * 2 + c * 16) : kFfnNowhere;
+    } else {
+      place(BROW, P.ldb[0], j0, BROW ? P.extB : P.N, p, offB[p], kB[p]);
+    }
+  }
+  const int dst = wave * 2048;  // this wave's part of an operand's tile, either layout
+  auto issue = [&](int slot, int kt) __attribute__((always_inline)) {
+    const int z = EPI == FFN_GLU ? 0 : kt >= KT0;
+    const int k0 = (z ? kt - KT0 : kt) * KB, left = P.K[z] - k0;
+    const uint64_t a = (uint64_t)P.A[z] + (AROW ? ((uint64_t)k0 * P.lda + i0) * 2 : ((uint64_t)i0 * P.lda + k0) * 2);
+    const int zb = EPI == FFN_GLU ? bsel : z;
+    const int64_t ldb = P.ldb[zb];
+    const uint64_t bb = (uint64_t)P.B[zb] + (BROW ? ((uint64_t)k0 * ldb + j0) * 2 : ((uint64_t)j0 * ldb + k0) * 2);
+    const fi32x4 ra = f_buffer(a), rb = f_buffer(bb);
+    const uint32_t s = __builtin_amdgcn_readfirstlane(lds_addr(lds) + slot * kSlot + dst);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) f_dma16(s + p * 1024, kA[p] < left ? offA[p] : kFfnNowhere, ra);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) f_dma16(s + kHalf + p * 1024, kB[p] < left ? offB[p] : kFfnNowhere, rb);
+  };
+
+  floatx4 acc[FM][FN];
+#pragma unroll
+  for (int fi = 0; fi < FM; ++fi)
+#pragma unroll
+    for (int fj = 0; fj < FN; ++fj) acc[fi][fj] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+  const int sw = swz4(lc);
+  auto frag = [&](const char* pan, int row0, auto rowc) __attribute__((always_inline)) {
+    if constexpr (decltype(rowc)::value) {
+      auto rd = [&](int k0) {
+        const int k = k0 + (lc >> 2), i = row0 + 4 * (lc & 3);
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s4_t)(pan + k * (TILE * 2) + (((i >> 3) ^ tswz(k)) << 4) + (i & 7) * 2));
+      };
+      const short4_t lo = rd(8 * lg), hi = rd(8 * lg + 4);
+      return __builtin_bit_cast(fbf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *(const fbf16x8*)(pan + (row0 + lc) * 64 + ((lg ^ sw) << 4));
+    }
+  };
+  constexpr auto kAr = std::bool_constant<AROW>{};
+  constexpr auto kBr = std::bool_constant<BROW>{};
+  fbf16x8 fb0[FN], fb1[FN], fax[2], fay[2];
+  auto load_a = [&](fbf16x8 (&fa)[2], const char* st, int qq) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f) fa[f] = frag(st, wm * WTM + (2 * qq + f) * 16, kAr);
+  };
+  auto load_b = [&](fbf16x8 (&fb)[FN], const char* st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int fj = 0; fj < FN; ++fj) fb[fj] = frag(st + kHalf, wn * 64 + fj * 16, kBr);
+  };
+  // operand roles swapped: a lane holds four consecutive columns of one row
+  auto mma = [&](const fbf16x8 (&fa)[2], const fbf16x8 (&fb)[FN], auto qc) __attribute__((always_inline)) {
+    constexpr int qq = decltype(qc)::value;
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+      for (int fj = 0; fj < FN; ++fj)
+        acc[2 * qq + f][fj] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[fj], fa[f], acc[2 * qq + f][fj], 0, 0, 0);
+  };
+  // One k-tile: all quarters but the last while the next quarter's fragments
+  // are read; then the slot is free for every wave, k-tile + 1 has landed (each
+  // k-tile is four loads per wave, two stay in flight), the slot is refilled,
+  // and the last quarter runs while the next k-tile's first fragments are read.
+  auto step = [&](int cur, int nxt, int kt, const fbf16x8 (&fb)[FN], fbf16x8 (&fbn)[FN]) __attribute__((always_inline)) {
+    const char* st = lds + cur * kSlot;
+    static_for<0, NQ - 1>([&](auto qc) __attribute__((always_inline)) {
+      constexpr int qq = decltype(qc)::value;
+      load_a(qq & 1 ? fax : fay, st, qq + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      mma(qq & 1 ? fay : fax, fb, qc);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    issue(cur, kt + 4);
+    const char* sn = lds + nxt * kSlot;
+    load_b(fbn, sn);
+    load_a(fax, sn, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    mma(fay, fb, std::integral_constant<int, NQ - 1>{});
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  static_assert(NQ % 2 == 0, "the last quarter's fragments are in fay");
+  if (n > 0) {
+    // loads past this split's k-tiles are zeros that no MFMA reads
+    issue(0, kt0);
+    issue(1, kt0 + 1);
+    issue(2, kt0 + 2);
+    issue(3, kt0 + 3);
+    asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
+    load_b(fb0, lds);
+    load_a(fax, lds, 0);
+    for (int kt = kt0; kt < kt0 + n; kt += 4) {
+      step(0, 1, kt, fb0, fb1);
+      step(1, 2, kt + 1, fb1, fb0);
+      step(2, 3, kt + 2, fb0, fb1);
+      step(3, 0, kt + 3, fb1, fb0);
+    }
+  }
+  // no load may still be on its way into LDS when the workgroup ends
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  // acc[fi][fj][r]: row fi·16 + lane%16, column fj·16 + 4·(lane/16) + r
+#pragma unroll
+  for (int fi = 0; fi < FM; ++fi) {
+    const int64_t i = i0 + wm * WTM + fi * 16 + lc;
+    if (i >= P.M) continue;
+    if constexpr (EPI == FFN_GLU) {
+#pragma unroll
+      for (int fj = 0; fj < 2; ++fj) {
+        const int64_t j = j0 + wn * 32 + fj * 16 + 4 * lg;
+        if (j >= L.ldh) continue;  // ldh is a multiple of 8; columns N .. ldh − 1 come out as zeros
+        uint32_t h[4], ca[4], cb[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float v, d;
+          const float u = acc[fi][fj + 2][r];
+          ffn_act<false>(L.act, acc[fi][fj][r], v, d);
+          h[r] = l_f32_bf16(v * u);
+          ca[r] = l_pack_e6m9(u * d);
+          cb[r] = l_pack_e6m9(v);
+        }
+        *(uint2*)((uint16_t*)P.C + i * P.ldc + j) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        if (L.ab) {
+          uint16_t* o = (uint16_t*)L.ab + i * 2 * L.ldh + j;
+          *(uint2*)o = make_uint2(ca[0] | (ca[1] << 16), ca[2] | (ca[3] << 16));
+          *(uint2*)(o + L.ldh) = make_uint2(cb[0] | (cb[1] << 16), cb[2] | (cb[3] << 16));
+        }
+      }
+    } else if constexpr (EPI == FFN_BACK) {
+#pragma unroll
+      for (int fj = 0; fj < FN; ++fj) {
+        const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;
+        if (j >= L.ldh) continue;
+        const uint16_t* o = (const uint16_t*)L.ab + i * 2 * L.ldh + j;
+        const uint2 ua = *(const uint2*)o, ub = *(const uint2*)(o + L.ldh);
+        uint32_t g[4], u[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t wa = r < 2 ? ua.x : ua.y, wb = r < 2 ? ub.x : ub.y;
+          g[r] = l_f32_bf16(acc[fi][fj][r] * l_unpack_e6m9((wa >> (16 * (r & 1))) & 0xffffu));
+          u[r] = l_f32_bf16(acc[fi][fj][r] * l_unpack_e6m9((wb >> (16 * (r & 1))) & 0xffffu));
+        }
+        uint16_t* c = (uint16_t*)P.C + i * 2 * L.ldh + j;
+        *(uint2*)c = make_uint2(g[0] | (g[1] << 16), g[2] | (g[3] << 16));
+        *(uint2*)(c + L.ldh) = make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
+      }
+    } else {
+#pragma unroll
+      for (int fj = 0; fj < FN; ++fj) {
+        const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;
+        if (j >= P.N) continue;
+        if (L.part) {
+          *(lf32x4*)(L.part + ((int64_t)split * P.M + i) * L.partN + j) =
+              lf32x4{acc[fi][fj][0], acc[fi][fj][1], acc[fi][fj][2], acc[fi][fj][3]};
+        } else {
+          f_store4(P.C, P.ldc, i, j, P.N, L.outBf16, L.accumulate, P.vecC, acc[fi][fj]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace muon

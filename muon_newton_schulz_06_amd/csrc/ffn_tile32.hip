@@ -20,7 +20,7 @@ constexpr int kT = 128, kKs = 16, kLd = kT + 4;
 
 // Four operand values as fp32: (row, k..k+3) of a k-contiguous operand or
 // (row..row+3, k) of a row-contiguous one; zeros outside rows × K.
-template <typename T, bool ROWC>
+template <bool ROWC>
 __device__ __forceinline__ lf32x4 fetch4(const void* p, int64_t ld, int row, int64_t k, int rows,
                                          int64_t K, bool vec) {
   lf32x4 v = {0.f, 0.f, 0.f, 0.f};
@@ -28,31 +28,21 @@ __device__ __forceinline__ lf32x4 fetch4(const void* p, int64_t ld, int row, int
   const bool in = row < rows && k < K;
   const int have = !in ? 0 : ROWC ? rows - row : (int)min((int64_t)4, K - k);
   if (have >= 4 && vec) {
-    if constexpr (LType<T>::kVec == 4) {
-      v = *(const lf32x4*)((const float*)p + e);
-    } else {
-      const uint2 u = *(const uint2*)((const uint16_t*)p + e);
-      v[0] = __uint_as_float(u.x << 16);
-      v[1] = __uint_as_float(u.x & 0xffff0000u);
-      v[2] = __uint_as_float(u.y << 16);
-      v[3] = __uint_as_float(u.y & 0xffff0000u);
-    }
+    v = *(const lf32x4*)((const float*)p + e);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < have) v[i] = LType<T>::get(p, e + i);
+      if (i < have) v[i] = ((const float*)p)[e + i];
   }
   return v;
 }
 
 // Whether 4-element accesses of an operand are aligned.
-template <typename T>
 __device__ __forceinline__ bool aligned4(const void* p, int64_t ld) {
-  constexpr int bytes = 4 * 16 / LType<T>::kVec;
-  return ((uintptr_t)p & (bytes - 1)) == 0 && (ld & 3) == 0;
+  return ((uintptr_t)p & 15) == 0 && (ld & 3) == 0;
 }
 
-template <typename T, int EPI, bool AROW, bool BROW>
+template <int EPI, bool AROW, bool BROW>
 __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
   __shared__ __attribute__((aligned(16))) float sa[2][kKs * kLd];
   __shared__ __attribute__((aligned(16))) float sb[2][kKs * kLd];
@@ -87,19 +77,19 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
     const int z = s >= steps0;
     const int64_t k0 = (int64_t)(z ? s - steps0 : s) * kKs;
     const int64_t K = P.K[z];
-    const bool va = aligned4<T>(P.A[z], P.lda);
+    const bool va = aligned4(P.A[z], P.lda);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      ra[h] = fetch4<T, AROW>(P.A[z], P.lda, i0 + at_row(AROW, h), k0 + at_k(AROW, h), P.M, K, va);
+      ra[h] = fetch4<AROW>(P.A[z], P.lda, i0 + at_row(AROW, h), k0 + at_k(AROW, h), P.M, K, va);
       const int r = at_row(BROW, h);
       if constexpr (EPI == FFN_GLU) {
         const int which = (r >> 5) & 1;
         const int j = j0 + (r >> 6) * 32 + (r & 31);
-        rb[h] = fetch4<T, false>(P.B[which], P.ldb[which], j, k0 + at_k(false, h), P.N, K,
-                                 aligned4<T>(P.B[which], P.ldb[which]));
+        rb[h] = fetch4<false>(P.B[which], P.ldb[which], j, k0 + at_k(false, h), P.N, K,
+                                 aligned4(P.B[which], P.ldb[which]));
       } else {
-        rb[h] = fetch4<T, BROW>(P.B[z], P.ldb[z], j0 + r, k0 + at_k(BROW, h), P.N, K,
-                                aligned4<T>(P.B[z], P.ldb[z]));
+        rb[h] = fetch4<BROW>(P.B[z], P.ldb[z], j0 + r, k0 + at_k(BROW, h), P.N, K,
+                                aligned4(P.B[z], P.ldb[z]));
       }
     }
   };
@@ -152,17 +142,12 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
         if (j >= L.ldh) continue;  // columns N .. ldh − 1 are written as zeros
         float v, d;
         const float g = acc[a][0][r], u = acc[a][1][r];
-        ffn_act<LType<T>::kVec == 4>(L.act, g, v, d);
-        LType<T>::put(P.C, i * P.ldc + j, v * u);
+        ffn_act<true>(L.act, g, v, d);
+        ((float*)P.C)[i * P.ldc + j] = v * u;
         if (L.ab) {
-          const int64_t e = i * 2 * L.ldh + j;
-          if constexpr (LType<T>::kVec == 4) {
-            ((float*)L.ab)[e] = u * d;
-            ((float*)L.ab)[e + L.ldh] = v;
-          } else {
-            ((uint16_t*)L.ab)[e] = (uint16_t)l_pack_e6m9(u * d);
-            ((uint16_t*)L.ab)[e + L.ldh] = (uint16_t)l_pack_e6m9(v);
-          }
+          float* ab = (float*)L.ab + i * 2 * L.ldh + j;
+          ab[0] = u * d;
+          ab[L.ldh] = v;
         }
       } else {
 #pragma unroll
@@ -172,16 +157,10 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
           if constexpr (EPI == FFN_BACK) {
             if (j >= L.ldh) continue;
             const int64_t e = i * 2 * L.ldh + j;
-            float fa, fb;
-            if constexpr (LType<T>::kVec == 4) {
-              fa = ((const float*)L.ab)[e];
-              fb = ((const float*)L.ab)[e + L.ldh];
-            } else {
-              fa = l_unpack_e6m9(((const uint16_t*)L.ab)[e]);
-              fb = l_unpack_e6m9(((const uint16_t*)L.ab)[e + L.ldh]);
-            }
-            LType<T>::put(P.C, e, c * fa);
-            LType<T>::put(P.C, e + L.ldh, c * fb);
+            const float* ab = (const float*)L.ab + e;
+            float* o = (float*)P.C + e;
+            o[0] = c * ab[0];
+            o[L.ldh] = c * ab[L.ldh];
           } else {
             if (j >= P.N) continue;
             const int64_t e = i * P.ldc + j;
@@ -199,23 +178,17 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
   }
 }
 
-template <typename T>
-hipError_t launch_t(int epi, bool ar, bool br, const FfnLaunch& L, hipStream_t st) {
-  const dim3 grid(L.tiles[L.nprob]), block(256);
-  if (epi == FFN_GLU) hipLaunchKernelGGL((ffn_tile32<T, FFN_GLU, false, false>), grid, block, 0, st, L);
-  else if (epi == FFN_BACK) hipLaunchKernelGGL((ffn_tile32<T, FFN_BACK, false, true>), grid, block, 0, st, L);
-  else if (ar) hipLaunchKernelGGL((ffn_tile32<T, FFN_STORE, true, true>), grid, block, 0, st, L);
-  else if (br) hipLaunchKernelGGL((ffn_tile32<T, FFN_STORE, false, true>), grid, block, 0, st, L);
-  else hipLaunchKernelGGL((ffn_tile32<T, FFN_STORE, false, false>), grid, block, 0, st, L);
-  return hipGetLastError();
-}
-
 }  // namespace
 
-hipError_t launch_ffn_tile32(int epi, bool aRowContig, bool bRowContig, bool bf16,
-                             const FfnLaunch& L, hipStream_t st) {
-  return bf16 ? launch_t<Bf16>(epi, aRowContig, bRowContig, L, st)
-              : launch_t<float>(epi, aRowContig, bRowContig, L, st);
+hipError_t launch_ffn_tile32(int epi, bool aRowContig, bool bRowContig, const FfnLaunch& L,
+                             hipStream_t st) {
+  const dim3 grid(L.tiles[L.nprob]), block(256);
+  if (epi == FFN_GLU) hipLaunchKernelGGL((ffn_tile32<FFN_GLU, false, false>), grid, block, 0, st, L);
+  else if (epi == FFN_BACK) hipLaunchKernelGGL((ffn_tile32<FFN_BACK, false, true>), grid, block, 0, st, L);
+  else if (aRowContig) hipLaunchKernelGGL((ffn_tile32<FFN_STORE, true, true>), grid, block, 0, st, L);
+  else if (bRowContig) hipLaunchKernelGGL((ffn_tile32<FFN_STORE, false, true>), grid, block, 0, st, L);
+  else hipLaunchKernelGGL((ffn_tile32<FFN_STORE, false, false>), grid, block, 0, st, L);
+  return hipGetLastError();
 }
 
 }  // namespace muon

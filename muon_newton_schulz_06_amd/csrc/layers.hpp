@@ -98,8 +98,11 @@ struct FfnProb {
   int64_t lda, ldb[2];
   int32_t M, N;
   int32_t K[2];
+  // elements of a row-contiguous operand's rows (tile16: a multiple of 8)
+  int32_t extA, extB;
   void* C;
   int64_t ldc;
+  int32_t vecC;  // four consecutive elements of C are one aligned access
 };
 
 struct FfnLaunch {
@@ -112,9 +115,39 @@ struct FfnLaunch {
   // FFN_BACK: reads them, C is dg, du (rows of 2·ldh)
   void* ab;
   int64_t ldh;  // hidden rounded up to 8: row length of h and of each half
+  // tile16: k-tiles of 32 per split (a multiple of four), and where FFN_STORE
+  // leaves each split's fp32 result (null: one split, C is written)
+  int32_t splitTiles;
+  float* part;    // [split][M][partN]
+  int64_t partN;  // N rounded up to 4
 };
-hipError_t launch_ffn_tile32(int epi, bool aRowContig, bool bRowContig, bool bf16,
-                             const FfnLaunch& L, hipStream_t st);
+hipError_t launch_ffn16_glu(int tile, const FfnLaunch& L, hipStream_t st);
+hipError_t launch_ffn16_back(int tile, const FfnLaunch& L, hipStream_t st);
+hipError_t launch_ffn16_store(int tile, bool aRowContig, bool bRowContig, const FfnLaunch& L,
+                              hipStream_t st);
+
+// Sum of the splits' results, [splits][M][N] → M × nReal.
+struct FfnJoin {
+  const float* part;
+  int64_t M, N, nReal;
+  int32_t splits;
+  void* C;
+  int64_t ldc;
+  int32_t vecC, outBf16;
+};
+hipError_t launch_ffn_join(const FfnJoin& J, hipStream_t st);
+
+// Aligned, zero-padded copy of a bf16 operand.
+struct FfnPack {
+  const void* src;
+  int64_t ld, rows, cols;
+  void* dst;
+  int64_t ldo;
+};
+hipError_t launch_ffn_pack(const FfnPack& K, hipStream_t st);
+
+hipError_t launch_ffn_tile32(int epi, bool aRowContig, bool bRowContig, const FfnLaunch& L,
+                             hipStream_t st);
 
 // ----- device helpers --------------------------------------------------------
 typedef float lf32x4 __attribute__((ext_vector_type(4)));

@@ -2,6 +2,7 @@
 // workspace layout and launches on the caller's stream.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <string>
@@ -169,24 +170,81 @@ EmbedLayout embed_layout(int64_t tokens, int64_t dim) {
 }
 
 // ----- gated feed-forward block ----------------------------------------------
+int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// Whether a bf16 operand can be read by the 16-byte buffer loads: aligned
+// rows of whole chunks, and a tile's rows within the loads' 31-bit offsets.
+bool direct16(const void* p, int64_t ld, int64_t cols) {
+  return whole_chunks(p, ld, cols, 2) && ld < (int64_t(1) << 22) - 64;
+}
+
+// Tile edge and k splits of a bf16 product of M × N with KT k-tiles of 32.
+// Estimated time: rounds of workgroups over the GPU × (k-tiles × time of one +
+// a fixed part), in µs, plus writing and adding up the splits' results.
+struct Plan16 {
+  int tile, splits, per;
+};
+Plan16 plan16(int64_t M, int64_t N, int64_t KT, bool maySplit) {
+  struct Kind {
+    int tile;
+    double slots, ktile, fixed;
+  };
+  const Kind kinds[2] = {{256, 256, 0.80, 8.0}, {128, 512, 0.50, 6.0}};
+  Plan16 best{};
+  double bestT = 0;
+  for (const Kind& k : kinds) {
+    const int64_t tiles = tiles_of(M, k.tile) * tiles_of(N, k.tile);
+    for (int s = 1; s <= (maySplit ? 32 : 1); ++s) {
+      const int64_t per = std::max<int64_t>(4, tiles_of(tiles_of(KT, s), 4) * 4);
+      if (s > 1 && (tiles_of(KT, per) != s || per < 16)) continue;
+      double t = std::ceil(tiles * s / k.slots) * (per * k.ktile + k.fixed);
+      if (s > 1) t += 4.0 + 8.0 * s * M * N / 4e6;
+      if (!best.tile || t < bestT) {
+        best = {k.tile, s, (int)per};
+        bestT = t;
+      }
+    }
+  }
+  return best;
+}
+
 struct FfnLayout {
   int64_t ldh;                  // hidden rounded up to 8
   size_t ab, savedH, saved;     // in `saved`
-  size_t h, fwd;                // workspace of the forward pass
-  size_t dgu, bwd;              // workspace of the backward pass
+  // workspace: what the call computes (h, or dg and du), aligned copies, and
+  // the splits' partial results
+  size_t mid, x, dy, gate, up, down, part, total;
+  Plan16 plan;                  // of y, or of dx
 };
-FfnLayout ffn_layout(const muon_ffn_t& f) {
+
+// Layout for the forward (grad = 0) or the backward pass.
+FfnLayout ffn_layout(const muon_ffn_t& f, bool grad) {
   FfnLayout l{};
   const size_t e = esize(f.dtype);
-  l.ldh = (f.hidden + 7) / 8 * 8;
+  l.ldh = round8(f.hidden);
   const size_t rows = (size_t)f.tokens * l.ldh * e;
   l.ab = 0;
   l.savedH = align256(2 * rows);
   l.saved = l.savedH + align256(rows);
-  l.h = 0;
-  l.fwd = align256(rows);
-  l.dgu = 0;
-  l.bwd = align256(2 * rows);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += align256(n);
+    return o;
+  };
+  l.mid = take(grad ? 2 * rows : rows);
+  if (f.dtype == MUON_DTYPE_BF16 && f.tokens > 0) {
+    const int64_t D8 = round8(f.model);
+    l.x = take((size_t)f.tokens * D8 * 2);
+    l.dy = take(grad ? (size_t)f.tokens * D8 * 2 : 0);
+    l.gate = take(direct16(f.w_gate, f.ld_gate, f.model) ? 0 : (size_t)f.hidden * D8 * 2);
+    l.up = take(direct16(f.w_up, f.ld_up, f.model) ? 0 : (size_t)f.hidden * D8 * 2);
+    l.down = take(direct16(f.w_down, f.ld_down, f.hidden) ? 0 : (size_t)f.model * l.ldh * 2);
+    l.plan = plan16(f.tokens, f.model, tiles_of(l.ldh, 32) * (grad ? 2 : 1), true);
+    l.part = take(l.plan.splits > 1 ? (size_t)l.plan.splits * f.tokens * (tiles_of(f.model, 4) * 4) * 4 : 0);
+  }
+  l.total = at;
   return l;
 }
 
@@ -205,14 +263,64 @@ void ffn_weights(Args& a, const muon_ffn_t& f) {
   a.matrix("w_down", f.w_down, f.model, f.hidden, f.ld_down, e, false);
 }
 
-constexpr int64_t kFfnTile = 128;
-int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
+constexpr int64_t kTile32 = 128;  // edge of the fp32 products' tiles
 
-// Sets prob q's tile range (tile edges tm × tn).
-void set_tiles(FfnLaunch& L, int q, int64_t tm, int64_t tn) {
-  L.tiles[q + 1] = L.tiles[q] + (int32_t)(tiles_of(L.prob[q].M, tm) * tiles_of(L.prob[q].N, tn));
+// Sets prob q's tile range (tile edges tm × tn, k splits).
+void set_tiles(FfnLaunch& L, int q, int64_t tm, int64_t tn, int splits = 1) {
+  L.tiles[q + 1] = L.tiles[q] + (int32_t)(tiles_of(L.prob[q].M, tm) * tiles_of(L.prob[q].N, tn) * splits);
   L.nprob = q + 1;
 }
+
+void set_out(FfnProb& p, void* C, int64_t ldc, bool bf16) {
+  p.C = C;
+  p.ldc = ldc;
+  p.vecC = ldc % 4 == 0 && (uintptr_t)C % (bf16 ? 8 : 16) == 0;
+}
+
+struct Op {
+  const void* p;
+  int64_t ld;
+  int64_t ext;  // elements of a row, a multiple of 8 on the bf16 path
+};
+
+// A call of the block: its layout, stream and (bf16) aligned operands.
+struct FfnCall {
+  const muon_ffn_t& f;
+  const FfnLayout& l;
+  char* ws;
+  hipStream_t st;
+  bool bf16() const { return f.dtype == MUON_DTYPE_BF16; }
+
+  // The operand itself, or its aligned copy at `at` in the workspace.
+  muon_status_t operand(const char* what, const void* p, int64_t ld, int64_t rows, int64_t cols, size_t at,
+                        Op* o) const {
+    if (!bf16() || direct16(p, ld, cols)) {
+      *o = {p, ld, cols};
+      return MUON_OK;
+    }
+    *o = {ws + at, round8(cols), round8(cols)};
+    FfnPack k{p, ld, rows, cols, ws + at, round8(cols)};
+    return launched(what, launch_ffn_pack(k, st), st);
+  }
+
+  // A plain product with one problem: bf16 with the layout's split plan.
+  muon_status_t product(const char* what, bool ar, bool br, FfnLaunch& L) const {
+    FfnProb& p = L.prob[0];
+    if (!bf16()) {
+      set_tiles(L, 0, kTile32, kTile32);
+      return launched(what, launch_ffn_tile32(FFN_STORE, ar, br, L, st), st);
+    }
+    const Plan16& g = l.plan;
+    L.splitTiles = g.per;
+    L.partN = tiles_of(p.N, 4) * 4;
+    L.part = g.splits > 1 ? (float*)(ws + l.part) : nullptr;
+    set_tiles(L, 0, g.tile, g.tile, g.splits);
+    const muon_status_t s = launched(what, launch_ffn16_store(g.tile, ar, br, L, st), st);
+    if (s != MUON_OK || g.splits == 1) return s;
+    FfnJoin J{L.part, p.M, L.partN, p.N, g.splits, p.C, p.ldc, p.vecC, L.outBf16};
+    return launched("sum of the k splits", launch_ffn_join(J, st), st);
+  }
+};
 
 }  // namespace
 }  // namespace muon
@@ -431,7 +539,7 @@ muon_status_t muon_gated_ffn_saved_size(const muon_ffn_t* ffn, size_t* bytes) {
     ffn_sizes(a, ffn);
     if (!bytes) a.fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
     if (!a.ok()) return a.report();
-    *bytes = ffn_layout(*ffn).saved;
+    *bytes = ffn_layout(*ffn, false).saved;
     return MUON_OK;
   });
 }
@@ -442,8 +550,7 @@ muon_status_t muon_gated_ffn_workspace_size(const muon_ffn_t* ffn, int32_t grad,
     ffn_sizes(a, ffn);
     if (!bytes) a.fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
     if (!a.ok()) return a.report();
-    const FfnLayout l = ffn_layout(*ffn);
-    *bytes = grad ? l.bwd : l.fwd;
+    *bytes = ffn_layout(*ffn, grad != 0).total;
     return MUON_OK;
   });
 }
@@ -458,13 +565,13 @@ muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x,
     if (a.ok()) {
       if (ffn->activation < MUON_ACT_SILU || ffn->activation > MUON_ACT_GELU_TANH)
         a.fail(MUON_ERR_INVALID_ARG, "unknown activation");
-      l = ffn_layout(*ffn);
+      l = ffn_layout(*ffn, false);
       const size_t e = esize(ffn->dtype);
       ffn_weights(a, *ffn);
       a.matrix("x", x, ffn->tokens, ffn->model, ld_x, e, false);
       a.matrix("y", y, ffn->tokens, ffn->model, ld_y, e, true);
       if (saved) a.buffer("saved", saved, saved_bytes, l.saved, true);
-      a.buffer("workspace", workspace, workspace_bytes, l.fwd, true);
+      a.buffer("workspace", workspace, workspace_bytes, l.total, true);
     }
     a.aliases();
     if (!a.ok()) return a.report();
@@ -472,42 +579,54 @@ muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x,
     muon_status_t s = check_device();
     if (s != MUON_OK) return s;
     const hipStream_t st = (hipStream_t)stream;
-    const bool bf16 = ffn->dtype == MUON_DTYPE_BF16;
-    void* h = saved ? (char*)saved + l.savedH : (char*)workspace + l.h;
+    const FfnCall call{*ffn, l, (char*)workspace, st};
+    const bool bf16 = call.bf16();
+    const int64_t T = ffn->tokens, D = ffn->model, F = ffn->hidden;
+    Op ox{}, og{}, ou{}, od{};
+    s = call.operand("copy of x", x, ld_x, T, D, l.x, &ox);
+    if (s == MUON_OK) s = call.operand("copy of w_gate", ffn->w_gate, ffn->ld_gate, F, D, l.gate, &og);
+    if (s == MUON_OK) s = call.operand("copy of w_up", ffn->w_up, ffn->ld_up, F, D, l.up, &ou);
+    if (s == MUON_OK) s = call.operand("copy of w_down", ffn->w_down, ffn->ld_down, D, F, l.down, &od);
+    if (s != MUON_OK) return s;
+    void* h = saved ? (char*)saved + l.savedH : (char*)workspace + l.mid;
     FfnLaunch L{};
     L.act = ffn->activation;
     L.ldh = l.ldh;
     L.ab = saved ? (char*)saved + l.ab : nullptr;
-    L.outBf16 = bf16;
     FfnProb& p = L.prob[0];
-    p.A[0] = x;
-    p.lda = ld_x;
-    p.B[0] = ffn->w_gate;
-    p.B[1] = ffn->w_up;
-    p.ldb[0] = ffn->ld_gate;
-    p.ldb[1] = ffn->ld_up;
-    p.M = (int32_t)ffn->tokens;
-    p.N = (int32_t)ffn->hidden;
-    p.K[0] = (int32_t)ffn->model;
-    p.C = h;
-    p.ldc = l.ldh;
-    set_tiles(L, 0, kFfnTile, kFfnTile / 2);
-    s = launched("gated projections", launch_ffn_tile32(FFN_GLU, false, false, bf16, L, st), st);
+    p.A[0] = ox.p;
+    p.lda = ox.ld;
+    p.B[0] = og.p;
+    p.B[1] = ou.p;
+    p.ldb[0] = og.ld;
+    p.ldb[1] = ou.ld;
+    p.M = (int32_t)T;
+    p.N = (int32_t)F;
+    p.K[0] = (int32_t)ox.ext;
+    set_out(p, h, l.ldh, bf16);
+    const char* what = "gated projections";
+    if (bf16) {
+      const Plan16 g = plan16(T, 2 * F, tiles_of(ox.ext, 32), false);
+      L.splitTiles = g.per;
+      set_tiles(L, 0, g.tile, g.tile / 2);
+      s = launched(what, launch_ffn16_glu(g.tile, L, st), st);
+    } else {
+      set_tiles(L, 0, kTile32, kTile32 / 2);
+      s = launched(what, launch_ffn_tile32(FFN_GLU, false, false, L, st), st);
+    }
     if (s != MUON_OK) return s;
-    FfnLaunch D{};
-    D.outBf16 = bf16;
-    FfnProb& d = D.prob[0];
+    FfnLaunch Y{};
+    Y.outBf16 = bf16;
+    FfnProb& d = Y.prob[0];
     d.A[0] = h;
     d.lda = l.ldh;
-    d.B[0] = ffn->w_down;
-    d.ldb[0] = ffn->ld_down;
-    d.M = (int32_t)ffn->tokens;
-    d.N = (int32_t)ffn->model;
-    d.K[0] = (int32_t)ffn->hidden;
-    d.C = y;
-    d.ldc = ld_y;
-    set_tiles(D, 0, kFfnTile, kFfnTile);
-    return launched("down projection", launch_ffn_tile32(FFN_STORE, false, false, bf16, D, st), st);
+    d.B[0] = od.p;
+    d.ldb[0] = od.ld;
+    d.M = (int32_t)T;
+    d.N = (int32_t)D;
+    d.K[0] = (int32_t)od.ext;
+    set_out(d, y, ld_y, bf16);
+    return call.product("down projection", false, false, Y);
   });
 }
 
@@ -522,7 +641,7 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
     FfnLayout l{};
     bool wantW = false;
     if (a.ok()) {
-      l = ffn_layout(*ffn);
+      l = ffn_layout(*ffn, true);
       const size_t e = esize(ffn->dtype);
       wantW = grads->dw_gate || grads->dw_up || grads->dw_down;
       if (wantW) a.dtype("grad_dtype", grads->grad_dtype);
@@ -537,7 +656,7 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
         a.matrix("dw_up", grads->dw_up, ffn->hidden, ffn->model, grads->ld_up, eg, true);
         a.matrix("dw_down", grads->dw_down, ffn->model, ffn->hidden, grads->ld_down, eg, true);
       }
-      a.buffer("workspace", workspace, workspace_bytes, l.bwd, true);
+      a.buffer("workspace", workspace, workspace_bytes, l.total, true);
     }
     a.aliases();
     if (!a.ok()) return a.report();
@@ -546,67 +665,96 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
     muon_status_t s = check_device();
     if (s != MUON_OK) return s;
     const hipStream_t st = (hipStream_t)stream;
-    const bool bf16 = ffn->dtype == MUON_DTYPE_BF16;
+    const FfnCall call{*ffn, l, (char*)workspace, st};
+    const bool bf16 = call.bf16();
     const size_t e = esize(ffn->dtype);
     const char* sv = (const char*)saved;
-    char* dgu = (char*)workspace + l.dgu;
+    char* dgu = (char*)workspace + l.mid;
     const int32_t T = (int32_t)ffn->tokens, D = (int32_t)ffn->model, F = (int32_t)ffn->hidden;
+    Op ox{x, ld_x, D}, oy{dy, ld_dy, D};
     if (T > 0) {
+      Op od{};
+      s = call.operand("copy of dy", dy, ld_dy, T, D, l.dy, &oy);
+      if (s == MUON_OK) s = call.operand("copy of w_down", ffn->w_down, ffn->ld_down, D, F, l.down, &od);
+      if (s != MUON_OK) return s;
       FfnLaunch L{};
       L.ldh = l.ldh;
       L.ab = (void*)(sv + l.ab);
       FfnProb& p = L.prob[0];
-      p.A[0] = dy;
-      p.lda = ld_dy;
-      p.B[0] = ffn->w_down;
-      p.ldb[0] = ffn->ld_down;
+      p.A[0] = oy.p;
+      p.lda = oy.ld;
+      p.B[0] = od.p;
+      p.ldb[0] = od.ld;
+      p.extB = (int32_t)od.ext;
       p.M = T;
       p.N = F;
       p.K[0] = D;
-      p.C = dgu;
-      p.ldc = 2 * l.ldh;
-      set_tiles(L, 0, kFfnTile, kFfnTile);
-      s = launched("gradient of the gated product", launch_ffn_tile32(FFN_BACK, false, true, bf16, L, st), st);
+      set_out(p, dgu, 2 * l.ldh, bf16);
+      const char* what = "gradient of the gated product";
+      if (bf16) {
+        const Plan16 g = plan16(T, F, tiles_of(D, 32), false);
+        L.splitTiles = g.per;
+        set_tiles(L, 0, g.tile, g.tile);
+        s = launched(what, launch_ffn16_back(g.tile, L, st), st);
+      } else {
+        set_tiles(L, 0, kTile32, kTile32);
+        s = launched(what, launch_ffn_tile32(FFN_BACK, false, true, L, st), st);
+      }
       if (s != MUON_OK) return s;
     }
     if (T > 0 && grads->dx) {
+      Op og{}, ou{};
+      s = call.operand("copy of w_gate", ffn->w_gate, ffn->ld_gate, F, D, l.gate, &og);
+      if (s == MUON_OK) s = call.operand("copy of w_up", ffn->w_up, ffn->ld_up, F, D, l.up, &ou);
+      if (s != MUON_OK) return s;
       FfnLaunch L{};
       L.outBf16 = bf16;
       FfnProb& p = L.prob[0];
       p.A[0] = dgu;
       p.A[1] = dgu + l.ldh * e;
       p.lda = 2 * l.ldh;
-      p.B[0] = ffn->w_gate;
-      p.B[1] = ffn->w_up;
-      p.ldb[0] = ffn->ld_gate;
-      p.ldb[1] = ffn->ld_up;
+      p.B[0] = og.p;
+      p.B[1] = ou.p;
+      p.ldb[0] = og.ld;
+      p.ldb[1] = ou.ld;
+      p.extB = (int32_t)og.ext;
       p.M = T;
       p.N = D;
       p.K[0] = p.K[1] = F;
-      p.C = grads->dx;
-      p.ldc = grads->ld_dx;
-      set_tiles(L, 0, kFfnTile, kFfnTile);
-      s = launched("gradient of the input", launch_ffn_tile32(FFN_STORE, false, true, bf16, L, st), st);
+      set_out(p, grads->dx, grads->ld_dx, bf16);
+      s = call.product("gradient of the input", false, true, L);
       if (s != MUON_OK) return s;
     }
     if (!wantW) return MUON_OK;
+    if (T > 0) {
+      s = call.operand("copy of x", x, ld_x, T, D, l.x, &ox);
+      if (s != MUON_OK) return s;
+    }
     FfnLaunch L{};
     L.outBf16 = grads->grad_dtype == MUON_DTYPE_BF16;
     L.accumulate = grads->accumulate != 0;
+    // three products over the tokens in one launch
+    const Plan16 g = plan16(3 * (int64_t)F, D, tiles_of(T, 32), false);
+    L.splitTiles = g.per;
     for (int q = 0; q < 3; ++q) {
       FfnProb& p = L.prob[q];
-      p.A[0] = q < 2 ? (const void*)(dgu + q * l.ldh * e) : dy;
-      p.lda = q < 2 ? 2 * l.ldh : ld_dy;
-      p.B[0] = q < 2 ? x : (const void*)(sv + l.savedH);
-      p.ldb[0] = q < 2 ? ld_x : l.ldh;
+      p.A[0] = q < 2 ? (const void*)(dgu + q * l.ldh * e) : oy.p;
+      p.lda = q < 2 ? 2 * l.ldh : oy.ld;
+      p.extA = (int32_t)(q < 2 ? l.ldh : oy.ext);
+      p.B[0] = q < 2 ? ox.p : (const void*)(sv + l.savedH);
+      p.ldb[0] = q < 2 ? ox.ld : l.ldh;
+      p.extB = (int32_t)(q < 2 ? ox.ext : l.ldh);
       p.M = q < 2 ? F : D;
       p.N = q < 2 ? D : F;
       p.K[0] = T;
-      p.C = q == 0 ? grads->dw_gate : q == 1 ? grads->dw_up : grads->dw_down;
-      p.ldc = q == 0 ? grads->ld_gate : q == 1 ? grads->ld_up : grads->ld_down;
-      set_tiles(L, q, kFfnTile, kFfnTile);
+      set_out(p, q == 0 ? grads->dw_gate : q == 1 ? grads->dw_up : grads->dw_down,
+              q == 0 ? grads->ld_gate : q == 1 ? grads->ld_up : grads->ld_down, L.outBf16);
+      if (bf16) set_tiles(L, q, g.tile, g.tile);
+      else set_tiles(L, q, kTile32, kTile32);
     }
-    return launched("gradients of the weights", launch_ffn_tile32(FFN_STORE, true, true, bf16, L, st), st);
+    const char* what = "gradients of the weights";
+    if (bf16) return launched(what, launch_ffn16_store(g.tile, true, true, L, st), st);
+    return launched(what, launch_ffn_tile32(FFN_STORE, true, true, L, st), st);
   });
 }
 
