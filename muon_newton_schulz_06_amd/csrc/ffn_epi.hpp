@@ -1,6 +1,8 @@
 // Activations of the gated feed-forward block.
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/muon_layers.h"
 #include "layers.hpp"
 
@@ -17,13 +19,13 @@ template <bool FULL> __device__ __forceinline__ float ffn_rcp(float x) {
 }
 
 // act(g) and act'(g).
-template <bool FULL>
-__device__ __forceinline__ void ffn_act(int kind, float g, float& v, float& d) {
-  if (kind == MUON_ACT_SILU) {
+template <int ACT, bool FULL>
+__device__ __forceinline__ void ffn_act(float g, float& v, float& d) {
+  if constexpr (ACT == MUON_ACT_SILU) {
     const float s = ffn_rcp<FULL>(1.0f + ffn_exp<FULL>(-g));
     v = g * s;
-    d = s * (1.0f + g * (1.0f - s));
-  } else if (kind == MUON_ACT_GELU) {
+    d = s + v * (1.0f - s);
+  } else if constexpr (ACT == MUON_ACT_GELU) {
     const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
     v = g * c;
     d = c + g * 0.39894228040143268f * ffn_exp<FULL>(-0.5f * g * g);
@@ -33,8 +35,15 @@ __device__ __forceinline__ void ffn_act(int kind, float g, float& v, float& d) {
     const float k = 1.59576912160573072f;
     const float s = ffn_rcp<FULL>(1.0f + ffn_exp<FULL>(-k * (g + 0.044715f * g * g * g)));
     v = g * s;
-    d = s + g * s * (1.0f - s) * k * (1.0f + 0.134145f * fminf(g * g, 1e6f));
+    d = s + v * (1.0f - s) * k * (1.0f + 0.134145f * fminf(g * g, 1e6f));
   }
+}
+
+// Runs f with the activation as a compile-time constant.
+template <typename F> __device__ __forceinline__ void ffn_with_act(int act, F&& f) {
+  if (act == MUON_ACT_SILU) f(std::integral_constant<int, MUON_ACT_SILU>{});
+  else if (act == MUON_ACT_GELU) f(std::integral_constant<int, MUON_ACT_GELU>{});
+  else f(std::integral_constant<int, MUON_ACT_GELU_TANH>{});
 }
 
 }  // namespace muon

@@ -27,11 +27,11 @@ namespace muon {
 typedef __bf16 fbf16x8 __attribute__((ext_vector_type(8)));
 typedef int32_t fi32x4 __attribute__((ext_vector_type(4)));
 
-// Buffer resource over [p, p + 2 GiB).
+// Buffer resource over [p, p + 2 GiB), p the same in every lane.
 __device__ __forceinline__ fi32x4 f_buffer(uint64_t p) {
   fi32x4 r;
-  r[0] = (int32_t)(uint32_t)p;
-  r[1] = (int32_t)(uint32_t)(p >> 32);
+  r[0] = __builtin_amdgcn_readfirstlane((int32_t)(uint32_t)p);
+  r[1] = __builtin_amdgcn_readfirstlane((int32_t)(uint32_t)(p >> 32));
   r[2] = (int32_t)0x80000000u;
   r[3] = 0x00020000;
   return r;
@@ -61,8 +61,7 @@ __device__ __forceinline__ void f_store4(void* C, int64_t ldc, int64_t i, int64_
         v[2] += __uint_as_float(u.y << 16);
         v[3] += __uint_as_float(u.y & 0xffff0000u);
       }
-      *(uint2*)o = make_uint2(l_f32_bf16(v[0]) | (l_f32_bf16(v[1]) << 16),
-                              l_f32_bf16(v[2]) | (l_f32_bf16(v[3]) << 16));
+      *(uint2*)o = make_uint2(l_f32_bf16x2(v[0], v[1]), l_f32_bf16x2(v[2], v[3]));
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -89,6 +88,8 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
   constexpr int kHalf = TILE * KB * 2, kSlot = 2 * kHalf;  // bytes of an operand's tile, of a slot
   constexpr int NQ = FM / 2;                          // quarters (pairs of block rows) per k-tile
   __shared__ __attribute__((aligned(1024))) char lds[4 * kSlot];
+
+  constexpr bool kTwo = EPI == FFN_STORE && !AROW && BROW;  // the launches with two k ranges
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -120,6 +121,7 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
   // from the operand's tile start, the k it holds, and whether its row (or
   // its chunk of a row-contiguous operand) exists.
   uint32_t offA[2], offB[2];
+  [[maybe_unused]] uint32_t offB1[2];  // the second k range's, whose stride may differ
   int kA[2], kB[2];
   auto place = [&](bool rowc, int64_t ld, int64_t first, int64_t extent, int p, uint32_t& off, int& k) {
     if (rowc) {
@@ -144,25 +146,37 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
       const int r = wave * 32 + p * 16 + (lane >> 2), c = (lane & 3) ^ swz4(r);
       const int f = (r >> 6) * 32 + (r & 31);
       kB[p] = c * 8;
-      offB[p] = j0 + f < P.N ? (uint32_t)(f * P.ldb[bsel] * 2 + c * 16) : kFfnNowhere;
+      offB[p] = j0 + f < P.N ? (uint32_t)(f * (bsel ? P.ldb[1] : P.ldb[0]) * 2 + c * 16) : kFfnNowhere;
     } else {
       place(BROW, P.ldb[0], j0, BROW ? P.extB : P.N, p, offB[p], kB[p]);
+      if constexpr (kTwo) place(BROW, P.ldb[1], j0, BROW ? P.extB : P.N, p, offB1[p], kB[p]);
     }
   }
   const int dst = wave * 2048;  // this wave's part of an operand's tile, either layout
-  auto issue = [&](int slot, int kt) __attribute__((always_inline)) {
-    const int z = EPI == FFN_GLU ? 0 : kt >= KT0;
-    const int k0 = (z ? kt - KT0 : kt) * KB, left = P.K[z] - k0;
-    const uint64_t a = (uint64_t)P.A[z] + (AROW ? ((uint64_t)k0 * P.lda + i0) * 2 : ((uint64_t)i0 * P.lda + k0) * 2);
-    const int zb = EPI == FFN_GLU ? bsel : z;
-    const int64_t ldb = P.ldb[zb];
-    const uint64_t bb = (uint64_t)P.B[zb] + (BROW ? ((uint64_t)k0 * ldb + j0) * 2 : ((uint64_t)j0 * ldb + k0) * 2);
-    const fi32x4 ra = f_buffer(a), rb = f_buffer(bb);
+  // tile starts and bytes per k of both k ranges (FFN_GLU: one range)
+  const uint64_t a0 = (uint64_t)P.A[0] + (AROW ? (uint64_t)i0 : (uint64_t)i0 * P.lda) * 2;
+  const uint64_t a1 = (uint64_t)P.A[1] + (AROW ? (uint64_t)i0 : (uint64_t)i0 * P.lda) * 2;
+  const void* const pb = bsel ? P.B[1] : P.B[0];
+  const int64_t lb = bsel ? P.ldb[1] : P.ldb[0];
+  const uint64_t b0 = (uint64_t)pb + (BROW ? (uint64_t)j0 : (uint64_t)j0 * lb) * 2;
+  const uint64_t b1 = (uint64_t)P.B[1] + (BROW ? (uint64_t)j0 : (uint64_t)j0 * P.ldb[1]) * 2;
+  const uint32_t ka = AROW ? (uint32_t)P.lda * 2 : 2, kb0 = BROW ? (uint32_t)lb * 2 : 2,
+                 kb1 = BROW ? (uint32_t)P.ldb[1] * 2 : 2;
+  const int K0 = P.K[0], K1 = P.K[1];
+  auto issue = [=](int slot, int kt) __attribute__((always_inline)) {
+    const bool z = kTwo && kt >= KT0;
+    const int k0 = (z ? kt - KT0 : kt) * KB, left = (z ? K1 : K0) - k0;
+    const fi32x4 ra = f_buffer((z ? a1 : a0) + (uint64_t)k0 * ka);
+    const fi32x4 rb = f_buffer((z ? b1 : b0) + (uint64_t)k0 * (z ? kb1 : kb0));
     const uint32_t s = __builtin_amdgcn_readfirstlane(lds_addr(lds) + slot * kSlot + dst);
 #pragma unroll
     for (int p = 0; p < 2; ++p) f_dma16(s + p * 1024, kA[p] < left ? offA[p] : kFfnNowhere, ra);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) f_dma16(s + kHalf + p * 1024, kB[p] < left ? offB[p] : kFfnNowhere, rb);
+    for (int p = 0; p < 2; ++p) {
+      uint32_t o = offB[p];
+      if constexpr (kTwo) o = z ? offB1[p] : o;
+      f_dma16(s + kHalf + p * 1024, kB[p] < left ? o : kFfnNowhere, rb);
+    }
   };
 
   floatx4 acc[FM][FN];
@@ -249,51 +263,80 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // acc[fi][fj][r]: row fi·16 + lane%16, column fj·16 + 4·(lane/16) + r
+  const int64_t iw = i0 + wm * WTM + lc;
+  if constexpr (EPI == FFN_GLU) {
+    auto write = [&](auto actc, auto savec) __attribute__((always_inline)) {
 #pragma unroll
-  for (int fi = 0; fi < FM; ++fi) {
-    const int64_t i = i0 + wm * WTM + fi * 16 + lc;
-    if (i >= P.M) continue;
-    if constexpr (EPI == FFN_GLU) {
+      for (int fi = 0; fi < FM; ++fi) {
+        const int64_t i = iw + fi * 16;
+        if (i >= P.M) continue;
 #pragma unroll
-      for (int fj = 0; fj < 2; ++fj) {
-        const int64_t j = j0 + wn * 32 + fj * 16 + 4 * lg;
-        if (j >= L.ldh) continue;  // ldh is a multiple of 8; columns N .. ldh − 1 come out as zeros
-        uint32_t h[4], ca[4], cb[4];
+        for (int fj = 0; fj < 2; ++fj) {
+          const int64_t j = j0 + wn * 32 + fj * 16 + 4 * lg;
+          if (j >= L.ldh) continue;  // ldh is a multiple of 8; columns N .. ldh − 1 come out as zeros
+          float v[4], d[4];
+          const floatx4 u = acc[fi][fj + 2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float v, d;
-          const float u = acc[fi][fj + 2][r];
-          ffn_act<false>(L.act, acc[fi][fj][r], v, d);
-          h[r] = l_f32_bf16(v * u);
-          ca[r] = l_pack_e6m9(u * d);
-          cb[r] = l_pack_e6m9(v);
-        }
-        *(uint2*)((uint16_t*)P.C + i * P.ldc + j) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        if (L.ab) {
-          uint16_t* o = (uint16_t*)L.ab + i * 2 * L.ldh + j;
-          *(uint2*)o = make_uint2(ca[0] | (ca[1] << 16), ca[2] | (ca[3] << 16));
-          *(uint2*)(o + L.ldh) = make_uint2(cb[0] | (cb[1] << 16), cb[2] | (cb[3] << 16));
+          for (int r = 0; r < 4; ++r) ffn_act<decltype(actc)::value, false>(acc[fi][fj][r], v[r], d[r]);
+          *(uint2*)((uint16_t*)P.C + i * P.ldc + j) =
+              make_uint2(l_f32_bf16x2(v[0] * u[0], v[1] * u[1]), l_f32_bf16x2(v[2] * u[2], v[3] * u[3]));
+          if constexpr (decltype(savec)::value) {
+            uint16_t* o = (uint16_t*)L.ab + i * 2 * L.ldh + j;
+            *(uint2*)o = make_uint2(l_pack_e6m9x2(u[0] * d[0], u[1] * d[1]),
+                                    l_pack_e6m9x2(u[2] * d[2], u[3] * d[3]));
+            *(uint2*)(o + L.ldh) = make_uint2(l_pack_e6m9x2(v[0], v[1]), l_pack_e6m9x2(v[2], v[3]));
+          }
         }
       }
-    } else if constexpr (EPI == FFN_BACK) {
+    };
+    ffn_with_act(L.act, [&](auto actc) __attribute__((always_inline)) {
+      if (L.ab) write(actc, std::true_type{});
+      else write(actc, std::false_type{});
+    });
+  } else if constexpr (EPI == FFN_BACK) {
+    // the factors of the next block row are read before the current one's
+    // results are stored
+    uint2 ua[2][FN], ub[2][FN];
+    auto fetch = [&](int fi, uint2 (&a)[FN], uint2 (&b)[FN]) __attribute__((always_inline)) {
+      const int64_t i = iw + fi * 16;
 #pragma unroll
       for (int fj = 0; fj < FN; ++fj) {
         const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;
-        if (j >= L.ldh) continue;
-        const uint16_t* o = (const uint16_t*)L.ab + i * 2 * L.ldh + j;
-        const uint2 ua = *(const uint2*)o, ub = *(const uint2*)(o + L.ldh);
-        uint32_t g[4], u[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t wa = r < 2 ? ua.x : ua.y, wb = r < 2 ? ub.x : ub.y;
-          g[r] = l_f32_bf16(acc[fi][fj][r] * l_unpack_e6m9((wa >> (16 * (r & 1))) & 0xffffu));
-          u[r] = l_f32_bf16(acc[fi][fj][r] * l_unpack_e6m9((wb >> (16 * (r & 1))) & 0xffffu));
+        a[fj] = b[fj] = make_uint2(0u, 0u);
+        if (i < P.M && j < L.ldh) {
+          const uint16_t* o = (const uint16_t*)L.ab + i * 2 * L.ldh + j;
+          a[fj] = *(const uint2*)o;
+          b[fj] = *(const uint2*)(o + L.ldh);
         }
-        uint16_t* c = (uint16_t*)P.C + i * 2 * L.ldh + j;
-        *(uint2*)c = make_uint2(g[0] | (g[1] << 16), g[2] | (g[3] << 16));
-        *(uint2*)(c + L.ldh) = make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
       }
-    } else {
+    };
+    fetch(0, ua[0], ub[0]);
+    static_for<0, FM>([&](auto fc) __attribute__((always_inline)) {
+      constexpr int fi = decltype(fc)::value;
+      const uint2 (&a)[FN] = ua[fi & 1];
+      const uint2 (&b)[FN] = ub[fi & 1];
+      if constexpr (fi + 1 < FM) fetch(fi + 1, ua[(fi + 1) & 1], ub[(fi + 1) & 1]);
+      const int64_t i = iw + fi * 16;
+      if (i < P.M) {
+#pragma unroll
+        for (int fj = 0; fj < FN; ++fj) {
+          const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;
+          if (j >= L.ldh) continue;
+          const floatx4 c = acc[fi][fj];
+          uint16_t* o = (uint16_t*)P.C + i * 2 * L.ldh + j;
+          *(uint2*)o = make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(a[fj].x), c[1] * l_unpack_hi(a[fj].x)),
+                                  l_f32_bf16x2(c[2] * l_unpack_lo(a[fj].y), c[3] * l_unpack_hi(a[fj].y)));
+          *(uint2*)(o + L.ldh) =
+              make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(b[fj].x), c[1] * l_unpack_hi(b[fj].x)),
+                         l_f32_bf16x2(c[2] * l_unpack_lo(b[fj].y), c[3] * l_unpack_hi(b[fj].y)));
+        }
+      }
+    });
+  } else {
+#pragma unroll
+    for (int fi = 0; fi < FM; ++fi) {
+      const int64_t i = iw + fi * 16;
+      if (i >= P.M) continue;
 #pragma unroll
       for (int fj = 0; fj < FN; ++fj) {
         const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;

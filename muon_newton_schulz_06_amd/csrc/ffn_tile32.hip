@@ -131,51 +131,60 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
   }
 
   // acc[a][b][r]: row 8·(r/4) + 4·(lane/32) + r%4, column lane%32
+  auto row = [&](int a, int r) { return i0 + wm * 64 + a * 32 + 8 * (r >> 2) + 4 * lk + (r & 3); };
+  if constexpr (EPI == FFN_GLU) {
+    const int64_t j = j0 + wn * 32 + lr;
+    if (j >= L.ldh) return;  // columns N .. ldh − 1 are written as zeros
+    ffn_with_act(L.act, [&](auto actc) {
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t i = row(a, r);
+          if (i >= P.M) continue;
+          float v, d;
+          const float u = acc[a][1][r];
+          ffn_act<decltype(actc)::value, true>(acc[a][0][r], v, d);
+          ((float*)P.C)[i * P.ldc + j] = v * u;
+          if (L.ab) {
+            float* ab = (float*)L.ab + i * 2 * L.ldh + j;
+            ab[0] = u * d;
+            ab[L.ldh] = v;
+          }
+        }
+    });
+    return;
+  }
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int64_t i = i0 + wm * 64 + a * 32 + 8 * (r >> 2) + 4 * lk + (r & 3);
+      const int64_t i = row(a, r);
       if (i >= P.M) continue;
-      if constexpr (EPI == FFN_GLU) {
-        const int64_t j = j0 + wn * 32 + lr;
-        if (j >= L.ldh) continue;  // columns N .. ldh − 1 are written as zeros
-        float v, d;
-        const float g = acc[a][0][r], u = acc[a][1][r];
-        ffn_act<true>(L.act, g, v, d);
-        ((float*)P.C)[i * P.ldc + j] = v * u;
-        if (L.ab) {
-          float* ab = (float*)L.ab + i * 2 * L.ldh + j;
-          ab[0] = u * d;
-          ab[L.ldh] = v;
-        }
-      } else {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int64_t j = j0 + wn * 64 + b * 32 + lr;
-          const float c = acc[a][b][r];
-          if constexpr (EPI == FFN_BACK) {
-            if (j >= L.ldh) continue;
-            const int64_t e = i * 2 * L.ldh + j;
-            const float* ab = (const float*)L.ab + e;
-            float* o = (float*)P.C + e;
-            o[0] = c * ab[0];
-            o[L.ldh] = c * ab[L.ldh];
+      for (int b = 0; b < 2; ++b) {
+        const int64_t j = j0 + wn * 64 + b * 32 + lr;
+        const float c = acc[a][b][r];
+        if constexpr (EPI == FFN_BACK) {
+          if (j >= L.ldh) continue;
+          const int64_t e = i * 2 * L.ldh + j;
+          const float* ab = (const float*)L.ab + e;
+          float* o = (float*)P.C + e;
+          o[0] = c * ab[0];
+          o[L.ldh] = c * ab[L.ldh];
+        } else {
+          if (j >= P.N) continue;
+          const int64_t e = i * P.ldc + j;
+          if (L.outBf16) {
+            const float old = L.accumulate ? LType<Bf16>::get(P.C, e) : 0.f;
+            LType<Bf16>::put(P.C, e, c + old);
           } else {
-            if (j >= P.N) continue;
-            const int64_t e = i * P.ldc + j;
-            if (L.outBf16) {
-              const float old = L.accumulate ? LType<Bf16>::get(P.C, e) : 0.f;
-              LType<Bf16>::put(P.C, e, c + old);
-            } else {
-              const float old = L.accumulate ? LType<float>::get(P.C, e) : 0.f;
-              LType<float>::put(P.C, e, c + old);
-            }
+            const float old = L.accumulate ? LType<float>::get(P.C, e) : 0.f;
+            LType<float>::put(P.C, e, c + old);
           }
         }
       }
     }
-  }
 }
 
 }  // namespace

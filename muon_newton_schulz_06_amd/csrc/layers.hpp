@@ -159,12 +159,15 @@ struct Bf16 {
 
 __device__ __forceinline__ float l_bf16_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
-// Round to nearest even; NaN stays NaN.
+// Round to nearest even (the hardware's conversion; NaN stays NaN): one value,
+// and two as the halves of a dword.
+typedef __bf16 lbf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t l_f32_bf16(float f) {
-  uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (u >> 16) | 0x40u;
-  u += 0x7fffu + ((u >> 16) & 1u);
-  return u >> 16;
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+__device__ __forceinline__ uint32_t l_f32_bf16x2(float lo, float hi) {
+  const lbf16x2 v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
 }
 
 template <typename T> struct LType;
@@ -201,7 +204,7 @@ template <typename T> __device__ __forceinline__ lu32x4 l_narrow(const float (&v
   lu32x4 c;
   if constexpr (LType<T>::kVec == 8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = l_f32_bf16(v[2 * i]) | (l_f32_bf16(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) c[i] = l_f32_bf16x2(v[2 * i], v[2 * i + 1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = __float_as_uint(v[i]);
@@ -251,26 +254,27 @@ __device__ __forceinline__ float l_wave_sum(float v) {
   return v;
 }
 
-// 16-bit float with 6 exponent bits (bias 31) and 9 mantissa bits, rounded to
-// nearest even: the fp32 exponent field less 96.  Magnitudes below 2^-30
-// become zero, those of 2^32 and more infinity; NaN stays NaN.
-__device__ __forceinline__ uint32_t l_pack_e6m9(float f) {
+// 16-bit float: sign, 6 exponent bits (the fp32 exponent less 96), 9 mantissa
+// bits rounded to nearest (ties away from zero: one addition).  Magnitudes
+// below 2^-30 keep an error of up to 2^-31; those of 2^32 and more, infinity
+// and NaN become the one NaN, all ones.  Five operations: 2·|x| has exponent
+// and mantissa in its top 31 bits, the saturating subtraction moves the
+// exponent and sends small magnitudes to 0, the minimum caps the large ones.
+__device__ __forceinline__ uint32_t l_e6m9_top(float f) {  // code in bits 31:16
   const uint32_t u = __float_as_uint(f);
-  const uint32_t m = u & 0x7fffffffu;
-  uint32_t r;
-  if (m > 0x7f800000u) {
-    r = 0x7fffu;
-  } else {
-    const uint32_t rounded = m + 0x1fffu + ((m >> 14) & 1u);
-    r = rounded < (97u << 23) ? 0u : min((rounded - (96u << 23)) >> 14, 0x7e00u);
-  }
-  return r | ((u >> 16) & 0x8000u);
+  const uint32_t m = min(__builtin_elementwise_sub_sat((u << 1) + 0x4000u, 96u << 24), 0x3fff8000u);
+  return (m << 1) | (u & 0x80000000u);
 }
-__device__ __forceinline__ float l_unpack_e6m9(uint32_t c) {
-  const uint32_t r = c & 0x7fffu;
-  uint32_t m = r < 0x200u ? 0u : (r << 14) + (96u << 23);
-  if (r >= 0x7e00u) m |= 0x7f800000u;
-  return __uint_as_float(m | ((c & 0x8000u) << 16));
+__device__ __forceinline__ uint32_t l_pack_e6m9x2(float lo, float hi) {
+  return (l_e6m9_top(lo) >> 16) | (l_e6m9_top(hi) & 0xffff0000u);
 }
+// The halves of a dword of two codes.  The code's bits as an fp32 with its own
+// exponent field, times 2^96 (a field of 0 is an fp32 subnormal there).
+__device__ __forceinline__ float l_e6m9_value(int32_t top) {
+  const float f = __uint_as_float((uint32_t)(top >> 2) & 0x9fffc000u) * 0x1p96f;
+  return fabsf(f) >= 8573157376.f ? __uint_as_float(0x7fc00000u) : f;  // 2^32·(1 + 511/512)
+}
+__device__ __forceinline__ float l_unpack_lo(uint32_t w) { return l_e6m9_value((int32_t)(w << 16)); }
+__device__ __forceinline__ float l_unpack_hi(uint32_t w) { return l_e6m9_value((int32_t)w); }
 
 }  // namespace muon

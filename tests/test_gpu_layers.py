@@ -321,6 +321,20 @@ def test_gated_ffn_grad_accumulates(lib, tokens, model, hidden, gdt):
     assert only[1:] == (None, None, None)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_ffn_mixed_strides(lib, dtype):
+    """Every operand and result with a row stride of its own."""
+    ts = ffn_inputs(70, 96, 136, dtype)
+    f, b = ffn_bounds(*(f64(t) for t in ts), "silu", dtype, dtype)
+    x, wg, wu, wd, dy = (strided(t, pad) for t, pad in zip(ts, (8, 16, 40, 0, 24)))
+    y, saved = lib.muon_gated_ffn(x, wg, wu, wd, save=True, out=strided(ts[0], 32))
+    check(y, f["y"], b["y"], "y")
+    outs = [strided(t, pad) for t, pad in zip(ts[1:4], (48, 8, 56))]
+    got = lib.muon_gated_ffn_grad(dy, x, wg, wu, wd, saved, grads=outs)
+    for n, g in zip(NAMES, got):
+        check(g, f[n], b[n], n)
+
+
 def test_gated_ffn_empty(lib):
     x, wg, wu, wd, _ = (t.cuda() for t in ffn_inputs(4, 24, 40, torch.bfloat16))
     x = x[:0]
