@@ -115,7 +115,7 @@ struct FfnLaunch {
   // FFN_BACK: reads them, C is dg, du (rows of 2·ldh)
   void* ab;
   int64_t ldh;  // hidden rounded up to 8: row length of h and of each half
-  // tile16: k-tiles of 32 per split (a multiple of four), and where FFN_STORE
+  // k-tiles of 32 per split (a multiple of four for bf16), and where FFN_STORE
   // leaves each split's fp32 result (null: one split, C is written)
   int32_t splitTiles;
   float* part;    // [split][M][partN]
@@ -146,7 +146,7 @@ struct FfnPack {
 };
 hipError_t launch_ffn_pack(const FfnPack& K, hipStream_t st);
 
-hipError_t launch_ffn_tile32(int epi, bool aRowContig, bool bRowContig, const FfnLaunch& L,
+hipError_t launch_ffn_tile32(int epi, int tileM, bool aRowContig, bool bRowContig, const FfnLaunch& L,
                              hipStream_t st);
 
 // ----- device helpers --------------------------------------------------------
@@ -212,15 +212,18 @@ template <typename T> __device__ __forceinline__ lu32x4 l_narrow(const float (&v
   return c;
 }
 
-// Elements [e, e + kVec) of a row of n elements as a chunk: one 16-byte
-// access when VEC, else one access per element that exists (others 0).
+// Elements [e, e + kVec) of a row of n elements as a chunk: one 16-byte access
+// when VEC, else one of any alignment where the chunk is whole and one access
+// per element that exists at the row's end (others 0).
 template <typename T, bool VEC>
 __device__ __forceinline__ lu32x4 l_load(const void* row, int64_t e, int64_t n) {
   if constexpr (VEC) {
     return *(const lu32x4*)((const char*)row + e * (16 / LType<T>::kVec));
   } else {
     lu32x4 c = {0u, 0u, 0u, 0u};
-    if constexpr (LType<T>::kVec == 8) {
+    if (e + LType<T>::kVec <= n) {
+      __builtin_memcpy(&c, (const char*)row + e * (16 / LType<T>::kVec), 16);
+    } else if constexpr (LType<T>::kVec == 8) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (e + i < n) c[i / 2] |= (uint32_t)((const uint16_t*)row)[e + i] << (16 * (i & 1));
@@ -237,6 +240,8 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void l_store(void* row, int64_t e, int64_t n, lu32x4 c) {
   if constexpr (VEC) {
     *(lu32x4*)((char*)row + e * (16 / LType<T>::kVec)) = c;
+  } else if (e + LType<T>::kVec <= n) {
+    __builtin_memcpy((char*)row + e * (16 / LType<T>::kVec), &c, 16);
   } else if constexpr (LType<T>::kVec == 8) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

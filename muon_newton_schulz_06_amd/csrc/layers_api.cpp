@@ -179,29 +179,33 @@ bool direct16(const void* p, int64_t ld, int64_t cols) {
   return whole_chunks(p, ld, cols, 2) && ld < (int64_t(1) << 22) - 64;
 }
 
-// Tile edge and k splits of a bf16 product of M × N with KT k-tiles of 32.
-// Estimated time: rounds of workgroups over the GPU × (k-tiles × time of one +
-// a fixed part), in µs, plus writing and adding up the splits' results.
-struct Plan16 {
-  int tile, splits, per;
+// Tile (rows × columns) and k splits of a product of M × N over KT k-tiles of
+// 32.  Estimated time: rounds of workgroups over the GPU × (k-tiles × time of
+// one + a fixed part), in µs, plus writing and adding up the splits' results.
+struct TilePlan {
+  int tm, tn, splits, per;
 };
-Plan16 plan16(int64_t M, int64_t N, int64_t KT, bool maySplit) {
+TilePlan plan_tiles(bool bf16, int64_t M, int64_t N, int64_t KT, bool maySplit) {
   struct Kind {
-    int tile;
+    int tm, tn;
     double slots, ktile, fixed;
   };
-  const Kind kinds[2] = {{256, 256, 0.80, 8.0}, {128, 512, 0.50, 6.0}};
-  Plan16 best{};
+  static const Kind k16[2] = {{256, 256, 256, 0.80, 8.0}, {128, 128, 512, 0.50, 6.0}};
+  static const Kind k32[2] = {{128, 128, 512, 3.6, 8.0}, {64, 128, 768, 2.8, 6.0}};
+  const Kind* kinds = bf16 ? k16 : k32;
+  const int unit = bf16 ? 4 : 1;  // the bf16 loop runs whole groups of four k-tiles
+  TilePlan best{};
   double bestT = 0;
-  for (const Kind& k : kinds) {
-    const int64_t tiles = tiles_of(M, k.tile) * tiles_of(N, k.tile);
+  for (int i = 0; i < 2; ++i) {
+    const Kind& k = kinds[i];
+    const int64_t tiles = tiles_of(M, k.tm) * tiles_of(N, k.tn);
     for (int s = 1; s <= (maySplit ? 32 : 1); ++s) {
-      const int64_t per = std::max<int64_t>(4, tiles_of(tiles_of(KT, s), 4) * 4);
-      if (s > 1 && (tiles_of(KT, per) != s || per < 16)) continue;
+      const int64_t per = std::max<int64_t>(unit, tiles_of(tiles_of(KT, s), unit) * unit);
+      if (s > 1 && (tiles_of(KT, per) != s || per < 2 * unit)) continue;
       double t = std::ceil(tiles * s / k.slots) * (per * k.ktile + k.fixed);
       if (s > 1) t += 4.0 + 8.0 * s * M * N / 4e6;
-      if (!best.tile || t < bestT) {
-        best = {k.tile, s, (int)per};
+      if (!best.tm || t < bestT) {
+        best = {k.tm, k.tn, s, (int)per};
         bestT = t;
       }
     }
@@ -215,7 +219,7 @@ struct FfnLayout {
   // workspace: what the call computes (h, or dg and du), aligned copies, and
   // the splits' partial results
   size_t mid, x, dy, gate, up, down, part, total;
-  Plan16 plan;                  // of y, or of dx
+  TilePlan plan;                // of y, or of dx
 };
 
 // Layout for the forward (grad = 0) or the backward pass.
@@ -234,14 +238,17 @@ FfnLayout ffn_layout(const muon_ffn_t& f, bool grad) {
     return o;
   };
   l.mid = take(grad ? 2 * rows : rows);
-  if (f.dtype == MUON_DTYPE_BF16 && f.tokens > 0) {
+  const bool bf16 = f.dtype == MUON_DTYPE_BF16;
+  if (bf16 && f.tokens > 0) {
     const int64_t D8 = round8(f.model);
     l.x = take((size_t)f.tokens * D8 * 2);
     l.dy = take(grad ? (size_t)f.tokens * D8 * 2 : 0);
     l.gate = take(direct16(f.w_gate, f.ld_gate, f.model) ? 0 : (size_t)f.hidden * D8 * 2);
     l.up = take(direct16(f.w_up, f.ld_up, f.model) ? 0 : (size_t)f.hidden * D8 * 2);
     l.down = take(direct16(f.w_down, f.ld_down, f.hidden) ? 0 : (size_t)f.model * l.ldh * 2);
-    l.plan = plan16(f.tokens, f.model, tiles_of(l.ldh, 32) * (grad ? 2 : 1), true);
+  }
+  if (f.tokens > 0) {
+    l.plan = plan_tiles(bf16, f.tokens, f.model, tiles_of(f.hidden, 32) * (grad ? 2 : 1), true);
     l.part = take(l.plan.splits > 1 ? (size_t)l.plan.splits * f.tokens * (tiles_of(f.model, 4) * 4) * 4 : 0);
   }
   l.total = at;
@@ -262,8 +269,6 @@ void ffn_weights(Args& a, const muon_ffn_t& f) {
   a.matrix("w_up", f.w_up, f.hidden, f.model, f.ld_up, e, false);
   a.matrix("w_down", f.w_down, f.model, f.hidden, f.ld_down, e, false);
 }
-
-constexpr int64_t kTile32 = 128;  // edge of the fp32 products' tiles
 
 // Sets prob q's tile range (tile edges tm × tn, k splits).
 void set_tiles(FfnLaunch& L, int q, int64_t tm, int64_t tn, int splits = 1) {
@@ -303,19 +308,22 @@ struct FfnCall {
     return launched(what, launch_ffn_pack(k, st), st);
   }
 
-  // A plain product with one problem: bf16 with the layout's split plan.
+  muon_status_t launch(const char* what, int epi, bool ar, bool br, const TilePlan& g, const FfnLaunch& L) const {
+    if (!bf16()) return launched(what, launch_ffn_tile32(epi, g.tm, ar, br, L, st), st);
+    if (epi == FFN_GLU) return launched(what, launch_ffn16_glu(g.tm, L, st), st);
+    if (epi == FFN_BACK) return launched(what, launch_ffn16_back(g.tm, L, st), st);
+    return launched(what, launch_ffn16_store(g.tm, ar, br, L, st), st);
+  }
+
+  // A plain product with one problem, by the layout's split plan.
   muon_status_t product(const char* what, bool ar, bool br, FfnLaunch& L) const {
     FfnProb& p = L.prob[0];
-    if (!bf16()) {
-      set_tiles(L, 0, kTile32, kTile32);
-      return launched(what, launch_ffn_tile32(FFN_STORE, ar, br, L, st), st);
-    }
-    const Plan16& g = l.plan;
+    const TilePlan& g = l.plan;
     L.splitTiles = g.per;
     L.partN = tiles_of(p.N, 4) * 4;
     L.part = g.splits > 1 ? (float*)(ws + l.part) : nullptr;
-    set_tiles(L, 0, g.tile, g.tile, g.splits);
-    const muon_status_t s = launched(what, launch_ffn16_store(g.tile, ar, br, L, st), st);
+    set_tiles(L, 0, g.tm, g.tn, g.splits);
+    const muon_status_t s = launch(what, FFN_STORE, ar, br, g, L);
     if (s != MUON_OK || g.splits == 1) return s;
     FfnJoin J{L.part, p.M, L.partN, p.N, g.splits, p.C, p.ldc, p.vecC, L.outBf16};
     return launched("sum of the k splits", launch_ffn_join(J, st), st);
@@ -604,16 +612,10 @@ muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x,
     p.N = (int32_t)F;
     p.K[0] = (int32_t)ox.ext;
     set_out(p, h, l.ldh, bf16);
-    const char* what = "gated projections";
-    if (bf16) {
-      const Plan16 g = plan16(T, 2 * F, tiles_of(ox.ext, 32), false);
-      L.splitTiles = g.per;
-      set_tiles(L, 0, g.tile, g.tile / 2);
-      s = launched(what, launch_ffn16_glu(g.tile, L, st), st);
-    } else {
-      set_tiles(L, 0, kTile32, kTile32 / 2);
-      s = launched(what, launch_ffn_tile32(FFN_GLU, false, false, L, st), st);
-    }
+    const TilePlan g = plan_tiles(bf16, T, 2 * F, tiles_of(ox.ext, 32), false);
+    L.splitTiles = g.per;
+    set_tiles(L, 0, g.tm, g.tn / 2);
+    s = call.launch("gated projections", FFN_GLU, false, false, g, L);
     if (s != MUON_OK) return s;
     FfnLaunch Y{};
     Y.outBf16 = bf16;
@@ -690,16 +692,10 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
       p.N = F;
       p.K[0] = D;
       set_out(p, dgu, 2 * l.ldh, bf16);
-      const char* what = "gradient of the gated product";
-      if (bf16) {
-        const Plan16 g = plan16(T, F, tiles_of(D, 32), false);
-        L.splitTiles = g.per;
-        set_tiles(L, 0, g.tile, g.tile);
-        s = launched(what, launch_ffn16_back(g.tile, L, st), st);
-      } else {
-        set_tiles(L, 0, kTile32, kTile32);
-        s = launched(what, launch_ffn_tile32(FFN_BACK, false, true, L, st), st);
-      }
+      const TilePlan g = plan_tiles(bf16, T, F, tiles_of(D, 32), false);
+      L.splitTiles = g.per;
+      set_tiles(L, 0, g.tm, g.tn);
+      s = call.launch("gradient of the gated product", FFN_BACK, false, true, g, L);
       if (s != MUON_OK) return s;
     }
     if (T > 0 && grads->dx) {
@@ -734,7 +730,7 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
     L.outBf16 = grads->grad_dtype == MUON_DTYPE_BF16;
     L.accumulate = grads->accumulate != 0;
     // three products over the tokens in one launch
-    const Plan16 g = plan16(3 * (int64_t)F, D, tiles_of(T, 32), false);
+    const TilePlan g = plan_tiles(bf16, 3 * (int64_t)F, D, tiles_of(T, 32), false);
     L.splitTiles = g.per;
     for (int q = 0; q < 3; ++q) {
       FfnProb& p = L.prob[q];
@@ -749,12 +745,9 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
       p.K[0] = T;
       set_out(p, q == 0 ? grads->dw_gate : q == 1 ? grads->dw_up : grads->dw_down,
               q == 0 ? grads->ld_gate : q == 1 ? grads->ld_up : grads->ld_down, L.outBf16);
-      if (bf16) set_tiles(L, q, g.tile, g.tile);
-      else set_tiles(L, q, kTile32, kTile32);
+      set_tiles(L, q, g.tm, g.tn);
     }
-    const char* what = "gradients of the weights";
-    if (bf16) return launched(what, launch_ffn16_store(g.tile, true, true, L, st), st);
-    return launched(what, launch_ffn_tile32(FFN_STORE, true, true, L, st), st);
+    return call.launch("gradients of the weights", FFN_STORE, true, true, g, L);
   });
 }
 
