@@ -19,8 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmuon_ns.so")
 SOURCES = ["gemm_axpy.hip", "gemm_sq.hip", "gemm_final.hip", "gemm_syrk.hip", "elementwise.hip",
            "select.hip", "noalloc.hip", "embedding.hip", "rmsnorm.hip", "ffn_tile32.hip", "ffn_tile16_glu.hip",
-           "ffn_tile16_store.hip", "plan.cpp",
-           "api.cpp", "layers_api.cpp"]
+           "ffn_tile16_store.hip", "ffn_few.hip", "ffn_join.hip", "plan.cpp", "api.cpp", "layers_api.cpp"]
 
 
 def hipcc() -> str:

@@ -1,4 +1,4 @@
-// Activations of the gated feed-forward block.
+// Activations and results of the gated feed-forward block's products.
 #pragma once
 
 #include <type_traits>
@@ -44,6 +44,99 @@ template <typename F> __device__ __forceinline__ void ffn_with_act(int act, F&& 
   if (act == MUON_ACT_SILU) f(std::integral_constant<int, MUON_ACT_SILU>{});
   else if (act == MUON_ACT_GELU) f(std::integral_constant<int, MUON_ACT_GELU>{});
   else f(std::integral_constant<int, MUON_ACT_GELU_TANH>{});
+}
+
+// ----- results, four columns [j, j + 4) of row i at a time -------------------
+
+// C ← c (+ C); vec: the four elements are one aligned access where they exist.
+__device__ __forceinline__ void ffn_store4(void* C, int64_t ldc, int64_t i, int64_t j, int64_t n, bool bf16,
+                                           bool accumulate, bool vec, const float (&c)[4]) {
+  const int64_t e = i * ldc + j;
+  if (bf16) {
+    uint16_t* o = (uint16_t*)C + e;
+    if (vec && j + 4 <= n) {
+      float v[4] = {c[0], c[1], c[2], c[3]};
+      if (accumulate) {
+        const uint2 u = *(const uint2*)o;
+        v[0] += __uint_as_float(u.x << 16);
+        v[1] += __uint_as_float(u.x & 0xffff0000u);
+        v[2] += __uint_as_float(u.y << 16);
+        v[3] += __uint_as_float(u.y & 0xffff0000u);
+      }
+      *(uint2*)o = make_uint2(l_f32_bf16x2(v[0], v[1]), l_f32_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (j + r < n) o[r] = (uint16_t)l_f32_bf16(c[r] + (accumulate ? l_bf16_f32(o[r]) : 0.f));
+    }
+  } else {
+    float* o = (float*)C + e;
+    if (vec && j + 4 <= n) {
+      lf32x4 v = {c[0], c[1], c[2], c[3]};
+      if (accumulate) v += *(const lf32x4*)o;
+      *(lf32x4*)o = v;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (j + r < n) o[r] = c[r] + (accumulate ? o[r] : 0.f);
+    }
+  }
+}
+
+// One split's sums (half 1: u of FFN_GLU, stored in the second half of a row).
+__device__ __forceinline__ void ffn_part4(const FfnProb& P, int split, int64_t i, int64_t j, bool glu, int half,
+                                          const float (&c)[4]) {
+  const int64_t w = glu ? P.partN / 2 : P.partN;
+  if (j < w)  // w is a multiple of 4
+    *(lf32x4*)(P.part + ((int64_t)split * P.M + i) * P.partN + half * w + j) = lf32x4{c[0], c[1], c[2], c[3]};
+}
+
+// FFN_GLU: h, and with SAVE a = u·act'(g) and b = act(g).  Rows of h and of
+// each half of ab have ldh elements, a multiple of 8.
+template <typename T, int ACT, bool SAVE>
+__device__ __forceinline__ void ffn_glu4(const FfnLaunch& L, const FfnProb& P, int64_t i, int64_t j,
+                                         const float (&g)[4], const float (&u)[4]) {
+  constexpr bool F32 = LType<T>::kVec == 4;
+  float v[4], d[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    ffn_act<ACT, F32>(g[r], v[r], d[r]);
+    d[r] *= u[r];
+  }
+  if constexpr (F32) {
+    *(lf32x4*)((float*)P.C + i * P.ldc + j) = lf32x4{v[0] * u[0], v[1] * u[1], v[2] * u[2], v[3] * u[3]};
+    if constexpr (SAVE) {
+      float* o = (float*)L.ab + i * 2 * L.ldh + j;
+      *(lf32x4*)o = lf32x4{d[0], d[1], d[2], d[3]};
+      *(lf32x4*)(o + L.ldh) = lf32x4{v[0], v[1], v[2], v[3]};
+    }
+  } else {
+    *(uint2*)((uint16_t*)P.C + i * P.ldc + j) =
+        make_uint2(l_f32_bf16x2(v[0] * u[0], v[1] * u[1]), l_f32_bf16x2(v[2] * u[2], v[3] * u[3]));
+    if constexpr (SAVE) {
+      uint16_t* o = (uint16_t*)L.ab + i * 2 * L.ldh + j;
+      *(uint2*)o = make_uint2(l_pack_e6m9x2(d[0], d[1]), l_pack_e6m9x2(d[2], d[3]));
+      *(uint2*)(o + L.ldh) = make_uint2(l_pack_e6m9x2(v[0], v[1]), l_pack_e6m9x2(v[2], v[3]));
+    }
+  }
+}
+
+// Runs f(activation, save) with both as compile-time constants.
+template <typename F> __device__ __forceinline__ void ffn_with_glu(const FfnLaunch& L, F&& f) {
+  ffn_with_act(L.act, [&](auto actc) __attribute__((always_inline)) {
+    if (L.ab) f(actc, std::true_type{});
+    else f(actc, std::false_type{});
+  });
+}
+
+// FFN_BACK, bf16: dg = dh·a and du = dh·b from the codes of a and b.
+__device__ __forceinline__ void ffn_back4_bf16(const FfnLaunch& L, const FfnProb& P, int64_t i, int64_t j,
+                                               const float (&c)[4], uint2 a, uint2 b) {
+  uint16_t* o = (uint16_t*)P.C + i * 2 * L.ldh + j;
+  *(uint2*)o = make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(a.x), c[1] * l_unpack_hi(a.x)),
+                          l_f32_bf16x2(c[2] * l_unpack_lo(a.y), c[3] * l_unpack_hi(a.y)));
+  *(uint2*)(o + L.ldh) = make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(b.x), c[1] * l_unpack_hi(b.x)),
+                                    l_f32_bf16x2(c[2] * l_unpack_lo(b.y), c[3] * l_unpack_hi(b.y)));
 }
 
 }  // namespace muon

@@ -46,41 +46,6 @@ __device__ __forceinline__ void f_dma16(uint32_t lds_base, uint32_t off, fi32x4 
                : "memory", "m0");
 }
 
-// Four accumulators of one row → columns [j, j + 4) of C.
-__device__ __forceinline__ void f_store4(void* C, int64_t ldc, int64_t i, int64_t j, int64_t n, bool bf16,
-                                         bool accumulate, bool vec, const floatx4& c) {
-  const int64_t e = i * ldc + j;
-  if (bf16) {
-    uint16_t* o = (uint16_t*)C + e;
-    if (vec && j + 4 <= n) {
-      float v[4] = {c[0], c[1], c[2], c[3]};
-      if (accumulate) {
-        const uint2 u = *(const uint2*)o;
-        v[0] += __uint_as_float(u.x << 16);
-        v[1] += __uint_as_float(u.x & 0xffff0000u);
-        v[2] += __uint_as_float(u.y << 16);
-        v[3] += __uint_as_float(u.y & 0xffff0000u);
-      }
-      *(uint2*)o = make_uint2(l_f32_bf16x2(v[0], v[1]), l_f32_bf16x2(v[2], v[3]));
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (j + r < n) o[r] = (uint16_t)l_f32_bf16(c[r] + (accumulate ? l_bf16_f32(o[r]) : 0.f));
-    }
-  } else {
-    float* o = (float*)C + e;
-    if (vec && j + 4 <= n) {
-      lf32x4 v = {c[0], c[1], c[2], c[3]};
-      if (accumulate) v += *(const lf32x4*)o;
-      *(lf32x4*)o = v;
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (j + r < n) o[r] = c[r] + (accumulate ? o[r] : 0.f);
-    }
-  }
-}
-
 template <int TILE, int EPI, bool AROW, bool BROW>
 __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
   constexpr int NW = TILE / 32, WN = TILE / 64, WTM = TILE / 2, FM = WTM / 16, FN = 4;
@@ -264,34 +229,53 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
 
   // acc[fi][fj][r]: row fi·16 + lane%16, column fj·16 + 4·(lane/16) + r
   const int64_t iw = i0 + wm * WTM + lc;
-  if constexpr (EPI == FFN_GLU) {
-    auto write = [&](auto actc, auto savec) __attribute__((always_inline)) {
+  // results: f(i, j, fi, fj) for every group of four columns inside the rows
+  // and the given width
+  auto groups = [&](auto nfj, int cols, int64_t width, auto&& f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int fi = 0; fi < FM; ++fi) {
-        const int64_t i = iw + fi * 16;
-        if (i >= P.M) continue;
+    for (int fi = 0; fi < FM; ++fi) {
+      const int64_t i = iw + fi * 16;
+      if (i >= P.M) continue;
 #pragma unroll
-        for (int fj = 0; fj < 2; ++fj) {
-          const int64_t j = j0 + wn * 32 + fj * 16 + 4 * lg;
-          if (j >= L.ldh) continue;  // ldh is a multiple of 8; columns N .. ldh − 1 come out as zeros
-          float v[4], d[4];
-          const floatx4 u = acc[fi][fj + 2];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) ffn_act<decltype(actc)::value, false>(acc[fi][fj][r], v[r], d[r]);
-          *(uint2*)((uint16_t*)P.C + i * P.ldc + j) =
-              make_uint2(l_f32_bf16x2(v[0] * u[0], v[1] * u[1]), l_f32_bf16x2(v[2] * u[2], v[3] * u[3]));
-          if constexpr (decltype(savec)::value) {
-            uint16_t* o = (uint16_t*)L.ab + i * 2 * L.ldh + j;
-            *(uint2*)o = make_uint2(l_pack_e6m9x2(u[0] * d[0], u[1] * d[1]),
-                                    l_pack_e6m9x2(u[2] * d[2], u[3] * d[3]));
-            *(uint2*)(o + L.ldh) = make_uint2(l_pack_e6m9x2(v[0], v[1]), l_pack_e6m9x2(v[2], v[3]));
-          }
-        }
+      for (int fj = 0; fj < decltype(nfj)::value; ++fj) {
+        const int64_t j = j0 + wn * cols + fj * 16 + 4 * lg;
+        if (j < width) f(i, j, fi, fj);
       }
-    };
-    ffn_with_act(L.act, [&](auto actc) __attribute__((always_inline)) {
-      if (L.ab) write(actc, std::true_type{});
-      else write(actc, std::false_type{});
+    }
+  };
+  auto four = [](const floatx4& c, float (&v)[4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = c[r];
+  };
+  constexpr auto kTwoF = std::integral_constant<int, 2>{};
+  constexpr auto kAllF = std::integral_constant<int, FN>{};
+  if (P.part) {
+    if constexpr (EPI == FFN_GLU) {
+      groups(kTwoF, 32, P.partN / 2, [&](int64_t i, int64_t j, int fi, int fj) __attribute__((always_inline)) {
+        float g[4], u[4];
+        four(acc[fi][fj], g);
+        four(acc[fi][fj + 2], u);
+        ffn_part4(P, split, i, j, true, 0, g);
+        ffn_part4(P, split, i, j, true, 1, u);
+      });
+    } else {
+      groups(kAllF, 64, P.partN, [&](int64_t i, int64_t j, int fi, int fj) __attribute__((always_inline)) {
+        float c[4];
+        four(acc[fi][fj], c);
+        ffn_part4(P, split, i, j, false, 0, c);
+      });
+    }
+    return;
+  }
+  if constexpr (EPI == FFN_GLU) {
+    // columns N .. ldh − 1 come out as zeros
+    ffn_with_glu(L, [&](auto actc, auto savec) __attribute__((always_inline)) {
+      groups(kTwoF, 32, L.ldh, [&](int64_t i, int64_t j, int fi, int fj) __attribute__((always_inline)) {
+        float g[4], u[4];
+        four(acc[fi][fj], g);
+        four(acc[fi][fj + 2], u);
+        ffn_glu4<Bf16, decltype(actc)::value, decltype(savec)::value>(L, P, i, j, g, u);
+      });
     });
   } else if constexpr (EPI == FFN_BACK) {
     // the factors of the next block row are read before the current one's
@@ -322,33 +306,18 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
         for (int fj = 0; fj < FN; ++fj) {
           const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;
           if (j >= L.ldh) continue;
-          const floatx4 c = acc[fi][fj];
-          uint16_t* o = (uint16_t*)P.C + i * 2 * L.ldh + j;
-          *(uint2*)o = make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(a[fj].x), c[1] * l_unpack_hi(a[fj].x)),
-                                  l_f32_bf16x2(c[2] * l_unpack_lo(a[fj].y), c[3] * l_unpack_hi(a[fj].y)));
-          *(uint2*)(o + L.ldh) =
-              make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(b[fj].x), c[1] * l_unpack_hi(b[fj].x)),
-                         l_f32_bf16x2(c[2] * l_unpack_lo(b[fj].y), c[3] * l_unpack_hi(b[fj].y)));
+          float c[4];
+          four(acc[fi][fj], c);
+          ffn_back4_bf16(L, P, i, j, c, a[fj], b[fj]);
         }
       }
     });
   } else {
-#pragma unroll
-    for (int fi = 0; fi < FM; ++fi) {
-      const int64_t i = iw + fi * 16;
-      if (i >= P.M) continue;
-#pragma unroll
-      for (int fj = 0; fj < FN; ++fj) {
-        const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;
-        if (j >= P.N) continue;
-        if (L.part) {
-          *(lf32x4*)(L.part + ((int64_t)split * P.M + i) * L.partN + j) =
-              lf32x4{acc[fi][fj][0], acc[fi][fj][1], acc[fi][fj][2], acc[fi][fj][3]};
-        } else {
-          f_store4(P.C, P.ldc, i, j, P.N, L.outBf16, L.accumulate, P.vecC, acc[fi][fj]);
-        }
-      }
-    }
+    groups(kAllF, 64, P.N, [&](int64_t i, int64_t j, int fi, int fj) __attribute__((always_inline)) {
+      float c[4];
+      four(acc[fi][fj], c);
+      ffn_store4(P.C, P.ldc, i, j, P.N, L.outBf16, L.accumulate, P.vecC, c);
+    });
   }
 }
 

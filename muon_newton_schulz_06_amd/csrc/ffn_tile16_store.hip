@@ -1,6 +1,6 @@
 // bf16 feed-forward products with a plain result: the down projection, the
-// gradient of the input, the gradients of the weights; the sum of the k
-// splits' partial results; the aligned copy of an operand.
+// gradient of the input, the gradients of the weights; the aligned copy of an
+// operand.
 #include "ffn_tile16.hpp"
 
 namespace muon {
@@ -11,20 +11,6 @@ void store_launch(int tile, const FfnLaunch& L, hipStream_t st) {
   const dim3 grid(L.tiles[L.nprob]);
   if (tile == 256) hipLaunchKernelGGL((ffn_tile16<256, FFN_STORE, AROW, BROW>), grid, dim3(512), 0, st, L);
   else hipLaunchKernelGGL((ffn_tile16<128, FFN_STORE, AROW, BROW>), grid, dim3(256), 0, st, L);
-}
-
-// C ← Σ over splits, in order; four columns per thread.
-__global__ __launch_bounds__(256) void ffn_join(const FfnJoin J) {
-  const int64_t quads = J.N / 4;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (e >= J.M * quads) return;
-  const int64_t i = e / quads, j = (e - i * quads) * 4;
-  const float* p = J.part + i * J.N + j;
-  lf32x4 s = *(const lf32x4*)p;
-#pragma unroll 4
-  for (int k = 1; k < J.splits; ++k) s += *(const lf32x4*)(p + (int64_t)k * J.M * J.N);
-  const floatx4 c = {s[0], s[1], s[2], s[3]};
-  f_store4(J.C, J.ldc, i, j, J.nReal, J.outBf16, false, J.vecC, c);
 }
 
 // rows × cols of any stride and alignment → rows of ldo (a multiple of 8),
@@ -44,12 +30,6 @@ hipError_t launch_ffn16_store(int tile, bool aRowContig, bool bRowContig, const 
   if (aRowContig) store_launch<true, true>(tile, L, st);
   else if (bRowContig) store_launch<false, true>(tile, L, st);
   else store_launch<false, false>(tile, L, st);
-  return hipGetLastError();
-}
-
-hipError_t launch_ffn_join(const FfnJoin& J, hipStream_t st) {
-  const int64_t n = J.M * (J.N / 4);
-  hipLaunchKernelGGL(ffn_join, dim3((n + 255) / 256), dim3(256), 0, st, J);
   return hipGetLastError();
 }
 

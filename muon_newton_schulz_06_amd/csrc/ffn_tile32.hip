@@ -4,8 +4,7 @@
 // TM/2 × 64 (32×32×2 MFMAs), k in steps of 32.  The operands are staged
 // through registers into k-major LDS panels (rows of TM + 4 or 132 floats: the
 // transposing writes of a k-contiguous operand then spread over the banks),
-// double buffered, one barrier per step, the next step's global loads issued
-// before the MFMAs.  A 32×32×2 MFMA takes 64 cycles and its two 4-byte LDS
+// double buffered, one barrier per step, the global loads two steps ahead.  A 32×32×2 MFMA takes 64 cycles and its two 4-byte LDS
 // reads are shared by two MFMAs each, so a full GPU is bound by the matrix
 // pipe; small products are bound by the latency of a step (load, barrier),
 // which is what the 64-row tile and the k splits are for.
@@ -23,20 +22,26 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr int kTN = 128, kKs = 32;
 
 // Four operand values: (row, k..k+3) of a k-contiguous operand or
-// (row..row+3, k) of a row-contiguous one; zeros outside rows × K.  Whole
-// groups are one 16-byte load at any 4-byte alignment.
-template <bool ROWC>
-__device__ __forceinline__ lf32x4 fetch4(const float* p, int64_t ld, int64_t row, int64_t k, int64_t rows,
-                                         int64_t K) {
+// (row..row+3, k) of a row-contiguous one, one 16-byte load at any 4-byte
+// alignment.  EDGE: a group may reach over the end of K, or of a
+// row-contiguous operand's rows, and gets zeros there.  Rows of a k-contiguous
+// operand past the last one repeat it (their results are not stored).
+template <bool ROWC, bool EDGE>
+__device__ __forceinline__ lf32x4 fetch4(const float* p, int64_t ld, int row, int k, int rows, int K) {
   lf32x4 v = {0.f, 0.f, 0.f, 0.f};
-  const int64_t e = ROWC ? k * ld + row : row * ld + k;
-  const int64_t have = row >= rows || k >= K ? 0 : ROWC ? rows - row : K - k;
-  if (have >= 4) {
-    __builtin_memcpy(&v, p + e, 16);
+  const int r = ROWC ? row : min(row, rows - 1);
+  const float* e = p + (ROWC ? k * ld + r : r * ld + k);
+  if constexpr (!EDGE) {
+    __builtin_memcpy(&v, e, 16);
   } else {
+    const int have = ROWC ? (k < K ? rows - row : 0) : K - k;
+    if (have >= 4) {
+      __builtin_memcpy(&v, e, 16);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (i < have) v[i] = p[e + i];
+      for (int i = 0; i < 3; ++i)
+        if (i < have) v[i] = e[i];
+    }
   }
   return v;
 }
@@ -61,7 +66,7 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
   const int split = t / (tilesM * tilesN);
   t -= split * (tilesM * tilesN);
   const int ti = t % tilesM, tj = t / tilesM;
-  const int64_t i0 = (int64_t)ti * TM, j0 = (int64_t)tj * TN;
+  const int i0 = ti * TM, j0 = tj * TN;
 
   f32x16 acc[FA][2];
 #pragma unroll
@@ -77,25 +82,31 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
   const int steps0 = (P.K[0] + kKs - 1) / kKs;
   const int all = steps0 + (P.K[1] + kKs - 1) / kKs;
   const int s0 = split * L.splitTiles, s1 = min(all, s0 + L.splitTiles);
-  lf32x4 ra[NA], rb[NB];
-  auto fetch = [&](int s) {
+  lf32x4 ra[2][NA], rb[2][NB];  // of the next two steps
+  auto fetch_as = [&](int s, lf32x4 (&fa)[NA], lf32x4 (&fb)[NB], auto edgec) __attribute__((always_inline)) {
+    constexpr bool EDGE = decltype(edgec)::value;
     const int z = s >= steps0;
-    const int64_t k0 = (int64_t)(z ? s - steps0 : s) * kKs;
-    const int64_t K = P.K[z];
+    const int k0 = (z ? s - steps0 : s) * kKs, K = P.K[z];
 #pragma unroll
     for (int h = 0; h < NA; ++h)
-      ra[h] = fetch4<AROW>((const float*)P.A[z], P.lda, i0 + at_row(AROW, TM, h), k0 + at_k(AROW, TM, h), P.M, K);
+      fa[h] = fetch4<AROW, EDGE>((const float*)P.A[z], P.lda, i0 + at_row(AROW, TM, h), k0 + at_k(AROW, TM, h), P.M, K);
 #pragma unroll
     for (int h = 0; h < NB; ++h) {
       const int r = at_row(BROW, kTN, h);
       if constexpr (EPI == FFN_GLU) {
-        const int which = (r >> 5) & 1;  // the same for the whole group h
-        rb[h] = fetch4<false>((const float*)P.B[which], P.ldb[which], j0 + (r >> 6) * 32 + (r & 31),
-                              k0 + at_k(false, kTN, h), P.N, K);
+        const int which = h & 1;  // rows 32·h .. of the tile
+        fb[h] = fetch4<false, EDGE>((const float*)P.B[which], P.ldb[which], j0 + (h >> 1) * 32 + (r & 31),
+                                    k0 + at_k(false, kTN, h), P.N, K);
       } else {
-        rb[h] = fetch4<BROW>((const float*)P.B[z], P.ldb[z], j0 + r, k0 + at_k(BROW, kTN, h), P.N, K);
+        fb[h] = fetch4<BROW, EDGE>((const float*)P.B[z], P.ldb[z], j0 + r, k0 + at_k(BROW, kTN, h), P.N, K);
       }
     }
+  };
+  const bool inside = (!AROW || i0 + TM <= P.M) && (!BROW || j0 + TN <= P.N);
+  auto fetch = [&](int s, lf32x4 (&fa)[NA], lf32x4 (&fb)[NB]) __attribute__((always_inline)) {
+    const int z = s >= steps0;
+    if (inside && ((z ? s - steps0 : s) + 1) * kKs <= P.K[z]) fetch_as(s, fa, fb, std::false_type{});
+    else fetch_as(s, fa, fb, std::true_type{});
   };
   auto put = [&](float* s, bool rowc, int T, int ld, int h, const lf32x4& v) {
     const int r = at_row(rowc, T, h), k = at_k(rowc, T, h);
@@ -107,16 +118,16 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
     }
   };
   const int lr = lane & 31, lk = lane >> 5;
-  if (s0 < s1) fetch(s0);
-  for (int s = s0; s < s1; ++s) {
-    float* pa = sa[s & 1];
-    float* pb = sb[s & 1];
+  auto step = [&](int s, auto parity) __attribute__((always_inline)) {
+    constexpr int h2 = decltype(parity)::value;
+    float* pa = sa[h2];
+    float* pb = sb[h2];
 #pragma unroll
-    for (int h = 0; h < NA; ++h) put(pa, AROW, TM, LA, h, ra[h]);
+    for (int h = 0; h < NA; ++h) put(pa, AROW, TM, LA, h, ra[h2][h]);
 #pragma unroll
-    for (int h = 0; h < NB; ++h) put(pb, BROW, kTN, LB, h, rb[h]);
+    for (int h = 0; h < NB; ++h) put(pb, BROW, kTN, LB, h, rb[h2][h]);
     __syncthreads();
-    if (s + 1 < s1) fetch(s + 1);
+    if (s + 2 < s1) fetch(s + 2, ra[h2], rb[h2]);
 #pragma unroll
     for (int k = 0; k < kKs; k += 2) {
       float fa[FA], fb[2];
@@ -130,65 +141,100 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
         for (int b = 0; b < 2; ++b)
           acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[a], fb[b], acc[a][b], 0, 0, 0);
     }
+  };
+  if (s0 < s1) fetch(s0, ra[0], rb[0]);
+  if (s0 + 1 < s1) fetch(s0 + 1, ra[1], rb[1]);
+  for (int s = s0; s < s1; s += 2) {
+    step(s, std::integral_constant<int, 0>{});
+    if (s + 1 < s1) step(s + 1, std::integral_constant<int, 1>{});
   }
 
   // acc[a][b][r]: row 8·(r/4) + 4·(lane/32) + r%4, column lane%32
-  auto row = [&](int a, int r) { return i0 + wm * (TM / 2) + a * 32 + 8 * (r >> 2) + 4 * lk + (r & 3); };
+  auto row = [&](int a, int r) { return (int64_t)i0 + wm * (TM / 2) + a * 32 + 8 * (r >> 2) + 4 * lk + (r & 3); };
   if constexpr (EPI == FFN_GLU) {
     const int64_t j = j0 + wn * 32 + lr;
-    if (j >= L.ldh) return;  // columns N .. ldh − 1 are written as zeros
-    ffn_with_act(L.act, [&](auto actc) {
+    if (j >= (P.part ? (int64_t)P.N : L.ldh)) return;  // columns N .. ldh − 1 of the results are zeros
+    auto each = [&](auto&& f) __attribute__((always_inline)) {
 #pragma unroll
       for (int a = 0; a < FA; ++a)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t i = row(a, r);
-          if (i >= P.M) continue;
-          float v, d;
-          const float u = acc[a][1][r];
-          ffn_act<decltype(actc)::value, true>(acc[a][0][r], v, d);
-          ((float*)P.C)[i * P.ldc + j] = v * u;
-          if (L.ab) {
-            float* ab = (float*)L.ab + i * 2 * L.ldh + j;
-            ab[0] = u * d;
-            ab[L.ldh] = v;
-          }
+        for (int r = 0; r < 16; ++r)
+          if (row(a, r) < P.M) f(row(a, r), acc[a][0][r], acc[a][1][r]);
+    };
+    if (P.part) {
+      each([&](int64_t i, float g, float u) __attribute__((always_inline)) {
+        float* o = P.part + ((int64_t)split * P.M + i) * P.partN + j;
+        o[0] = g;
+        o[P.partN / 2] = u;
+      });
+      return;
+    }
+    const bool real = j < P.N;  // the rows past w_gate's and w_up's last one repeat it
+    ffn_with_glu(L, [&](auto actc, auto savec) __attribute__((always_inline)) {
+      each([&](int64_t i, float g, float u) __attribute__((always_inline)) {
+        float v, d;
+        ffn_act<decltype(actc)::value, true>(real ? g : 0.f, v, d);
+        u = real ? u : 0.f;
+        ((float*)P.C)[i * P.ldc + j] = v * u;
+        if constexpr (decltype(savec)::value) {
+          float* ab = (float*)L.ab + i * 2 * L.ldh + j;
+          ab[0] = u * d;
+          ab[L.ldh] = v;
         }
+      });
     });
     return;
   }
-#pragma unroll
-  for (int a = 0; a < FA; ++a)
+  // one 32×32 block at a time: what it reads first (one wait), then its stores
+  auto block = [&](const f32x16& c, int a, int b, auto read, auto write) __attribute__((always_inline)) {
+    const int64_t j = j0 + wn * 64 + b * 32 + lr;
+    if (j >= (EPI == FFN_BACK && !P.part ? L.ldh : (int64_t)P.N)) return;
+    float u[16], v[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int64_t i = row(a, r);
-      if (i >= P.M) continue;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int64_t j = j0 + wn * 64 + b * 32 + lr;
-        const float c = acc[a][b][r];
-        if constexpr (EPI == FFN_BACK) {
-          if (j >= L.ldh) continue;
-          const int64_t e = i * 2 * L.ldh + j;
-          const float* ab = (const float*)L.ab + e;
-          float* o = (float*)P.C + e;
-          o[0] = c * ab[0];
-          o[L.ldh] = c * ab[L.ldh];
-        } else {
-          if (j >= P.N) continue;
-          const int64_t e = i * P.ldc + j;
-          if (L.part) {
-            L.part[((int64_t)split * P.M + i) * L.partN + j] = c;
-          } else if (L.outBf16) {
-            const float old = L.accumulate ? LType<Bf16>::get(P.C, e) : 0.f;
-            LType<Bf16>::put(P.C, e, c + old);
-          } else {
-            const float old = L.accumulate ? LType<float>::get(P.C, e) : 0.f;
-            LType<float>::put(P.C, e, c + old);
-          }
-        }
-      }
+      u[r] = v[r] = 0.f;
+      if (row(a, r) < P.M) read(row(a, r), j, u[r], v[r]);
     }
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (row(a, r) < P.M) write(row(a, r), j, c[r], u[r], v[r]);
+  };
+  auto blocks = [&](auto read, auto write) __attribute__((always_inline)) {
+#pragma unroll
+    for (int a = 0; a < FA; ++a)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) block(acc[a][b], a, b, read, write);
+  };
+  auto nothing = [](int64_t, int64_t, float&, float&) {};
+  if (P.part) {
+    blocks(nothing, [&](int64_t i, int64_t j, float c, float, float) {
+      P.part[((int64_t)split * P.M + i) * P.partN + j] = c;
+    });
+  } else if constexpr (EPI == FFN_BACK) {
+    blocks(
+        [&](int64_t i, int64_t j, float& u, float& v) {
+          const float* ab = (const float*)L.ab + i * 2 * L.ldh + j;
+          u = ab[0];
+          v = ab[L.ldh];
+        },
+        [&](int64_t i, int64_t j, float c, float u, float v) {
+          float* o = (float*)P.C + i * 2 * L.ldh + j;
+          o[0] = c * u;
+          o[L.ldh] = c * v;
+        });
+  } else if (L.outBf16) {
+    blocks(
+        [&](int64_t i, int64_t j, float& u, float&) {
+          if (L.accumulate) u = LType<Bf16>::get(P.C, i * P.ldc + j);
+        },
+        [&](int64_t i, int64_t j, float c, float u, float) { LType<Bf16>::put(P.C, i * P.ldc + j, c + u); });
+  } else {
+    blocks(
+        [&](int64_t i, int64_t j, float& u, float&) {
+          if (L.accumulate) u = ((const float*)P.C)[i * P.ldc + j];
+        },
+        [&](int64_t i, int64_t j, float c, float u, float) { ((float*)P.C)[i * P.ldc + j] = c + u; });
+  }
 }
 
 template <int TM>

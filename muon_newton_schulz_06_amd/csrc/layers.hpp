@@ -103,6 +103,10 @@ struct FfnProb {
   void* C;
   int64_t ldc;
   int32_t vecC;  // four consecutive elements of C are one aligned access
+  // where the k splits leave their fp32 sums, [split][M][partN] (null: one
+  // split, C is written); partN: N rounded up to 4, for FFN_GLU twice that
+  float* part;
+  int64_t partN;
 };
 
 struct FfnLaunch {
@@ -115,27 +119,19 @@ struct FfnLaunch {
   // FFN_BACK: reads them, C is dg, du (rows of 2·ldh)
   void* ab;
   int64_t ldh;  // hidden rounded up to 8: row length of h and of each half
-  // k-tiles of 32 per split (a multiple of four for bf16), and where FFN_STORE
-  // leaves each split's fp32 result (null: one split, C is written)
-  int32_t splitTiles;
-  float* part;    // [split][M][partN]
-  int64_t partN;  // N rounded up to 4
+  int32_t splitTiles;  // k-tiles of 32 per split (a multiple of four for bf16 tiles)
 };
 hipError_t launch_ffn16_glu(int tile, const FfnLaunch& L, hipStream_t st);
 hipError_t launch_ffn16_back(int tile, const FfnLaunch& L, hipStream_t st);
 hipError_t launch_ffn16_store(int tile, bool aRowContig, bool bRowContig, const FfnLaunch& L,
                               hipStream_t st);
 
-// Sum of the splits' results, [splits][M][N] → M × nReal.
-struct FfnJoin {
-  const float* part;
-  int64_t M, N, nReal;
-  int32_t splits;
-  void* C;
-  int64_t ldc;
-  int32_t vecC, outBf16;
-};
-hipError_t launch_ffn_join(const FfnJoin& J, hipStream_t st);
+// The few-token forward products (tokens ≤ kFfnFew), any alignment.
+constexpr int64_t kFfnFew = 64;
+hipError_t launch_ffn_few(int epi, bool bf16, int splits, const FfnLaunch& L, hipStream_t st);
+
+// Sums of the splits' results, with the products' epilogue.
+hipError_t launch_ffn_join(int epi, bool bf16, int splits, const FfnLaunch& L, hipStream_t st);
 
 // Aligned, zero-padded copy of a bf16 operand.
 struct FfnPack {

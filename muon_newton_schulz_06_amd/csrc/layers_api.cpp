@@ -179,33 +179,38 @@ bool direct16(const void* p, int64_t ld, int64_t cols) {
   return whole_chunks(p, ld, cols, 2) && ld < (int64_t(1) << 22) - 64;
 }
 
-// Tile (rows × columns) and k splits of a product of M × N over KT k-tiles of
-// 32.  Estimated time: rounds of workgroups over the GPU × (k-tiles × time of
-// one + a fixed part), in µs, plus writing and adding up the splits' results.
+// How a product runs: the tile (rows × columns; tm = 0: the few-token kernel)
+// and its k splits.
 struct TilePlan {
-  int tm, tn, splits, per;
+  int tm, tn, splits, per;  // per: k-tiles of 32 in a split
 };
-TilePlan plan_tiles(bool bf16, int64_t M, int64_t N, int64_t KT, bool maySplit) {
-  struct Kind {
-    int tm, tn;
-    double slots, ktile, fixed;
-  };
-  static const Kind k16[2] = {{256, 256, 256, 0.80, 8.0}, {128, 128, 512, 0.50, 6.0}};
-  static const Kind k32[2] = {{128, 128, 512, 3.6, 8.0}, {64, 128, 768, 2.8, 6.0}};
-  const Kind* kinds = bf16 ? k16 : k32;
+
+// Estimated time of n workgroups of `per` k-tiles, in µs, fitted to measured
+// products (bf16 tiles 256² run one to a CU, 128² two; the fp32 tiles are
+// bound by the matrix pipe or, alone on a CU, by a step's latency).
+double tile_time(bool bf16, int tm, int64_t n, int64_t per) {
+  const double cu = std::ceil(n / 256.0);  // workgroups on the busiest CU
+  if (bf16) return tm == 256 ? cu * (per * 0.80 + 8) : std::ceil(n / 512.0) * (per * (n <= 256 ? 0.36 : 0.50) + 6);
+  return 10 + per * (tm == 128 ? std::max(2.7, 2.48 * cu) : std::max(1.45, 1.28 * cu));
+}
+
+// Tile and splits of a product of M × N results (all problems of a launch
+// together) over KT k-tiles.
+TilePlan plan_tiles(bool bf16, int64_t M, int64_t N, int64_t KT) {
+  static const int k16[2][2] = {{256, 256}, {128, 128}}, k32[2][2] = {{128, 128}, {64, 128}};
   const int unit = bf16 ? 4 : 1;  // the bf16 loop runs whole groups of four k-tiles
   TilePlan best{};
   double bestT = 0;
   for (int i = 0; i < 2; ++i) {
-    const Kind& k = kinds[i];
-    const int64_t tiles = tiles_of(M, k.tm) * tiles_of(N, k.tn);
-    for (int s = 1; s <= (maySplit ? 32 : 1); ++s) {
+    const int tm = bf16 ? k16[i][0] : k32[i][0], tn = bf16 ? k16[i][1] : k32[i][1];
+    const int64_t tiles = tiles_of(M, tm) * tiles_of(N, tn);
+    for (int s = 1; s <= 32; ++s) {
       const int64_t per = std::max<int64_t>(unit, tiles_of(tiles_of(KT, s), unit) * unit);
       if (s > 1 && (tiles_of(KT, per) != s || per < 2 * unit)) continue;
-      double t = std::ceil(tiles * s / k.slots) * (per * k.ktile + k.fixed);
-      if (s > 1) t += 4.0 + 8.0 * s * M * N / 4e6;
+      double t = tile_time(bf16, tm, tiles * s, per);
+      if (s > 1) t += 5.0 + 8.0 * s * M * N / 4e6;  // the splits' sums written and read
       if (!best.tm || t < bestT) {
-        best = {k.tm, k.tn, s, (int)per};
+        best = {tm, tn, s, (int)per};
         bestT = t;
       }
     }
@@ -213,21 +218,36 @@ TilePlan plan_tiles(bool bf16, int64_t M, int64_t N, int64_t KT, bool maySplit) 
   return best;
 }
 
+// The few-token kernel: about 1024 workgroups of 16 weight rows, each split at
+// least one step (4 waves × 4 loads of 32 k) long.
+TilePlan plan_few(int64_t N, int64_t K) {
+  constexpr int64_t step = 16;  // k-tiles
+  const int64_t KT = tiles_of(K, 32), want = std::max<int64_t>(1, tiles_of(1024, tiles_of(N, 16)));
+  const int64_t per = std::max(step, tiles_of(tiles_of(KT, want), step) * step);
+  return {0, 16, (int)tiles_of(KT, per), (int)per};
+}
+
 struct FfnLayout {
-  int64_t ldh;                  // hidden rounded up to 8
-  size_t ab, savedH, saved;     // in `saved`
+  int64_t ldh;               // hidden rounded up to 8
+  size_t ab, savedH, saved;  // in `saved`
   // workspace: what the call computes (h, or dg and du), aligned copies, and
-  // the splits' partial results
+  // the splits' sums
   size_t mid, x, dy, gate, up, down, part, total;
-  TilePlan plan;                // of y, or of dx
+  bool few;
+  // forward: the gated projections and y; backward: dh, dx and the weights'
+  TilePlan first, second, third;
 };
+
+int64_t round4(int64_t n) { return (n + 3) / 4 * 4; }
 
 // Layout for the forward (grad = 0) or the backward pass.
 FfnLayout ffn_layout(const muon_ffn_t& f, bool grad) {
   FfnLayout l{};
   const size_t e = esize(f.dtype);
-  l.ldh = round8(f.hidden);
-  const size_t rows = (size_t)f.tokens * l.ldh * e;
+  const bool bf16 = f.dtype == MUON_DTYPE_BF16;
+  const int64_t T = f.tokens, D = f.model, F = f.hidden, D8 = round8(D);
+  l.ldh = round8(F);
+  const size_t rows = (size_t)T * l.ldh * e;
   l.ab = 0;
   l.savedH = align256(2 * rows);
   l.saved = l.savedH + align256(rows);
@@ -238,19 +258,42 @@ FfnLayout ffn_layout(const muon_ffn_t& f, bool grad) {
     return o;
   };
   l.mid = take(grad ? 2 * rows : rows);
-  const bool bf16 = f.dtype == MUON_DTYPE_BF16;
-  if (bf16 && f.tokens > 0) {
-    const int64_t D8 = round8(f.model);
-    l.x = take((size_t)f.tokens * D8 * 2);
-    l.dy = take(grad ? (size_t)f.tokens * D8 * 2 : 0);
-    l.gate = take(direct16(f.w_gate, f.ld_gate, f.model) ? 0 : (size_t)f.hidden * D8 * 2);
-    l.up = take(direct16(f.w_up, f.ld_up, f.model) ? 0 : (size_t)f.hidden * D8 * 2);
-    l.down = take(direct16(f.w_down, f.ld_down, f.hidden) ? 0 : (size_t)f.model * l.ldh * 2);
+  if (T == 0) {
+    l.third = plan_tiles(bf16, 3 * F, D, 0);
+    l.total = at;
+    return l;
   }
-  if (f.tokens > 0) {
-    l.plan = plan_tiles(bf16, f.tokens, f.model, tiles_of(f.hidden, 32) * (grad ? 2 : 1), true);
-    l.part = take(l.plan.splits > 1 ? (size_t)l.plan.splits * f.tokens * (tiles_of(f.model, 4) * 4) * 4 : 0);
+  l.few = !grad && T <= kFfnFew;
+  if (bf16 && !l.few) {
+    l.x = take((size_t)T * D8 * 2);
+    l.dy = take(grad ? (size_t)T * D8 * 2 : 0);
+    l.gate = take(direct16(f.w_gate, f.ld_gate, D) ? 0 : (size_t)F * D8 * 2);
+    l.up = take(direct16(f.w_up, f.ld_up, D) ? 0 : (size_t)F * D8 * 2);
+    l.down = take(direct16(f.w_down, f.ld_down, F) ? 0 : (size_t)D * l.ldh * 2);
   }
+  size_t part = 0;  // floats
+  auto splits = [&](const TilePlan& p, int64_t n) {
+    if (p.splits > 1) part = std::max(part, (size_t)p.splits * n);
+  };
+  if (l.few) {
+    l.first = plan_few(F, D);
+    l.second = plan_few(D, F);
+    splits(l.first, T * 2 * round4(F));
+    splits(l.second, T * round4(D));
+  } else if (!grad) {
+    l.first = plan_tiles(bf16, T, 2 * F, tiles_of(D, 32));
+    l.second = plan_tiles(bf16, T, D, tiles_of(F, 32));
+    splits(l.first, T * 2 * round4(F));
+    splits(l.second, T * round4(D));
+  } else {
+    l.first = plan_tiles(bf16, T, F, tiles_of(D, 32));
+    l.second = plan_tiles(bf16, T, D, 2 * tiles_of(F, 32));
+    l.third = plan_tiles(bf16, 3 * F, D, tiles_of(T, 32));
+    splits(l.first, T * round4(F));
+    splits(l.second, T * round4(D));
+    splits(l.third, 2 * F * round4(D) + D * round4(F));
+  }
+  l.part = take(part * 4);
   l.total = at;
   return l;
 }
@@ -268,12 +311,6 @@ void ffn_weights(Args& a, const muon_ffn_t& f) {
   a.matrix("w_gate", f.w_gate, f.hidden, f.model, f.ld_gate, e, false);
   a.matrix("w_up", f.w_up, f.hidden, f.model, f.ld_up, e, false);
   a.matrix("w_down", f.w_down, f.model, f.hidden, f.ld_down, e, false);
-}
-
-// Sets prob q's tile range (tile edges tm × tn, k splits).
-void set_tiles(FfnLaunch& L, int q, int64_t tm, int64_t tn, int splits = 1) {
-  L.tiles[q + 1] = L.tiles[q] + (int32_t)(tiles_of(L.prob[q].M, tm) * tiles_of(L.prob[q].N, tn) * splits);
-  L.nprob = q + 1;
 }
 
 void set_out(FfnProb& p, void* C, int64_t ldc, bool bf16) {
@@ -299,7 +336,7 @@ struct FfnCall {
   // The operand itself, or its aligned copy at `at` in the workspace.
   muon_status_t operand(const char* what, const void* p, int64_t ld, int64_t rows, int64_t cols, size_t at,
                         Op* o) const {
-    if (!bf16() || direct16(p, ld, cols)) {
+    if (!bf16() || l.few || direct16(p, ld, cols)) {
       *o = {p, ld, cols};
       return MUON_OK;
     }
@@ -308,25 +345,29 @@ struct FfnCall {
     return launched(what, launch_ffn_pack(k, st), st);
   }
 
-  muon_status_t launch(const char* what, int epi, bool ar, bool br, const TilePlan& g, const FfnLaunch& L) const {
-    if (!bf16()) return launched(what, launch_ffn_tile32(epi, g.tm, ar, br, L, st), st);
-    if (epi == FFN_GLU) return launched(what, launch_ffn16_glu(g.tm, L, st), st);
-    if (epi == FFN_BACK) return launched(what, launch_ffn16_back(g.tm, L, st), st);
-    return launched(what, launch_ffn16_store(g.tm, ar, br, L, st), st);
-  }
-
-  // A plain product with one problem, by the layout's split plan.
-  muon_status_t product(const char* what, bool ar, bool br, FfnLaunch& L) const {
-    FfnProb& p = L.prob[0];
-    const TilePlan& g = l.plan;
+  // The launch's products by plan g, and the sums of their splits.
+  muon_status_t run(const char* what, int epi, bool ar, bool br, const TilePlan& g, FfnLaunch& L, int nprob) const {
+    L.ldh = l.ldh;
+    L.nprob = nprob;
     L.splitTiles = g.per;
-    L.partN = tiles_of(p.N, 4) * 4;
-    L.part = g.splits > 1 ? (float*)(ws + l.part) : nullptr;
-    set_tiles(L, 0, g.tm, g.tn, g.splits);
-    const muon_status_t s = launch(what, FFN_STORE, ar, br, g, L);
+    float* part = (float*)(ws + l.part);
+    for (int q = 0; q < nprob; ++q) {
+      FfnProb& p = L.prob[q];
+      const int64_t tn = epi == FFN_GLU ? g.tn / 2 : g.tn;  // a tile holds both projections' columns
+      if (g.tm) L.tiles[q + 1] = L.tiles[q] + (int32_t)(tiles_of(p.M, g.tm) * tiles_of(p.N, tn) * g.splits);
+      p.partN = round4(p.N) * (epi == FFN_GLU ? 2 : 1);
+      p.part = g.splits > 1 ? part : nullptr;
+      part += (size_t)g.splits * p.M * p.partN;
+    }
+    hipError_t e;
+    if (!g.tm) e = launch_ffn_few(epi, bf16(), g.splits, L, st);
+    else if (!bf16()) e = launch_ffn_tile32(epi, g.tm, ar, br, L, st);
+    else if (epi == FFN_GLU) e = launch_ffn16_glu(g.tm, L, st);
+    else if (epi == FFN_BACK) e = launch_ffn16_back(g.tm, L, st);
+    else e = launch_ffn16_store(g.tm, ar, br, L, st);
+    const muon_status_t s = launched(what, e, st);
     if (s != MUON_OK || g.splits == 1) return s;
-    FfnJoin J{L.part, p.M, L.partN, p.N, g.splits, p.C, p.ldc, p.vecC, L.outBf16};
-    return launched("sum of the k splits", launch_ffn_join(J, st), st);
+    return launched("sum of the k splits", launch_ffn_join(epi, bf16(), g.splits, L, st), st);
   }
 };
 
@@ -599,7 +640,6 @@ muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x,
     void* h = saved ? (char*)saved + l.savedH : (char*)workspace + l.mid;
     FfnLaunch L{};
     L.act = ffn->activation;
-    L.ldh = l.ldh;
     L.ab = saved ? (char*)saved + l.ab : nullptr;
     FfnProb& p = L.prob[0];
     p.A[0] = ox.p;
@@ -612,10 +652,7 @@ muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x,
     p.N = (int32_t)F;
     p.K[0] = (int32_t)ox.ext;
     set_out(p, h, l.ldh, bf16);
-    const TilePlan g = plan_tiles(bf16, T, 2 * F, tiles_of(ox.ext, 32), false);
-    L.splitTiles = g.per;
-    set_tiles(L, 0, g.tm, g.tn / 2);
-    s = call.launch("gated projections", FFN_GLU, false, false, g, L);
+    s = call.run("gated projections", FFN_GLU, false, false, l.first, L, 1);
     if (s != MUON_OK) return s;
     FfnLaunch Y{};
     Y.outBf16 = bf16;
@@ -628,7 +665,7 @@ muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x,
     d.N = (int32_t)D;
     d.K[0] = (int32_t)od.ext;
     set_out(d, y, ld_y, bf16);
-    return call.product("down projection", false, false, Y);
+    return call.run("down projection", FFN_STORE, false, false, l.second, Y, 1);
   });
 }
 
@@ -680,7 +717,6 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
       if (s == MUON_OK) s = call.operand("copy of w_down", ffn->w_down, ffn->ld_down, D, F, l.down, &od);
       if (s != MUON_OK) return s;
       FfnLaunch L{};
-      L.ldh = l.ldh;
       L.ab = (void*)(sv + l.ab);
       FfnProb& p = L.prob[0];
       p.A[0] = oy.p;
@@ -692,10 +728,7 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
       p.N = F;
       p.K[0] = D;
       set_out(p, dgu, 2 * l.ldh, bf16);
-      const TilePlan g = plan_tiles(bf16, T, F, tiles_of(D, 32), false);
-      L.splitTiles = g.per;
-      set_tiles(L, 0, g.tm, g.tn);
-      s = call.launch("gradient of the gated product", FFN_BACK, false, true, g, L);
+      s = call.run("gradient of the gated product", FFN_BACK, false, true, l.first, L, 1);
       if (s != MUON_OK) return s;
     }
     if (T > 0 && grads->dx) {
@@ -718,7 +751,7 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
       p.N = D;
       p.K[0] = p.K[1] = F;
       set_out(p, grads->dx, grads->ld_dx, bf16);
-      s = call.product("gradient of the input", false, true, L);
+      s = call.run("gradient of the input", FFN_STORE, false, true, l.second, L, 1);
       if (s != MUON_OK) return s;
     }
     if (!wantW) return MUON_OK;
@@ -730,8 +763,6 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
     L.outBf16 = grads->grad_dtype == MUON_DTYPE_BF16;
     L.accumulate = grads->accumulate != 0;
     // three products over the tokens in one launch
-    const TilePlan g = plan_tiles(bf16, 3 * (int64_t)F, D, tiles_of(T, 32), false);
-    L.splitTiles = g.per;
     for (int q = 0; q < 3; ++q) {
       FfnProb& p = L.prob[q];
       p.A[0] = q < 2 ? (const void*)(dgu + q * l.ldh * e) : oy.p;
@@ -745,9 +776,8 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
       p.K[0] = T;
       set_out(p, q == 0 ? grads->dw_gate : q == 1 ? grads->dw_up : grads->dw_down,
               q == 0 ? grads->ld_gate : q == 1 ? grads->ld_up : grads->ld_down, L.outBf16);
-      set_tiles(L, q, g.tm, g.tn);
     }
-    return call.launch("gradients of the weights", FFN_STORE, true, true, g, L);
+    return call.run("gradients of the weights", FFN_STORE, true, true, l.third, L, 3);
   });
 }
 
