@@ -4,13 +4,12 @@
 //
 // Gradient: dW[v] = scale·Σ_{t: id_t = v} dy[t] without float atomics (their
 // order, and so the last bits, would change from run to run):
-//   1. a stable radix sort of (id, t) by id;
+//   1. a stable radix sort of (id, t) by id, while dweight is zeroed;
 //   2. pieces: the sorted list is cut every kEmbedPiece positions; a piece
 //      that lies wholly inside one run of equal ids is summed to an fp32 row
 //      in the workspace, so that no run is summed by one lane group alone;
 //   3. one lane group per run: the rows before its first whole piece, the
-//      pieces' sums, the rows after the last one, in that order; the same
-//      launch writes the zero rows of the ids that do not occur.
+//      pieces' sums, the rows after the last one, in that order.
 // Ids outside [0, vocab) sort to the end as the key `vocab` and are skipped.
 #include <hip/hip_runtime.h>
 
@@ -61,6 +60,8 @@ __global__ __launch_bounds__(256) void embedding_kernel(const EmbedLaunch L, int
     }
   }
 }
+
+__device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t w, int64_t W);
 
 // ----- sort ------------------------------------------------------------------
 __device__ __forceinline__ uint32_t sort_key(const EmbedGradLaunch& L, int64_t t) {
@@ -133,7 +134,9 @@ __device__ __forceinline__ void scan_counts(uint32_t* cnt, int n, uint32_t* wsum
 
 // The whole sort of up to kEmbedSmallSort tokens in one workgroup: keys live
 // in registers, each pass permutes them through shared memory.  9-bit digits,
-// so a vocabulary of up to 2^18 − 1 takes two passes.
+// so a vocabulary of up to 2^18 − 1 takes two passes.  The launch's other
+// workgroups write dweight's zeros meanwhile (rows of ids that occur are
+// written again by the sums: at most tokens · dim elements more).
 template <int ITEMS>
 __global__ __launch_bounds__(1024) void embed_sort_small(const EmbedGradLaunch L, int passes) {
   constexpr int BITS = 9, WAVES = 16, BINS = 1 << BITS;
@@ -143,6 +146,10 @@ __global__ __launch_bounds__(1024) void embed_sort_small(const EmbedGradLaunch L
   __shared__ uint32_t wsum[WAVES];
   static_assert(ITEMS * 1024 <= 65536, "token positions are kept in 16 bits");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (blockIdx.x > 0) {
+    zero_rows(L, (int64_t)(blockIdx.x - 1) * 16 + wave, (int64_t)(gridDim.x - 1) * 16);
+    return;
+  }
   const int n = (int)L.tokens;
   uint32_t key[ITEMS], idx[ITEMS], rank[ITEMS];
   bool have[ITEMS];
@@ -279,11 +286,51 @@ __global__ __launch_bounds__(256) void embed_sort_scatter(const EmbedGradLaunch 
 }
 
 // ----- segmented sums --------------------------------------------------------
+// A lane group adds the rows idx[p0 .. p0 + n) of dy at its columns, in order;
+// the indices are read by the group's lanes at once and four rows are in
+// flight.  The group's lanes are active together.
+template <typename T, bool VEC>
+__device__ __forceinline__ void add_rows(const EmbedGradLaunch& L, const uint32_t* idx, int64_t p0, int n,
+                                         int64_t e, int l, int lanes, float (&acc)[LType<T>::kVec]) {
+  constexpr int V = LType<T>::kVec, E = 16 / V;
+  const int first = (threadIdx.x & 63) - l;  // the group's first lane in the wave
+  const bool in = e < L.dim;
+  for (int base = 0; base < n; base += lanes) {
+    const int cnt = min(lanes, n - base);
+    const int mine = l < cnt ? (int)idx[p0 + base + l] : 0;
+    int j = 0;
+    for (; j + 4 <= cnt; j += 4) {
+      lu32x4 c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t t = (uint32_t)__shfl(mine, first + j + i, 64);
+        c[i] = lu32x4{0u, 0u, 0u, 0u};
+        if (in) c[i] = l_load<T, VEC>((const char*)L.dy + t * L.ldy * E, e, L.dim);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[V];
+        l_widen<T>(c[i], f);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] += f[k];
+      }
+    }
+    for (; j < cnt; ++j) {
+      const int64_t t = (uint32_t)__shfl(mine, first + j, 64);
+      if (!in) continue;
+      float f[V];
+      l_widen<T>(l_load<T, VEC>((const char*)L.dy + t * L.ldy * E, e, L.dim), f);
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] += f[k];
+    }
+  }
+}
+
 // Sums of whole pieces inside one run.  One lane group per (piece, slice).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void embed_pieces(const EmbedGradLaunch L, const uint32_t* key,
                                                     const uint32_t* idx, int lanes, int shift) {
-  constexpr int V = LType<T>::kVec, E = 16 / V;
+  constexpr int V = LType<T>::kVec;
   const int g = threadIdx.x >> shift, l = threadIdx.x & (lanes - 1);
   const int64_t c = (int64_t)blockIdx.x * (256 >> shift) + g;
   const int64_t p0 = c * kEmbedPiece;
@@ -291,20 +338,12 @@ __global__ __launch_bounds__(256) void embed_pieces(const EmbedGradLaunch L, con
   const uint32_t k = key[p0];
   if (k != key[p0 + kEmbedPiece - 1] || k >= (uint32_t)L.vocab) return;
   const int64_t e = ((int64_t)blockIdx.y * lanes + l) * V;
-  if (e >= L.dim) return;
   float acc[V] = {};
-#pragma unroll 8
-  for (int j = 0; j < kEmbedPiece; ++j) {
-    const char* row = (const char*)L.dy + (int64_t)idx[p0 + j] * L.ldy * E;
-    float f[V];
-    l_widen<T>(l_load<T, VEC>(row, e, L.dim), f);
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += f[i];
-  }
+  add_rows<T, VEC>(L, idx, p0, kEmbedPiece, e, l, lanes, acc);
   float* out = L.pieces + c * L.dim + e;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (VEC || e + i < L.dim) out[i] = acc[i];
+    if (e + i < L.dim) out[i] = acc[i];
 }
 
 // Stores V values of a dweight row (adding to it when accumulating).
@@ -312,19 +351,19 @@ template <typename TW, bool VECW, int V>
 __device__ __forceinline__ void put_dw(const EmbedGradLaunch& L, int64_t v, int64_t e, const float (&f)[V]) {
   constexpr int VW = LType<TW>::kVec, EW = 16 / VW;
   char* row = (char*)L.dw + v * L.ldw * EW;
-  if constexpr (VECW && V % VW == 0) {
+  if constexpr (V % VW == 0) {
 #pragma unroll
     for (int h = 0; h < V; h += VW) {
-      if (e + h >= L.dim) break;  // the row is whole chunks of dweight's type, not always of dy's
+      if (e + h >= L.dim) break;  // whole chunks of dy's type may be two of dweight's
       float o[VW];
-      if (L.accumulate) l_widen<TW>(l_load<TW, true>(row, e + h, L.dim), o);
+      if (L.accumulate) l_widen<TW>(l_load<TW, VECW>(row, e + h, L.dim), o);
       else {
 #pragma unroll
         for (int i = 0; i < VW; ++i) o[i] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < VW; ++i) o[i] = fmaf(L.scale, f[h + i], o[i]);
-      l_store<TW, true>(row, e + h, L.dim, l_narrow<TW>(o));
+      l_store<TW, VECW>(row, e + h, L.dim, l_narrow<TW>(o));
     }
   } else {
 #pragma unroll
@@ -336,73 +375,70 @@ __device__ __forceinline__ void put_dw(const EmbedGradLaunch& L, int64_t v, int6
   }
 }
 
-// blockIdx.x < runBlocks: lane groups look at one sorted position each and
-// sum the run that starts there.  The other workgroups write zero rows: 64
-// ids each, present ones found by binary search in the sorted keys.
+// Number of positions p, p + 1, .. < limit whose key is k, looked at by the
+// group's lanes at once.
+__device__ __forceinline__ int run_length(const uint32_t* key, int64_t p, int64_t limit, uint32_t k, int l,
+                                          int lanes) {
+  const int first = (threadIdx.x & 63) - l;
+  int n = 0;
+  for (;;) {
+    const int64_t at = p + n + l;
+    const uint64_t same = __ballot(at < limit && key[at] == k) >> first;
+    const uint64_t miss = lanes == 64 ? ~same : ~same & ((1ull << lanes) - 1ull);
+    if (miss) return n + (__ffsll((unsigned long long)miss) - 1);
+    n += lanes;
+  }
+}
+
+// One lane group per sorted position and slice: sums the run that starts
+// there.
 template <typename T, bool VEC, typename TW, bool VECW>
 __global__ __launch_bounds__(256) void embed_rows(const EmbedGradLaunch L, const uint32_t* key,
-                                                  const uint32_t* idx, int lanes, int shift,
-                                                  int64_t runBlocks) {
-  constexpr int V = LType<T>::kVec, E = 16 / V;
-  if (blockIdx.x < runBlocks) {
-    const int g = threadIdx.x >> shift, l = threadIdx.x & (lanes - 1);
-    const int64_t s = (int64_t)blockIdx.x * (256 >> shift) + g;
-    if (s >= L.tokens) return;
-    const uint32_t k = key[s];
-    if (k >= (uint32_t)L.vocab || (s > 0 && key[s - 1] == k)) return;
-    const int64_t e = ((int64_t)blockIdx.y * lanes + l) * V;
-    if (e >= L.dim) return;
-    float acc[V] = {};
-    auto add_row = [&](int64_t p) {
-      const char* row = (const char*)L.dy + (int64_t)idx[p] * L.ldy * E;
-      float f[V];
-      l_widen<T>(l_load<T, VEC>(row, e, L.dim), f);
+                                                  const uint32_t* idx, int lanes, int shift) {
+  constexpr int V = LType<T>::kVec;
+  const int g = threadIdx.x >> shift, l = threadIdx.x & (lanes - 1);
+  const int64_t s = (int64_t)blockIdx.x * (256 >> shift) + g;
+  if (s >= L.tokens) return;
+  const uint32_t k = key[s];
+  if (k >= (uint32_t)L.vocab || (s > 0 && key[s - 1] == k)) return;
+  const int64_t e = ((int64_t)blockIdx.y * lanes + l) * V;
+  float acc[V] = {};
+  // rows up to the first piece boundary, whole pieces, the rest
+  const int64_t b = min((s + kEmbedPiece - 1) / kEmbedPiece * kEmbedPiece, L.tokens);
+  const int head = run_length(key, s, b, k, l, lanes);
+  add_rows<T, VEC>(L, idx, s, head, e, l, lanes, acc);
+  int64_t p = s + head;
+  if (p == b) {
+    while (p + kEmbedPiece <= L.tokens && key[p + kEmbedPiece - 1] == k) {
+      const float* pc = L.pieces + (p / kEmbedPiece) * L.dim + e;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += f[i];
-    };
-    int64_t p = s;
-    // rows up to the first piece boundary
-    const int64_t b = (s + kEmbedPiece - 1) / kEmbedPiece * kEmbedPiece;
-    for (; p < b && p < L.tokens && key[p] == k; ++p) add_row(p);
-    if (p == b) {
-      while (p + kEmbedPiece <= L.tokens && key[p + kEmbedPiece - 1] == k) {
-        const float* pc = L.pieces + (p / kEmbedPiece) * L.dim + e;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (VEC || e + i < L.dim) acc[i] += pc[i];
-        p += kEmbedPiece;
-      }
-      for (; p < L.tokens && key[p] == k; ++p) add_row(p);
+      for (int i = 0; i < V; ++i)
+        if (e + i < L.dim) acc[i] += pc[i];
+      p += kEmbedPiece;
     }
-    put_dw<TW, VECW, V>(L, k, e, acc);
-    return;
+    const int tail = run_length(key, p, L.tokens, k, l, lanes);
+    add_rows<T, VEC>(L, idx, p, tail, e, l, lanes, acc);
   }
-  // zero rows
-  __shared__ uint64_t present;
-  const int64_t v0 = ((int64_t)blockIdx.x - runBlocks) * 64;
-  if (threadIdx.x < 64) {
-    const int64_t v = v0 + threadIdx.x;
-    int64_t lo = 0, hi = L.tokens;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if ((int64_t)key[mid] < v) lo = mid + 1;
-      else hi = mid;
+  if (e < L.dim) put_dw<TW, VECW, V>(L, k, e, acc);
+}
+
+// Zeros the whole dweight: wave w of the W waves takes rows w, w + W, ..
+__device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t w, int64_t W) {
+  const int esz = L.dwBf16 ? 2 : 4, lane = threadIdx.x & 63;
+  for (int64_t v = w; v < L.vocab; v += W) {
+    char* row = (char*)L.dw + v * L.ldw * esz;
+    const int64_t n = L.dim * esz, whole = n & ~(int64_t)15;
+    const lu32x4 z = {0u, 0u, 0u, 0u};
+    for (int64_t e = lane * 16; e < whole; e += 1024) {
+      if (L.vecw) *(lu32x4*)(row + e) = z;
+      else __builtin_memcpy(row + e, &z, 16);
     }
-    const bool here = v < L.vocab && lo < L.tokens && (int64_t)key[lo] == v;
-    const uint64_t m = __ballot(here);
-    if (threadIdx.x == 0) present = m;
+    for (int64_t e = whole + lane * 2; e < n; e += 128) *(uint16_t*)(row + e) = 0;
   }
-  __syncthreads();
-  const uint64_t m = present;
-  constexpr int VW = LType<TW>::kVec, EW = 16 / VW;
-  const int64_t rows = min((int64_t)64, L.vocab - v0);
-  for (int64_t r = threadIdx.x >> 6; r < rows; r += 4) {
-    if ((m >> r) & 1ull) continue;
-    char* row = (char*)L.dw + (v0 + r) * L.ldw * EW;
-    for (int64_t e = ((int64_t)blockIdx.y * 64 + (threadIdx.x & 63)) * VW; e < L.dim;
-         e += (int64_t)gridDim.y * 64 * VW)
-      l_store<TW, VECW>(row, e, L.dim, lu32x4{0u, 0u, 0u, 0u});
-  }
+}
+
+__global__ __launch_bounds__(256) void embed_zero(const EmbedGradLaunch L) {
+  zero_rows(L, (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), (int64_t)gridDim.x * 4);
 }
 
 // Lanes of a group: the chunks of a row, at most a wave's.
@@ -425,11 +461,9 @@ hipError_t rows_launch(const EmbedGradLaunch& L, hipStream_t st) {
     hipLaunchKernelGGL((embed_pieces<T, VEC>), dim3((np + per - 1) / per, slices), dim3(256), 0, st, L,
                        key, idx, lanes, sh);
   }
-  const int64_t runBlocks = (L.tokens + per - 1) / per;
-  const int64_t zeroBlocks = L.accumulate ? 0 : (L.vocab + 63) / 64;
-  if (runBlocks + zeroBlocks > 0)
-    hipLaunchKernelGGL((embed_rows<T, VEC, TW, VECW>), dim3(runBlocks + zeroBlocks, slices), dim3(256), 0,
-                       st, L, key, idx, lanes, sh, runBlocks);
+  if (L.tokens > 0)
+    hipLaunchKernelGGL((embed_rows<T, VEC, TW, VECW>), dim3((L.tokens + per - 1) / per, slices), dim3(256), 0,
+                       st, L, key, idx, lanes, sh);
   return hipGetLastError();
 }
 
@@ -461,11 +495,17 @@ hipError_t launch_embedding_grad(const EmbedGradLaunch& L0, hipStream_t st) {
   EmbedGradLaunch L = L0;
   int bits = 1;  // of the largest key, vocab
   while ((L.vocab >> bits) != 0) ++bits;
+  // workgroups that write zeros: one per CU, or what the rows are worth
+  const int64_t zero = L.accumulate ? 0 : std::min<int64_t>(256, (L.vocab * L.dim + 65535) / 65536);
+  if (L.tokens == 0 || L.tokens > kEmbedSmallSort) {
+    if (zero > 0) hipLaunchKernelGGL(embed_zero, dim3(zero * 4), dim3(256), 0, st, L);
+  }
   if (L.tokens > 0 && L.tokens <= kEmbedSmallSort) {
     const int passes = (bits + 8) / 9;
-    if (L.tokens <= 1024) hipLaunchKernelGGL(embed_sort_small<1>, dim3(1), dim3(1024), 0, st, L, passes);
-    else if (L.tokens <= 4096) hipLaunchKernelGGL(embed_sort_small<4>, dim3(1), dim3(1024), 0, st, L, passes);
-    else hipLaunchKernelGGL(embed_sort_small<16>, dim3(1), dim3(1024), 0, st, L, passes);
+    const dim3 grid(1 + zero), block(1024);
+    if (L.tokens <= 1024) hipLaunchKernelGGL(embed_sort_small<1>, grid, block, 0, st, L, passes);
+    else if (L.tokens <= 4096) hipLaunchKernelGGL(embed_sort_small<4>, grid, block, 0, st, L, passes);
+    else hipLaunchKernelGGL(embed_sort_small<16>, grid, block, 0, st, L, passes);
   } else if (L.tokens > 0) {
     const int passes = (bits + kEmbedSortBits - 1) / kEmbedSortBits;
     const int blocks = (int)((L.tokens + kEmbedSortBlock - 1) / kEmbedSortBlock);

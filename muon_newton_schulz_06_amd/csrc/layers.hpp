@@ -79,7 +79,7 @@ struct NormGradLaunch {
   int32_t bf16, wBf16, vec, accumulate;
 };
 // Workgroups (and rows of partial sums) of the backward pass.
-int rms_norm_grad_blocks(int64_t tokens, int64_t dim);
+int rms_norm_grad_blocks(int64_t tokens);
 hipError_t launch_rms_norm_grad(const NormGradLaunch& L, hipStream_t st);
 
 // ----- gated feed-forward block ----------------------------------------------

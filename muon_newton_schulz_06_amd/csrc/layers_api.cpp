@@ -520,7 +520,7 @@ muon_status_t muon_rms_norm_grad_workspace_size(int64_t tokens, int64_t dim, siz
     a.size("dim", dim, 1, kMaxWidth);
     if (!bytes) a.fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
     if (!a.ok()) return a.report();
-    *bytes = tokens == 0 ? 0 : align256((size_t)rms_norm_grad_blocks(tokens, dim) * dim * 4);
+    *bytes = tokens == 0 ? 0 : align256((size_t)rms_norm_grad_blocks(tokens) * dim * 4);
     return MUON_OK;
   });
 }
@@ -540,7 +540,7 @@ muon_status_t muon_rms_norm_grad(const void* dy, int64_t ld_dy, const void* s, i
     const size_t e = esize(dtype);
     size_t need = 0;
     if (a.ok()) {
-      if (dweight && tokens > 0) need = align256((size_t)rms_norm_grad_blocks(tokens, dim) * dim * 4);
+      if (dweight && tokens > 0) need = align256((size_t)rms_norm_grad_blocks(tokens) * dim * 4);
       a.matrix("dy", dy, tokens, dim, ld_dy, e, false);
       a.matrix("s", s, tokens, dim, ld_s, e, false);
       a.matrix("weight", weight, tokens > 0, dim, dim, esize(weight_dtype), false);
@@ -572,7 +572,7 @@ muon_status_t muon_rms_norm_grad(const void* dy, int64_t ld_dy, const void* s, i
     L.ldx = ld_dx;
     L.tokens = tokens;
     L.dim = dim;
-    L.blocks = tokens > 0 ? rms_norm_grad_blocks(tokens, dim) : 0;
+    L.blocks = tokens > 0 ? rms_norm_grad_blocks(tokens) : 0;
     L.bf16 = dtype == MUON_DTYPE_BF16;
     L.wBf16 = weight_dtype == MUON_DTYPE_BF16;
     L.vec = whole_chunks(dy, ld_dy, dim, e) && whole_chunks(s, ld_s, dim, e) && whole_chunks(dx, ld_dx, dim, e) &&
