@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "layers.hpp"
 
@@ -287,7 +288,7 @@ __global__ __launch_bounds__(256) void embed_sort_scatter(const EmbedGradLaunch 
 
 // ----- segmented sums --------------------------------------------------------
 // A lane group adds the rows idx[p0 .. p0 + n) of dy at its columns, in order;
-// the indices are read by the group's lanes at once and four rows are in
+// the indices are read by the group's lanes at once and eight rows are in
 // flight.  The group's lanes are active together.
 template <typename T, bool VEC>
 __device__ __forceinline__ void add_rows(const EmbedGradLaunch& L, const uint32_t* idx, int64_t p0, int n,
@@ -299,30 +300,28 @@ __device__ __forceinline__ void add_rows(const EmbedGradLaunch& L, const uint32_
     const int cnt = min(lanes, n - base);
     const int mine = l < cnt ? (int)idx[p0 + base + l] : 0;
     int j = 0;
-    for (; j + 4 <= cnt; j += 4) {
-      lu32x4 c[4];
+    auto batch = [&](auto nc) __attribute__((always_inline)) {
+      constexpr int N = decltype(nc)::value;
+      for (; j + N <= cnt; j += N) {
+        lu32x4 c[N];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t t = (uint32_t)__shfl(mine, first + j + i, 64);
-        c[i] = lu32x4{0u, 0u, 0u, 0u};
-        if (in) c[i] = l_load<T, VEC>((const char*)L.dy + t * L.ldy * E, e, L.dim);
+        for (int i = 0; i < N; ++i) {
+          const int64_t t = (uint32_t)__shfl(mine, first + j + i, 64);
+          c[i] = lu32x4{0u, 0u, 0u, 0u};
+          if (in) c[i] = l_load<T, VEC>((const char*)L.dy + t * L.ldy * E, e, L.dim);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float f[V];
+          l_widen<T>(c[i], f);
+#pragma unroll
+          for (int k = 0; k < V; ++k) acc[k] += f[k];
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[V];
-        l_widen<T>(c[i], f);
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += f[k];
-      }
-    }
-    for (; j < cnt; ++j) {
-      const int64_t t = (uint32_t)__shfl(mine, first + j, 64);
-      if (!in) continue;
-      float f[V];
-      l_widen<T>(l_load<T, VEC>((const char*)L.dy + t * L.ldy * E, e, L.dim), f);
-#pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] += f[k];
-    }
+    };
+    batch(std::integral_constant<int, 8>{});
+    batch(std::integral_constant<int, 2>{});
+    batch(std::integral_constant<int, 1>{});
   }
 }
 
@@ -375,14 +374,14 @@ __device__ __forceinline__ void put_dw(const EmbedGradLaunch& L, int64_t v, int6
   }
 }
 
-// Number of positions p, p + 1, .. < limit whose key is k, looked at by the
-// group's lanes at once.
+// Number of leading positions p, p + step, .. < limit whose key is k, looked
+// at by the group's lanes at once.
 __device__ __forceinline__ int run_length(const uint32_t* key, int64_t p, int64_t limit, uint32_t k, int l,
-                                          int lanes) {
+                                          int lanes, int step) {
   const int first = (threadIdx.x & 63) - l;
   int n = 0;
   for (;;) {
-    const int64_t at = p + n + l;
+    const int64_t at = p + (int64_t)(n + l) * step;
     const uint64_t same = __ballot(at < limit && key[at] == k) >> first;
     const uint64_t miss = lanes == 64 ? ~same : ~same & ((1ull << lanes) - 1ull);
     if (miss) return n + (__ffsll((unsigned long long)miss) - 1);
@@ -405,18 +404,23 @@ __global__ __launch_bounds__(256) void embed_rows(const EmbedGradLaunch L, const
   float acc[V] = {};
   // rows up to the first piece boundary, whole pieces, the rest
   const int64_t b = min((s + kEmbedPiece - 1) / kEmbedPiece * kEmbedPiece, L.tokens);
-  const int head = run_length(key, s, b, k, l, lanes);
+  const int head = run_length(key, s, b, k, l, lanes, 1);
   add_rows<T, VEC>(L, idx, s, head, e, l, lanes, acc);
   int64_t p = s + head;
   if (p == b) {
-    while (p + kEmbedPiece <= L.tokens && key[p + kEmbedPiece - 1] == k) {
-      const float* pc = L.pieces + (p / kEmbedPiece) * L.dim + e;
+    // a piece is whole if its last key is k too
+    const int whole = run_length(key, p + kEmbedPiece - 1, L.tokens, k, l, lanes, kEmbedPiece);
+    const float* pc = L.pieces + (p / kEmbedPiece) * L.dim + e;
+    if (e < L.dim) {
+#pragma unroll 8
+      for (int j = 0; j < whole; ++j) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (e + i < L.dim) acc[i] += pc[i];
-      p += kEmbedPiece;
+        for (int i = 0; i < V; ++i)
+          if (VEC || e + i < L.dim) acc[i] += pc[j * L.dim + i];
+      }
     }
-    const int tail = run_length(key, p, L.tokens, k, l, lanes);
+    p += (int64_t)whole * kEmbedPiece;
+    const int tail = run_length(key, p, L.tokens, k, l, lanes, 1);
     add_rows<T, VEC>(L, idx, p, tail, e, l, lanes, acc);
   }
   if (e < L.dim) put_dw<TW, VECW, V>(L, k, e, acc);

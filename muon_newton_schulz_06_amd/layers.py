@@ -18,6 +18,7 @@ it).  A workspace is cached per device and stream unless one is passed.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -135,26 +136,25 @@ def _vector(t, name, n):
         raise ValueError(f"{name} must be a contiguous vector of {n} values, got shape {tuple(t.shape)}")
 
 
+# The raw handle of a device's current stream (without building a Stream).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
-    """The device guard and stream of a call: the given stream's (made
-    current, so that outputs are allocated for it) or the current one."""
-    __slots__ = ("guard", "stream", "handle")
+    """The device guard and stream of a call that cannot run as it is: the
+    given stream is made current (so that outputs are allocated for it), and
+    so is the tensors' device."""
+    __slots__ = ("guard",)
 
     def __init__(self, dev, stream):
-        self.guard = []
-        if dev.index is not None and dev.index != torch.cuda.current_device():
-            self.guard.append(torch.cuda.device(dev))
+        self.guard = [torch.cuda.device(dev)]
         if stream is not None:
             self.guard.append(torch.cuda.stream(stream))
-        self.stream = stream
-        self.handle = None
 
     def __enter__(self):
         for g in self.guard:
             g.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream()
-        self.handle = s.cuda_stream
-        return self
 
     def __exit__(self, *exc):
         for g in reversed(self.guard):
@@ -162,15 +162,28 @@ class _On:
         return False
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev, stream):
+    if stream is None and dev.index == torch.cuda.current_device():
+        return _HERE
+    return _On(dev, stream)
+
+
 def _out(out, shape, dtype, dev, name):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _empty(shape, dtype, dev)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(out.shape)}, expected {tuple(shape)}")
     _same(dev, dtype, **{name: out})
     if out.dim() != 2 and not out.is_contiguous():
         raise ValueError(f"{name} must be contiguous (or 2-D)")
     return out
+
+
+def _empty(shape, dtype, dev):
+    return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _ptr(t):
@@ -199,12 +212,12 @@ def muon_embedding(ids, weight, scale: float = 1.0, out=None, stream=None):
     _same(dev, None, ids=ids)
     vocab, dim = weight.shape
     _, ldw = _rows(weight, "weight")
-    with _On(dev, stream) as on:
+    with _on(dev, stream):
         ids, nb = _ids(ids)
         out = _out(out, (*ids.shape, dim), weight.dtype, dev, "out")
         o, ldo = _rows(out, "out")
         _check(L.muon_embedding(_ptr(ids), nb, ids.numel(), _ptr(weight), ldw, vocab, dim, scale, _ptr(o),
-                                ldo, code, on.handle))
+                                ldo, code, _raw_stream(dev.index)))
     return out
 
 
@@ -224,7 +237,7 @@ def muon_embedding_grad(dy, ids, vocab: int, scale: float = 1.0, out=None, dtype
         raise ValueError("accumulate needs out")
     dim, tokens = dy.shape[-1], ids.numel()
     vocab = int(vocab)
-    with _On(dev, stream) as on:
+    with _on(dev, stream):
         ids, nb = _ids(ids)
         d, ldy = _rows(dy, "dy")
         if out is None:
@@ -236,7 +249,7 @@ def muon_embedding_grad(dy, ids, vocab: int, scale: float = 1.0, out=None, dtype
         ws, nbytes = _workspace(need.value, dev, workspace, stream)
         _check(L.muon_embedding_grad(_ptr(d), ldy, _ptr(ids), nb, tokens, vocab, dim, scale, _ptr(out), ldo,
                                      code, _code(out, "out"), int(bool(accumulate)), _ptr(ws), nbytes,
-                                     on.handle))
+                                     _raw_stream(dev.index)))
     return out
 
 
@@ -259,7 +272,7 @@ def muon_rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, sum_out
         raise ValueError(f"residual has shape {tuple(residual.shape)}, x {tuple(x.shape)}")
     if sum_out is not None and residual is None:
         raise ValueError("sum_out needs residual")
-    with _On(dev, stream) as on:
+    with _on(dev, stream):
         x2, ldx = _rows(x, "x")
         r2, ldr = _rows(residual, "residual") if residual is not None else (None, 0)
         y = _out(out, x.shape, x.dtype, dev, "out")
@@ -270,7 +283,7 @@ def muon_rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, sum_out
             s2, lds = _rows(s, "sum_out")
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
         _check(L.muon_rms_norm(_ptr(x2), ldx, _ptr(r2), ldr, _ptr(weight), _code(weight, "weight"), eps,
-                               _ptr(y2), ldy, _ptr(s2), lds, _ptr(rstd), x2.shape[0], dim, code, on.handle))
+                               _ptr(y2), ldy, _ptr(s2), lds, _ptr(rstd), x2.shape[0], dim, code, _raw_stream(dev.index)))
     return y, s, rstd
 
 
@@ -293,7 +306,7 @@ def muon_rms_norm_grad(dy, s, weight, rstd, dsum=None, out=None, dweight=None, a
             raise ValueError(f"{name} has shape {tuple(t.shape)}, dy {tuple(dy.shape)}")
     if accumulate and dweight is None:
         raise ValueError("accumulate needs dweight")
-    with _On(dev, stream) as on:
+    with _on(dev, stream):
         dy2, ldy = _rows(dy, "dy")
         s2, lds = _rows(s, "s")
         d2, ldd = _rows(dsum, "dsum") if dsum is not None else (None, 0)
@@ -312,7 +325,7 @@ def muon_rms_norm_grad(dy, s, weight, rstd, dsum=None, out=None, dweight=None, a
             dweight = None
         _check(L.muon_rms_norm_grad(_ptr(dy2), ldy, _ptr(s2), lds, _ptr(weight), _code(weight, "weight"),
                                     _ptr(rstd), _ptr(d2), ldd, _ptr(dx2), ldx, _ptr(dweight),
-                                    int(bool(accumulate)), tokens, dim, code, _ptr(ws), nbytes, on.handle))
+                                    int(bool(accumulate)), tokens, dim, code, _ptr(ws), nbytes, _raw_stream(dev.index)))
     return dx, dweight
 
 
@@ -368,7 +381,7 @@ def muon_gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", save: bool
     muon_gated_ffn_grad takes."""
     L = _lib()
     dev, f, x2, ldx = _ffn(x, w_gate, w_up, w_down, activation)
-    with _On(dev, stream) as on:
+    with _on(dev, stream):
         y = _out(out, x.shape, x.dtype, dev, "out")
         y2, ldy = _rows(y, "out")
         n = ctypes.c_size_t(0)
@@ -380,7 +393,7 @@ def muon_gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", save: bool
         _check(L.muon_gated_ffn_workspace_size(ctypes.byref(f), 0, ctypes.byref(n)))
         ws, nbytes = _workspace(n.value, dev, workspace, stream)
         _check(L.muon_gated_ffn(ctypes.byref(f), _ptr(x2), ldx, _ptr(y2), ldy, _ptr(saved), nsaved,
-                                _ptr(ws), nbytes, on.handle))
+                                _ptr(ws), nbytes, _raw_stream(dev.index)))
     return (y, saved) if save else y
 
 
@@ -399,7 +412,7 @@ def muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx: bool = True
         raise ValueError(f"dy has shape {tuple(dy.shape)}, x {tuple(x.shape)}")
     if accumulate and grads is None:
         raise ValueError("accumulate needs grads")
-    with _On(dev, stream) as on:
+    with _on(dev, stream):
         dy2, ldy = _rows(dy, "dy")
         dx, dx2, lddx = None, None, 0
         if want_dx:
@@ -424,7 +437,7 @@ def muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx: bool = True
         _check(L.muon_gated_ffn_workspace_size(ctypes.byref(f), 1, ctypes.byref(n)))
         ws, nbytes = _workspace(n.value, dev, workspace, stream)
         _check(L.muon_gated_ffn_grad(ctypes.byref(f), _ptr(x2), ldx, _ptr(dy2), ldy, _ptr(saved),
-                                     saved.numel(), ctypes.byref(g), _ptr(ws), nbytes, on.handle))
+                                     saved.numel(), ctypes.byref(g), _ptr(ws), nbytes, _raw_stream(dev.index)))
     return (dx, *out)
 
 
