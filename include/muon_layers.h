@@ -56,7 +56,7 @@ muon_status_t muon_embedding(const void* ids, int32_t id_bytes, int64_t tokens, 
  * contribute nothing.
  *   dy: tokens × dim of `dtype`; dweight: vocab × dim of `dweight_dtype`.
  * The tokens are sorted by id (stable), each run of equal ids is summed in
- * token order (runs longer than 32 in pieces of 32 sorted positions). */
+ * token order (long runs in pieces of 16 sorted positions). */
 muon_status_t muon_embedding_grad(const void* dy, int64_t ld_dy, const void* ids, int32_t id_bytes,
                                   int64_t tokens, int64_t vocab, int64_t dim, float scale,
                                   void* dweight, int64_t ld_dweight, muon_dtype_t dtype,

@@ -62,7 +62,11 @@ __global__ __launch_bounds__(256) void embedding_kernel(const EmbedLaunch L, int
   }
 }
 
-__device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t w, int64_t W);
+// Zeros rows [v0, v1) of dweight: wave w of W waves takes rows v0 + w, v0 + w +
+// W, ..  Non-temporal stores: with ordinary ones the zeros filled the last-level
+// cache and their write-back ran into the sums (sums 76 -> 40 µs, sort beside
+// them 67 -> 47 µs for 131072×3584 bf16).
+__device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t v0, int64_t v1, int64_t w, int64_t W);
 
 // ----- sort ------------------------------------------------------------------
 __device__ __forceinline__ uint32_t sort_key(const EmbedGradLaunch& L, int64_t t) {
@@ -136,7 +140,7 @@ __device__ __forceinline__ void scan_counts(uint32_t* cnt, int n, uint32_t* wsum
 // The whole sort of up to kEmbedSmallSort tokens in one workgroup: keys live
 // in registers, each pass permutes them through shared memory.  9-bit digits,
 // so a vocabulary of up to 2^18 − 1 takes two passes.  The launch's other
-// workgroups write dweight's zeros meanwhile (rows of ids that occur are
+// workgroups write zeros of dweight meanwhile (rows of ids that occur are
 // written again by the sums: at most tokens · dim elements more).
 template <int ITEMS>
 __global__ __launch_bounds__(1024) void embed_sort_small(const EmbedGradLaunch L, int passes) {
@@ -148,7 +152,7 @@ __global__ __launch_bounds__(1024) void embed_sort_small(const EmbedGradLaunch L
   static_assert(ITEMS * 1024 <= 65536, "token positions are kept in 16 bits");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (blockIdx.x > 0) {
-    zero_rows(L, (int64_t)(blockIdx.x - 1) * 16 + wave, (int64_t)(gridDim.x - 1) * 16);
+    zero_rows(L, 0, L.zeroRows, (int64_t)(blockIdx.x - 1) * 16 + wave, (int64_t)(gridDim.x - 1) * 16);
     return;
   }
   const int n = (int)L.tokens;
@@ -325,18 +329,25 @@ __device__ __forceinline__ void add_rows(const EmbedGradLaunch& L, const uint32_
   }
 }
 
-// Sums of whole pieces inside one run.  One lane group per (piece, slice).
+// Sums of whole pieces inside one run.  One lane group per (piece, slice); the
+// workgroups from sumBlocks on write the zeros the sort's launch left.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void embed_pieces(const EmbedGradLaunch L, const uint32_t* key,
-                                                    const uint32_t* idx, int lanes, int shift) {
+                                                    const uint32_t* idx, int lanes, int shift, int slices,
+                                                    int sumBlocks) {
   constexpr int V = LType<T>::kVec;
+  if ((int)blockIdx.x >= sumBlocks) {
+    zero_rows(L, L.zeroRows, L.vocab, (int64_t)(blockIdx.x - sumBlocks) * 4 + (threadIdx.x >> 6),
+              (int64_t)(gridDim.x - sumBlocks) * 4);
+    return;
+  }
   const int g = threadIdx.x >> shift, l = threadIdx.x & (lanes - 1);
-  const int64_t c = (int64_t)blockIdx.x * (256 >> shift) + g;
+  const int64_t c = (int64_t)(blockIdx.x / slices) * (256 >> shift) + g;
   const int64_t p0 = c * kEmbedPiece;
   if (p0 + kEmbedPiece > L.tokens) return;
   const uint32_t k = key[p0];
   if (k != key[p0 + kEmbedPiece - 1] || k >= (uint32_t)L.vocab) return;
-  const int64_t e = ((int64_t)blockIdx.y * lanes + l) * V;
+  const int64_t e = ((int64_t)(blockIdx.x % slices) * lanes + l) * V;
   float acc[V] = {};
   add_rows<T, VEC>(L, idx, p0, kEmbedPiece, e, l, lanes, acc);
   float* out = L.pieces + c * L.dim + e;
@@ -426,15 +437,14 @@ __global__ __launch_bounds__(256) void embed_rows(const EmbedGradLaunch L, const
   if (e < L.dim) put_dw<TW, VECW, V>(L, k, e, acc);
 }
 
-// Zeros the whole dweight: wave w of the W waves takes rows w, w + W, ..
-__device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t w, int64_t W) {
+__device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t v0, int64_t v1, int64_t w, int64_t W) {
   const int esz = L.dwBf16 ? 2 : 4, lane = threadIdx.x & 63;
-  for (int64_t v = w; v < L.vocab; v += W) {
+  for (int64_t v = v0 + w; v < v1; v += W) {
     char* row = (char*)L.dw + v * L.ldw * esz;
     const int64_t n = L.dim * esz, whole = n & ~(int64_t)15;
     const lu32x4 z = {0u, 0u, 0u, 0u};
     for (int64_t e = lane * 16; e < whole; e += 1024) {
-      if (L.vecw) *(lu32x4*)(row + e) = z;
+      if (L.vecw) __builtin_nontemporal_store(z, (lu32x4*)(row + e));
       else __builtin_memcpy(row + e, &z, 16);
     }
     for (int64_t e = whole + lane * 2; e < n; e += 128) *(uint16_t*)(row + e) = 0;
@@ -442,7 +452,7 @@ __device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t w, i
 }
 
 __global__ __launch_bounds__(256) void embed_zero(const EmbedGradLaunch L) {
-  zero_rows(L, (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), (int64_t)gridDim.x * 4);
+  zero_rows(L, 0, L.zeroRows, (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), (int64_t)gridDim.x * 4);
 }
 
 // Lanes of a group: the chunks of a row, at most a wave's.
@@ -461,10 +471,11 @@ hipError_t rows_launch(const EmbedGradLaunch& L, hipStream_t st) {
   const int64_t np = L.tokens / kEmbedPiece;
   // the device-memory sort ends in the buffer its last pass wrote
   const uint32_t *key = L.key[0], *idx = L.idx[0];
-  if (np > 0) {
-    hipLaunchKernelGGL((embed_pieces<T, VEC>), dim3((np + per - 1) / per, slices), dim3(256), 0, st, L,
-                       key, idx, lanes, sh);
-  }
+  const int64_t sums = (np + per - 1) / per * slices;
+  const int64_t zeros = L.zeroRows < L.vocab ? std::min<int64_t>(1024, L.vocab - L.zeroRows) : 0;
+  if (sums + zeros > 0)
+    hipLaunchKernelGGL((embed_pieces<T, VEC>), dim3(sums + zeros), dim3(256), 0, st, L, key, idx, lanes, sh,
+                       (int)slices, (int)sums);
   if (L.tokens > 0)
     hipLaunchKernelGGL((embed_rows<T, VEC, TW, VECW>), dim3((L.tokens + per - 1) / per, slices), dim3(256), 0,
                        st, L, key, idx, lanes, sh);
@@ -499,12 +510,17 @@ hipError_t launch_embedding_grad(const EmbedGradLaunch& L0, hipStream_t st) {
   EmbedGradLaunch L = L0;
   int bits = 1;  // of the largest key, vocab
   while ((L.vocab >> bits) != 0) ++bits;
-  // workgroups that write zeros: one per CU, or what the rows are worth
-  const int64_t zero = L.accumulate ? 0 : std::min<int64_t>(256, (L.vocab * L.dim + 65535) / 65536);
-  if (L.tokens == 0 || L.tokens > kEmbedSmallSort) {
-    if (zero > 0) hipLaunchKernelGGL(embed_zero, dim3(zero * 4), dim3(256), 0, st, L);
-  }
-  if (L.tokens > 0 && L.tokens <= kEmbedSmallSort) {
+  // Zeros: what HBM takes while the one-workgroup sort runs (7, 14 or 44 µs
+  // for its three sizes) is written beside it,
+  // the rest beside the pieces' sums; all at once where there is no such sort.
+  const bool small = L.tokens > 0 && L.tokens <= kEmbedSmallSort;
+  const int64_t row = L.dim * (L.dwBf16 ? 2 : 4);
+  const int64_t hidden = L.tokens <= 1024 ? 35 << 20 : L.tokens <= 4096 ? 70 << 20 : 240 << 20;
+  if (L.accumulate) L.zeroRows = L.vocab;  // nothing to write
+  else L.zeroRows = small ? std::min(L.vocab, hidden / row + 1) : L.vocab;
+  const int64_t zero = L.accumulate ? 0 : std::min<int64_t>(256, (L.zeroRows * row + 65535) / 65536);
+  if (!small && zero > 0) hipLaunchKernelGGL(embed_zero, dim3(zero * 4), dim3(256), 0, st, L);
+  if (small) {
     const int passes = (bits + 8) / 9;
     const dim3 grid(1 + zero), block(1024);
     if (L.tokens <= 1024) hipLaunchKernelGGL(embed_sort_small<1>, grid, block, 0, st, L, passes);

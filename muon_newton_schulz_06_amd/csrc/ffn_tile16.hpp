@@ -47,12 +47,14 @@ __device__ __forceinline__ void f_dma16(uint32_t lds_base, uint32_t off, fi32x4 
 }
 
 template <int TILE, int EPI, bool AROW, bool BROW>
-__global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
-  constexpr int NW = TILE / 32, WN = TILE / 64, WTM = TILE / 2, FM = WTM / 16, FN = 4;
-  constexpr int KB = 32;                              // k per k-tile
-  constexpr int kHalf = TILE * KB * 2, kSlot = 2 * kHalf;  // bytes of an operand's tile, of a slot
-  constexpr int NQ = FM / 2;                          // quarters (pairs of block rows) per k-tile
-  __shared__ __attribute__((aligned(1024))) char lds[4 * kSlot];
+__global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
+  constexpr int TM = TILE, TN = TILE, SLOTS = 4;
+  constexpr int NW = TILE / 32, WN = TN / 64, WTM = TM / 2, FM = WTM / 16, FN = 4;
+  constexpr int KB = 32;                                             // k per k-tile
+  constexpr int kA = TM * KB * 2, kB = TN * KB * 2, kSlot = kA + kB;  // bytes of the operands' tiles, of a slot
+  constexpr int NA = TM / (16 * NW), NB = TN / (16 * NW);            // loads of a wave per operand and k-tile
+  constexpr int NQ = FM / 2;  // quarters (pairs of block rows) per k-tile
+  __shared__ __attribute__((aligned(1024))) char lds[SLOTS * kSlot];
 
   constexpr bool kTwo = EPI == FFN_STORE && !AROW && BROW;  // the launches with two k ranges
 
@@ -66,15 +68,15 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
   int q = 0;
   while (q + 1 < L.nprob && b >= L.tiles[q + 1]) ++q;
   const FfnProb& P = L.prob[q];
-  constexpr int TN = EPI == FFN_GLU ? TILE / 2 : TILE;
-  const int tilesM = (P.M + TILE - 1) / TILE, tilesN = (P.N + TN - 1) / TN;
+  constexpr int TC = EPI == FFN_GLU ? TN / 2 : TN;  // columns of the result
+  const int tilesM = (P.M + TM - 1) / TM, tilesN = (P.N + TC - 1) / TC;
   int t = b - L.tiles[q];
   const int split = t / (tilesM * tilesN);
   t -= split * (tilesM * tilesN);
   // bands of four tile rows, column by column inside a band
   const int band = t / (kBand * tilesN), r0 = band * kBand, bh = min(kBand, tilesM - r0);
   const int tb = t - r0 * tilesN, tj = tb / bh, ti = r0 + tb - tj * bh;
-  const int64_t i0 = (int64_t)ti * TILE, j0 = (int64_t)tj * TN;
+  const int64_t i0 = (int64_t)ti * TM, j0 = (int64_t)tj * TC;
 
   const int KT0 = (P.K[0] + KB - 1) / KB;
   const int KT = KT0 + (P.K[1] + KB - 1) / KB;
@@ -82,65 +84,73 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
   const int kt0 = split * per;
   const int n = min(per, (KT - kt0 + 3) & ~3);
 
-  // Each lane's place in the loads (two per operand and k-tile): byte offset
-  // from the operand's tile start, the k it holds, and whether its row (or
-  // its chunk of a row-contiguous operand) exists.
-  uint32_t offA[2], offB[2];
-  [[maybe_unused]] uint32_t offB1[2];  // the second k range's, whose stride may differ
-  int kA[2], kB[2];
-  auto place = [&](bool rowc, int64_t ld, int64_t first, int64_t extent, int p, uint32_t& off, int& k) {
+  // Each lane's place in the loads: byte offset from the operand's tile start
+  // (nowhere if its row, or its chunk of a row-contiguous operand, does not
+  // exist) and the k it holds.
+  uint32_t offA[NA], offB[NB];
+  [[maybe_unused]] uint32_t offB1[NB];  // the second k range's, whose stride may differ
+  int kkA[NA], kkB[NB];
+  auto place = [&](bool rowc, int T, int N, int64_t ld, int64_t first, int64_t extent, int p, uint32_t& off, int& k)
+                   __attribute__((always_inline)) {
     if (rowc) {
-      constexpr int CH = TILE / 8, RPI = 64 / CH;  // chunks of a k-row, k-rows per load
-      const int r = wave * (KB / NW) + p * RPI + lane / CH;
+      const int CH = T / 8, RPI = 64 / CH;  // chunks of a k-row, k-rows per load
+      const int r = (wave * N + p) * RPI + lane / CH;
       const int c = (lane % CH) ^ tswz(r);
       k = r;
       off = first + c * 8 < extent ? (uint32_t)(r * ld * 2 + c * 16) : kFfnNowhere;
     } else {
-      const int r = wave * 32 + p * 16 + (lane >> 2);
+      const int r = (wave * N + p) * 16 + (lane >> 2);
       const int c = (lane & 3) ^ swz4(r);
       k = c * 8;
       off = first + r < extent ? (uint32_t)(r * ld * 2 + c * 16) : kFfnNowhere;
     }
   };
-  const int bsel = EPI == FFN_GLU ? (wave & 1) : 0;
+  // FFN_GLU: rows 64·c + 0..31 of the B tile are w_gate's rows 32·c.., the next
+  // 32 w_up's, so load p of a wave reads one of the two matrices
+  auto up = [&](int p) { return EPI == FFN_GLU ? ((wave * NB + p) >> 1) & 1 : 0; };
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    place(AROW, P.lda, i0, AROW ? P.extA : P.M, p, offA[p], kA[p]);
+  for (int p = 0; p < NA; ++p) place(AROW, TM, NA, P.lda, i0, AROW ? P.extA : P.M, p, offA[p], kkA[p]);
+#pragma unroll
+  for (int p = 0; p < NB; ++p) {
     if constexpr (EPI == FFN_GLU) {
-      // rows 64·c + 0..31 of the tile are w_gate's rows 32·c.., the next 32 w_up's
-      const int r = wave * 32 + p * 16 + (lane >> 2), c = (lane & 3) ^ swz4(r);
+      const int r = (wave * NB + p) * 16 + (lane >> 2), c = (lane & 3) ^ swz4(r);
       const int f = (r >> 6) * 32 + (r & 31);
-      kB[p] = c * 8;
-      offB[p] = j0 + f < P.N ? (uint32_t)(f * (bsel ? P.ldb[1] : P.ldb[0]) * 2 + c * 16) : kFfnNowhere;
+      kkB[p] = c * 8;
+      offB[p] = j0 + f < P.N ? (uint32_t)(f * (up(p) ? P.ldb[1] : P.ldb[0]) * 2 + c * 16) : kFfnNowhere;
     } else {
-      place(BROW, P.ldb[0], j0, BROW ? P.extB : P.N, p, offB[p], kB[p]);
-      if constexpr (kTwo) place(BROW, P.ldb[1], j0, BROW ? P.extB : P.N, p, offB1[p], kB[p]);
+      place(BROW, TN, NB, P.ldb[0], j0, BROW ? P.extB : P.N, p, offB[p], kkB[p]);
+      if constexpr (kTwo) place(BROW, TN, NB, P.ldb[1], j0, BROW ? P.extB : P.N, p, offB1[p], kkB[p]);
     }
   }
-  const int dst = wave * 2048;  // this wave's part of an operand's tile, either layout
-  // tile starts and bytes per k of both k ranges (FFN_GLU: one range)
+  // tile starts and bytes per k of both k ranges (FFN_GLU: of both matrices)
   const uint64_t a0 = (uint64_t)P.A[0] + (AROW ? (uint64_t)i0 : (uint64_t)i0 * P.lda) * 2;
   const uint64_t a1 = (uint64_t)P.A[1] + (AROW ? (uint64_t)i0 : (uint64_t)i0 * P.lda) * 2;
-  const void* const pb = bsel ? P.B[1] : P.B[0];
-  const int64_t lb = bsel ? P.ldb[1] : P.ldb[0];
-  const uint64_t b0 = (uint64_t)pb + (BROW ? (uint64_t)j0 : (uint64_t)j0 * lb) * 2;
+  const uint64_t b0 = (uint64_t)P.B[0] + (BROW ? (uint64_t)j0 : (uint64_t)j0 * P.ldb[0]) * 2;
   const uint64_t b1 = (uint64_t)P.B[1] + (BROW ? (uint64_t)j0 : (uint64_t)j0 * P.ldb[1]) * 2;
-  const uint32_t ka = AROW ? (uint32_t)P.lda * 2 : 2, kb0 = BROW ? (uint32_t)lb * 2 : 2,
+  const uint32_t ka = AROW ? (uint32_t)P.lda * 2 : 2, kb0 = BROW ? (uint32_t)P.ldb[0] * 2 : 2,
                  kb1 = BROW ? (uint32_t)P.ldb[1] * 2 : 2;
   const int K0 = P.K[0], K1 = P.K[1];
-  auto issue = [=](int slot, int kt) __attribute__((always_inline)) {
+  const uint32_t dst = __builtin_amdgcn_readfirstlane(lds_addr(lds) + wave * (NA * 1024));
+  const uint32_t dstB = __builtin_amdgcn_readfirstlane(lds_addr(lds) + kA + wave * (NB * 1024));
+  auto issue = [=](int slot, int kt) __attribute__((always_inline)) {  // slot: byte offset
     const bool z = kTwo && kt >= KT0;
     const int k0 = (z ? kt - KT0 : kt) * KB, left = (z ? K1 : K0) - k0;
     const fi32x4 ra = f_buffer((z ? a1 : a0) + (uint64_t)k0 * ka);
-    const fi32x4 rb = f_buffer((z ? b1 : b0) + (uint64_t)k0 * (z ? kb1 : kb0));
-    const uint32_t s = __builtin_amdgcn_readfirstlane(lds_addr(lds) + slot * kSlot + dst);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) f_dma16(s + p * 1024, kA[p] < left ? offA[p] : kFfnNowhere, ra);
+    for (int p = 0; p < NA; ++p) f_dma16(dst + slot + p * 1024, kkA[p] < left ? offA[p] : kFfnNowhere, ra);
+    if constexpr (EPI == FFN_GLU) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      uint32_t o = offB[p];
-      if constexpr (kTwo) o = z ? offB1[p] : o;
-      f_dma16(s + kHalf + p * 1024, kB[p] < left ? o : kFfnNowhere, rb);
+      for (int p = 0; p < NB; ++p)
+        f_dma16(dstB + slot + p * 1024, kkB[p] < left ? offB[p] : kFfnNowhere,
+                f_buffer((up(p) ? b1 : b0) + (uint64_t)k0 * 2));
+    } else {
+      const fi32x4 rb = f_buffer((z ? b1 : b0) + (uint64_t)k0 * (z ? kb1 : kb0));
+#pragma unroll
+      for (int p = 0; p < NB; ++p) {
+        uint32_t o = offB[p];
+        if constexpr (kTwo) o = z ? offB1[p] : o;
+        f_dma16(dstB + slot + p * 1024, kkB[p] < left ? o : kFfnNowhere, rb);
+      }
     }
   };
 
@@ -151,12 +161,13 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
     for (int fj = 0; fj < FN; ++fj) acc[fi][fj] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   const int sw = swz4(lc);
-  auto frag = [&](const char* pan, int row0, auto rowc) __attribute__((always_inline)) {
+  auto frag = [&](const char* pan, int row0, auto rowc, auto tc) __attribute__((always_inline)) {
     if constexpr (decltype(rowc)::value) {
+      constexpr int T = decltype(tc)::value;
       auto rd = [&](int k0) {
         const int k = k0 + (lc >> 2), i = row0 + 4 * (lc & 3);
         return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s4_t)(pan + k * (TILE * 2) + (((i >> 3) ^ tswz(k)) << 4) + (i & 7) * 2));
+            (lds_s4_t)(pan + k * (T * 2) + (((i >> 3) ^ tswz(k)) << 4) + (i & 7) * 2));
       };
       const short4_t lo = rd(8 * lg), hi = rd(8 * lg + 4);
       return __builtin_bit_cast(fbf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -169,11 +180,11 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
   fbf16x8 fb0[FN], fb1[FN], fax[2], fay[2];
   auto load_a = [&](fbf16x8 (&fa)[2], const char* st, int qq) __attribute__((always_inline)) {
 #pragma unroll
-    for (int f = 0; f < 2; ++f) fa[f] = frag(st, wm * WTM + (2 * qq + f) * 16, kAr);
+    for (int f = 0; f < 2; ++f) fa[f] = frag(st, wm * WTM + (2 * qq + f) * 16, kAr, std::integral_constant<int, TM>{});
   };
   auto load_b = [&](fbf16x8 (&fb)[FN], const char* st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int fj = 0; fj < FN; ++fj) fb[fj] = frag(st + kHalf, wn * 64 + fj * 16, kBr);
+    for (int fj = 0; fj < FN; ++fj) fb[fj] = frag(st + kA, wn * 64 + fj * 16, kBr, std::integral_constant<int, TN>{});
   };
   // operand roles swapped: a lane holds four consecutive columns of one row
   auto mma = [&](const fbf16x8 (&fa)[2], const fbf16x8 (&fb)[FN], auto qc) __attribute__((always_inline)) {
@@ -185,12 +196,13 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
         acc[2 * qq + f][fj] =
             __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[fj], fa[f], acc[2 * qq + f][fj], 0, 0, 0);
   };
-  // One k-tile: all quarters but the last while the next quarter's fragments
-  // are read; then the slot is free for every wave, k-tile + 1 has landed (each
-  // k-tile is four loads per wave, two stay in flight), the slot is refilled,
-  // and the last quarter runs while the next k-tile's first fragments are read.
+  // One k-tile (its slot at byte cur, the next one's at nxt): all quarters but
+  // the last while the next quarter's fragments are read; then the slot is free
+  // for every wave, the next k-tile has landed (each is NA + NB loads per wave,
+  // SLOTS − 2 stay in flight), the slot is refilled, and the last quarter runs
+  // while the next k-tile's first fragments are read.
   auto step = [&](int cur, int nxt, int kt, const fbf16x8 (&fb)[FN], fbf16x8 (&fbn)[FN]) __attribute__((always_inline)) {
-    const char* st = lds + cur * kSlot;
+    const char* st = lds + cur;
     static_for<0, NQ - 1>([&](auto qc) __attribute__((always_inline)) {
       constexpr int qq = decltype(qc)::value;
       load_a(qq & 1 ? fax : fay, st, qq + 1);
@@ -198,9 +210,9 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
       mma(qq & 1 ? fay : fax, fb, qc);
       __builtin_amdgcn_sched_barrier(0);
     });
-    asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    issue(cur, kt + 4);
-    const char* sn = lds + nxt * kSlot;
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((SLOTS - 2) * (NA + NB)) : "memory");
+    issue(cur, kt + SLOTS);
+    const char* sn = lds + nxt;
     load_b(fbn, sn);
     load_a(fax, sn, 0);
     __builtin_amdgcn_sched_barrier(0);
@@ -210,18 +222,16 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
   static_assert(NQ % 2 == 0, "the last quarter's fragments are in fay");
   if (n > 0) {
     // loads past this split's k-tiles are zeros that no MFMA reads
-    issue(0, kt0);
-    issue(1, kt0 + 1);
-    issue(2, kt0 + 2);
-    issue(3, kt0 + 3);
-    asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) issue(i * kSlot, kt0 + i);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"((SLOTS - 1) * (NA + NB)) : "memory");
     load_b(fb0, lds);
     load_a(fax, lds, 0);
     for (int kt = kt0; kt < kt0 + n; kt += 4) {
-      step(0, 1, kt, fb0, fb1);
-      step(1, 2, kt + 1, fb1, fb0);
-      step(2, 3, kt + 2, fb0, fb1);
-      step(3, 0, kt + 3, fb1, fb0);
+      step(0, kSlot, kt, fb0, fb1);
+      step(kSlot, 2 * kSlot, kt + 1, fb1, fb0);
+      step(2 * kSlot, 3 * kSlot, kt + 2, fb0, fb1);
+      step(3 * kSlot, 0, kt + 3, fb1, fb0);
     }
   }
   // no load may still be on its way into LDS when the workgroup ends
@@ -319,6 +329,13 @@ __global__ __launch_bounds__(TILE * 2) void ffn_tile16(const FfnLaunch L) {
       ffn_store4(P.C, P.ldc, i, j, P.N, L.outBf16, L.accumulate, P.vecC, c);
     });
   }
+}
+
+template <int EPI, bool AROW, bool BROW>
+void ffn16_launch(int tile, const FfnLaunch& L, hipStream_t st) {
+  const dim3 grid(L.tiles[L.nprob]);
+  if (tile == 256) hipLaunchKernelGGL((ffn_tile16<256, EPI, AROW, BROW>), grid, dim3(512), 0, st, L);
+  else hipLaunchKernelGGL((ffn_tile16<128, EPI, AROW, BROW>), grid, dim3(256), 0, st, L);
 }
 
 }  // namespace muon

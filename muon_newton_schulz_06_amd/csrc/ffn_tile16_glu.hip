@@ -5,16 +5,12 @@
 namespace muon {
 
 hipError_t launch_ffn16_glu(int tile, const FfnLaunch& L, hipStream_t st) {
-  const dim3 grid(L.tiles[L.nprob]);
-  if (tile == 256) hipLaunchKernelGGL((ffn_tile16<256, FFN_GLU, false, false>), grid, dim3(512), 0, st, L);
-  else hipLaunchKernelGGL((ffn_tile16<128, FFN_GLU, false, false>), grid, dim3(256), 0, st, L);
+  ffn16_launch<FFN_GLU, false, false>(tile, L, st);
   return hipGetLastError();
 }
 
 hipError_t launch_ffn16_back(int tile, const FfnLaunch& L, hipStream_t st) {
-  const dim3 grid(L.tiles[L.nprob]);
-  if (tile == 256) hipLaunchKernelGGL((ffn_tile16<256, FFN_BACK, false, true>), grid, dim3(512), 0, st, L);
-  else hipLaunchKernelGGL((ffn_tile16<128, FFN_BACK, false, true>), grid, dim3(256), 0, st, L);
+  ffn16_launch<FFN_BACK, false, true>(tile, L, st);
   return hipGetLastError();
 }
 

@@ -6,13 +6,6 @@
 namespace muon {
 namespace {
 
-template <bool AROW, bool BROW>
-void store_launch(int tile, const FfnLaunch& L, hipStream_t st) {
-  const dim3 grid(L.tiles[L.nprob]);
-  if (tile == 256) hipLaunchKernelGGL((ffn_tile16<256, FFN_STORE, AROW, BROW>), grid, dim3(512), 0, st, L);
-  else hipLaunchKernelGGL((ffn_tile16<128, FFN_STORE, AROW, BROW>), grid, dim3(256), 0, st, L);
-}
-
 // rows × cols of any stride and alignment → rows of ldo (a multiple of 8),
 // zeros beyond cols.
 __global__ __launch_bounds__(256) void ffn_pack(const FfnPack K) {
@@ -26,10 +19,11 @@ __global__ __launch_bounds__(256) void ffn_pack(const FfnPack K) {
 
 }  // namespace
 
-hipError_t launch_ffn16_store(int tile, bool aRowContig, bool bRowContig, const FfnLaunch& L, hipStream_t st) {
-  if (aRowContig) store_launch<true, true>(tile, L, st);
-  else if (bRowContig) store_launch<false, true>(tile, L, st);
-  else store_launch<false, false>(tile, L, st);
+hipError_t launch_ffn16_store(int tile, bool aRowContig, bool bRowContig, const FfnLaunch& L,
+                              hipStream_t st) {
+  if (aRowContig) ffn16_launch<FFN_STORE, true, true>(tile, L, st);
+  else if (bRowContig) ffn16_launch<FFN_STORE, false, true>(tile, L, st);
+  else ffn16_launch<FFN_STORE, false, false>(tile, L, st);
   return hipGetLastError();
 }
 

@@ -22,8 +22,9 @@ struct EmbedLaunch {
 };
 hipError_t launch_embedding(const EmbedLaunch& L, hipStream_t st);
 
-// Positions per piece of a long run of equal ids.
-constexpr int kEmbedPiece = 32;
+// Positions per piece of a long run of equal ids: a run's sum is a chain of at
+// most two pieces' rows and its whole pieces, and each piece costs an fp32 row.
+constexpr int kEmbedPiece = 16;
 // Tokens sorted by one workgroup in shared memory.
 constexpr int64_t kEmbedSmallSort = 16384;
 // Tokens per workgroup and digit bits of the sort in device memory.
@@ -42,6 +43,7 @@ struct EmbedGradLaunch {
   float scale;
   int32_t vec;       // dy rows are whole aligned 16-byte chunks
   int32_t vecw;      // so are dweight's
+  int64_t zeroRows;  // rows zeroed before the pieces' launch (set by the launcher)
   uint32_t* key[2];  // sorted ids (vocab: none), ping-pong
   uint32_t* idx[2];  // their token positions
   uint32_t* counts;  // digit counts of the device-memory sort

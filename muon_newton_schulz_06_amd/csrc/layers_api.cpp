@@ -190,7 +190,7 @@ struct TilePlan {
 // bound by the matrix pipe or, alone on a CU, by a step's latency).
 double tile_time(bool bf16, int tm, int64_t n, int64_t per) {
   const double cu = std::ceil(n / 256.0);  // workgroups on the busiest CU
-  if (bf16) return tm == 256 ? cu * (per * 0.80 + 8) : std::ceil(n / 512.0) * (per * (n <= 256 ? 0.36 : 0.50) + 6);
+  if (bf16) return tm == 256 ? cu * (per * 0.77 + 14) : std::ceil(n / 512.0) * (per * (n <= 256 ? 0.40 : 0.62) + 10);
   return 10 + per * (tm == 128 ? std::max(2.7, 2.48 * cu) : std::max(1.45, 1.28 * cu));
 }
 
@@ -206,7 +206,7 @@ TilePlan plan_tiles(bool bf16, int64_t M, int64_t N, int64_t KT) {
     const int64_t tiles = tiles_of(M, tm) * tiles_of(N, tn);
     for (int s = 1; s <= 32; ++s) {
       const int64_t per = std::max<int64_t>(unit, tiles_of(tiles_of(KT, s), unit) * unit);
-      if (s > 1 && (tiles_of(KT, per) != s || per < 2 * unit)) continue;
+      if (s > 1 && (tiles_of(KT, per) != s || per < 8)) continue;
       double t = tile_time(bf16, tm, tiles * s, per);
       if (s > 1) t += 5.0 + 8.0 * s * M * N / 4e6;  // the splits' sums written and read
       if (!best.tm || t < bestT) {
