@@ -58,10 +58,11 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
 
   constexpr bool kTwo = EPI == FFN_STORE && !AROW && BROW;  // the launches with two k ranges
 
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x;
+  int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int lc = lane & 15, lg = lane >> 4;
+  int lc = lane & 15, lg = lane >> 4;
 
   // problem, tile and k split of this workgroup
   const int b = xcd_window_remap(blockIdx.x, gridDim.x, kXcdShift);
@@ -236,6 +237,10 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
   }
   // no load may still be on its way into LDS when the workgroup ends
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // the epilogue's addresses are formed here, not kept through the loop
+  asm volatile("" : "+v"(lane));
+  lc = lane & 15;
+  lg = lane >> 4;
 
   // acc[fi][fj][r]: row fi·16 + lane%16, column fj·16 + 4·(lane/16) + r
   const int64_t iw = i0 + wm * WTM + lc;
@@ -277,51 +282,122 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
     }
     return;
   }
+  // bf16 results are staged in the ring, which every wave has left behind,
+  // and stored as whole rows, 16 bytes per lane: stored from the registers a
+  // 256-tile's results (8 bytes per lane, 16 rows at a time) took about 15 µs.
+  // A staged tile of W columns: chunk c of row r at c ^ r (mod W/8).
+  auto soff = [](int W, int row, int col) __attribute__((always_inline)) {
+    return row * W * 2 + (((col >> 3) ^ (row & (W / 8 - 1))) << 4) + (col & 7) * 2;
+  };
+  auto put = [&](char* st, int W, int row, int col, uint2 v) __attribute__((always_inline)) {
+    *(uint2*)(st + soff(W, row, col)) = v;
+  };
+  // Rows of a staged tile → C, rows staged in `parts` groups per row half (the
+  // staged row r is row (r / HR)·WTM + r % HR of part `part`).
+  auto rows_out = [&](const char* st, auto wc, auto partsc, int part, void* C, int64_t ldc, int64_t width)
+                      __attribute__((always_inline)) {
+    constexpr int W = decltype(wc)::value, CH = W / 8, RPI = 64 / CH;
+    constexpr int PARTS = decltype(partsc)::value, HR = WTM / PARTS, RW = TM / PARTS / NW;  // rows of a wave
+#pragma unroll 4
+    for (int p = 0; p < RW / RPI; ++p) {
+      const int r = wave * RW + p * RPI + lane / CH, c = lane % CH;
+      const int64_t i = i0 + (r / HR) * WTM + part * HR + r % HR, j = j0 + c * 8;
+      const lu32x4 v = *(const lu32x4*)(st + soff(W, r, c * 8));
+      if (i >= P.M || j >= width) continue;
+      uint16_t* o = (uint16_t*)C + i * ldc + j;
+      if (j + 8 <= width) {
+        *(lu32x4*)o = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (j + e < width) o[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+      }
+    }
+  };
+  constexpr auto kOne = std::integral_constant<int, 1>{};
+  const int lrow = wm * WTM + lc;  // a lane's row of block row 0, and its column below
   if constexpr (EPI == FFN_GLU) {
+    // half of every wave's rows at a time: h, a and b of a tile side by side
+    constexpr int W = TN / 2, HR = WTM / 2;
+    constexpr auto kW = std::integral_constant<int, W>{};
+    constexpr int kPart = TM / 2 * W * 2;  // bytes of one array's half tile
+    static_assert(3 * kPart <= SLOTS * kSlot, "staged arrays fit");
     // columns N .. ldh − 1 come out as zeros
     ffn_with_glu(L, [&](auto actc, auto savec) __attribute__((always_inline)) {
-      groups(kTwoF, 32, L.ldh, [&](int64_t i, int64_t j, int fi, int fj) __attribute__((always_inline)) {
-        float g[4], u[4];
-        four(acc[fi][fj], g);
-        four(acc[fi][fj + 2], u);
-        ffn_glu4<Bf16, decltype(actc)::value, decltype(savec)::value>(L, P, i, j, g, u);
+      constexpr bool SAVE = decltype(savec)::value;
+      static_for<0, 2>([&](auto pc) __attribute__((always_inline)) {
+        constexpr int part = decltype(pc)::value;
+        __syncthreads();
+#pragma unroll
+        for (int fi = part * (FM / 2); fi < (part + 1) * (FM / 2); ++fi)
+#pragma unroll
+          for (int fj = 0; fj < 2; ++fj) {
+            const int row = wm * HR + (fi - part * (FM / 2)) * 16 + lc, col = wn * 32 + fj * 16 + 4 * lg;
+            float v[4], d[4], h[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float u = acc[fi][fj + 2][r];
+              ffn_act<decltype(actc)::value, false>(acc[fi][fj][r], v[r], d[r]);
+              h[r] = v[r] * u;
+              d[r] *= u;
+            }
+            put(lds, W, row, col, make_uint2(l_f32_bf16x2(h[0], h[1]), l_f32_bf16x2(h[2], h[3])));
+            if constexpr (SAVE) {
+              put(lds + kPart, W, row, col, make_uint2(l_pack_e6m9x2(d[0], d[1]), l_pack_e6m9x2(d[2], d[3])));
+              put(lds + 2 * kPart, W, row, col, make_uint2(l_pack_e6m9x2(v[0], v[1]), l_pack_e6m9x2(v[2], v[3])));
+            }
+          }
+        __syncthreads();
+        constexpr auto kHalves = std::integral_constant<int, 2>{};
+        rows_out(lds, kW, kHalves, part, P.C, P.ldc, L.ldh);
+        if constexpr (SAVE) {
+          rows_out(lds + kPart, kW, kHalves, part, L.ab, 2 * L.ldh, L.ldh);
+          rows_out(lds + 2 * kPart, kW, kHalves, part, (uint16_t*)L.ab + L.ldh, 2 * L.ldh, L.ldh);
+        }
       });
     });
   } else if constexpr (EPI == FFN_BACK) {
-    // the factors of the next block row are read before the current one's
-    // results are stored
-    uint2 ua[2][FN], ub[2][FN];
-    auto fetch = [&](int fi, uint2 (&a)[FN], uint2 (&b)[FN]) __attribute__((always_inline)) {
-      const int64_t i = iw + fi * 16;
+    // a, then b: the tile of the factor is loaded into the staging, multiplied
+    // in place (a lane reads and writes the same address) and stored
+    constexpr auto kW = std::integral_constant<int, TN>{};
+    constexpr int CH = TN / 8, RPI = 64 / CH;
 #pragma unroll
-      for (int fj = 0; fj < FN; ++fj) {
-        const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;
-        a[fj] = b[fj] = make_uint2(0u, 0u);
-        if (i < P.M && j < L.ldh) {
-          const uint16_t* o = (const uint16_t*)L.ab + i * 2 * L.ldh + j;
-          a[fj] = *(const uint2*)o;
-          b[fj] = *(const uint2*)(o + L.ldh);
-        }
+    for (int half = 0; half < 2; ++half) {
+      __syncthreads();
+      const fi32x4 rs = f_buffer((uint64_t)L.ab + ((uint64_t)i0 * 2 * L.ldh + half * L.ldh + j0) * 2);
+#pragma unroll 4
+      for (int p = 0; p < TM / NW / RPI; ++p) {
+        const int r = wave * (TM / NW) + p * RPI + lane / CH, c = (lane % CH) ^ (r & (CH - 1));
+        const uint32_t off = i0 + r < P.M && j0 + c * 8 < L.ldh ? (uint32_t)((int64_t)r * 4 * L.ldh + c * 16) : kFfnNowhere;
+        f_dma16(__builtin_amdgcn_readfirstlane(lds_addr(lds) + (wave * (TM / NW) + p * RPI) * TN * 2), off, rs);
       }
-    };
-    fetch(0, ua[0], ub[0]);
-    static_for<0, FM>([&](auto fc) __attribute__((always_inline)) {
-      constexpr int fi = decltype(fc)::value;
-      const uint2 (&a)[FN] = ua[fi & 1];
-      const uint2 (&b)[FN] = ub[fi & 1];
-      if constexpr (fi + 1 < FM) fetch(fi + 1, ua[(fi + 1) & 1], ub[(fi + 1) & 1]);
-      const int64_t i = iw + fi * 16;
-      if (i < P.M) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+#pragma unroll
+      for (int fi = 0; fi < FM; ++fi)
 #pragma unroll
         for (int fj = 0; fj < FN; ++fj) {
-          const int64_t j = j0 + wn * 64 + fj * 16 + 4 * lg;
-          if (j >= L.ldh) continue;
-          float c[4];
-          four(acc[fi][fj], c);
-          ffn_back4_bf16(L, P, i, j, c, a[fj], b[fj]);
+          char* const at = lds + soff(TN, lrow + fi * 16, wn * 64 + fj * 16 + 4 * lg);
+          const uint2 f = *(const uint2*)at;
+          const floatx4 c = acc[fi][fj];
+          *(uint2*)at = make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(f.x), c[1] * l_unpack_hi(f.x)),
+                                   l_f32_bf16x2(c[2] * l_unpack_lo(f.y), c[3] * l_unpack_hi(f.y)));
         }
+      __syncthreads();
+      rows_out(lds, kW, kOne, 0, (uint16_t*)P.C + half * L.ldh, P.ldc, L.ldh);
+    }
+  } else if (L.outBf16 && !L.accumulate && ((uintptr_t)P.C & 15) == 0 && (P.ldc & 7) == 0) {
+    __syncthreads();
+#pragma unroll
+    for (int fi = 0; fi < FM; ++fi)
+#pragma unroll
+      for (int fj = 0; fj < FN; ++fj) {
+        const floatx4 c = acc[fi][fj];
+        put(lds, TN, lrow + fi * 16, wn * 64 + fj * 16 + 4 * lg,
+            make_uint2(l_f32_bf16x2(c[0], c[1]), l_f32_bf16x2(c[2], c[3])));
       }
-    });
+    __syncthreads();
+    rows_out(lds, std::integral_constant<int, TN>{}, kOne, 0, P.C, P.ldc, P.N);
   } else {
     groups(kAllF, 64, P.N, [&](int64_t i, int64_t j, int fi, int fj) __attribute__((always_inline)) {
       float c[4];
