@@ -23,27 +23,48 @@ constexpr int kTN = 128, kKs = 32;
 
 // Four operand values: (row, k..k+3) of a k-contiguous operand or
 // (row..row+3, k) of a row-contiguous one, one 16-byte load at any 4-byte
-// alignment.  EDGE: a group may reach over the end of K, or of a
-// row-contiguous operand's rows, and gets zeros there.  Rows of a k-contiguous
-// operand past the last one repeat it (their results are not stored).
+// alignment.  Rows past the last one hold anything that lies in the operand
+// (their results are not stored).  EDGE: the group may reach over the end of
+// the rows or of k; it is loaded from the last place where it fits, without a
+// branch, and put right by fix4 when it is used, a step or two later (operands
+// with fewer than four values along the group are read one by one).
 template <bool ROWC, bool EDGE>
 __device__ __forceinline__ lf32x4 fetch4(const float* p, int64_t ld, int row, int k, int rows, int K) {
   lf32x4 v = {0.f, 0.f, 0.f, 0.f};
-  const int r = ROWC ? row : min(row, rows - 1);
-  const float* e = p + (ROWC ? k * ld + r : r * ld + k);
   if constexpr (!EDGE) {
-    __builtin_memcpy(&v, e, 16);
-  } else {
+    const int r = ROWC ? row : min(row, rows - 1);
+    __builtin_memcpy(&v, p + (ROWC ? k * ld + r : r * ld + k), 16);
+  } else if ((ROWC ? rows : K) < 4) {
     const int have = ROWC ? (k < K ? rows - row : 0) : K - k;
-    if (have >= 4) {
-      __builtin_memcpy(&v, e, 16);
-    } else {
+    const int r = ROWC ? row : min(row, rows - 1);
+    const float* e = p + (ROWC ? k * ld + r : r * ld + k);
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < have) v[i] = e[i];
-    }
+    for (int i = 0; i < 3; ++i)
+      if (i < have) v[i] = e[i];
+  } else if constexpr (ROWC) {
+    __builtin_memcpy(&v, p + min(k, K - 1) * ld + min(row, rows - 4), 16);
+  } else {
+    __builtin_memcpy(&v, p + min(row, rows - 1) * ld + min(k, K - 4), 16);
   }
   return v;
+}
+
+// An EDGE group's values moved to their places, zeros past the last k.
+template <bool ROWC>
+__device__ __forceinline__ void fix4(lf32x4& v, int row, int k, int rows, int K) {
+  if ((ROWC ? rows : K) < 4) return;  // read one by one
+  const int d = ROWC ? row - min(row, rows - 4) : k - min(k, K - 4);
+  if (d & 1) {
+    v[0] = v[1];
+    v[1] = v[2];
+    v[2] = v[3];
+  }
+  if (d & 2) {
+    v[0] = v[2];
+    v[1] = v[3];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (ROWC ? k : k + i) < K ? v[i] : 0.f;
 }
 
 template <int TM, int EPI, bool AROW, bool BROW>
@@ -103,10 +124,21 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
     }
   };
   const bool inside = (!AROW || i0 + TM <= P.M) && (!BROW || j0 + TN <= P.N);
-  auto fetch = [&](int s, lf32x4 (&fa)[NA], lf32x4 (&fb)[NB]) __attribute__((always_inline)) {
+  auto whole = [&](int s) {
     const int z = s >= steps0;
-    if (inside && ((z ? s - steps0 : s) + 1) * kKs <= P.K[z]) fetch_as(s, fa, fb, std::false_type{});
+    return inside && ((z ? s - steps0 : s) + 1) * kKs <= P.K[z];
+  };
+  auto fetch = [&](int s, lf32x4 (&fa)[NA], lf32x4 (&fb)[NB]) __attribute__((always_inline)) {
+    if (whole(s)) fetch_as(s, fa, fb, std::false_type{});
     else fetch_as(s, fa, fb, std::true_type{});
+  };
+  auto fix = [&](int s, lf32x4 (&fa)[NA], lf32x4 (&fb)[NB]) __attribute__((always_inline)) {
+    const int z = s >= steps0;
+    const int k0 = (z ? s - steps0 : s) * kKs, K = P.K[z];
+#pragma unroll
+    for (int h = 0; h < NA; ++h) fix4<AROW>(fa[h], i0 + at_row(AROW, TM, h), k0 + at_k(AROW, TM, h), P.M, K);
+#pragma unroll
+    for (int h = 0; h < NB; ++h) fix4<BROW>(fb[h], j0 + at_row(BROW, kTN, h), k0 + at_k(BROW, kTN, h), P.N, K);
   };
   auto put = [&](float* s, bool rowc, int T, int ld, int h, const lf32x4& v) {
     const int r = at_row(rowc, T, h), k = at_k(rowc, T, h);
@@ -122,6 +154,7 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
     constexpr int h2 = decltype(parity)::value;
     float* pa = sa[h2];
     float* pb = sb[h2];
+    if (!whole(s)) fix(s, ra[h2], rb[h2]);
 #pragma unroll
     for (int h = 0; h < NA; ++h) put(pa, AROW, TM, LA, h, ra[h2][h]);
 #pragma unroll
@@ -219,8 +252,8 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
         },
         [&](int64_t i, int64_t j, float c, float u, float v) {
           float* o = (float*)P.C + i * 2 * L.ldh + j;
-          o[0] = c * u;
-          o[L.ldh] = c * v;
+          o[0] = j < P.N ? c * u : 0.f;
+          o[L.ldh] = j < P.N ? c * v : 0.f;
         });
   } else if (L.outBf16) {
     blocks(
