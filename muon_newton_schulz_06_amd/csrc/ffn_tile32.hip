@@ -21,6 +21,13 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTN = 128, kKs = 32;
 
+template <int B, int E, typename F> __device__ __forceinline__ void static_for32(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    static_for32<B + 1, E>(f);
+  }
+}
+
 // Four operand values: (row, k..k+3) of a k-contiguous operand or
 // (row..row+3, k) of a row-contiguous one, one 16-byte load at any 4-byte
 // alignment.  Rows past the last one hold anything that lies in the operand
@@ -68,7 +75,7 @@ __device__ __forceinline__ void fix4(lf32x4& v, int row, int k, int rows, int K)
 }
 
 template <int TM, int EPI, bool AROW, bool BROW>
-__global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
+__global__ __launch_bounds__(256, 2) void ffn_tile32(const FfnLaunch L) {
   constexpr int FA = TM / 64;                         // 32-row blocks of a wave
   constexpr int NA = TM * kKs / 1024, NB = kTN * kKs / 1024;  // groups of four per thread and step
   constexpr int LA = TM + 4, LB = kTN + 4;
@@ -100,45 +107,51 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
   // group h of a thread: eight lanes cover 32 k of a row, or T/4 lanes a k-row
   auto at_row = [&](bool rowc, int T, int h) { return rowc ? (tid % (T / 4)) * 4 : (tid >> 3) + 32 * h; };
   auto at_k = [&](bool rowc, int T, int h) { return rowc ? tid / (T / 4) + (1024 / T) * h : (tid & 7) * 4; };
-  const int steps0 = (P.K[0] + kKs - 1) / kKs;
-  const int all = steps0 + (P.K[1] + kKs - 1) / kKs;
+  // copies of the arguments, so that no step reads them again
+  const float* const a0 = (const float*)P.A[0];
+  const float* const a1 = (const float*)P.A[1];
+  const float* const b0 = (const float*)P.B[0];
+  const float* const b1 = (const float*)P.B[1];
+  const int64_t lda = P.lda, ldb0 = P.ldb[0], ldb1 = P.ldb[1];
+  const int M = P.M, N = P.N, K0 = P.K[0], K1 = P.K[1];
+  const int steps0 = (K0 + kKs - 1) / kKs;
+  const int all = steps0 + (K1 + kKs - 1) / kKs;
   const int s0 = split * L.splitTiles, s1 = min(all, s0 + L.splitTiles);
   lf32x4 ra[2][NA], rb[2][NB];  // of the next two steps
   auto fetch_as = [&](int s, lf32x4 (&fa)[NA], lf32x4 (&fb)[NB], auto edgec) __attribute__((always_inline)) {
     constexpr bool EDGE = decltype(edgec)::value;
-    const int z = s >= steps0;
-    const int k0 = (z ? s - steps0 : s) * kKs, K = P.K[z];
+    const bool z = s >= steps0;
+    const int k0 = (z ? s - steps0 : s) * kKs, K = z ? K1 : K0;
+    const float* const a = z ? a1 : a0;
 #pragma unroll
     for (int h = 0; h < NA; ++h)
-      fa[h] = fetch4<AROW, EDGE>((const float*)P.A[z], P.lda, i0 + at_row(AROW, TM, h), k0 + at_k(AROW, TM, h), P.M, K);
+      fa[h] = fetch4<AROW, EDGE>(a, lda, i0 + at_row(AROW, TM, h), k0 + at_k(AROW, TM, h), M, K);
 #pragma unroll
     for (int h = 0; h < NB; ++h) {
       const int r = at_row(BROW, kTN, h);
-      if constexpr (EPI == FFN_GLU) {
-        const int which = h & 1;  // rows 32·h .. of the tile
-        fb[h] = fetch4<false, EDGE>((const float*)P.B[which], P.ldb[which], j0 + (h >> 1) * 32 + (r & 31),
-                                    k0 + at_k(false, kTN, h), P.N, K);
-      } else {
-        fb[h] = fetch4<BROW, EDGE>((const float*)P.B[z], P.ldb[z], j0 + r, k0 + at_k(BROW, kTN, h), P.N, K);
-      }
+      if constexpr (EPI == FFN_GLU)  // rows 32·h .. of the tile are one matrix's
+        fb[h] = fetch4<false, EDGE>(h & 1 ? b1 : b0, h & 1 ? ldb1 : ldb0, j0 + (h >> 1) * 32 + (r & 31),
+                                    k0 + at_k(false, kTN, h), N, K);
+      else
+        fb[h] = fetch4<BROW, EDGE>(z ? b1 : b0, z ? ldb1 : ldb0, j0 + r, k0 + at_k(BROW, kTN, h), N, K);
     }
   };
-  const bool inside = (!AROW || i0 + TM <= P.M) && (!BROW || j0 + TN <= P.N);
+  const bool inside = (!AROW || i0 + TM <= M) && (!BROW || j0 + TN <= N);
   auto whole = [&](int s) {
-    const int z = s >= steps0;
-    return inside && ((z ? s - steps0 : s) + 1) * kKs <= P.K[z];
+    const bool z = s >= steps0;
+    return inside && ((z ? s - steps0 : s) + 1) * kKs <= (z ? K1 : K0);
   };
   auto fetch = [&](int s, lf32x4 (&fa)[NA], lf32x4 (&fb)[NB]) __attribute__((always_inline)) {
     if (whole(s)) fetch_as(s, fa, fb, std::false_type{});
     else fetch_as(s, fa, fb, std::true_type{});
   };
   auto fix = [&](int s, lf32x4 (&fa)[NA], lf32x4 (&fb)[NB]) __attribute__((always_inline)) {
-    const int z = s >= steps0;
-    const int k0 = (z ? s - steps0 : s) * kKs, K = P.K[z];
+    const bool z = s >= steps0;
+    const int k0 = (z ? s - steps0 : s) * kKs, K = z ? K1 : K0;
 #pragma unroll
-    for (int h = 0; h < NA; ++h) fix4<AROW>(fa[h], i0 + at_row(AROW, TM, h), k0 + at_k(AROW, TM, h), P.M, K);
+    for (int h = 0; h < NA; ++h) fix4<AROW>(fa[h], i0 + at_row(AROW, TM, h), k0 + at_k(AROW, TM, h), M, K);
 #pragma unroll
-    for (int h = 0; h < NB; ++h) fix4<BROW>(fb[h], j0 + at_row(BROW, kTN, h), k0 + at_k(BROW, kTN, h), P.N, K);
+    for (int h = 0; h < NB; ++h) fix4<BROW>(fb[h], j0 + at_row(BROW, kTN, h), k0 + at_k(BROW, kTN, h), N, K);
   };
   auto put = [&](float* s, bool rowc, int T, int ld, int h, const lf32x4& v) {
     const int r = at_row(rowc, T, h), k = at_k(rowc, T, h);
@@ -161,19 +174,34 @@ __global__ __launch_bounds__(256) void ffn_tile32(const FfnLaunch L) {
     for (int h = 0; h < NB; ++h) put(pb, BROW, kTN, LB, h, rb[h2][h]);
     __syncthreads();
     if (s + 2 < s1) fetch(s + 2, ra[h2], rb[h2]);
+    // four pairs of k at a time, the next four's operands read before their
+    // MFMAs are issued
+    constexpr int G = 4;
+    float fa[2][G][FA], fb[2][G][2];
+    auto read = [&](int g, float (&xa)[G][FA], float (&xb)[G][2]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < kKs; k += 2) {
-      float fa[FA], fb[2];
+      for (int i = 0; i < G; ++i) {
+        const int k = (g * G + i) * 2 + lk;
 #pragma unroll
-      for (int a = 0; a < FA; ++a) fa[a] = pa[(k + lk) * LA + wm * (TM / 2) + a * 32 + lr];
+        for (int a = 0; a < FA; ++a) xa[i][a] = pa[k * LA + wm * (TM / 2) + a * 32 + lr];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) fb[b] = pb[(k + lk) * LB + wn * 64 + b * 32 + lr];
+        for (int b = 0; b < 2; ++b) xb[i][b] = pb[k * LB + wn * 64 + b * 32 + lr];
+      }
+    };
+    read(0, fa[0], fb[0]);
+    static_for32<0, kKs / (2 * G)>([&](auto gc) __attribute__((always_inline)) {
+      constexpr int g = decltype(gc)::value;
+      if constexpr ((g + 1) * 2 * G < kKs) read(g + 1, fa[(g + 1) & 1], fb[(g + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int a = 0; a < FA; ++a)
+      for (int i = 0; i < G; ++i)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[a], fb[b], acc[a][b], 0, 0, 0);
-    }
+        for (int a = 0; a < FA; ++a)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[g & 1][i][a], fb[g & 1][i][b], acc[a][b], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
   if (s0 < s1) fetch(s0, ra[0], rb[0]);
   if (s0 + 1 < s1) fetch(s0 + 1, ra[1], rb[1]);

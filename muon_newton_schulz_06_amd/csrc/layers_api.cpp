@@ -191,7 +191,7 @@ struct TilePlan {
 double tile_time(bool bf16, int tm, int64_t n, int64_t per) {
   const double cu = std::ceil(n / 256.0);  // workgroups on the busiest CU
   if (bf16) return tm == 256 ? cu * (per * 0.77 + 14) : std::ceil(n / 512.0) * (per * (n <= 256 ? 0.40 : 0.62) + 10);
-  return 10 + per * (tm == 128 ? std::max(2.7, 2.48 * cu) : std::max(1.45, 1.28 * cu));
+  return 10 + per * (tm == 128 ? std::max(2.3, 2.1 * cu) : std::max(1.3, 1.1 * cu));
 }
 
 // Tile and splits of a product of M × N results (all problems of a launch
