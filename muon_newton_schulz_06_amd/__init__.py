@@ -179,6 +179,10 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# The raw handle of a device's current stream (without building a Stream).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 _ws_cache: dict = {}
 _ws_lock = threading.Lock()
 
@@ -198,13 +202,13 @@ def _workspace(nbytes: int, device, user, stream=None):
         if user.device != device:
             raise ValueError("workspace on another device")
         return user, user.numel() * user.element_size()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (device.type, device.index, s.cuda_stream)
+    handle = stream.cuda_stream if stream is not None else _raw_stream(device.index)
+    key = (device.type, device.index, handle)
     with _ws_lock:
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
             _ws_cache.pop(key, None)
-            with torch.cuda.stream(s):
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
                 buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
             _ws_cache[key] = buf
     return buf, buf.numel()

@@ -218,6 +218,16 @@ TilePlan plan_tiles(bool bf16, int64_t M, int64_t N, int64_t KT) {
   return best;
 }
 
+// Whether the forward pass of T tokens takes the few-token kernel.  It reads
+// every weight once at HBM's rate, but its workgroups each read the tokens
+// again, so its time grows with tokens × weights.  Measured (µs, few-token
+// kernel against tiles): bf16 3584×18944 T 1: 85 / 113, 12: 109 / 103, 64: 216 /
+// 130; bf16 1024×4096 T 64: 25 / 28; fp32 3584×18944 T 32: 336 / 364, 64: 567 /
+// 309; fp32 1024×4096 T 64: 42 / 47.
+bool few_tokens(bool bf16, int64_t T, int64_t weights) {
+  return T <= kFfnFew && (double)T * weights <= (bf16 ? 2e9 : 7e9);
+}
+
 // The few-token kernel: about 1024 workgroups of 16 weight rows, each split at
 // least one step (4 waves × 4 loads of 32 k) long.
 TilePlan plan_few(int64_t N, int64_t K) {
@@ -263,7 +273,7 @@ FfnLayout ffn_layout(const muon_ffn_t& f, bool grad) {
     l.total = at;
     return l;
   }
-  l.few = !grad && T <= kFfnFew;
+  l.few = !grad && few_tokens(bf16, T, 3 * D * F);
   if (bf16 && !l.few) {
     l.x = take((size_t)T * D8 * 2);
     l.dy = take(grad ? (size_t)T * D8 * 2 : 0);

@@ -25,7 +25,7 @@ import math
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (MUON_DTYPE_BF16, MUON_DTYPE_F32, _check, _workspace, load)
+from . import MUON_DTYPE_BF16, MUON_DTYPE_F32, _check, _raw_stream, _workspace, load
 
 __all__ = [
     "ACTIVATIONS", "muon_embedding", "muon_embedding_grad", "muon_rms_norm", "muon_rms_norm_grad",
@@ -134,11 +134,6 @@ def _matrix(t, name, rows, cols):
 def _vector(t, name, n):
     if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} values, got shape {tuple(t.shape)}")
-
-
-# The raw handle of a device's current stream (without building a Stream).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _On:

@@ -471,3 +471,19 @@ def test_other_stream_and_graph(lib):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(ref, outs))
         step()
+
+
+def test_example_trains(lib):
+    """The example model learns: from ln(vocab) at the start (the logits of
+    an untrained model say nothing about the successor) to less than half of
+    it, on fresh data every step."""
+    import importlib.util
+    import math
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_ffn_lm.py")
+    spec = importlib.util.spec_from_file_location("train_ffn_lm", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    losses = ex.train(steps=60, tokens=2048, vocab=256, model=128, hidden=384, depth=2, log=lambda s: None)
+    assert all(math.isfinite(v) for v in losses)
+    assert losses[-1] < 0.5 * math.log(256)
