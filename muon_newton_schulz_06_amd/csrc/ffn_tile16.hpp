@@ -57,6 +57,11 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
   __shared__ __attribute__((aligned(1024))) char lds[SLOTS * kSlot];
 
   constexpr bool kTwo = EPI == FFN_STORE && !AROW && BROW;  // the launches with two k ranges
+  // A slot's refill spread over the last quarter's MFMAs, one load after each:
+  // dx 957 -> 900 µs, weight gradients 1390 -> 1341 µs, dh 571 -> 562 µs (4096
+  // tokens, 3584×18944); FFN_GLU, whose loads need a buffer each, 1066 -> 1090
+  // µs, so it issues them ahead of the MFMAs.
+  constexpr bool kSpread = EPI != FFN_GLU;
 
   const int tid = threadIdx.x;
   int lane = tid & 63;
@@ -107,8 +112,10 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
     }
   };
   // FFN_GLU: rows 64·c + 0..31 of the B tile are w_gate's rows 32·c.., the next
-  // 32 w_up's, so load p of a wave reads one of the two matrices
-  auto up = [&](int p) { return EPI == FFN_GLU ? ((wave * NB + p) >> 1) & 1 : 0; };
+  // 32 w_up's, so a wave's 32 rows are one matrix's
+  static_assert(NB == 2, "a wave loads 32 rows of B");
+  const bool up = EPI == FFN_GLU && (wave & 1);
+  const int64_t ldB = up ? P.ldb[1] : P.ldb[0];
 #pragma unroll
   for (int p = 0; p < NA; ++p) place(AROW, TM, NA, P.lda, i0, AROW ? P.extA : P.M, p, offA[p], kkA[p]);
 #pragma unroll
@@ -117,42 +124,40 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
       const int r = (wave * NB + p) * 16 + (lane >> 2), c = (lane & 3) ^ swz4(r);
       const int f = (r >> 6) * 32 + (r & 31);
       kkB[p] = c * 8;
-      offB[p] = j0 + f < P.N ? (uint32_t)(f * (up(p) ? P.ldb[1] : P.ldb[0]) * 2 + c * 16) : kFfnNowhere;
+      offB[p] = j0 + f < P.N ? (uint32_t)(f * ldB * 2 + c * 16) : kFfnNowhere;
     } else {
       place(BROW, TN, NB, P.ldb[0], j0, BROW ? P.extB : P.N, p, offB[p], kkB[p]);
       if constexpr (kTwo) place(BROW, TN, NB, P.ldb[1], j0, BROW ? P.extB : P.N, p, offB1[p], kkB[p]);
     }
   }
-  // tile starts and bytes per k of both k ranges (FFN_GLU: of both matrices)
+  // tile starts and bytes per k of both k ranges
   const uint64_t a0 = (uint64_t)P.A[0] + (AROW ? (uint64_t)i0 : (uint64_t)i0 * P.lda) * 2;
   const uint64_t a1 = (uint64_t)P.A[1] + (AROW ? (uint64_t)i0 : (uint64_t)i0 * P.lda) * 2;
-  const uint64_t b0 = (uint64_t)P.B[0] + (BROW ? (uint64_t)j0 : (uint64_t)j0 * P.ldb[0]) * 2;
+  const uint64_t b0 = (uint64_t)(up ? P.B[1] : P.B[0]) + (BROW ? (uint64_t)j0 : (uint64_t)j0 * ldB) * 2;
   const uint64_t b1 = (uint64_t)P.B[1] + (BROW ? (uint64_t)j0 : (uint64_t)j0 * P.ldb[1]) * 2;
   const uint32_t ka = AROW ? (uint32_t)P.lda * 2 : 2, kb0 = BROW ? (uint32_t)P.ldb[0] * 2 : 2,
                  kb1 = BROW ? (uint32_t)P.ldb[1] * 2 : 2;
   const int K0 = P.K[0], K1 = P.K[1];
   const uint32_t dst = __builtin_amdgcn_readfirstlane(lds_addr(lds) + wave * (NA * 1024));
   const uint32_t dstB = __builtin_amdgcn_readfirstlane(lds_addr(lds) + kA + wave * (NB * 1024));
-  auto issue = [=](int slot, int kt) __attribute__((always_inline)) {  // slot: byte offset
+  // load j of k-tile kt (A's, then B's) into the slot at byte `slot`
+  auto issue_one = [=](int slot, int kt, auto jc) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value;
     const bool z = kTwo && kt >= KT0;
     const int k0 = (z ? kt - KT0 : kt) * KB, left = (z ? K1 : K0) - k0;
-    const fi32x4 ra = f_buffer((z ? a1 : a0) + (uint64_t)k0 * ka);
-#pragma unroll
-    for (int p = 0; p < NA; ++p) f_dma16(dst + slot + p * 1024, kkA[p] < left ? offA[p] : kFfnNowhere, ra);
-    if constexpr (EPI == FFN_GLU) {
-#pragma unroll
-      for (int p = 0; p < NB; ++p)
-        f_dma16(dstB + slot + p * 1024, kkB[p] < left ? offB[p] : kFfnNowhere,
-                f_buffer((up(p) ? b1 : b0) + (uint64_t)k0 * 2));
+    if constexpr (j < NA) {
+      f_dma16(dst + slot + j * 1024, kkA[j] < left ? offA[j] : kFfnNowhere,
+              f_buffer((z ? a1 : a0) + (uint64_t)k0 * ka));
     } else {
-      const fi32x4 rb = f_buffer((z ? b1 : b0) + (uint64_t)k0 * (z ? kb1 : kb0));
-#pragma unroll
-      for (int p = 0; p < NB; ++p) {
-        uint32_t o = offB[p];
-        if constexpr (kTwo) o = z ? offB1[p] : o;
-        f_dma16(dstB + slot + p * 1024, kkB[p] < left ? o : kFfnNowhere, rb);
-      }
+      constexpr int p = j - NA;
+      uint32_t o = offB[p];
+      if constexpr (kTwo) o = z ? offB1[p] : o;
+      f_dma16(dstB + slot + p * 1024, kkB[p] < left ? o : kFfnNowhere,
+              f_buffer((z ? b1 : b0) + (uint64_t)k0 * (z ? kb1 : kb0)));
     }
+  };
+  auto issue = [=](int slot, int kt) __attribute__((always_inline)) {
+    static_for<0, NA + NB>([&](auto jc) __attribute__((always_inline)) { issue_one(slot, kt, jc); });
   };
 
   floatx4 acc[FM][FN];
@@ -212,13 +217,24 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
       __builtin_amdgcn_sched_barrier(0);
     });
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((SLOTS - 2) * (NA + NB)) : "memory");
-    issue(cur, kt + SLOTS);
     const char* sn = lds + nxt;
+    if constexpr (!kSpread) issue(cur, kt + SLOTS);
     load_b(fbn, sn);
     load_a(fax, sn, 0);
     __builtin_amdgcn_sched_barrier(0);
-    mma(fay, fb, std::integral_constant<int, NQ - 1>{});
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kSpread) {
+      static_for<0, 2 * FN>([&](auto jc) __attribute__((always_inline)) {
+        constexpr int j = decltype(jc)::value, f = j / FN, fj = j % FN, qq = NQ - 1;
+        acc[2 * qq + f][fj] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[fj], fay[f], acc[2 * qq + f][fj], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (j < NA + NB) issue_one(cur, kt + SLOTS, jc);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    } else {
+      mma(fay, fb, std::integral_constant<int, NQ - 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   static_assert(NQ % 2 == 0, "the last quarter's fragments are in fay");
   if (n > 0) {
