@@ -7,8 +7,9 @@ namespace muon {
 namespace {
 
 // rows × cols of any stride and alignment → rows of ldo (a multiple of 8),
-// zeros beyond cols.
-__global__ __launch_bounds__(256) void ffn_pack(const FfnPack K) {
+// zeros beyond cols; one operand per blockIdx.y.
+__global__ __launch_bounds__(256) void ffn_pack(const FfnPacks L) {
+  const FfnPack& K = L.p[blockIdx.y];
   const int64_t chunks = K.ldo / 8;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < K.rows * chunks; e += (int64_t)gridDim.x * 256) {
     const int64_t r = e / chunks, c = (e - r * chunks) * 8;
@@ -27,9 +28,13 @@ hipError_t launch_ffn16_store(int tile, bool aRowContig, bool bRowContig, const 
   return hipGetLastError();
 }
 
-hipError_t launch_ffn_pack(const FfnPack& K, hipStream_t st) {
-  const int64_t n = K.rows * (K.ldo / 8), blocks = (n + 255) / 256;
-  hipLaunchKernelGGL(ffn_pack, dim3(blocks < 16384 ? blocks : 16384), dim3(256), 0, st, K);
+hipError_t launch_ffn_pack(const FfnPacks& K, hipStream_t st) {
+  int64_t blocks = 1;
+  for (int i = 0; i < K.n; ++i) {
+    const int64_t b = (K.p[i].rows * (K.p[i].ldo / 8) + 255) / 256;
+    blocks = b > blocks ? b : blocks;
+  }
+  hipLaunchKernelGGL(ffn_pack, dim3(blocks < 16384 ? blocks : 16384, K.n), dim3(256), 0, st, K);
   return hipGetLastError();
 }
 

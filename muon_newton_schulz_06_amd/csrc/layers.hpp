@@ -135,14 +135,18 @@ hipError_t launch_ffn_few(int epi, bool bf16, int splits, const FfnLaunch& L, hi
 // Sums of the splits' results, with the products' epilogue.
 hipError_t launch_ffn_join(int epi, bool bf16, int splits, const FfnLaunch& L, hipStream_t st);
 
-// Aligned, zero-padded copy of a bf16 operand.
+// Aligned, zero-padded copies of a call's bf16 operands.
 struct FfnPack {
   const void* src;
   int64_t ld, rows, cols;
   void* dst;
   int64_t ldo;
 };
-hipError_t launch_ffn_pack(const FfnPack& K, hipStream_t st);
+struct FfnPacks {
+  FfnPack p[5];
+  int32_t n;
+};
+hipError_t launch_ffn_pack(const FfnPacks& K, hipStream_t st);
 
 hipError_t launch_ffn_tile32(int epi, int tileM, bool aRowContig, bool bRowContig, const FfnLaunch& L,
                              hipStream_t st);

@@ -341,18 +341,19 @@ struct FfnCall {
   const FfnLayout& l;
   char* ws;
   hipStream_t st;
+  FfnPacks packs{};
   bool bf16() const { return f.dtype == MUON_DTYPE_BF16; }
 
-  // The operand itself, or its aligned copy at `at` in the workspace.
-  muon_status_t operand(const char* what, const void* p, int64_t ld, int64_t rows, int64_t cols, size_t at,
-                        Op* o) const {
-    if (!bf16() || l.few || direct16(p, ld, cols)) {
-      *o = {p, ld, cols};
-      return MUON_OK;
-    }
-    *o = {ws + at, round8(cols), round8(cols)};
-    FfnPack k{p, ld, rows, cols, ws + at, round8(cols)};
-    return launched(what, launch_ffn_pack(k, st), st);
+  // The operand itself, or its aligned copy at `at` in the workspace, which
+  // copies() then makes.
+  Op operand(const void* p, int64_t ld, int64_t rows, int64_t cols, size_t at) {
+    if (!bf16() || l.few || direct16(p, ld, cols)) return {p, ld, cols};
+    const int64_t ldo = round8(cols);
+    packs.p[packs.n++] = {p, ld, rows, cols, ws + at, ldo};
+    return {ws + at, ldo, ldo};
+  }
+  muon_status_t copies() const {
+    return packs.n ? launched("aligned copies", launch_ffn_pack(packs, st), st) : MUON_OK;
   }
 
   // The launch's products by plan g, and the sums of their splits.
@@ -638,14 +639,14 @@ muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x,
     muon_status_t s = check_device();
     if (s != MUON_OK) return s;
     const hipStream_t st = (hipStream_t)stream;
-    const FfnCall call{*ffn, l, (char*)workspace, st};
+    FfnCall call{*ffn, l, (char*)workspace, st};
     const bool bf16 = call.bf16();
     const int64_t T = ffn->tokens, D = ffn->model, F = ffn->hidden;
-    Op ox{}, og{}, ou{}, od{};
-    s = call.operand("copy of x", x, ld_x, T, D, l.x, &ox);
-    if (s == MUON_OK) s = call.operand("copy of w_gate", ffn->w_gate, ffn->ld_gate, F, D, l.gate, &og);
-    if (s == MUON_OK) s = call.operand("copy of w_up", ffn->w_up, ffn->ld_up, F, D, l.up, &ou);
-    if (s == MUON_OK) s = call.operand("copy of w_down", ffn->w_down, ffn->ld_down, D, F, l.down, &od);
+    const Op ox = call.operand(x, ld_x, T, D, l.x);
+    const Op og = call.operand(ffn->w_gate, ffn->ld_gate, F, D, l.gate);
+    const Op ou = call.operand(ffn->w_up, ffn->ld_up, F, D, l.up);
+    const Op od = call.operand(ffn->w_down, ffn->ld_down, D, F, l.down);
+    s = call.copies();
     if (s != MUON_OK) return s;
     void* h = saved ? (char*)saved + l.savedH : (char*)workspace + l.mid;
     FfnLaunch L{};
@@ -714,17 +715,22 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
     muon_status_t s = check_device();
     if (s != MUON_OK) return s;
     const hipStream_t st = (hipStream_t)stream;
-    const FfnCall call{*ffn, l, (char*)workspace, st};
+    FfnCall call{*ffn, l, (char*)workspace, st};
     const bool bf16 = call.bf16();
     const size_t e = esize(ffn->dtype);
     const char* sv = (const char*)saved;
     char* dgu = (char*)workspace + l.mid;
     const int32_t T = (int32_t)ffn->tokens, D = (int32_t)ffn->model, F = (int32_t)ffn->hidden;
-    Op ox{x, ld_x, D}, oy{dy, ld_dy, D};
+    Op ox{x, ld_x, D}, oy{dy, ld_dy, D}, og{}, ou{}, od{};
     if (T > 0) {
-      Op od{};
-      s = call.operand("copy of dy", dy, ld_dy, T, D, l.dy, &oy);
-      if (s == MUON_OK) s = call.operand("copy of w_down", ffn->w_down, ffn->ld_down, D, F, l.down, &od);
+      oy = call.operand(dy, ld_dy, T, D, l.dy);
+      od = call.operand(ffn->w_down, ffn->ld_down, D, F, l.down);
+      if (wantW) ox = call.operand(x, ld_x, T, D, l.x);
+      if (grads->dx) {
+        og = call.operand(ffn->w_gate, ffn->ld_gate, F, D, l.gate);
+        ou = call.operand(ffn->w_up, ffn->ld_up, F, D, l.up);
+      }
+      s = call.copies();
       if (s != MUON_OK) return s;
       FfnLaunch L{};
       L.ab = (void*)(sv + l.ab);
@@ -742,10 +748,6 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
       if (s != MUON_OK) return s;
     }
     if (T > 0 && grads->dx) {
-      Op og{}, ou{};
-      s = call.operand("copy of w_gate", ffn->w_gate, ffn->ld_gate, F, D, l.gate, &og);
-      if (s == MUON_OK) s = call.operand("copy of w_up", ffn->w_up, ffn->ld_up, F, D, l.up, &ou);
-      if (s != MUON_OK) return s;
       FfnLaunch L{};
       L.outBf16 = bf16;
       FfnProb& p = L.prob[0];
@@ -765,10 +767,6 @@ muon_status_t muon_gated_ffn_grad(const muon_ffn_t* ffn, const void* x, int64_t 
       if (s != MUON_OK) return s;
     }
     if (!wantW) return MUON_OK;
-    if (T > 0) {
-      s = call.operand("copy of x", x, ld_x, T, D, l.x, &ox);
-      if (s != MUON_OK) return s;
-    }
     FfnLaunch L{};
     L.outBf16 = grads->grad_dtype == MUON_DTYPE_BF16;
     L.accumulate = grads->accumulate != 0;
