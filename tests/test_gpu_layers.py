@@ -247,14 +247,20 @@ def ffn_inputs(tokens, model, hidden, dtype, seed=10):
 
 
 def ffn_bounds(x, wg, wu, wd, dy, act, dtype, gdt):
-    """Element-wise error bounds of every result.  The activation's slopes are
-    at most 1.13 and its second derivative at most 0.8, the errors of its
-    fp32 evaluation at most 2^-19 of 1 + |g| (hardware exponential)."""
+    """(results, element-wise error bounds of them), numpy."""
+    f = ol.gated_ffn_grad(dy, x, wg, wu, wd, act)
+    return f, ffn_errors(f, x, wg, wu, wd, dy, dtype, gdt)
+
+
+def ffn_errors(f, x, wg, wu, wd, dy, dtype, gdt):
+    """Element-wise error bounds of every result (numpy or torch, fp64).  The
+    activation's slopes are at most 1.13 and its second derivative at most
+    0.8, the errors of its fp32 evaluation at most 2^-19 of 1 + |g| (hardware
+    exponential)."""
     u, ug = UNIT[dtype], UNIT[gdt]
     s = 2.0 ** -10 if dtype == torch.bfloat16 else E  # saved factors
-    f = ol.gated_ffn_grad(dy, x, wg, wu, wd, act)
     D, F, T = x.shape[1], wd.shape[1], x.shape[0]
-    ab = np.abs
+    ab = abs
     eg, eu = 1.01 * D * E * (ab(x) @ ab(wg).T), 1.01 * D * E * (ab(x) @ ab(wu).T)
     fe = 2.0 ** -19 * (1 + ab(f["g"]))
     eb = 1.13 * eg + fe                                   # act(g)
@@ -270,7 +276,7 @@ def ffn_bounds(x, wg, wu, wd, dy, act, dtype, gdt):
          "dw_gate": (edg + k * ab(f["dg"])).T @ ab(x) + ug * ab(f["dw_gate"]),
          "dw_up": (edu + k * ab(f["du"])).T @ ab(x) + ug * ab(f["dw_up"]),
          "dw_down": ab(dy).T @ (eh + k * ab(f["h"])) + ug * ab(f["dw_down"])}
-    return f, {n: 1.02 * v + 2.0 ** -100 for n, v in b.items()}
+    return {n: 1.02 * v + 2.0 ** -100 for n, v in b.items()}
 
 
 NAMES = ("dx", "dw_gate", "dw_up", "dw_down")
@@ -333,6 +339,41 @@ def test_gated_ffn_mixed_strides(lib, dtype):
     got = lib.muon_gated_ffn_grad(dy, x, wg, wu, wd, saved, grads=outs)
     for n, g in zip(NAMES, got):
         check(g, f[n], b[n], n)
+
+
+@pytest.mark.parametrize("tokens,model,hidden", [(4096, 1024, 4096), (4096, 4096, 1024), (4001, 1032, 4104),
+                                                 (2500, 4090, 1000)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_ffn_large(lib, tokens, model, hidden, dtype):
+    """Sizes at which every product runs on its largest tile (each of y, dx,
+    dh and the weight gradients at one of them), with ragged edges, against
+    plain fp64 torch."""
+    x, wg, wu, wd, dy = ffn_inputs(tokens, model, hidden, dtype)
+    x, wg, wu, wd, dy = (t.cuda() for t in (x, wg, wu, wd, dy))
+    X, G, U, W, Y = (t.double() for t in (x, wg, wu, wd, dy))
+    f = {"g": X @ G.t(), "u": X @ U.t()}
+    s = torch.sigmoid(f["g"])
+    f["b"] = f["g"] * s
+    f["a"] = f["u"] * (s + f["b"] * (1 - s))
+    f["h"] = f["b"] * f["u"]
+    f["y"] = f["h"] @ W.t()
+    f["dh"] = Y @ W
+    f["dg"], f["du"] = f["dh"] * f["a"], f["dh"] * f["b"]
+    f["dx"] = f["dg"] @ G + f["du"] @ U
+    f["dw_gate"], f["dw_up"], f["dw_down"] = f["dg"].t() @ X, f["du"].t() @ X, Y.t() @ f["h"]
+    b = ffn_errors(f, X, G, U, W, Y, dtype, dtype)
+    y, saved = lib.muon_gated_ffn(x, wg, wu, wd, save=True)
+    got = dict(zip(("y", *NAMES), (y, *lib.muon_gated_ffn_grad(dy, x, wg, wu, wd, saved))))
+    for n, t in got.items():
+        assert bool(((t.double() - f[n]).abs() <= b[n]).all()), n
+    again = lib.muon_gated_ffn_grad(dy, x, wg, wu, wd, saved)
+    assert all(torch.equal(p, q) for p, q in zip(again, list(got.values())[1:]))
+    # fp32 gradients added to what is there
+    olds = [torch.full(w.shape, 0.5, device="cuda") for w in (wg, wu, wd)]
+    lib.muon_gated_ffn_grad(dy, x, wg, wu, wd, saved, want_dx=False, grads=olds, accumulate=True)
+    b32 = ffn_errors(f, X, G, U, W, Y, dtype, torch.float32)
+    for n, t in zip(NAMES[1:], olds):
+        assert bool(((t.double() - 0.5 - f[n]).abs() <= b32[n] + E * (0.5 + f[n].abs())).all()), n
 
 
 def test_gated_ffn_empty(lib):
