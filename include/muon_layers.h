@@ -29,7 +29,8 @@
  *   - sums run in a fixed order that depends on the sizes alone: equal calls
  *     give equal bits.
  *   - an output may not overlap an input or another output unless the entry
- *     point says so (MUON_ERR_ALIAS).
+ *     point says so (MUON_ERR_ALIAS); overlap is judged by the address ranges
+ *     from a tensor's first to its last element.
  *   - 0 ≤ tokens ≤ 2^24; 1 ≤ vocab ≤ 2^24; dim, model and hidden are
  *     1 … 2^20; strides are at most 2^32 elements.  With zero tokens nothing is read; gradients of weights are still written.
  */

@@ -3,7 +3,8 @@
 // The splits' fp32 results lie in the workspace as [split][M][partN]; four
 // columns per thread are added up in split order and finished as the
 // unsplit product would finish them.  HBM-bound (usually cache-bound: the
-// results were just written).
+// results were just written): 5 µs for one token's five splits of 3584 columns,
+// 12 µs for two splits of 2048 × 3584.
 #include <hip/hip_runtime.h>
 
 #include "ffn_epi.hpp"

@@ -15,6 +15,12 @@
 //  * FFN_GLU: a tile is TILE rows × TILE/2 columns of both projections.  Of a
 //    wave's 64 B rows 32 are w_gate's and 32 w_up's, so g and u of one element
 //    meet in one lane and the activation runs on fp32 registers.
+// Bound by the matrix pipe at the power-limited clock (1.9–2.0 GHz, MFMA busy
+// 49–62%): 0.77 µs per k-tile of a 256-tile on every CU.  At 4096 tokens,
+// 3584×18944: gated projections with a, b 1060 µs (1050 TFLOP/s), dh 555 (1000),
+// dx 870 (1280), weight gradients 1310 (1270), y 484 (1150).  The 128-tile takes
+// 0.62 µs per k-tile and pair of workgroups on a CU, which wins where 256-tiles
+// would leave CUs idle (see the time estimate on the host).
 // Operands need 16-byte aligned rows of whole 16-byte chunks; the host copies
 // others once.
 #pragma once
