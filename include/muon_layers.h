@@ -71,7 +71,8 @@ muon_status_t muon_embedding_grad_workspace_size(int64_t tokens, int64_t vocab, 
  *   x, residual (NULL: none), y, sum: tokens × dim of `dtype`; weight: dim
  *   values of `weight_dtype`; rstd: tokens float32 (NULL: not wanted).
  *   sum receives s rounded to dtype (NULL: not wanted; only with residual).
- *   y uses s before that rounding.  eps ≥ 0 finite.
+ *   y uses s before that rounding.  eps ≥ 0 finite (with eps = 0 a row of
+ *   zeros gives NaN, as the formula does).
  * y or sum may be x or residual itself (same address and stride). */
 muon_status_t muon_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
                             const void* weight, muon_dtype_t weight_dtype, float eps, void* y,

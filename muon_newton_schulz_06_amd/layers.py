@@ -328,9 +328,8 @@ def muon_rms_norm_grad(dy, s, weight, rstd, dsum=None, out=None, dweight=None, a
 
 def _ffn(x, w_gate, w_up, w_down, activation):
     """The call's sizes and weights, with x as rows."""
-    dev = _device(x, "x")
     code = _code(x, "x")
-    _same(dev, x.dtype, w_gate=w_gate, w_up=w_up, w_down=w_down)
+    _same(x.device, x.dtype, w_gate=w_gate, w_up=w_up, w_down=w_down)
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r}; use one of {sorted(ACTIVATIONS)}")
@@ -342,7 +341,7 @@ def _ffn(x, w_gate, w_up, w_down, activation):
     f = MuonFfn(tokens, model, hidden, _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                 _matrix(w_gate, "w_gate", hidden, model), _matrix(w_up, "w_up", hidden, model),
                 _matrix(w_down, "w_down", model, hidden), code, act)
-    return dev, f, x2, ldx
+    return f, x2, ldx
 
 
 def _ffn_size(tokens, model, hidden, dtype, grad):
@@ -375,8 +374,9 @@ def muon_gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", save: bool
     Returns y, or (y, saved) with save: an opaque uint8 tensor that
     muon_gated_ffn_grad takes."""
     L = _lib()
-    dev, f, x2, ldx = _ffn(x, w_gate, w_up, w_down, activation)
+    dev = _device(x, "x")
     with _on(dev, stream):
+        f, x2, ldx = _ffn(x, w_gate, w_up, w_down, activation)
         y = _out(out, x.shape, x.dtype, dev, "out")
         y2, ldy = _rows(y, "out")
         n = ctypes.c_size_t(0)
@@ -400,7 +400,7 @@ def muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx: bool = True
     float32 or bfloat16; added to them with accumulate) or are allocated in
     grad_dtype (by default the weights')."""
     L = _lib()
-    dev, f, x2, ldx = _ffn(x, w_gate, w_up, w_down, "silu")
+    dev = _device(x, "x")
     _same(dev, x.dtype, dy=dy)
     _same(dev, torch.uint8, saved=saved)
     if dy.shape != x.shape:
@@ -408,6 +408,7 @@ def muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx: bool = True
     if accumulate and grads is None:
         raise ValueError("accumulate needs grads")
     with _on(dev, stream):
+        f, x2, ldx = _ffn(x, w_gate, w_up, w_down, "silu")
         dy2, ldy = _rows(dy, "dy")
         dx, dx2, lddx = None, None, 0
         if want_dx:

@@ -141,6 +141,21 @@ def test_embedding_empty(lib):
     assert (lib.muon_embedding(ids, torch.full((5, 8), float("inf"), device="cuda")) == 0).all()
 
 
+def test_embedding_masked_places(lib):
+    """NaN and infinity where the id is padding, or in rows no token names,
+    reach nothing."""
+    ids = make_ids(500, 60, 9, torch.int64)
+    ids[ids == 7] = 8
+    off = (ids < 0) | (ids >= 60)
+    w, dy = rand((60, 24), 1, torch.bfloat16), rand((500, 24), 2, torch.bfloat16)
+    clean = lib.muon_embedding_grad(torch.where(off[:, None], 0, dy).cuda(), ids.cuda(), 60)
+    dy[off] = float("nan")
+    w[7] = float("inf")
+    assert torch.isfinite(lib.muon_embedding(ids.cuda(), w.cuda())).all()
+    assert torch.equal(lib.muon_embedding_grad(dy.cuda(), ids.cuda(), 60), clean)
+    assert (clean[7] == 0).all()
+
+
 # ----------------------------------------------------------------- RMS norm
 
 NORMS = [(1, 1), (1, 3584), (3, 17), (5, 512), (300, 1001), (2100, 96), (2048, 1001), (2500, 4096), (9, 8200),
@@ -499,9 +514,13 @@ def test_other_stream_and_graph(lib):
         got = step()
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(a, b) for a, b in zip(ref, got))
-    y = lib.muon_gated_ffn(x, wg, wu, wd, stream=side)
+    # an input that has to be copied to rows is copied on that stream too
+    x3 = x.reshape(11, 3, 64).transpose(0, 1)
+    side.wait_stream(torch.cuda.current_stream())
+    y, y3 = lib.muon_gated_ffn(x, wg, wu, wd, stream=side), lib.muon_gated_ffn(x3, wg, wu, wd, stream=side)
     side.synchronize()
     assert torch.equal(y, lib.muon_gated_ffn(x, wg, wu, wd))
+    assert torch.equal(y3, y.reshape(11, 3, 64).transpose(0, 1))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         outs = step()

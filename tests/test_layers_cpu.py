@@ -117,6 +117,20 @@ def test_nothing_to_do_needs_no_device(L):
     assert ffn(L, grad=True, tokens=0, acc=1, x=None, dy=None, saved=None, ws=None, dx=None) == 0
 
 
+def test_header_and_exports(L):
+    """Every function the header declares is exported, and takes as many
+    arguments as the binding gives it."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "include", "muon_layers.h"), encoding="utf-8") as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    found = re.findall(r"muon_status_t\s+(muon_\w+)\s*\(([^)]*)\)", text)
+    assert len(found) == 10
+    for name, args in found:
+        assert len(getattr(L, name).argtypes) == args.count(",") + 1, name
+
+
 def test_sizes():
     n = mns.gated_ffn_saved_size(100, 64, 33)
     assert n >= 100 * 40 * 2 * 3 and n % 256 == 0
