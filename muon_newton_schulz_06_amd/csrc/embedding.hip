@@ -15,7 +15,7 @@
 // HBM-bound for large vocabularies, whose bytes are mostly zero rows: 16384 ×
 // 3584 bf16 tokens into 131072 rows take 65 + 145 + 59 µs (sort, pieces, runs,
 // the first two beside 940 MB of zeros), about 4 TB/s; a run is a chain of
-// dependent reads, which bounds small calls (4093 × 1023 fp32: 16 + 25 + 22).
+// dependent reads, which bounds small calls (4093 × 1023 fp32: 15 + 29 + 22).
 // Ids outside [0, vocab) sort to the end as the key `vocab` and are skipped.
 #include <hip/hip_runtime.h>
 
@@ -68,10 +68,11 @@ __global__ __launch_bounds__(256) void embedding_kernel(const EmbedLaunch L, int
   }
 }
 
-// Zeros rows [v0, v1) of dweight: wave w of W waves takes rows v0 + w, v0 + w +
-// W, ..  Non-temporal stores: with ordinary ones the zeros filled the last-level
-// cache and their write-back ran into the sums (sums 76 -> 40 µs, sort beside
-// them 67 -> 47 µs for 131072×3584 bf16).
+// Zeros rows [v0, v1) of dweight by W waves, of which this is wave w: pieces of
+// 8 KiB of a contiguous dweight in turn, whatever its rows' alignment, else row
+// by row.  Non-temporal stores: with ordinary ones the zeros filled the
+// last-level cache and their write-back ran into the sums (sums 76 -> 40 µs,
+// sort beside them 67 -> 47 µs for 131072×3584 bf16).
 __device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t v0, int64_t v1, int64_t w, int64_t W);
 
 // ----- sort ------------------------------------------------------------------
@@ -445,15 +446,23 @@ __global__ __launch_bounds__(256) void embed_rows(const EmbedGradLaunch L, const
 
 __device__ __forceinline__ void zero_rows(const EmbedGradLaunch& L, int64_t v0, int64_t v1, int64_t w, int64_t W) {
   const int esz = L.dwBf16 ? 2 : 4, lane = threadIdx.x & 63;
-  for (int64_t v = v0 + w; v < v1; v += W) {
-    char* row = (char*)L.dw + v * L.ldw * esz;
-    const int64_t n = L.dim * esz, whole = n & ~(int64_t)15;
+  auto zero = [lane](char* p, int64_t n, int64_t w, int64_t W) {
+    constexpr int64_t kPiece = 8192;
     const lu32x4 z = {0u, 0u, 0u, 0u};
-    for (int64_t e = lane * 16; e < whole; e += 1024) {
-      if (L.vecw) __builtin_nontemporal_store(z, (lu32x4*)(row + e));
-      else __builtin_memcpy(row + e, &z, 16);
+    const int64_t head = min(n, (int64_t)(-(uintptr_t)p & 15)), body = (n - head) & ~(int64_t)15;
+    for (int64_t c = w * kPiece; c < body; c += W * kPiece) {
+      const int64_t end = min(c + kPiece, body);
+      for (int64_t e = c + lane * 16; e < end; e += 1024) __builtin_nontemporal_store(z, (lu32x4*)(p + head + e));
     }
-    for (int64_t e = whole + lane * 2; e < n; e += 128) *(uint16_t*)(row + e) = 0;
+    if (w == 0) {  // less than 16 bytes at either end
+      if (lane * 2 < head) *(uint16_t*)(p + lane * 2) = 0;
+      if (head + body + lane * 2 < n) *(uint16_t*)(p + head + body + lane * 2) = 0;
+    }
+  };
+  if (L.ldw == L.dim) {
+    zero((char*)L.dw + v0 * L.ldw * esz, (v1 - v0) * L.dim * esz, w, W);
+  } else {
+    for (int64_t v = v0 + w; v < v1; v += W) zero((char*)L.dw + v * L.ldw * esz, L.dim * esz, 0, 1);
   }
 }
 
