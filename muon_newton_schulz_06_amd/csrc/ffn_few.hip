@@ -168,6 +168,7 @@ void few_launch(const FfnLaunch& L, int splits, hipStream_t st) {
   const int tb = (L.prob[0].M + 15) / 16;
   if (tb == 1) hipLaunchKernelGGL((ffn_few<T, 1, EPI>), grid, block, 0, st, L);
   else if (tb == 2) hipLaunchKernelGGL((ffn_few<T, 2, EPI>), grid, block, 0, st, L);
+  else if (tb == 3) hipLaunchKernelGGL((ffn_few<T, 3, EPI>), grid, block, 0, st, L);
   else hipLaunchKernelGGL((ffn_few<T, 4, EPI>), grid, block, 0, st, L);
 }
 

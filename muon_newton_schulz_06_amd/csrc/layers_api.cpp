@@ -187,11 +187,15 @@ struct TilePlan {
 
 // Estimated time of n workgroups of `per` k-tiles, in µs, fitted to measured
 // products (bf16 tiles 256² run one to a CU, 128² two; the fp32 tiles are
-// bound by the matrix pipe or, alone on a CU, by a step's latency).
+// bound by the matrix pipe or, alone on a CU, by a step's latency, and the
+// stores of a 128-row one overlap less: 38 tokens, 2944×6681, the weights'
+// gradients 158 µs with 128 rows, 131 with 64; 1024 tokens, 2048×8192, y 309 /
+// 344).
 double tile_time(bool bf16, int tm, int64_t n, int64_t per) {
   const double cu = std::ceil(n / 256.0);  // workgroups on the busiest CU
   if (bf16) return tm == 256 ? cu * (per * 0.77 + 14) : std::ceil(n / 512.0) * (per * (n <= 256 ? 0.40 : 0.62) + 10);
-  return 10 + per * (tm == 128 ? std::max(2.3, 2.1 * cu) : std::max(1.3, 1.1 * cu));
+  if (tm == 128) return 10 + 8.5 * cu + per * std::max(2.75, 2.2 * cu);
+  return 10 + 3 * cu + per * std::max(1.65, 1.2 * cu);
 }
 
 // Tile and splits of a product of M × N results (all problems of a launch
@@ -222,10 +226,12 @@ TilePlan plan_tiles(bool bf16, int64_t M, int64_t N, int64_t KT) {
 // every weight once at HBM's rate, but its workgroups each read the tokens
 // again, so its time grows with tokens × weights.  Measured (µs, few-token
 // kernel against tiles): bf16 3584×18944 T 1: 85 / 113, 12: 109 / 103, 64: 216 /
-// 130; bf16 1024×4096 T 64: 25 / 28; fp32 3584×18944 T 32: 336 / 364, 64: 567 /
-// 309; fp32 1024×4096 T 64: 42 / 47.
+// 130; bf16 1024×4096 T 64: 25 / 28; fp32 (blocks of 16 tokens, so whole blocks
+// count) 3584×18944 T 16: 231 / 331, 32: 311 / 329, 48: 302 / 301; 2944×6681
+// T 32: 89 / 106, 38: 121 / 113; 1024×4096 T 40: 35 / 46, 64: 43 / 47.
 bool few_tokens(bool bf16, int64_t T, int64_t weights) {
-  return T <= kFfnFew && (double)T * weights <= (bf16 ? 2e9 : 7e9);
+  if (bf16) return T <= kFfnFew && (double)T * weights <= 2e9;
+  return T <= 32 || (T <= kFfnFew && (double)tiles_of(T, 16) * weights <= 1.5e8);
 }
 
 // The few-token kernel: about 1024 workgroups of 16 weight rows, each split at

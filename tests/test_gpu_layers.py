@@ -316,6 +316,20 @@ def test_gated_ffn(lib, tokens, model, hidden, act, dtype):
         assert all(torch.equal(p, q) for p, q in zip(got, again))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tokens", [15, 16, 32, 33, 40, 47, 48, 49])
+def test_gated_ffn_token_blocks(lib, tokens, dtype):
+    """Tokens around whole blocks of 16, and weight gradients whose one sum
+    over tokens ends inside a step of 32 (at and off a multiple of 8)."""
+    ts = ffn_inputs(tokens, 300, 700, dtype)
+    f, b = ffn_bounds(*(f64(t) for t in ts), "silu", dtype, dtype)
+    x, wg, wu, wd, dy = (t.cuda() for t in ts)
+    y, saved = lib.muon_gated_ffn(x, wg, wu, wd, save=True)
+    check(y, f["y"], b["y"], "y")
+    for n, g in zip(NAMES, lib.muon_gated_ffn_grad(dy, x, wg, wu, wd, saved)):
+        check(g, f[n], b[n], n)
+
+
 @pytest.mark.parametrize("tokens,model,hidden", [(5, 24, 40), (130, 136, 264), (300, 72, 200), (64, 33, 50)])
 @pytest.mark.parametrize("gdt", DTYPES)
 def test_gated_ffn_grad_accumulates(lib, tokens, model, hidden, gdt):
