@@ -4,12 +4,12 @@
 // TM/2 × 64 (32×32×2 MFMAs), k in steps of 32.  The operands are staged
 // through registers into k-major LDS panels (rows of TM + 4 or 132 floats: the
 // transposing writes of a k-contiguous operand then spread over the banks),
-// double buffered, one barrier per step, the global loads two steps ahead.  A 32×32×2 MFMA takes 64 cycles and its two 4-byte LDS
-// reads are shared by two MFMAs each, so a full GPU is bound by the matrix
-// pipe; small products are bound by the latency of a step (load, barrier),
-// which is what the 64-row tile and the k splits are for.  1024 tokens,
-// 2048×8192: 107 TFLOP/s (dh 330 µs), MFMA busy 71%; 501 tokens, 509×1021: 20–42
-// µs per product.
+// double buffered, one barrier per step, the global loads two steps ahead.  A
+// 32×32×2 MFMA takes 64 cycles and its two 4-byte LDS reads are shared by two
+// MFMAs each, so a full GPU is bound by the matrix pipe; small products are
+// bound by the latency of a step (load, barrier), which is what the 64-row
+// tile and the k splits are for.  1024 tokens, 2048×8192: 107 TFLOP/s (dh 320
+// µs), MFMA busy 71%; 501 tokens, 509×1021: 20–41 µs per product.
 #include <hip/hip_runtime.h>
 
 #include <cstring>
