@@ -118,9 +118,8 @@ typedef struct muon_ffn {
  *   saved: NULL, or muon_gated_ffn_saved_size bytes (256-byte aligned) that
  *   receive what muon_gated_ffn_grad reads: h in dtype, and the factors
  *   a = u·act'(g) and b = act(g) — float32 for MUON_DTYPE_F32; for
- *   MUON_DTYPE_BF16 in 16 bits with 6 exponent and 9 mantissa bits (errors
- *   below 2^-10 relative or 2^-31, magnitudes of 2^32 and more become NaN):
- *   two bits more precise than bf16, since their products are rounded again.
+ *   MUON_DTYPE_BF16 the upper 24 bits of the float32 values (its whole range,
+ *   errors below 2^-15 relative), since their products are rounded again.
  * g and u are never rounded before h; h is rounded to dtype. */
 muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x, void* y,
                              int64_t ld_y, void* saved, size_t saved_bytes, void* workspace,

@@ -114,9 +114,10 @@ __device__ __forceinline__ void ffn_glu4(const FfnLaunch& L, const FfnProb& P, i
     *(uint2*)((uint16_t*)P.C + i * P.ldc + j) =
         make_uint2(l_f32_bf16x2(v[0] * u[0], v[1] * u[1]), l_f32_bf16x2(v[2] * u[2], v[3] * u[3]));
     if constexpr (SAVE) {
-      uint16_t* o = (uint16_t*)L.ab + i * 2 * L.ldh + j;
-      *(uint2*)o = make_uint2(l_pack_e6m9x2(d[0], d[1]), l_pack_e6m9x2(d[2], d[3]));
-      *(uint2*)(o + L.ldh) = make_uint2(l_pack_e6m9x2(v[0], v[1]), l_pack_e6m9x2(v[2], v[3]));
+      uint16_t* o = (uint16_t*)L.ab + i * 3 * L.ldh + j;
+      *(uint2*)o = make_uint2(l_upper2(d[0], d[1]), l_upper2(d[2], d[3]));
+      *(uint2*)(o + L.ldh) = make_uint2(l_upper2(v[0], v[1]), l_upper2(v[2], v[3]));
+      *(uint2*)(o + 2 * L.ldh) = make_uint2(l_lower2(d[0], v[0], d[1], v[1]), l_lower2(d[2], v[2], d[3], v[3]));
     }
   }
 }
@@ -129,14 +130,12 @@ template <typename F> __device__ __forceinline__ void ffn_with_glu(const FfnLaun
   });
 }
 
-// FFN_BACK, bf16: dg = dh·a and du = dh·b from the codes of a and b.
-__device__ __forceinline__ void ffn_back4_bf16(const FfnLaunch& L, const FfnProb& P, int64_t i, int64_t j,
-                                               const float (&c)[4], uint2 a, uint2 b) {
-  uint16_t* o = (uint16_t*)P.C + i * 2 * L.ldh + j;
-  *(uint2*)o = make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(a.x), c[1] * l_unpack_hi(a.x)),
-                          l_f32_bf16x2(c[2] * l_unpack_lo(a.y), c[3] * l_unpack_hi(a.y)));
-  *(uint2*)(o + L.ldh) = make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(b.x), c[1] * l_unpack_hi(b.x)),
-                                    l_f32_bf16x2(c[2] * l_unpack_lo(b.y), c[3] * l_unpack_hi(b.y)));
+// dh times value V (0: a, 1: b) of four columns, as bf16: from the upper halves
+// of V and the bytes below of both.
+template <int V, typename F> __device__ __forceinline__ uint2 ffn_times24(const F& c, uint2 upper, uint2 lower) {
+  return make_uint2(
+      l_f32_bf16x2(c[0] * l_join24<V, 0>(upper.x, lower.x), c[1] * l_join24<V, 1>(upper.x, lower.x)),
+      l_f32_bf16x2(c[2] * l_join24<V, 0>(upper.y, lower.y), c[3] * l_join24<V, 1>(upper.y, lower.y)));
 }
 
 }  // namespace muon

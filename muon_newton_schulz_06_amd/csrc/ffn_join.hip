@@ -43,8 +43,11 @@ __global__ __launch_bounds__(256) void ffn_join(const FfnLaunch L, int splits) {
     });
   } else if constexpr (EPI == FFN_BACK) {
     if constexpr (LType<T>::kVec == 8) {
-      const uint16_t* o = (const uint16_t*)L.ab + i * 2 * L.ldh + j;
-      ffn_back4_bf16(L, P, i, j, c, *(const uint2*)o, *(const uint2*)(o + L.ldh));
+      const uint16_t* ab = (const uint16_t*)L.ab + i * 3 * L.ldh + j;
+      const uint2 lower = *(const uint2*)(ab + 2 * L.ldh);
+      uint16_t* o = (uint16_t*)P.C + i * 2 * L.ldh + j;
+      *(uint2*)o = ffn_times24<0>(c, *(const uint2*)ab, lower);
+      *(uint2*)(o + L.ldh) = ffn_times24<1>(c, *(const uint2*)(ab + L.ldh), lower);
     } else {
       const float* ab = (const float*)L.ab + i * 2 * L.ldh + j;
       const lf32x4 va = *(const lf32x4*)ab, vb = *(const lf32x4*)(ab + L.ldh);

@@ -339,11 +339,11 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
   constexpr auto kOne = std::integral_constant<int, 1>{};
   const int lrow = wm * WTM + lc;  // a lane's row of block row 0, and its column below
   if constexpr (EPI == FFN_GLU) {
-    // half of every wave's rows at a time: h, a and b of a tile side by side
+    // half of every wave's rows at a time: h and the three planes of a and b
     constexpr int W = TN / 2, HR = WTM / 2;
     constexpr auto kW = std::integral_constant<int, W>{};
     constexpr int kPart = TM / 2 * W * 2;  // bytes of one array's half tile
-    static_assert(3 * kPart <= SLOTS * kSlot, "staged arrays fit");
+    static_assert(4 * kPart <= SLOTS * kSlot, "staged arrays fit");
     // columns N .. ldh − 1 come out as zeros
     ffn_with_glu(L, [&](auto actc, auto savec) __attribute__((always_inline)) {
       constexpr bool SAVE = decltype(savec)::value;
@@ -365,49 +365,61 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
             }
             put(lds, W, row, col, make_uint2(l_f32_bf16x2(h[0], h[1]), l_f32_bf16x2(h[2], h[3])));
             if constexpr (SAVE) {
-              put(lds + kPart, W, row, col, make_uint2(l_pack_e6m9x2(d[0], d[1]), l_pack_e6m9x2(d[2], d[3])));
-              put(lds + 2 * kPart, W, row, col, make_uint2(l_pack_e6m9x2(v[0], v[1]), l_pack_e6m9x2(v[2], v[3])));
+              put(lds + kPart, W, row, col, make_uint2(l_upper2(d[0], d[1]), l_upper2(d[2], d[3])));
+              put(lds + 2 * kPart, W, row, col, make_uint2(l_upper2(v[0], v[1]), l_upper2(v[2], v[3])));
+              put(lds + 3 * kPart, W, row, col,
+                  make_uint2(l_lower2(d[0], v[0], d[1], v[1]), l_lower2(d[2], v[2], d[3], v[3])));
             }
           }
         __syncthreads();
         constexpr auto kHalves = std::integral_constant<int, 2>{};
         rows_out(lds, kW, kHalves, part, P.C, P.ldc, L.ldh);
         if constexpr (SAVE) {
-          rows_out(lds + kPart, kW, kHalves, part, L.ab, 2 * L.ldh, L.ldh);
-          rows_out(lds + 2 * kPart, kW, kHalves, part, (uint16_t*)L.ab + L.ldh, 2 * L.ldh, L.ldh);
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            rows_out(lds + (p + 1) * kPart, kW, kHalves, part, (uint16_t*)L.ab + p * L.ldh, 3 * L.ldh, L.ldh);
         }
       });
     });
   } else if constexpr (EPI == FFN_BACK) {
-    // a, then b: the tile of the factor is loaded into the staging, multiplied
-    // in place (a lane reads and writes the same address) and stored
+    // a quarter of every wave's rows at a time: the planes of a and b are loaded
+    // into the staging, the upper halves multiplied in place (a lane reads and
+    // writes the same addresses) and stored as dg and du
     constexpr auto kW = std::integral_constant<int, TN>{};
-    constexpr int CH = TN / 8, RPI = 64 / CH;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    constexpr auto kQuarters = std::integral_constant<int, 4>{};
+    constexpr int CH = TN / 8, RPI = 64 / CH, HR = WTM / 4, RW = TM / 4 / NW;
+    constexpr int kPlane = TM / 4 * TN * 2;  // bytes
+    static_assert(3 * kPlane <= SLOTS * kSlot, "staged planes fit");
+    static_for<0, 4>([&](auto pc) __attribute__((always_inline)) {
+      constexpr int part = decltype(pc)::value;
       __syncthreads();
-      const fi32x4 rs = f_buffer((uint64_t)L.ab + ((uint64_t)i0 * 2 * L.ldh + half * L.ldh + j0) * 2);
-#pragma unroll 4
-      for (int p = 0; p < TM / NW / RPI; ++p) {
-        const int r = wave * (TM / NW) + p * RPI + lane / CH, c = (lane % CH) ^ (r & (CH - 1));
-        const uint32_t off = i0 + r < P.M && j0 + c * 8 < L.ldh ? (uint32_t)((int64_t)r * 4 * L.ldh + c * 16) : kFfnNowhere;
-        f_dma16(__builtin_amdgcn_readfirstlane(lds_addr(lds) + (wave * (TM / NW) + p * RPI) * TN * 2), off, rs);
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        const fi32x4 rs = f_buffer((uint64_t)L.ab + ((uint64_t)i0 * 3 * L.ldh + pl * L.ldh + j0) * 2);
+#pragma unroll
+        for (int p = 0; p < RW / RPI; ++p) {
+          const int r = wave * RW + p * RPI + lane / CH, c = (lane % CH) ^ (r & (CH - 1));
+          const int i = (r / HR) * WTM + part * HR + r % HR;
+          const uint32_t off = i0 + i < P.M && j0 + c * 8 < L.ldh ? (uint32_t)((int64_t)i * 6 * L.ldh + c * 16) : kFfnNowhere;
+          f_dma16(__builtin_amdgcn_readfirstlane(lds_addr(lds) + pl * kPlane + (wave * RW + p * RPI) * TN * 2), off, rs);
+        }
       }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
 #pragma unroll
-      for (int fi = 0; fi < FM; ++fi)
+      for (int f = 0; f < FM / 4; ++f)
 #pragma unroll
         for (int fj = 0; fj < FN; ++fj) {
-          char* const at = lds + soff(TN, lrow + fi * 16, wn * 64 + fj * 16 + 4 * lg);
-          const uint2 f = *(const uint2*)at;
-          const floatx4 c = acc[fi][fj];
-          *(uint2*)at = make_uint2(l_f32_bf16x2(c[0] * l_unpack_lo(f.x), c[1] * l_unpack_hi(f.x)),
-                                   l_f32_bf16x2(c[2] * l_unpack_lo(f.y), c[3] * l_unpack_hi(f.y)));
+          char* const at = lds + soff(TN, wm * HR + f * 16 + lc, wn * 64 + fj * 16 + 4 * lg);
+          const uint2 a = *(const uint2*)at, b = *(const uint2*)(at + kPlane), lower = *(const uint2*)(at + 2 * kPlane);
+          const floatx4 c = acc[part * (FM / 4) + f][fj];
+          *(uint2*)at = ffn_times24<0>(c, a, lower);
+          *(uint2*)(at + kPlane) = ffn_times24<1>(c, b, lower);
         }
       __syncthreads();
-      rows_out(lds, kW, kOne, 0, (uint16_t*)P.C + half * L.ldh, P.ldc, L.ldh);
-    }
+      rows_out(lds, kW, kQuarters, part, P.C, P.ldc, L.ldh);
+      rows_out(lds + kPlane, kW, kQuarters, part, (uint16_t*)P.C + L.ldh, P.ldc, L.ldh);
+    });
   } else if (L.outBf16 && !L.accumulate && ((uintptr_t)P.C & 15) == 0 && (P.ldc & 7) == 0) {
     __syncthreads();
 #pragma unroll

@@ -117,8 +117,9 @@ struct FfnLaunch {
   int32_t nprob;
   int32_t act;
   int32_t outBf16, accumulate;
-  // FFN_GLU: a, b (rows of 2·ldh: a then b; null: not wanted), C is h;
-  // FFN_BACK: reads them, C is dg, du (rows of 2·ldh)
+  // FFN_GLU: a, b (null: not wanted), C is h; FFN_BACK: reads them, C is dg, du
+  // (rows of 2·ldh).  Rows of a, b: fp32 2·ldh values, a then b; bf16 3·ldh
+  // 16-bit pieces, the upper halves of a, those of b, the bytes below of both
   void* ab;
   int64_t ldh;  // hidden rounded up to 8: row length of h and of each half
   int32_t splitTiles;  // k-tiles of 32 per split (a multiple of four for bf16 tiles)
@@ -261,27 +262,25 @@ __device__ __forceinline__ float l_wave_sum(float v) {
   return v;
 }
 
-// 16-bit float: sign, 6 exponent bits (the fp32 exponent less 96), 9 mantissa
-// bits rounded to nearest (ties away from zero: one addition).  Magnitudes
-// below 2^-30 keep an error of up to 2^-31; those of 2^32 and more, infinity
-// and NaN become the one NaN, all ones.  Five operations: 2·|x| has exponent
-// and mantissa in its top 31 bits, the saturating subtraction moves the
-// exponent and sends small magnitudes to 0, the minimum caps the large ones.
-__device__ __forceinline__ uint32_t l_e6m9_top(float f) {  // code in bits 31:16
-  const uint32_t u = __float_as_uint(f);
-  const uint32_t m = min(__builtin_elementwise_sub_sat((u << 1) + 0x4000u, 96u << 24), 0x3fff8000u);
-  return (m << 1) | (u & 0x80000000u);
+// The upper 24 bits of an fp32 value (sign, its 8 exponent bits, 15 mantissa
+// bits): the whole range of fp32, infinities and NaN (arithmetic makes quiet
+// ones, whose mark is the top mantissa bit) included.  Cut off, not rounded:
+// the error, below 2^-15 of a normal value, is far below that of the rounding
+// to bf16 that follows, and a byte selection is all it takes either way.
+// Columns c, c + 1 of two values a, b are kept in three dwords: the upper
+// halves of a, those of b, and the bytes below (a, b of c, then of c + 1).
+__device__ __forceinline__ uint32_t l_upper2(float v0, float v1) {
+  return __builtin_amdgcn_perm(__float_as_uint(v1), __float_as_uint(v0), 0x07060302u);
 }
-__device__ __forceinline__ uint32_t l_pack_e6m9x2(float lo, float hi) {
-  return (l_e6m9_top(lo) >> 16) | (l_e6m9_top(hi) & 0xffff0000u);
+__device__ __forceinline__ uint32_t l_lower2(float a0, float b0, float a1, float b1) {
+  return __builtin_amdgcn_perm(__float_as_uint(b0), __float_as_uint(a0), 0x0c0c0501u) |
+         __builtin_amdgcn_perm(__float_as_uint(b1), __float_as_uint(a1), 0x05010c0cu);
 }
-// The halves of a dword of two codes.  The code's bits as an fp32 with its own
-// exponent field, times 2^96 (a field of 0 is an fp32 subnormal there).
-__device__ __forceinline__ float l_e6m9_value(int32_t top) {
-  const float f = __uint_as_float((uint32_t)(top >> 2) & 0x9fffc000u) * 0x1p96f;
-  return fabsf(f) >= 8573157376.f ? __uint_as_float(0x7fc00000u) : f;  // 2^32·(1 + 511/512)
+// Value V (0: a, 1: b) of column c + H from its dword of upper halves and the
+// dword of lower bytes.
+template <int V, int H> __device__ __forceinline__ float l_join24(uint32_t upper, uint32_t lower) {
+  return __uint_as_float(
+      __builtin_amdgcn_perm(upper, lower, (H ? 0x07060000u : 0x05040000u) | (2 * H + V) << 8 | 0x0cu));
 }
-__device__ __forceinline__ float l_unpack_lo(uint32_t w) { return l_e6m9_value((int32_t)(w << 16)); }
-__device__ __forceinline__ float l_unpack_hi(uint32_t w) { return l_e6m9_value((int32_t)w); }
 
 }  // namespace muon

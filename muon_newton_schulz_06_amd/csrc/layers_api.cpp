@@ -265,7 +265,7 @@ FfnLayout ffn_layout(const muon_ffn_t& f, bool grad) {
   l.ldh = round8(F);
   const size_t rows = (size_t)T * l.ldh * e;
   l.ab = 0;
-  l.savedH = align256(2 * rows);
+  l.savedH = align256((size_t)T * l.ldh * (bf16 ? 6 : 8));  // a and b: 24 bits each, or fp32
   l.saved = l.savedH + align256(rows);
   size_t at = 0;
   auto take = [&](size_t n) {
