@@ -13,6 +13,7 @@ Names follow the C ABI:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import json
 import os
@@ -187,37 +188,74 @@ _ws_cache: dict = {}
 _ws_lock = threading.Lock()
 
 
+class _Slot:
+    """The cached buffer of one (device, stream).  Its lock is held from the
+    moment a call takes the buffer until its last kernel is enqueued: the
+    kernels of two threads' calls on one stream must not come between one
+    another, since both use the buffer across several kernels."""
+    __slots__ = ("lock", "buf")
+
+    def __init__(self):
+        self.lock = threading.RLock()  # a destructor that runs inside may call again
+        self.buf = None
+
+
+class _Leased:
+    """A cached buffer of at least nbytes, for the `with` body."""
+    __slots__ = ("slot", "nbytes", "device", "stream")
+
+    def __init__(self, slot, nbytes, device, stream):
+        self.slot, self.nbytes, self.device, self.stream = slot, nbytes, device, stream
+
+    def __enter__(self):
+        slot = self.slot
+        slot.lock.acquire()
+        try:
+            buf = slot.buf
+            if buf is None or buf.numel() < self.nbytes:
+                slot.buf = buf = None
+                s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+                with torch.cuda.stream(s):
+                    slot.buf = buf = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
+            return buf, buf.numel()
+        except BaseException:
+            slot.lock.release()
+            raise
+
+    def __exit__(self, *exc):
+        self.slot.lock.release()
+        return False
+
+
 def _workspace(nbytes: int, device, user, stream=None):
-    """The workspace of a call: the caller's buffer, or a cached one.
+    """`with _workspace(...) as (buffer, bytes):` enqueues a call's kernels with
+    the caller's buffer, or with a cached one.
 
     Cached buffers are kept per (device, stream) and allocated while that
     stream is current, so the caching allocator files them under the stream
-    the library's kernels use: calls on one stream reuse its buffer in stream
-    order, calls on different streams never share one, and a buffer dropped
-    for a larger one is only handed out again for work on that same stream
-    (after the kernels already enqueued there)."""
+    the library's kernels use: calls on one stream, of any thread, reuse its
+    buffer in stream order, calls on different streams never share one, and a
+    buffer dropped for a larger one is only handed out again for work on that
+    same stream (after the kernels already enqueued there)."""
     if nbytes == 0:
-        return None, 0
+        return contextlib.nullcontext((None, 0))
     if user is not None:
         if user.device != device:
             raise ValueError("workspace on another device")
-        return user, user.numel() * user.element_size()
-    handle = stream.cuda_stream if stream is not None else _raw_stream(device.index)
-    key = (device.type, device.index, handle)
+        return contextlib.nullcontext((user, user.numel() * user.element_size()))
+    key = (device.type, device.index, stream.cuda_stream if stream is not None else _raw_stream(device.index))
     with _ws_lock:
-        buf = _ws_cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            _ws_cache.pop(key, None)
-            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-                buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            _ws_cache[key] = buf
-    return buf, buf.numel()
+        slot = _ws_cache.get(key)
+        if slot is None:
+            slot = _ws_cache[key] = _Slot()
+    return _Leased(slot, nbytes, device, stream)
 
 
 def release_workspace():
     """Drop the cached workspace buffers (the next call allocates anew)."""
     with _ws_lock:
-        _ws_cache.clear()
+        for slot in _ws_cache.values():
+            slot.buf = None  # a call that is using it holds a reference of its own
 
 
 def _mat_fields(t: torch.Tensor):
@@ -326,8 +364,7 @@ def muon_ns_batched(xs, outs=None, steps: int = 5, coeffs=QUINTIC, eps: float = 
     arr = _ns_descs(xs, outs)
     need = ctypes.c_size_t(0)
     _check(L.muon_ns_workspace_size(arr, len(xs), code, ctypes.byref(need)))
-    ws, ws_bytes = _workspace(int(need.value), dev, workspace, stream)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _workspace(int(need.value), dev, workspace, stream) as (ws, ws_bytes):
         _check(L.muon_ns_batched(arr, len(xs), int(steps), _coeffs(coeffs), code, float(eps),
                                  ctypes.c_void_p(ws.data_ptr() if ws is not None else 0),
                                  ws_bytes, _stream_handle(stream, dev)))
@@ -407,10 +444,9 @@ def muon_step(params, grads, momenta, beta: float = 0.95, lr: float = 0.02, step
     nbytes = int(need.value)
     if max_workspace_bytes:
         nbytes = min(nbytes, int(max_workspace_bytes))
-    ws, ws_bytes = _workspace(nbytes, dev, workspace, stream)
     plain = ((not nesterov) and float(weight_decay) == 0.0 and gdt == torch.float32 and not overlap
              and not max_workspace_bytes and scale_exp is None)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _workspace(nbytes, dev, workspace, stream) as (ws, ws_bytes):
         wsp = ctypes.c_void_p(ws.data_ptr() if ws is not None else 0)
         if plain:
             _check(L.muon_step(P, G, M, rows, cols, n, _dtype_code(pdt), float(beta), float(lr),
@@ -460,8 +496,7 @@ def muon_step_selected(params, grads, momenta, fraction: float, beta: float = 0.
     cols = (ctypes.c_int64 * n)(*[int(p.shape[1]) for p in params])
     need = ctypes.c_size_t(0)
     _check(L.muon_step_selected_workspace_size(rows, cols, n, float(fraction), ctypes.byref(need)))
-    ws, ws_bytes = _workspace(int(need.value), dev, workspace, stream)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _workspace(int(need.value), dev, workspace, stream) as (ws, ws_bytes):
         wsp = ctypes.c_void_p(ws.data_ptr() if ws is not None else 0)
         _check(L.muon_step_selected(P, G, M, rows, cols, n, _dtype_code(pdt), float(beta), float(lr),
                                     int(steps), _coeffs(coeffs), float(eps), float(fraction), wsp,

@@ -241,10 +241,10 @@ def muon_embedding_grad(dy, ids, vocab: int, scale: float = 1.0, out=None, dtype
         _same(dev, dtype, out=out)
         need = ctypes.c_size_t(0)
         _check(L.muon_embedding_grad_workspace_size(tokens, vocab, dim, ctypes.byref(need)))
-        ws, nbytes = _workspace(need.value, dev, workspace, stream)
-        _check(L.muon_embedding_grad(_ptr(d), ldy, _ptr(ids), nb, tokens, vocab, dim, scale, _ptr(out), ldo,
-                                     code, _code(out, "out"), int(bool(accumulate)), _ptr(ws), nbytes,
-                                     _raw_stream(dev.index)))
+        with _workspace(need.value, dev, workspace, stream) as (ws, nbytes):
+            _check(L.muon_embedding_grad(_ptr(d), ldy, _ptr(ids), nb, tokens, vocab, dim, scale, _ptr(out), ldo,
+                                         code, _code(out, "out"), int(bool(accumulate)), _ptr(ws), nbytes,
+                                         _raw_stream(dev.index)))
     return out
 
 
@@ -310,17 +310,17 @@ def muon_rms_norm_grad(dy, s, weight, rstd, dsum=None, out=None, dweight=None, a
             raise ValueError(f"rstd must hold {tokens} contiguous values, got shape {tuple(rstd.shape)}")
         dx = _out(out, dy.shape, dy.dtype, dev, "out")
         dx2, ldx = _rows(dx, "out")
-        ws, nbytes = None, 0
+        need = ctypes.c_size_t(0)
         if want_dweight:
             dweight = _out(dweight, (dim,), weight.dtype, dev, "dweight")
-            need = ctypes.c_size_t(0)
             _check(L.muon_rms_norm_grad_workspace_size(tokens, dim, ctypes.byref(need)))
-            ws, nbytes = _workspace(need.value, dev, workspace, stream)
         else:
             dweight = None
-        _check(L.muon_rms_norm_grad(_ptr(dy2), ldy, _ptr(s2), lds, _ptr(weight), _code(weight, "weight"),
-                                    _ptr(rstd), _ptr(d2), ldd, _ptr(dx2), ldx, _ptr(dweight),
-                                    int(bool(accumulate)), tokens, dim, code, _ptr(ws), nbytes, _raw_stream(dev.index)))
+        with _workspace(need.value, dev, workspace, stream) as (ws, nbytes):
+            _check(L.muon_rms_norm_grad(_ptr(dy2), ldy, _ptr(s2), lds, _ptr(weight), _code(weight, "weight"),
+                                        _ptr(rstd), _ptr(d2), ldd, _ptr(dx2), ldx, _ptr(dweight),
+                                        int(bool(accumulate)), tokens, dim, code, _ptr(ws), nbytes,
+                                        _raw_stream(dev.index)))
     return dx, dweight
 
 
@@ -386,9 +386,9 @@ def muon_gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", save: bool
             nsaved = n.value
             saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
         _check(L.muon_gated_ffn_workspace_size(ctypes.byref(f), 0, ctypes.byref(n)))
-        ws, nbytes = _workspace(n.value, dev, workspace, stream)
-        _check(L.muon_gated_ffn(ctypes.byref(f), _ptr(x2), ldx, _ptr(y2), ldy, _ptr(saved), nsaved,
-                                _ptr(ws), nbytes, _raw_stream(dev.index)))
+        with _workspace(n.value, dev, workspace, stream) as (ws, nbytes):
+            _check(L.muon_gated_ffn(ctypes.byref(f), _ptr(x2), ldx, _ptr(y2), ldy, _ptr(saved), nsaved,
+                                    _ptr(ws), nbytes, _raw_stream(dev.index)))
     return (y, saved) if save else y
 
 
@@ -431,9 +431,10 @@ def muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx: bool = True
             g.grad_dtype = _code(out[0], "dw_gate")
         n = ctypes.c_size_t(0)
         _check(L.muon_gated_ffn_workspace_size(ctypes.byref(f), 1, ctypes.byref(n)))
-        ws, nbytes = _workspace(n.value, dev, workspace, stream)
-        _check(L.muon_gated_ffn_grad(ctypes.byref(f), _ptr(x2), ldx, _ptr(dy2), ldy, _ptr(saved),
-                                     saved.numel(), ctypes.byref(g), _ptr(ws), nbytes, _raw_stream(dev.index)))
+        with _workspace(n.value, dev, workspace, stream) as (ws, nbytes):
+            _check(L.muon_gated_ffn_grad(ctypes.byref(f), _ptr(x2), ldx, _ptr(dy2), ldy, _ptr(saved),
+                                         saved.numel(), ctypes.byref(g), _ptr(ws), nbytes,
+                                         _raw_stream(dev.index)))
     return (dx, *out)
 
 
