@@ -186,6 +186,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 _ws_cache: dict = {}
 _ws_lock = threading.Lock()
+_AS_IS = contextlib.nullcontext()
 
 
 class _Slot:
@@ -236,13 +237,21 @@ def _workspace(nbytes: int, device, user, stream=None):
     the library's kernels use: calls on one stream, of any thread, reuse its
     buffer in stream order, calls on different streams never share one, and a
     buffer dropped for a larger one is only handed out again for work on that
-    same stream (after the kernels already enqueued there)."""
+    same stream (after the kernels already enqueued there).
+
+    A call that is captured into a graph gets a buffer of its own, which
+    belongs to the graph's memory pool: the graph is replayed when it likes, on
+    any stream, and no later call may share or replace what it uses.  Called
+    with the tensors' device current."""
     if nbytes == 0:
         return contextlib.nullcontext((None, 0))
     if user is not None:
         if user.device != device:
             raise ValueError("workspace on another device")
         return contextlib.nullcontext((user, user.numel() * user.element_size()))
+    with torch.cuda.stream(stream) if stream is not None else _AS_IS:
+        if torch.cuda.is_current_stream_capturing():
+            return contextlib.nullcontext((torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes))
     key = (device.type, device.index, stream.cuda_stream if stream is not None else _raw_stream(device.index))
     with _ws_lock:
         slot = _ws_cache.get(key)

@@ -138,3 +138,42 @@ def test_failing_call_lets_the_next_one_in(fake):
     t.start()
     t.join(10)
     assert not t.is_alive()
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_not_cached_while_capturing(fake, monkeypatch, call):
+    """A call that is captured into a graph takes a buffer of its own from
+    the capture's memory: neither one that eager calls use, and may replace by
+    a larger one, nor one that another captured call has."""
+    seen = []
+    fake.inside = lambda name, ws: seen.append(ws)
+    call()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    call()
+    call()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    call()
+    assert seen[3] == seen[0] and len(set(seen[:3])) == 3
+
+
+def test_captured_call_on_a_given_stream(fake, monkeypatch):
+    """Whether to capture is a matter of the stream the call runs on."""
+    on = []
+
+    @contextlib.contextmanager
+    def stream(s):
+        on.append(s)
+        yield
+        on.pop()
+    side = type("Stream", (), {"cuda_stream": 9})()
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: on == [side])
+    dev = torch.device("cpu")
+    with mns._workspace(4096, dev, None, side) as (buf, n):
+        assert n == 4096
+    with mns._workspace(4096, dev, None) as (other, _):
+        assert other is not buf
+    with mns._workspace(4096, dev, None, side) as (again, _):
+        assert again is not buf and again is not other
+    with mns._workspace(4096, dev, None) as (last, _):
+        assert last is other
