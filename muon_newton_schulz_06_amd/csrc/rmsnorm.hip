@@ -19,6 +19,15 @@
 namespace muon {
 namespace {
 
+// Forward launches have a workgroup per row (or four rows): up to 2^24 of up to
+// 1024 threads, where a grid dimension holds less than 2^32 threads, so the
+// rows are spread over two dimensions.
+constexpr int64_t kRowGrid = int64_t(1) << 21;
+dim3 row_grid(int64_t blocks) {
+  return dim3(std::min(blocks, kRowGrid), (blocks + kRowGrid - 1) / kRowGrid);  // the last ones may have no row
+}
+__device__ __forceinline__ int64_t row_block() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Sum over the WAVES waves that share a row.  `slot` alternates between two
 // halves of red from row to row, so one barrier per row is enough.
 template <int WAVES>
@@ -72,7 +81,7 @@ template <typename T, bool VEC, int WAVES, int ITEMS>
 __global__ __launch_bounds__(WAVES == 1 ? 256 : 64 * WAVES) void norm_fwd(const NormFwdLaunch L) {
   constexpr int V = LType<T>::kVec, E = 16 / V, TPR = 64 * WAVES;
   __shared__ float red[2 * WAVES];
-  const int64_t t = WAVES == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
+  const int64_t t = WAVES == 1 ? row_block() * 4 + (threadIdx.x >> 6) : row_block();
   if (t >= L.tokens) return;  // whole waves; a shared row's waves leave together
   const int l = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
   const char* x = (const char*)L.x + t * L.ldx * E;
@@ -125,7 +134,8 @@ template <typename T, bool VEC>
 __global__ __launch_bounds__(1024) void norm_fwd_long(const NormFwdLaunch L) {
   constexpr int V = LType<T>::kVec, E = 16 / V;
   __shared__ float red[32];
-  const int64_t t = blockIdx.x;
+  const int64_t t = row_block();
+  if (t >= L.tokens) return;
   const char* x = (const char*)L.x + t * L.ldx * E;
   const char* r = L.res ? (const char*)L.res + t * L.ldr * E : nullptr;
   auto load = [&](int64_t e, float (&s)[V]) {
@@ -383,12 +393,12 @@ hipError_t fwd_launch(const NormFwdLaunch& L, hipStream_t st) {
   constexpr int V = LType<T>::kVec;
   const RowPlan p = plan_row((L.dim + V - 1) / V, V);
   if (!p.waves) {
-    hipLaunchKernelGGL((norm_fwd_long<T, VEC>), dim3(L.tokens), dim3(1024), 0, st, L);
+    hipLaunchKernelGGL((norm_fwd_long<T, VEC>), row_grid(L.tokens), dim3(1024), 0, st, L);
     return hipGetLastError();
   }
   with_plan<V>(p, [&](auto waves, auto items) {
     constexpr int W = decltype(waves)::value;
-    const dim3 grid(W == 1 ? (L.tokens + 3) / 4 : L.tokens), block(W == 1 ? 256 : 64 * W);
+    const dim3 grid = row_grid(W == 1 ? (L.tokens + 3) / 4 : L.tokens), block(W == 1 ? 256 : 64 * W);
     hipLaunchKernelGGL((norm_fwd<T, VEC, W, decltype(items)::value>), grid, block, 0, st, L);
   });
   return hipGetLastError();
