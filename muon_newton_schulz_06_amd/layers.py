@@ -10,6 +10,9 @@ modules with autograd on top of them:
     muon_rms_norm / muon_rms_norm_grad          RMSNorm
     muon_gated_ffn / muon_gated_ffn_grad        GatedFFN
 
+The functions record nothing for autograd (and drop tangents); the modules
+have a backward pass, and refuse forward-mode tangents.
+
 Tensors are float32 or bfloat16 on one CUDA/HIP device.  Leading dimensions
 are flattened to rows; the last dimension must have stride 1, rows may have
 any stride.  Work runs on the current stream, or on ``stream`` (outputs are
@@ -486,7 +489,9 @@ class _RMSNormFn(torch.autograd.Function):
 
 class _GatedFFNFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, w_down, activation):
+    def forward(ctx, x, w_gate, w_up, w_down, activation, save=True):
+        if not save:  # no backward pass will come
+            return muon_gated_ffn(x, w_gate, w_up, w_down, activation)
         y, saved = muon_gated_ffn(x, w_gate, w_up, w_down, activation, save=True)
         ctx.save_for_backward(x, w_gate, w_up, w_down, saved)
         return y
@@ -499,7 +504,7 @@ class _GatedFFNFn(torch.autograd.Function):
         need = ctx.needs_input_grad
         grads = muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx=need[0],
                                     want_dweights=any(need[1:4]))
-        return (*grads, None)
+        return (*grads, None, None)
 
 
 class Embedding(torch.nn.Module):
@@ -546,6 +551,8 @@ class GatedFFN(torch.nn.Module):
             torch.nn.init.normal_(w, std=1.0 / math.sqrt(w.shape[1]))
 
     def forward(self, x):
-        if torch.is_grad_enabled() and any(t.requires_grad for t in (x, *self.parameters())):
-            return _GatedFFNFn.apply(x, self.w_gate, self.w_up, self.w_down, self.activation)
-        return muon_gated_ffn(x, self.w_gate, self.w_up, self.w_down, self.activation)
+        w = (self.w_gate, self.w_up, self.w_down)
+        # always through the autograd function: it refuses forward-mode tangents,
+        # which the plain call would drop
+        return _GatedFFNFn.apply(x, *w, self.activation,
+                                 torch.is_grad_enabled() and any(t.requires_grad for t in (x, *w)))
