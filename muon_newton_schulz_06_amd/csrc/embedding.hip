@@ -94,6 +94,14 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t d, uint64_t in) {
   return m;
 }
 
+// Orders a wave's shared-memory accesses before it, of all lanes, ahead of
+// those after it.  No instruction: the LDS serves a wave in order.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // One stable counting pass over a workgroup's items, held in registers in
 // wave order: wave w's items are consecutive, ITEMS rounds of 64 lanes.
 // cnt[digit·WAVES + wave] must be zero on entry and holds the wave's digit
@@ -110,10 +118,11 @@ __device__ __forceinline__ void rank_items(const uint32_t (&key)[ITEMS], const b
     uint32_t* c = cnt + d * WAVES + wave;
     const uint32_t before = have[i] ? *c : 0u;
     rank[i] = before + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
-    // the last lane of each digit stores the new count; the LDS serves a
-    // wave's accesses in order, so the next round reads it
+    // every lane has read; the last lane of each digit stores the new count,
+    // which the next round reads
+    wave_order();
     if (have[i] && (m >> lane) == 1ull) *c = rank[i] + 1u;
-    __builtin_amdgcn_wave_barrier();
+    wave_order();
   }
 }
 
