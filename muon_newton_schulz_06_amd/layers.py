@@ -14,8 +14,9 @@ The functions record nothing for autograd (and drop tangents); the modules
 have a backward pass, and refuse forward-mode tangents.
 
 Tensors are float32 or bfloat16 on one CUDA/HIP device.  Leading dimensions
-are flattened to rows; the last dimension must have stride 1, rows may have
-any stride.  Work runs on the current stream, or on ``stream`` (outputs are
+are flattened to rows, which may have any stride; inputs whose rows are not
+contiguous (stride(-1) != 1), or overlap, are copied, weights and outputs may
+not have such rows.  Work runs on the current stream, or on ``stream`` (outputs are
 then allocated for that stream; the caller orders the inputs' writes before
 it).  A workspace is cached per device and stream unless one is passed.
 """
@@ -110,21 +111,42 @@ def _device(t, name):
     return t.device
 
 
-def _rows(t, name):
-    """(2-D view, row stride) of a tensor whose last dimension has stride 1;
-    the leading dimensions are flattened."""
-    if t.dim() != 2:
-        if t.dim() == 0:
-            raise ValueError(f"{name} must have at least one dimension")
-        t = t.reshape(-1, t.shape[-1]) if t.numel() else t.new_empty((math.prod(t.shape[:-1]), t.shape[-1]))
+def _flat(t, name):
+    """The tensor's rows, leading dimensions flattened."""
+    if t.dim() == 2:
+        return t
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    return t.reshape(-1, t.shape[-1]) if t.numel() else t.new_empty((math.prod(t.shape[:-1]), t.shape[-1]))
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor, None if its rows are not contiguous or
+    overlap."""
     rows, cols = t.shape
     s0, s1 = t.stride()
     if cols > 1 and s1 != 1 and rows > 0:
-        raise ValueError(f"{name}: rows must be contiguous (stride(-1) == 1)")
+        return None
     ld = s0 if rows > 1 else cols
-    if ld < cols:
-        raise ValueError(f"{name}: row stride smaller than the row length")
+    return ld if ld >= cols else None
+
+
+def _rows(t, name):
+    """(2-D view, row stride) of a weight or an output."""
+    t = _flat(t, name)
+    ld = _ld(t)
+    if ld is None:
+        raise ValueError(f"{name}: rows must be contiguous (stride(-1) == 1) and not overlap")
     return t, ld
+
+
+def _input(t, name):
+    """(2-D tensor, row stride) of an input: its view, or a copy where its
+    rows are not contiguous (a transposed or broadcast tensor, as autograd may
+    hand over)."""
+    t = _flat(t, name)
+    ld = _ld(t)
+    return (t, ld) if ld is not None else (t.contiguous(), t.shape[1])
 
 
 def _matrix(t, name, rows, cols):
@@ -237,7 +259,7 @@ def muon_embedding_grad(dy, ids, vocab: int, scale: float = 1.0, out=None, dtype
     vocab = int(vocab)
     with _on(dev, stream):
         ids, nb = _ids(ids)
-        d, ldy = _rows(dy, "dy")
+        d, ldy = _input(dy, "dy")
         if out is None:
             out = torch.empty((vocab, dim), dtype=dtype or dy.dtype, device=dev)
         ldo = _matrix(out, "out", vocab, dim)
@@ -271,8 +293,8 @@ def muon_rms_norm(x, weight, residual=None, eps: float = 1e-6, out=None, sum_out
     if sum_out is not None and residual is None:
         raise ValueError("sum_out needs residual")
     with _on(dev, stream):
-        x2, ldx = _rows(x, "x")
-        r2, ldr = _rows(residual, "residual") if residual is not None else (None, 0)
+        x2, ldx = _input(x, "x")
+        r2, ldr = _input(residual, "residual") if residual is not None else (None, 0)
         y = _out(out, x.shape, x.dtype, dev, "out")
         y2, ldy = _rows(y, "out")
         s, s2, lds = x, None, 0
@@ -305,9 +327,9 @@ def muon_rms_norm_grad(dy, s, weight, rstd, dsum=None, out=None, dweight=None, a
     if accumulate and dweight is None:
         raise ValueError("accumulate needs dweight")
     with _on(dev, stream):
-        dy2, ldy = _rows(dy, "dy")
-        s2, lds = _rows(s, "s")
-        d2, ldd = _rows(dsum, "dsum") if dsum is not None else (None, 0)
+        dy2, ldy = _input(dy, "dy")
+        s2, lds = _input(s, "s")
+        d2, ldd = _input(dsum, "dsum") if dsum is not None else (None, 0)
         tokens = dy2.shape[0]
         if rstd.numel() != tokens or not rstd.is_contiguous():
             raise ValueError(f"rstd must hold {tokens} contiguous values, got shape {tuple(rstd.shape)}")
@@ -336,7 +358,7 @@ def _ffn(x, w_gate, w_up, w_down, activation):
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"unknown activation {activation!r}; use one of {sorted(ACTIVATIONS)}")
-    x2, ldx = _rows(x, "x")
+    x2, ldx = _input(x, "x")
     tokens, model = x2.shape
     if w_gate.dim() != 2:
         raise ValueError(f"w_gate must be 2-D, got shape {tuple(w_gate.shape)}")
@@ -412,7 +434,7 @@ def muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx: bool = True
         raise ValueError("accumulate needs grads")
     with _on(dev, stream):
         f, x2, ldx = _ffn(x, w_gate, w_up, w_down, "silu")
-        dy2, ldy = _rows(dy, "dy")
+        dy2, ldy = _input(dy, "dy")
         dx, dx2, lddx = None, None, 0
         if want_dx:
             dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
@@ -443,16 +465,6 @@ def muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx: bool = True
 
 # ------------------------------------------------------------------ autograd
 
-def _as_rows(t):
-    """An incoming gradient as rows the kernels can read: autograd may hand
-    over broadcast or transposed views, which are copied."""
-    if t is None or t.is_contiguous():
-        return t
-    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
-        return t
-    return t.contiguous()
-
-
 class _EmbeddingFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, weight, scale):
@@ -464,7 +476,7 @@ class _EmbeddingFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         (ids,) = ctx.saved_tensors
-        return None, muon_embedding_grad(_as_rows(dy), ids, ctx.vocab, ctx.scale, dtype=ctx.dtype), None
+        return None, muon_embedding_grad(dy, ids, ctx.vocab, ctx.scale, dtype=ctx.dtype), None
 
 
 class _RMSNormFn(torch.autograd.Function):
@@ -482,7 +494,7 @@ class _RMSNormFn(torch.autograd.Function):
         s, weight, rstd = ctx.saved_tensors
         if dy is None:
             return dsum, None, dsum, None
-        dx, dw = muon_rms_norm_grad(_as_rows(dy), s, weight, rstd, dsum=_as_rows(dsum),
+        dx, dw = muon_rms_norm_grad(dy, s, weight, rstd, dsum=dsum,
                                     want_dweight=ctx.needs_input_grad[1])
         return dx, dw, dx if ctx.two else None, None
 
@@ -500,7 +512,6 @@ class _GatedFFNFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, w_gate, w_up, w_down, saved = ctx.saved_tensors
-        dy = _as_rows(dy)
         need = ctx.needs_input_grad
         grads = muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx=need[0],
                                     want_dweights=any(need[1:4]))
