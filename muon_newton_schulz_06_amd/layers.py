@@ -369,27 +369,37 @@ def _ffn(x, w_gate, w_up, w_down, activation):
     return f, x2, ldx
 
 
-def _ffn_size(tokens, model, hidden, dtype, grad):
+def _ffn_sizes(tokens, model, hidden, dtype, weights=None):
+    """The call's sizes alone; without weights as if those lay off every
+    alignment, which takes the most workspace."""
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
-    f = MuonFfn(int(tokens), int(model), int(hidden), None, None, None, 0, 0, 0, code, 0)
-    n = ctypes.c_size_t(0)
-    if grad is None:
-        _check(_lib().muon_gated_ffn_saved_size(ctypes.byref(f), ctypes.byref(n)))
-    else:
-        _check(_lib().muon_gated_ffn_workspace_size(ctypes.byref(f), int(grad), ctypes.byref(n)))
-    return n.value
+    tokens, model, hidden = int(tokens), int(model), int(hidden)
+    if weights is None:
+        return MuonFfn(tokens, model, hidden, 1, 1, 1, model, model, hidden, code, 0)
+    w_gate, w_up, w_down = weights
+    _same(w_gate.device, dtype, w_gate=w_gate, w_up=w_up, w_down=w_down)
+    return MuonFfn(tokens, model, hidden, _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                   _matrix(w_gate, "w_gate", hidden, model), _matrix(w_up, "w_up", hidden, model),
+                   _matrix(w_down, "w_down", model, hidden), code, 0)
 
 
 def gated_ffn_saved_size(tokens, model, hidden, dtype=torch.bfloat16) -> int:
     """Bytes muon_gated_ffn(save=True) keeps for the backward pass."""
-    return _ffn_size(tokens, model, hidden, dtype, None)
+    f, n = _ffn_sizes(tokens, model, hidden, dtype), ctypes.c_size_t(0)
+    _check(_lib().muon_gated_ffn_saved_size(ctypes.byref(f), ctypes.byref(n)))
+    return n.value
 
 
-def gated_ffn_workspace_size(tokens, model, hidden, dtype=torch.bfloat16, grad: bool = False) -> int:
-    """Workspace bytes of muon_gated_ffn, or of muon_gated_ffn_grad."""
-    return _ffn_size(tokens, model, hidden, dtype, bool(grad))
+def gated_ffn_workspace_size(tokens, model, hidden, dtype=torch.bfloat16, grad: bool = False,
+                             weights=None) -> int:
+    """Workspace bytes of muon_gated_ffn, or of muon_gated_ffn_grad: for the
+    given weights (w_gate, w_up, w_down), or enough for any.  bfloat16 weights
+    whose rows are not whole aligned 16-byte chunks need room for a copy."""
+    f, n = _ffn_sizes(tokens, model, hidden, dtype, weights), ctypes.c_size_t(0)
+    _check(_lib().muon_gated_ffn_workspace_size(ctypes.byref(f), int(bool(grad)), ctypes.byref(n)))
+    return n.value
 
 
 def muon_gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", save: bool = False, out=None,
