@@ -438,6 +438,8 @@ def muon_gated_ffn_grad(dy, x, w_gate, w_up, w_down, saved, want_dx: bool = True
     dev = _device(x, "x")
     _same(dev, x.dtype, dy=dy)
     _same(dev, torch.uint8, saved=saved)
+    if not saved.is_contiguous():
+        raise ValueError("saved must be contiguous, as muon_gated_ffn returned it")
     if dy.shape != x.shape:
         raise ValueError(f"dy has shape {tuple(dy.shape)}, x {tuple(x.shape)}")
     if accumulate and grads is None:

@@ -119,3 +119,11 @@ def test_outputs_and_weights_are_not_copied(fake, layout):
     with pytest.raises(ValueError):
         mns.muon_embedding(torch.zeros(2, dtype=torch.int64), bad)
     assert not fake.seen
+
+
+def test_saved_must_be_whole(fake):
+    """`saved` is read as the bytes that follow its address."""
+    x, w, wd = values(6, 8), values(10, 8), values(8, 10)
+    with pytest.raises(ValueError, match="saved"):
+        mns.muon_gated_ffn_grad(x, x, w, w, wd, torch.zeros(1024, dtype=torch.uint8)[::2])
+    assert not fake.seen
