@@ -20,10 +20,10 @@
  * Shared by every entry point:
  *   - matrices are row-major with rows of contiguous elements and a row
  *     stride `ld_*` ≥ the row length, in elements.  Any stride and any
- *     alignment of the element type is accepted; 16-byte aligned rows are
- *     read and written with 16-byte accesses, others element by element (or,
- *     for the bf16 feed-forward products, through one aligned copy in the
- *     workspace).
+ *     alignment of the element type is accepted.  Rows of whole aligned
+ *     16-byte chunks are the fast case; others take unaligned accesses and
+ *     single elements at a row's end (or, for the bf16 feed-forward products
+ *     of more than a few tokens, one aligned copy in the workspace).
  *   - dtype is MUON_DTYPE_F32 or MUON_DTYPE_BF16.  Arithmetic, sums and
  *     statistics are fp32; an output is rounded once, when it is stored.
  *   - sums run in a fixed order that depends on the sizes alone: equal calls
@@ -120,7 +120,8 @@ typedef struct muon_ffn {
  *   a = u·act'(g) and b = act(g) — float32 for MUON_DTYPE_F32; for
  *   MUON_DTYPE_BF16 the upper 24 bits of the float32 values (its whole range,
  *   errors below 2^-15 relative), since their products are rounded again.
- * g and u are never rounded before h; h is rounded to dtype. */
+ * g and u are never rounded before h; h, an operand of the next product, is
+ * rounded to dtype. */
 muon_status_t muon_gated_ffn(const muon_ffn_t* ffn, const void* x, int64_t ld_x, void* y,
                              int64_t ld_y, void* saved, size_t saved_bytes, void* workspace,
                              size_t workspace_bytes, void* stream);

@@ -8,9 +8,9 @@
 
 namespace muon {
 
-// e^x and 1/x: correctly rounded library forms for fp32 results, the hardware's
-// (relative errors of about 2^-22 over the range that matters, far below
-// bf16's 2^-9) for results that are rounded to 16 bits.
+// e^x and 1/x: the library's exponential and an IEEE division for fp32 results,
+// the hardware's (relative errors of about 2^-22 over the range that matters,
+// far below bf16's 2^-9) for results that are rounded to bf16.
 template <bool FULL> __device__ __forceinline__ float ffn_exp(float x) {
   return FULL ? expf(x) : __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
 }
@@ -92,7 +92,11 @@ __device__ __forceinline__ void ffn_part4(const FfnProb& P, int split, int64_t i
 }
 
 // FFN_GLU: h, and with SAVE a = u·act'(g) and b = act(g).  Rows of h and of
-// each half of ab have ldh elements, a multiple of 8.
+// each part of ab have ldh elements, a multiple of 8.
+// Of bf16 calls h, and dg and du below, are rounded to bf16: they are operands
+// of the next product's MFMA, which takes no wider type at its rate.  That and
+// the results' own rounding are 1.65e-3 each (2-norm, against fp64), 2.3e-3
+// together; a and b, kept in 24 bits, add nothing to it.
 template <typename T, int ACT, bool SAVE>
 __device__ __forceinline__ void ffn_glu4(const FfnLaunch& L, const FfnProb& P, int64_t i, int64_t j,
                                          const float (&g)[4], const float (&u)[4]) {

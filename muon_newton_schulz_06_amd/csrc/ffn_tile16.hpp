@@ -17,8 +17,8 @@
 //    meet in one lane and the activation runs on fp32 registers.
 // Bound by the matrix pipe at the power-limited clock (1.9–2.0 GHz, MFMA busy
 // 49–62%): 0.77 µs per k-tile of a 256-tile on every CU.  At 4096 tokens,
-// 3584×18944: gated projections with a, b 1060 µs (1050 TFLOP/s), dh 555 (1000),
-// dx 870 (1280), weight gradients 1310 (1270), y 484 (1150).  The 128-tile takes
+// 3584×18944: gated projections with a, b 1087 µs (1020 TFLOP/s), dh 560 (990),
+// dx 888 (1250), weight gradients 1310 (1270), y 490 (1130).  The 128-tile takes
 // 0.62 µs per k-tile and pair of workgroups on a CU, which wins where 256-tiles
 // would leave CUs idle (see the time estimate on the host).
 // Operands need 16-byte aligned rows of whole 16-byte chunks; the host copies
@@ -244,7 +244,8 @@ __global__ __launch_bounds__(TILE * 2, 2) void ffn_tile16(const FfnLaunch L) {
   };
   static_assert(NQ % 2 == 0, "the last quarter's fragments are in fay");
   if (n > 0) {
-    // loads past this split's k-tiles are zeros that no MFMA reads
+    // loads past this split's k-tiles, the next split's or zeros past the last
+    // k, are never read
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) issue(i * kSlot, kt0 + i);
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"((SLOTS - 1) * (NA + NB)) : "memory");

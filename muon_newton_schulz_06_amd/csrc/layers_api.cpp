@@ -235,7 +235,9 @@ bool few_tokens(bool bf16, int64_t T, int64_t weights) {
 }
 
 // The few-token kernel: about 1024 workgroups of 16 weight rows, each split at
-// least one step (4 waves × 4 loads of 32 k) long.
+// least 16 k-tiles long: a step of four waves × four loads.  With one block of
+// tokens a wave takes eight loads, so that a split of 16 k-tiles leaves two of
+// its waves without work (measured with this step length only).
 TilePlan plan_few(int64_t N, int64_t K) {
   constexpr int64_t step = 16;  // k-tiles
   const int64_t KT = tiles_of(K, 32), want = std::max<int64_t>(1, tiles_of(1024, tiles_of(N, 16)));

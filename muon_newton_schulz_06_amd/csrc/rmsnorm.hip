@@ -8,7 +8,8 @@
 // the rows of a workgroup, written once per workgroup, and the workgroups'
 // rows are added in workgroup order by a second kernel (no atomics).
 // Both are HBM-bound: 16384 × 3584 bf16 with residual forward 88 µs (5.3 TB/s),
-// backward 89 + 5 µs (5.0 TB/s).
+// backward 89 + 5 µs (5.0 TB/s).  Rows of more than 8192 elements are not, in
+// the backward pass (see plan_row).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -363,8 +364,14 @@ struct RowPlan {
 };
 
 // The fewest waves per row that leave a thread at most 16 elements (which
-// keeps several workgroups on a CU); rows above 16 waves × 16 elements take
-// more elements per thread, up to 8 chunks.
+// keeps several workgroups on a CU); rows that 16 waves do not hold so take more
+// per thread, up to 8 chunks.  The forward pass keeps its rate there (4096 rows
+// with residual: 8192 bf16 47 µs, 5.7 TB/s; 16384 104, 5.2; 32768 209, 5.1).  The
+// backward pass does not: a lane of 16 waves has 128 registers, and from two
+// chunks of bf16 or four of fp32 on (above 8192 elements) two rows, the weights
+// and the column sums spill to scratch memory (4096 rows with dsum: 8192 bf16 64
+// µs, 4.2 TB/s; 12288 133, 3.0; 16384 157, 3.4; 32768 926, 1.2; fp32 8192 110,
+// 4.9; 16384 439, 2.4; 32768 1764, 1.2).
 RowPlan plan_row(int64_t chunks, int V) {
   for (int waves = 1; waves <= 16; waves *= 4)
     for (int items = 1; items <= (waves == 16 ? 8 : 16 / V); items *= 2)
