@@ -549,6 +549,8 @@ from .optim import Muon  # noqa: E402  (torch.optim front end)
 
 from . import layers  # noqa: E402  (embedding, RMS norm, gated FFN)
 from .layers import *  # noqa: E402,F401,F403
+from . import attention  # noqa: E402  (rotary positions, differential attention, dropout)
+from .attention import *  # noqa: E402,F401,F403
 
 __all__.append("Muon")
-__all__ += ["layers", *layers.__all__]
+__all__ += ["layers", *layers.__all__, "attention", *attention.__all__]

@@ -1,0 +1,380 @@
+// Differential attention, forward: with S_m = scale·Q_m·K_mᵀ for the two maps
+// of a head, P_m = softmax(S_m) over the keys a row sees,
+//   out = (P_1 − λ·P_2)·V = P_1·V − λ·(P_2·V).
+//
+// One pass over the keys with each map's running maximum and sum: the two
+// products P_m·V are accumulated apart, since A = P_1 − λ·P_2 needs the final
+// sums.  (Two passes, the first for the sums alone, would take as many
+// products and twice the exponentials.)
+//
+// A wave has one map of 32·RS rows; RG groups of rows times two maps make a
+// workgroup, whose waves share the tiles of K_1, K_2 and V in LDS (two
+// buffers, loaded without passing through registers).  It forms the transposed
+// scores K·Qᵀ, so that a lane holds scores of one row only: the maximum and
+// sum run within the lane and one exchange between its two halves, and the
+// probabilities are the next product's operand as they lie (Vᵀ·Pᵀ).  At the
+// end the second map's wave hands λ·P_2·V over through LDS.
+//
+// Rounding: scores, maxima, sums and results are fp32; for bf16 tensors the
+// probabilities, relative to a maximum that lags by at most 2^8, are rounded
+// to bf16 as operands of the second product (their sum is of the unrounded).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "attention.hpp"
+#include "attn_tile.hpp"
+
+namespace muon {
+namespace {
+
+// Row blocks and tiles of a kernel: RS·32 rows per wave, RG groups of waves,
+// BN keys per tile.
+template <typename T, int DP, bool FEW> struct Fwd {
+  static constexpr int kRS = !FEW && AT<T>::kBytes == 2 && DP == 64 ? 2 : 1;
+  static constexpr int kRG = FEW ? 1 : 2;
+  static constexpr int kBM = 32 * kRS * kRG;
+  static constexpr int kWaves = 2 * kRG, kThreads = 64 * kWaves;
+  static constexpr int kBN = AT<T>::kBytes == 2 && DP == 64 ? 64 : 32;
+  static constexpr int kK = DP * AT<T>::kBytes, kV = 2 * kK;  // bytes of a row
+  static constexpr int kStage = kBN * (2 * kK + kV);
+};
+
+template <typename T, int DP, bool FEW>
+__global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const AttnFwdLaunch L) {
+  using F = Fwd<T, DP, FEW>;
+  constexpr int RS = F::kRS, BN = F::kBN, E = AT<T>::kBytes;
+  constexpr int NC = DP / AT<T>::kStep;   // steps over a head's values
+  constexpr int NV = 2 * DP / 32;         // 32-column groups of V
+  constexpr int SP = AT<T>::kSteps32;     // steps over 32 keys
+  __shared__ __attribute__((aligned(1024))) char lds[2 * F::kStage];
+
+  const AttnShape& S = L.s;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int map = wave & 1, rg = wave >> 1;
+
+  // this workgroup's combo, rows and split
+  int id = blockIdx.x;
+  const int combo = id % S.combos;
+  id /= S.combos;
+  const int split = id % L.splits;
+  id /= L.splits;
+  int tok0 = 0, nq = (int)S.nq, nk = (int)S.nk, at = 0;
+  if (L.list.blocks) {
+    const int n = *L.list.count;
+    if (id >= n) return;
+    const AttnBlock B = L.list.blocks[n - 1 - id];
+    tok0 = B.tok;
+    nq = B.n;
+    nk = B.nk;
+    at = B.at;
+  } else {  // the rows that see most keys first
+    at = (L.rowBlocks - 1 - id) * F::kBM;
+  }
+  const int batch = combo / S.kv, hk = combo % S.kv, G = S.group;
+  const int rows = nq * G;  // of this sequence
+  const int shift = nk - nq + 1;
+
+  // each lane's rows: their token and head, and how many keys they see
+  int64_t qoff[RS];
+  int lim[RS], head[RS];
+  bool valid[RS];
+  int tok[RS];
+#pragma unroll
+  for (int r = 0; r < RS; ++r) {
+    const int row = at + (rg * RS + r) * 32 + (lane & 31);
+    valid[r] = row < rows;
+    tok[r] = row / G;
+    const int g = row - tok[r] * G;
+    head[r] = hk * G + g;
+    lim[r] = !valid[r] ? 0 : S.causal ? min(max(tok[r] + shift, 0), nk) : nk;
+    tok[r] += tok0;
+    qoff[r] = batch * S.qs[0] + tok[r] * S.qs[1] + (2 * head[r] + map) * S.qs[2];
+  }
+  // keys any row of the workgroup sees, and those all of them see
+  const int last = min(at + F::kBM, rows) - 1;
+  const int most = S.causal ? min(max(last / G + shift, 0), nk) : nk;
+  const int least = S.causal ? min(max(at / G + shift, 0), nk) : nk;
+  int kBegin = 0, kEnd = most;
+  if (L.splits > 1) {
+    kBegin = split * L.splitKeys;
+    kEnd = min(most, kBegin + L.splitKeys);
+  }
+
+  lu32x4 q[RS][NC];
+#pragma unroll
+  for (int r = 0; r < RS; ++r)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      q[r][c] = lu32x4{0, 0, 0, 0};
+      if (valid[r] && (2 * c + half) * 16 < S.dim * E)
+        q[r][c] = *(const lu32x4*)((const char*)S.q + qoff[r] * E + (2 * c + half) * 16);
+    }
+
+  TileLoader<F::kK, BN, F::kWaves> ldk;
+  TileLoader<F::kV, BN, F::kWaves> ldv;
+  ldk.init(lane, wave, S.ks[1] * E, S.dim * E);
+  ldv.init(lane, wave, S.vs[1] * E, 2 * S.dim * E);
+  const char* k1 = (const char*)S.k + (batch * S.ks[0] + tok0 * S.ks[1] + 2 * hk * S.ks[2]) * E;
+  const char* v0 = (const char*)S.v + (batch * S.vs[0] + tok0 * S.vs[1] + hk * S.vs[2]) * E;
+  const uint32_t base = a_lds(lds);
+  auto issue = [&](int key, uint32_t buf) __attribute__((always_inline)) {
+    const char* k = k1 + (int64_t)key * S.ks[1] * E;
+    ldk.issue(k, nk - key, buf);
+    ldk.issue(k + S.ks[2] * E, nk - key, buf + BN * F::kK);
+    ldv.issue(v0 + (int64_t)key * S.vs[1] * E, nk - key, buf + 2 * BN * F::kK);
+  };
+  const RowReader<F::kK> rd(lane);
+  const ColReader<T, F::kV> cd(lane);
+
+  af32x16 o[RS][NV];
+  float m[RS], l[RS];
+#pragma unroll
+  for (int r = 0; r < RS; ++r) {
+    m[r] = kNegInf;
+    l[r] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) o[r][n] = af32x16{};
+  }
+
+  // 32 keys of a tile
+  auto step = [&](uint32_t kt, uint32_t vt, int key, bool masked) __attribute__((always_inline)) {
+    af32x16 s[RS];
+#pragma unroll
+    for (int r = 0; r < RS; ++r) s[r] = af32x16{};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const lu32x4 a = rd.get(kt, c);
+#pragma unroll
+      for (int r = 0; r < RS; ++r) s[r] = a_mma<T>(a, q[r][c], s[r]);
+    }
+    lu32x4 p[RS][SP];
+#pragma unroll
+    for (int r = 0; r < RS; ++r) {
+      if (masked) {
+        const int n = lim[r] - key - 4 * half;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[r][i] = 8 * (i >> 2) + (i & 3) < n ? s[r][i] : kNegInf;
+      }
+      float mx = fmaxf(s[r][0], s[r][1]);
+#pragma unroll
+      for (int i = 2; i < 16; ++i) mx = fmaxf(mx, s[r][i]);
+      mx = a_half_max(mx) * S.c;
+      // the maximum that the exponents refer to lags behind the true one by at
+      // most 8: the results are rescaled seldom
+      if (__any(mx > m[r] + 8.f)) {
+        const float mn = fmaxf(m[r], mx);
+        const float f = mn == kNegInf ? 1.f : a_exp2(m[r] - mn);
+        m[r] = mn;
+        l[r] *= f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[r][n][i] *= f;
+      }
+      const float mu = m[r] == kNegInf ? 0.f : m[r];
+      float e[16], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        e[i] = a_exp2(s[r][i] * S.c - mu);
+        sum += e[i];
+      }
+      l[r] += sum;
+#pragma unroll
+      for (int t = 0; t < SP; ++t) p[r][t] = a_operand<T>(e, t);
+    }
+#pragma unroll
+    for (int t = 0; t < SP; ++t)
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const lu32x4 a = cd.get(vt + t * AT<T>::kStep * F::kV, n);
+#pragma unroll
+        for (int r = 0; r < RS; ++r) o[r][n] = a_mma<T>(a, p[r][t], o[r][n]);
+      }
+  };
+
+  if (kBegin < kEnd) issue(kBegin, base);
+  uint32_t buf = base;
+  for (int key = kBegin; key < kEnd; key += BN) {
+    a_landed();  // this tile; the other buffer is free
+    const uint32_t other = 2 * base + F::kStage - buf;
+    if (key + BN < kEnd) issue(key + BN, other);
+#pragma unroll
+    for (int j = 0; j < BN; j += 32) {
+      if (key + j >= kEnd) break;
+      const uint32_t kt = buf + map * (BN * F::kK) + j * F::kK, vt = buf + 2 * BN * F::kK + j * F::kV;
+      step(kt, vt, key + j, key + j + 32 > least);
+    }
+    buf = other;
+  }
+  __syncthreads();
+
+#pragma unroll
+  for (int r = 0; r < RS; ++r) {
+    l[r] = a_half_sum(l[r]);
+    const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;  // a row that sees no key: zeros
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[r][n][i] *= inv;
+  }
+  if (L.splits > 1) {
+#pragma unroll
+    for (int r = 0; r < RS; ++r) {
+      if (!valid[r]) continue;
+      const int64_t row = (int64_t)(tok[r]) * G + head[r] - hk * G;
+      const int64_t slot = (((int64_t)split * S.combos + combo) * (S.nq * G) + row) * 2 + map;
+      if (half == 0) L.partStat[slot] = l[r] == 0.f ? kNegInf : m[r] + a_log2(l[r]);
+      float* d = L.part + slot * (2 * DP);
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *(lf32x4*)(d + n * 32 + 8 * g + 4 * half) =
+              lf32x4{o[r][n][4 * g], o[r][n][4 * g + 1], o[r][n][4 * g + 2], o[r][n][4 * g + 3]};
+    }
+    return;
+  }
+
+  // the second map's results pass to the wave of the first, λ times, register
+  // by register
+  constexpr int kWaveX = RS * NV * 4 * 1024;
+  static_assert(F::kRG * kWaveX <= 2 * F::kStage, "exchange fits");
+  lf32x4* x = (lf32x4*)(lds + rg * kWaveX) + lane;
+#pragma unroll
+  for (int r = 0; r < RS; ++r) {
+    const int64_t row = (int64_t)tok[r] * G + head[r] - hk * G, rowsAll = S.nq * G;
+    if (S.stat && half == 0 && valid[r])  // a row that sees no key: +∞, so that its probabilities are 0
+      S.stat[((int64_t)combo * 2 + map) * rowsAll + row] = l[r] == 0.f ? -kNegInf : m[r] + a_log2(l[r]);
+    if (map == 1) {
+      const float lam = valid[r] ? S.lam[head[r]] : 0.f;
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = o[r][n][i];
+        if (S.o2)
+          a_store_row<T>((char*)S.o2 + ((int64_t)combo * rowsAll + row) * S.pitch * E, v, n * 32, 2 * S.dim,
+                         true, valid[r], half);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          x[((r * NV + n) * 4 + g) * 64] = lf32x4{v[4 * g] * lam, v[4 * g + 1] * lam, v[4 * g + 2] * lam, v[4 * g + 3] * lam};
+      }
+    }
+  }
+  __syncthreads();
+  if (map == 1) return;
+#pragma unroll
+  for (int r = 0; r < RS; ++r) {
+    char* d = (char*)L.out + (batch * L.os[0] + tok[r] * L.os[1] + head[r] * L.os[2]) * E;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      float v[16];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const lf32x4 y = x[((r * NV + n) * 4 + g) * 64];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * g + i] = o[r][n][4 * g + i] - y[i];
+      }
+      a_store_row<T>(d, v, n * 32, 2 * S.dim, L.vec, valid[r], half);
+    }
+  }
+}
+
+// The splits' results of a row joined, a wave per row: weights from the
+// logarithms of their sums, in split order.
+template <typename T, int DP> __global__ __launch_bounds__(256) void attn_join(const AttnFwdLaunch L) {
+  constexpr int E = AT<T>::kBytes, PER = 2 * DP / 64;
+  const AttnShape& S = L.s;
+  const int lane = threadIdx.x & 63;
+  const int64_t rows = S.nq * S.group, all = rows * S.combos;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (id >= all) return;
+  const int combo = (int)(id / rows);
+  const int64_t row = id - combo * rows;
+  const int64_t tok = row / S.group;
+  const int batch = combo / S.kv, head = (combo % S.kv) * S.group + (int)(row - tok * S.group);
+  float res[2][PER], top[2], sum[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    top[m] = kNegInf;
+    for (int s = lane; s < L.splits; s += 64) {
+      const float v = L.partStat[(s * all + id) * 2 + m];
+      top[m] = v != v || v > top[m] ? v : top[m];
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const float v = __shfl_xor(top[m], o, 64);
+      top[m] = v != v || v > top[m] ? v : top[m];
+    }
+    sum[m] = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) res[m][i] = 0.f;
+  }
+  for (int s = 0; s < L.splits; ++s) {
+    const float* d = L.part + (s * all + id) * (4 * DP) + lane * PER;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const float v = L.partStat[(s * all + id) * 2 + m];
+      if (v == kNegInf) continue;
+      const float w = a_exp2(v - top[m]);
+      sum[m] += w;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) res[m][i] += w * d[m * 2 * DP + i];
+    }
+  }
+  const float lam = S.lam[head];
+  char* o = (char*)L.out + (batch * L.os[0] + tok * L.os[1] + head * L.os[2]) * E;
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const float inv = top[m] == kNegInf ? 0.f : 1.f / sum[m];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) res[m][i] *= inv;
+    if (S.stat && lane == 0)
+      S.stat[((int64_t)combo * 2 + m) * rows + row] = top[m] == kNegInf ? -kNegInf : top[m] + a_log2(sum[m]);
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = lane * PER + i;
+    if (c >= 2 * S.dim) continue;
+    LType<T>::put(o, c, res[0][i] - lam * res[1][i]);
+    if (S.o2) LType<T>::put((char*)S.o2 + (id * S.pitch) * E, c, res[1][i]);
+  }
+}
+
+template <typename T, int DP, bool FEW> hipError_t run(const AttnFwdLaunch& L, hipStream_t st) {
+  attn_fwd<T, DP, FEW><<<dim3((unsigned)(L.s.combos * L.rowBlocks * L.splits)), Fwd<T, DP, FEW>::kThreads, 0, st>>>(L);
+  return hipGetLastError();
+}
+template <typename T, int DP> hipError_t join(const AttnFwdLaunch& L, hipStream_t st) {
+  const int64_t rows = L.s.nq * L.s.group * L.s.combos;
+  attn_join<T, DP><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, st>>>(L);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int attn_fwd_rows(bool bf16, int dp, bool few) { return few ? 32 : bf16 && dp == 64 ? 128 : 64; }
+int attn_fwd_keys(bool bf16, int dp) { return bf16 && dp == 64 ? 64 : 32; }
+static_assert(Fwd<Bf16, 64, false>::kBM == 128 && Fwd<Bf16, 128, false>::kBM == 64 && Fwd<float, 64, false>::kBM == 64 &&
+                  Fwd<float, 128, false>::kBM == 64 && Fwd<float, 128, true>::kBM == 32 && Fwd<Bf16, 64, true>::kBM == 32,
+              "attn_fwd_rows");
+static_assert(Fwd<Bf16, 64, false>::kBN == 64 && Fwd<Bf16, 128, false>::kBN == 32 && Fwd<float, 64, true>::kBN == 32,
+              "attn_fwd_keys");
+
+hipError_t launch_attn_fwd(bool bf16, int dp, bool few, const AttnFwdLaunch& L, hipStream_t st) {
+  if (bf16) {
+    if (dp == 64) return few ? run<Bf16, 64, true>(L, st) : run<Bf16, 64, false>(L, st);
+    return few ? run<Bf16, 128, true>(L, st) : run<Bf16, 128, false>(L, st);
+  }
+  if (dp == 64) return few ? run<float, 64, true>(L, st) : run<float, 64, false>(L, st);
+  return few ? run<float, 128, true>(L, st) : run<float, 128, false>(L, st);
+}
+
+hipError_t launch_attn_join(bool bf16, int dp, const AttnFwdLaunch& L, hipStream_t st) {
+  if (bf16) return dp == 64 ? join<Bf16, 64>(L, st) : join<Bf16, 128>(L, st);
+  return dp == 64 ? join<float, 64>(L, st) : join<float, 128>(L, st);
+}
+
+}  // namespace muon

@@ -1,0 +1,112 @@
+// What precedes the attention products: a packed batch's block lists, and
+// aligned copies of tensors that the 16-byte loads into LDS cannot read.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "attention.hpp"
+#include "attn_tile.hpp"
+
+namespace muon {
+namespace {
+
+constexpr int kPrep = 1024;
+
+// Inclusive scan over the workgroup; f combines, `id` is neutral.
+template <typename F> __device__ __forceinline__ int64_t scan(int64_t v, int64_t* red, F f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t u = __shfl_up(v, o, 64);
+    if (lane >= o) v = f(v, u);
+  }
+  if (lane == 63) red[wave] = v;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) v = f(v, red[w]);
+  __syncthreads();
+  return v;
+}
+
+// The block lists of a packed batch, one workgroup per list.  The spans are the
+// rows before the first offset, each sequence, and the rows after the last one;
+// the first and last of these have no keys.  Offsets are cut to [0, tokens] and
+// one below its predecessor is raised to it, so whatever they hold, every row
+// belongs to exactly one span.
+__global__ __launch_bounds__(kPrep) void attn_prep(const AttnPrepLaunch L) {
+  __shared__ int64_t red[kPrep / 64];
+  __shared__ int begin[kPrep], size[kPrep], first[kPrep];  // a chunk of spans: tokens, blocks before
+  const auto& D = L.list[blockIdx.x];
+  const int tid = threadIdx.x, spans = L.sequences + 2;
+  auto larger = [](int64_t a, int64_t b) { return a > b ? a : b; };
+  auto sum = [](int64_t a, int64_t b) { return a + b; };
+  int64_t edge = 0;  // where the chunk's first span begins
+  int done = 0;      // blocks of the chunks before
+  for (int s0 = 0; s0 < spans; s0 += kPrep) {
+    const int s = s0 + tid;
+    int64_t end = L.tokens;  // of span s
+    if (s <= L.sequences) end = min(max(L.offsets[s], 0), L.tokens);
+    end = scan(larger(end, edge), red, larger);
+    size[tid] = (int)end;  // for the neighbour
+    __syncthreads();
+    const int64_t start = tid ? size[tid - 1] : edge;
+    edge = size[kPrep - 1];
+    __syncthreads();
+    const int64_t n = s < spans ? end - start : 0;
+    const int blocks = (int)((n * D.units + D.per - 1) / D.per);
+    const int upto = (int)scan(blocks, red, sum);
+    begin[tid] = (int)start;
+    size[tid] = (int)n;
+    first[tid] = upto - blocks;
+    __syncthreads();
+    const int total = first[kPrep - 1] + (int)((size[kPrep - 1] * (int64_t)D.units + D.per - 1) / D.per);
+    for (int b = tid; b < total; b += kPrep) {
+      int lo = 0, hi = kPrep - 1;  // the last span whose blocks begin at or before b
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (first[mid] <= b) lo = mid;
+        else hi = mid - 1;
+      }
+      const bool inside = s0 + lo > 0 && s0 + lo <= L.sequences;
+      D.blocks[done + b] = AttnBlock{begin[lo], size[lo], inside ? size[lo] : 0, (b - first[lo]) * D.per};
+    }
+    done += total;
+    __syncthreads();
+  }
+  if (tid == 0) *D.count = done;
+}
+
+// One workgroup per 256 chunks of a tensor's copy; the pitch's end holds zeros.
+template <typename T> __global__ __launch_bounds__(256) void attn_copy(const AttnCopies K) {
+  constexpr int V = LType<T>::kVec, E = AT<T>::kBytes;
+  const AttnCopy& C = K.c[blockIdx.y];
+  const int per = C.pitch / V;
+  const int64_t n = C.batch * C.tokens * C.heads * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    int64_t r = i / per;
+    const int e = (int)(i - r * per) * V;
+    const int h = (int)(r % C.heads);
+    r /= C.heads;
+    const int64_t b = r / C.tokens, t = r - b * C.tokens;
+    const char* src = (const char*)C.src + (b * C.s[0] + t * C.s[1] + h * C.s[2]) * E;
+    ((lu32x4*)C.dst)[i] = l_load<T, false>(src, e, C.dim);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attn_prep(const AttnPrepLaunch& L, hipStream_t st) {
+  attn_prep<<<dim3(L.lists), kPrep, 0, st>>>(L);
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_copy(bool bf16, const AttnCopies& K, hipStream_t st) {
+  int64_t most = 1;
+  for (int i = 0; i < K.n; ++i)
+    most = std::max(most, K.c[i].batch * K.c[i].tokens * K.c[i].heads * K.c[i].pitch / (bf16 ? 8 : 4));
+  const dim3 grid((unsigned)std::min<int64_t>((most + 255) / 256, 1 << 16), K.n);
+  if (bf16) attn_copy<Bf16><<<grid, 256, 0, st>>>(K);
+  else attn_copy<float><<<grid, 256, 0, st>>>(K);
+  return hipGetLastError();
+}
+
+}  // namespace muon

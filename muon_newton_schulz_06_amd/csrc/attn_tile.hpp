@@ -1,0 +1,198 @@
+// Tiles of the attention kernels: 32×32 MFMA products whose operands lie in
+// LDS rows or come from the result of another product.
+//
+// Results of a 32×32 product: lane l holds column l % 32, rows
+// 8·(i / 4) + 4·(l / 32) + i % 4 in its 16 registers.  An operand gives lane l
+// the 16 bytes of row l % 32 that its half l / 32 is due at a step of the
+// contraction: 8 bf16 (a step is 16 long) or 4 fp32 (8 long, four products of
+// 2).  Which of the step's indexes a half holds is free as long as both
+// operands agree, so a result's registers serve as the next product's operand
+// as they are, its rows being the contraction: a step takes rows
+// 16·s + 4·half + {0…3, 8…11} (bf16) or 8·s + 4·half + {0…3} (fp32).
+#pragma once
+
+#include "dma.hpp"
+#include "layers.hpp"
+
+namespace muon {
+
+typedef float af32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 abf16x8 __attribute__((ext_vector_type(8)));
+typedef short as16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) as16x4* a_lds_s4;
+typedef __attribute__((address_space(3))) const lu32x4* a_lds_u4;
+typedef __attribute__((address_space(3))) const uint32_t* a_lds_u1;
+
+template <typename T> struct AT {
+  static constexpr int kBytes = 16 / LType<T>::kVec;
+  static constexpr int kStep = 2 * LType<T>::kVec;  // contraction of a step
+  static constexpr int kSteps32 = 32 / kStep;       // steps over the rows of a result
+};
+
+__device__ __forceinline__ uint32_t a_lds(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+
+template <typename T> __device__ __forceinline__ af32x16 a_mma(lu32x4 a, lu32x4 b, af32x16 c) {
+  if constexpr (AT<T>::kBytes == 2) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(abf16x8, a), __builtin_bit_cast(abf16x8, b), c,
+                                                   0, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
+    return c;
+  }
+}
+
+// Step s of a result as an operand.
+template <typename T> __device__ __forceinline__ lu32x4 a_operand(const float (&p)[16], int s) {
+  lu32x4 r;
+  if constexpr (AT<T>::kBytes == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = l_f32_bf16x2(p[8 * s + 2 * i], p[8 * s + 2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(p[4 * s + i]);
+  }
+  return r;
+}
+
+// LDS tiles of rows of RB bytes; 16-byte chunk c of row r lies at c ^ a_swz(r).
+// Row reads take the same chunk of 32 rows: eight consecutive rows differ in
+// the chunk's low three bits.  Column reads take 64 (bf16) bytes of four
+// consecutive rows: those differ in which 64 bytes of 256 they fall into.
+template <int RB> __device__ __forceinline__ int a_swz(int r) {
+  if constexpr (RB == 128) return (r >> 1 & 1) << 2 | (r & 1) << 1 | (r >> 2 & 1);
+  else return (r & 1) << 2 | (r >> 1 & 1) * 10 | (r >> 2 & 1);
+}
+
+// A lane's reads of row operands: rows 32·n + lane % 32, step c.
+template <int RB> struct RowReader {
+  uint32_t at;
+  __device__ __forceinline__ RowReader(int lane) {
+    const int r = lane & 31;
+    at = r * RB + (((lane >> 5) ^ a_swz<RB>(r)) << 4);
+  }
+  // tile: LDS address of row 32·n (a multiple of RB); c a constant
+  __device__ __forceinline__ lu32x4 get(uint32_t tile, int c) const {
+    return *(a_lds_u4)(uintptr_t)((at ^ (c << 5)) + tile);
+  }
+};
+
+// A lane's reads of column operands: columns 32·n + lane % 32, the step's rows.
+template <typename T, int RB> struct ColReader {
+  uint32_t at;
+  __device__ __forceinline__ ColReader(int lane) {
+    if constexpr (AT<T>::kBytes == 2) {
+      // transposing reads: 16 lanes point at four rows of four values each and
+      // receive one column each
+      const int j = lane & 15, r = 4 * (lane >> 5) + (j >> 2);
+      at = r * RB + (((2 * (lane >> 4 & 1) + (j >> 1 & 1)) ^ a_swz<RB>(r)) << 4) + (j & 1) * 8;
+    } else {
+      // rows 8·s + 4·half + i: i's part of the address follows in get
+      const int r = 4 * (lane >> 5);
+      at = r * RB + ((((lane & 31) >> 2) ^ a_swz<RB>(r)) << 4) + (lane & 3) * 4;
+    }
+  }
+  // tile: LDS address of the step's first row; n a constant
+  __device__ __forceinline__ lu32x4 get(uint32_t tile, int n) const {
+    if constexpr (AT<T>::kBytes == 2) {
+      const uint32_t a = (at ^ (n << 6)) + tile;
+      const as16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((a_lds_s4)(uintptr_t)a);
+      const as16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((a_lds_s4)(uintptr_t)(a + 8 * RB));
+      return __builtin_bit_cast(lu32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      lu32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = *(a_lds_u1)(uintptr_t)((at ^ (n << 7) ^ (a_swz<RB>(i) << 4)) + i * RB + tile);
+      return v;
+    }
+  }
+};
+
+// Copies a tile of ROWS rows of RB bytes into LDS with 16-byte buffer loads of
+// NW waves; rows past `left` and bytes past `bytes` of a row arrive as zeros.
+template <int RB, int ROWS, int NW> struct TileLoader {
+  static constexpr int kChunks = RB / 16, kRowsPer = 64 / kChunks, N = ROWS / (kRowsPer * NW);
+  static_assert(N * kRowsPer * NW == ROWS, "whole loads");
+  uint32_t off[N];
+  int row0, wave;
+  __device__ __forceinline__ void init(int lane, int w, int64_t ldBytes, int bytes) {
+    wave = w;
+    row0 = w * N * kRowsPer + lane / kChunks;
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+      const int r = row0 + p * kRowsPer, c = (lane % kChunks) ^ a_swz<RB>(r);
+      off[p] = c * 16 < bytes ? (uint32_t)(r * ldBytes) + c * 16 : kFfnNowhere;
+    }
+  }
+  __device__ __forceinline__ void issue(const char* base, int64_t left, uint32_t dst) const {
+    const fi32x4 buf = f_buffer((uint64_t)base);
+#pragma unroll
+    for (int p = 0; p < N; ++p)
+      f_dma16(__builtin_amdgcn_readfirstlane(dst + (wave * N + p) * 1024),
+              row0 + p * kRowsPer < left ? off[p] : kFfnNowhere, buf);
+  }
+};
+
+// Every load into LDS has landed and every wave is here.
+__device__ __forceinline__ void a_landed() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The value and its counterpart of the lane 32 further on (or back).
+__device__ __forceinline__ float a_half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float a_half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float a_exp2(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ __forceinline__ float a_log2(float v) { return __builtin_amdgcn_logf(v); }
+
+constexpr float kNegInf = -__builtin_inff();
+
+// Values of one row and the 32 columns of a result's transpose (lane: row
+// l % 32, registers: columns 8·(i / 4) + 4·half + i % 4) as stores of four,
+// or, for bf16 with 16-byte stores, of eight columns.
+template <typename T> __device__ __forceinline__ void a_store_row(char* row, const float (&v)[16], int col0, int width,
+                                                                  bool vec, bool valid, int half) {
+  if constexpr (AT<T>::kBytes == 2) {
+    if (vec) {  // the halves exchange groups of four columns, so that each lane has eight in a row
+#pragma unroll
+      for (int g = 0; g < 4; g += 2) {
+        uint32_t x[2], y[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const auto s = __builtin_amdgcn_permlane32_swap(l_f32_bf16x2(v[4 * g + 2 * i], v[4 * g + 2 * i + 1]),
+                                                          l_f32_bf16x2(v[4 * g + 4 + 2 * i], v[4 * g + 5 + 2 * i]),
+                                                          false, false);
+          x[i] = s[0];
+          y[i] = s[1];
+        }
+        const int c = col0 + 8 * (g + half);
+        if (valid && c < width) *(lu32x4*)(row + c * 2) = lu32x4{x[0], x[1], y[0], y[1]};
+      }
+      return;
+    }
+  } else {
+    if (vec) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = col0 + 8 * g + 4 * half;
+        if (valid && c < width) *(lf32x4*)(row + c * 4) = lf32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = col0 + 8 * (i >> 2) + 4 * half + (i & 3);
+    if (valid && c < width) LType<T>::put(row, c, v[i]);
+  }
+}
+
+}  // namespace muon
