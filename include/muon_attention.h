@@ -115,7 +115,8 @@ muon_status_t muon_dropout_grad(const void* dy, int64_t ld_dy, double p, uint64_
  *     last offset on give zeros.  Offsets outside [0, tokens] are cut to it, one
  *     below its predecessor is raised to it.
  *   1 ≤ dim ≤ 128; kv_heads divides heads; scale finite and > 0;
- *   batch · queries, batch · keys ≤ 2^24; queries · group < 2^30.
+ *   batch · queries, batch · keys ≤ 2^24; queries · group < 2^30;
+ *   batch · queries · heads ≤ 2^28.
  * Keys behind the end of a sequence are never read.  Keys of the same sequence
  * that only the causal rule hides enter with probability 0: an infinite or NaN
  * value of v there reaches the row as 0 · v does.
@@ -142,13 +143,36 @@ muon_status_t muon_diff_attention(const muon_diff_attention_t* attention, void* 
                                   const int64_t out_strides[3], void* saved, size_t saved_bytes,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of `saved`, and of the workspaces of muon_diff_attention (grad = 0) and
- * muon_diff_attention_grad (grad = 1).  The pointers and strides of q, k, v
- * decide whether room for their copies is needed; the workspace of the backward
- * pass always has room for copies of out and its gradient. */
+/* Gradients of muon_diff_attention from the gradient of out, out itself and
+ * `saved`.  With dA = dout·vᵀ, δ_m = Σ_j P_m · dA:
+ *   dS_1 = P_1·(dA − δ_1), dS_2 = −lambda·P_2·(dA − δ_2),
+ *   dq_m = scale·dS_m·k_m, dk_m = scale·Σ dS_mᵀ·q_m over the group's heads,
+ *   dv = Σ (P_1 − lambda·P_2)ᵀ·dout over them, dlambda[h] = −Σ P_2·dA.
+ *   dq, dk, dv have the shapes of q, k, v; dq, dlambda (heads float32 values) and
+ *   the pair dk, dv may each be NULL: not wanted.
+ * For MUON_DTYPE_BF16 A, dS and the probabilities are rounded to bf16 as operands
+ * of the next product; scores, statistics and sums are fp32, dlambda is summed
+ * from unrounded terms. */
+typedef struct muon_diff_attention_grads {
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dlambda;
+  int64_t dq_strides[3], dk_strides[3], dv_strides[3];
+} muon_diff_attention_grads_t;
+
+muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* attention, const void* dout,
+                                       const int64_t dout_strides[3], const void* out,
+                                       const int64_t out_strides[3], const void* saved, size_t saved_bytes,
+                                       const muon_diff_attention_grads_t* grads, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* Bytes of `saved`, and of the workspaces of muon_diff_attention (dout = NULL)
+ * and muon_diff_attention_grad.  The addresses and strides of q, k, v and dout
+ * decide whether room for their copies is needed; addresses are not read. */
 muon_status_t muon_diff_attention_saved_size(const muon_diff_attention_t* attention, size_t* bytes);
-muon_status_t muon_diff_attention_workspace_size(const muon_diff_attention_t* attention, int32_t grad,
-                                                 size_t* bytes);
+muon_status_t muon_diff_attention_workspace_size(const muon_diff_attention_t* attention, const void* dout,
+                                                 const int64_t dout_strides[3], size_t* bytes);
 
 #ifdef __cplusplus
 }

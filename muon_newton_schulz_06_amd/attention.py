@@ -27,11 +27,12 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _check, _raw_stream, _workspace, load
-from .layers import _code, _device, _input, _on, _out, _ptr, _rows, _same, muon_rms_norm, muon_rms_norm_grad
+from .layers import _code, _device, _input, _on, _out, _ptr, _RMSNormFn, _rows, _same
 
 __all__ = [
     "rotary_frequencies", "muon_rotary", "muon_rotary_grad", "muon_dropout", "muon_dropout_grad",
-    "muon_diff_attention", "diff_attention_saved_size", "diff_attention_workspace_size",
+    "muon_diff_attention", "muon_diff_attention_grad", "diff_attention_saved_size",
+    "diff_attention_workspace_size", "Rotary", "DiffAttention", "Dropout",
 ]
 
 _i64x3 = ctypes.c_int64 * 3
@@ -83,8 +84,9 @@ def _lib():
         "muon_dropout": [vp, i64, vp, i64, f64, u64, u64, vp, vp, i64, i64, i64, i32, vp],
         "muon_dropout_grad": [vp, i64, f64, u64, u64, vp, vp, i64, i64, i64, i32, vp],
         "muon_diff_attention": [pa, vp, ps, vp, sz, vp, sz, vp],
+        "muon_diff_attention_grad": [pa, vp, ps, vp, ps, vp, sz, pg, vp, sz, vp],
         "muon_diff_attention_saved_size": [pa, psz],
-        "muon_diff_attention_workspace_size": [pa, i32, psz],
+        "muon_diff_attention_workspace_size": [pa, vp, ps, psz],
     }.items():
         f = getattr(L, name)
         f.argtypes, f.restype = args, i32
@@ -340,7 +342,8 @@ def diff_attention_workspace_size(batch, queries, keys, heads, kv_heads, dim, dt
     """Workspace bytes of muon_diff_attention, or of its gradient, enough for
     tensors of any strides; sequences: those of a packed batch."""
     f, n = _attention_sizes(batch, queries, keys, heads, kv_heads, dim, dtype, sequences), ctypes.c_size_t(0)
-    _check(_lib().muon_diff_attention_workspace_size(ctypes.byref(f), int(bool(grad)), ctypes.byref(n)))
+    _check(_lib().muon_diff_attention_workspace_size(ctypes.byref(f), 1 if grad else None, _i64x3(1, 1, 1),
+                                                     ctypes.byref(n)))
     return n.value
 
 
@@ -367,8 +370,188 @@ def muon_diff_attention(q, k, v, lam, causal: bool = True, scale: float | None =
             _check(L.muon_diff_attention_saved_size(ctypes.byref(f), ctypes.byref(n)))
             nsaved = n.value
             saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
-        _check(L.muon_diff_attention_workspace_size(ctypes.byref(f), 0, ctypes.byref(n)))
+        _check(L.muon_diff_attention_workspace_size(ctypes.byref(f), None, None, ctypes.byref(n)))
         with _workspace(n.value, dev, workspace, stream) as (ws, nbytes):
             _check(L.muon_diff_attention(ctypes.byref(f), _ptr(y), _strides(_heads(y, "out")), _ptr(saved), nsaved,
                                          _ptr(ws), nbytes, _raw_stream(dev.index)))
     return (y, saved) if save else y
+
+
+def muon_diff_attention_grad(dout, q, k, v, lam, out, saved, causal: bool = True, scale: float | None = None,
+                             offsets=None, want_dq: bool = True, want_dkv: bool = True, want_dlam: bool = True,
+                             workspace=None, stream=None):
+    """(dq, dk, dv, dlam) of muon_diff_attention from dout, its result ``out``
+    and ``saved``, with the arguments of that call; None for those not
+    wanted."""
+    L = _lib()
+    dev = _device(q, "q")
+    _same(dev, q.dtype, dout=dout, out=out)
+    _same(dev, torch.uint8, saved=saved)
+    if not saved.is_contiguous():
+        raise ValueError("saved must be contiguous, as muon_diff_attention returned it")
+    with _on(dev, stream):
+        f, kept = _attention(q, k, v, lam, causal, scale, offsets)
+        shape = (f.batch, f.queries, f.heads, 2 * f.dim)[4 - q.dim():]
+        for name, t in (("dout", dout), ("out", out)):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        d4, o4 = _input_heads(dout, "dout"), _input_heads(out, "out")
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=dev) if want else None
+                 for t, want in ((q, want_dq), (k, want_dkv), (v, want_dkv))]
+        dlam = torch.empty(f.heads, dtype=torch.float32, device=dev) if want_dlam else None
+        none = _i64x3(0, 0, 0)
+        g = MuonDiffAttentionGrads(*(_ptr(t) for t in grads), _ptr(dlam),
+                                   *(none if t is None else _strides(_heads(t, "gradient")) for t in grads))
+        n, ds = ctypes.c_size_t(0), _strides(d4)
+        # an empty dout has no address, but the size is that of the backward pass
+        _check(L.muon_diff_attention_workspace_size(ctypes.byref(f), _ptr(d4) or 16, ds, ctypes.byref(n)))
+        with _workspace(n.value, dev, workspace, stream) as (ws, nbytes):
+            _check(L.muon_diff_attention_grad(ctypes.byref(f), _ptr(d4), ds, _ptr(o4), _strides(o4), _ptr(saved),
+                                              saved.numel(), ctypes.byref(g), _ptr(ws), nbytes,
+                                              _raw_stream(dev.index)))
+    return (*grads, dlam)
+
+
+# ------------------------------------------------------------------ autograd
+
+class _RotaryFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, freqs, positions, start, interleaved, scale):
+        ctx.save_for_backward(freqs, positions)
+        ctx.how = (start, interleaved, scale)
+        ctx.set_materialize_grads(False)
+        return muon_rotary(q, k, freqs, positions, start, interleaved, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        freqs, positions = ctx.saved_tensors
+        if dq is None or dk is None:  # one of the two alone
+            one = dk if dq is None else dq
+            if one is not None:
+                one, _ = muon_rotary_grad(one, None, freqs, positions, *ctx.how)
+            dq, dk = (None, one) if dq is None else (one, None)
+        else:
+            dq, dk = muon_rotary_grad(dq, dk, freqs, positions, *ctx.how)
+        return dq, dk, None, None, None, None, None
+
+
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        ctx.how = (p, seed)
+        ctx.save_for_backward(offset)
+        return muon_dropout(x, p, seed, offset, residual=residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        (offset,) = ctx.saved_tensors
+        dx = muon_dropout_grad(dy, *ctx.how, offset) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
+
+
+class _DiffAttentionFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lam, causal, scale, offsets, save):
+        ctx.how = (causal, scale)
+        if not save:  # no backward pass will come
+            return muon_diff_attention(q, k, v, lam, causal, scale, offsets)
+        out, saved = muon_diff_attention(q, k, v, lam, causal, scale, offsets, save=True)
+        ctx.save_for_backward(q, k, v, lam, out, saved, offsets)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        q, k, v, lam, out, saved, offsets = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        grads = muon_diff_attention_grad(dout, q, k, v, lam, out, saved, *ctx.how, offsets, want_dq=need[0],
+                                         want_dkv=need[1] or need[2], want_dlam=need[3])
+        return (*grads, None, None, None, None)
+
+
+class Rotary(torch.nn.Module):
+    """Rotates queries and keys by their positions.  rotated: the values of a
+    head that take part (by default all ``dim``); the scalings for long contexts
+    are rotary_frequencies'."""
+
+    def __init__(self, dim: int, rotated: int | None = None, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str | None = None, factor: float = 1.0, original_length: int = 0):
+        super().__init__()
+        rotated = dim if rotated is None else rotated
+        if rotated > dim:
+            raise ValueError(f"rotated ({rotated}) above dim ({dim})")
+        self.freqs, self.scale = rotary_frequencies(rotated, base, scaling, factor, original_length)
+        self.dim, self.interleaved = dim, bool(interleaved)
+        self._here = {}  # the frequencies per device: fp64 whatever dtype the module is cast to
+
+    def forward(self, q, k=None, positions=None, start: int = 0):
+        """(q', k') of q and k (batch, tokens, heads, dim), q' alone without k."""
+        if q.shape[-1] != self.dim:
+            raise ValueError(f"heads of {q.shape[-1]} values, expected {self.dim}")
+        freqs = self._here.get(q.device)
+        if freqs is None:
+            freqs = self._here[q.device] = self.freqs.to(q.device)
+        q, k = _RotaryFn.apply(q, k, freqs, positions, start, self.interleaved, self.scale)
+        return q if k is None else (q, k)
+
+
+class Dropout(torch.nn.Module):
+    """residual + dropout(x): each call of the training mode draws anew, from
+    the seed and a counter of the calls on the device (so that replays of a
+    captured graph draw anew too).  In evaluation mode, or with p = 0, the
+    addition alone."""
+
+    def __init__(self, p: float, seed: int = 0, device=None):
+        super().__init__()
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p must be in [0, 1], got {p}")
+        self.p, self.seed = float(p), int(seed)
+        self.register_buffer("calls", torch.zeros(1, dtype=torch.int64, device=device))
+
+    def forward(self, x, residual=None):
+        if not self.training or self.p == 0.0:
+            return x if residual is None else x + residual
+        offset = self.calls.clone()
+        self.calls.add_(1)
+        return _DropoutFn.apply(x, residual, self.p, self.seed, offset)
+
+
+class DiffAttention(torch.nn.Module):
+    """Differential attention of projected (and rotated) queries, keys and
+    values, with its learned λ and the norm of each head's result:
+
+        λ = exp(λ_q1·λ_k1) − exp(λ_q2·λ_k2) + λ_init,
+        (1 − λ_init) · RMSNorm(attention(q, k, v, λ)) over the 2·dim values of a
+        head, one weight vector for all heads.
+
+    forward(q, k, v, offsets=None): (batch, tokens, 2·heads, dim), (batch, tokens,
+    2·kv_heads, dim), (batch, tokens, kv_heads, 2·dim) to (batch, tokens, heads,
+    2·dim); a packed batch without the batch dimension and with offsets."""
+
+    def __init__(self, heads: int, dim: int, kv_heads: int | None = None, lambda_init: float = 0.8,
+                 causal: bool = True, eps: float = 1e-5, device=None, dtype=None):
+        super().__init__()
+        self.heads, self.kv_heads, self.dim = heads, heads if kv_heads is None else kv_heads, dim
+        if heads < 1 or self.kv_heads < 1 or heads % self.kv_heads:
+            raise ValueError(f"kv_heads ({self.kv_heads}) must divide heads ({heads})")
+        self.lambda_init, self.causal, self.eps = float(lambda_init), bool(causal), float(eps)
+        for name in ("lambda_q1", "lambda_k1", "lambda_q2", "lambda_k2"):
+            setattr(self, name, torch.nn.Parameter(torch.empty(dim, device=device, dtype=torch.float32).normal_(std=0.1)))
+        self.weight = torch.nn.Parameter(torch.ones(2 * dim, device=device, dtype=dtype))
+
+    def lam(self):
+        """λ, one value per head (the same for all), float32."""
+        one = (self.lambda_q1.float() * self.lambda_k1.float()).sum().exp()
+        two = (self.lambda_q2.float() * self.lambda_k2.float()).sum().exp()
+        return (one - two + self.lambda_init).expand(self.heads)
+
+    def forward(self, q, k, v, offsets=None):
+        if q.shape[-2:] != (2 * self.heads, self.dim) or k.shape[-2:] != (2 * self.kv_heads, self.dim):
+            raise ValueError(f"q and k have shapes {tuple(q.shape)} and {tuple(k.shape)}, expected heads of "
+                             f"({2 * self.heads}, {self.dim}) and ({2 * self.kv_heads}, {self.dim})")
+        lam = self.lam()
+        save = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, lam))
+        out = _DiffAttentionFn.apply(q, k, v, lam, self.causal, None, offsets, save)
+        return _RMSNormFn.apply(out, self.weight * (1.0 - self.lambda_init), None, self.eps)

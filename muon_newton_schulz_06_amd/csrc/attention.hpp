@@ -7,6 +7,13 @@
 
 namespace muon {
 
+struct lf4 {
+  float v[4];
+};
+struct lu4 {
+  uint32_t v[4];
+};
+
 // ----- rotary positions ------------------------------------------------------
 struct RotarySide {
   const void* in;
@@ -97,6 +104,37 @@ int attn_fwd_rows(bool bf16, int dp, bool few);
 int attn_fwd_keys(bool bf16, int dp);
 hipError_t launch_attn_fwd(bool bf16, int dp, bool few, const AttnFwdLaunch& L, hipStream_t st);
 hipError_t launch_attn_join(bool bf16, int dp, const AttnFwdLaunch& L, hipStream_t st);
+
+// What the backward products need of a row: {L1, L2, δ1, δ2}, and for bf16 the
+// same as operands of a product (see attn_dkv), two 16-byte records per row.
+// All are [batch][head][token].
+struct AttnGradLaunch {
+  AttnShape s;
+  const void* dout;  // whole aligned chunks
+  int64_t gs[3];
+  const void* out;  // any alignment
+  int64_t os[3];
+  int32_t outVec;  // out is whole aligned chunks too
+  lf4* rec;
+  lu4 *recL, *recD;  // bf16 only
+  float* rowLam;     // per row δ2 as the products give it, [batch][head][token]
+  void *dq, *dk, *dv;
+  int64_t dqs[3], dks[3], dvs[3];
+  int32_t dqVec;
+  float* dlam;  // null: not wanted
+  float scale;
+  int32_t batch, heads;
+  // attn_dkv: blocks of keys, splits of the rows; attn_dq: blocks of rows
+  AttnList keyList, rowList;
+  int32_t keyBlocks, rowBlocks, splits;
+  float* part;  // splits > 1: [split][combo][key][4·DP] sums of dk1, dk2, dv
+};
+constexpr int kDkvKeys = 128, kDqRows = 128;
+hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, hipStream_t st);
+hipError_t launch_attn_dkv(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
+hipError_t launch_attn_dkv_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
+hipError_t launch_attn_dq(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
+hipError_t launch_attn_dlam(const AttnGradLaunch& L, hipStream_t st);
 
 // A packed batch's block lists: units·n rows of a sequence of n tokens are cut
 // into blocks of `per`.

@@ -345,6 +345,51 @@ AttnLayout attn_layout(const muon_diff_attention_t& f) {
   return l;
 }
 
+struct AttnGradLayout {
+  size_t list[2], q, k, v, dout, rec, recL, recD, rowLam, part, total;
+  int64_t keyBlocks, rowBlocks;
+  int splits;
+};
+
+AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout& l, const void* dout,
+                                const int64_t ds[3]) {
+  AttnGradLayout g{};
+  const bool bf16 = f.dtype == MUON_DTYPE_BF16;
+  const size_t e = esize(f.dtype);
+  AttnTensors t = attn_tensors(f);
+  for (int i = 0; i < 3; ++i) t.out.s[i] = ds[i];
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += align256(n);
+    return o;
+  };
+  g.keyBlocks = blocks_of(f.keys, kDkvKeys);
+  g.rowBlocks = blocks_of(l.rows, kDqRows);
+  const int64_t base = l.combos * g.keyBlocks;
+  if (f.sequences > 0) {
+    g.keyBlocks = f.keys / kDkvKeys + f.sequences + 2;
+    g.rowBlocks = l.rows / kDqRows + f.sequences + 2;
+    g.list[0] = take(256 + (size_t)g.keyBlocks * sizeof(AttnBlock));
+    g.list[1] = take(256 + (size_t)g.rowBlocks * sizeof(AttnBlock));
+  }
+  g.q = take(direct(f.q, t.q, e) ? 0 : copy_bytes(t.q, e));
+  g.k = take(direct(f.k, t.k, e) ? 0 : copy_bytes(t.k, e));
+  g.v = take(direct(f.v, t.v, e) ? 0 : copy_bytes(t.v, e));
+  g.dout = take(direct(dout, t.out, e) ? 0 : copy_bytes(t.out, e));
+  const size_t rows = (size_t)t.out.count();
+  g.rec = take(rows * 16);
+  g.recL = take(bf16 ? rows * 16 : 0);
+  g.recD = take(bf16 ? rows * 16 : 0);
+  g.rowLam = take(rows * 4);
+  // few blocks of keys: the rows that see them are split over several workgroups
+  const int64_t tiles = f.heads / f.kv_heads * blocks_of(f.queries, 32);
+  g.splits = base > 0 && base < 256 ? (int)std::max<int64_t>(1, std::min({blocks_of(512, base), tiles / 4, int64_t(16)})) : 1;
+  if (g.splits > 1) g.part = take((size_t)g.splits * l.combos * f.keys * 4 * l.dp * 4);
+  g.total = at;
+  return g;
+}
+
 void attn_sizes(Args& a, const muon_diff_attention_t* f) {
   if (!f) return a.fail(MUON_ERR_INVALID_ARG, "attention is NULL");
   a.size("batch", f->batch, 0, kMaxTokens);
@@ -360,6 +405,7 @@ void attn_sizes(Args& a, const muon_diff_attention_t* f) {
   a.size("batch * queries", f->batch * f->queries, 0, kMaxTokens);
   a.size("batch * keys", f->batch * f->keys, 0, kMaxTokens);
   a.size("queries * group", f->queries * (f->heads / f->kv_heads), 0, (int64_t(1) << 30) - 1);
+  a.size("batch * queries * heads", f->batch * f->queries * f->heads, 0, int64_t(1) << 28);
   if (f->sequences > 0 && (f->batch != 1 || f->queries != f->keys))
     a.fail(MUON_ERR_INVALID_ARG, "a packed batch needs batch = 1 and queries = keys");
 }
@@ -394,10 +440,38 @@ struct AttnCall {
     c.pitch = (int32_t)pitch;
     return ws + at;
   }
+  // Adds a list to the launch that makes them.
+  AttnList list(AttnPrepLaunch& P, size_t at, int32_t units, int32_t per) const {
+    auto& l = P.list[P.lists++];
+    l.count = (int32_t*)(ws + at);
+    l.blocks = (AttnBlock*)(ws + at + 256);
+    l.units = units;
+    l.per = per;
+    return {l.blocks, l.count};
+  }
   muon_status_t copy() const {
     return copies.n ? launched("aligned copies", launch_attn_copy(bf16(), copies, st), st) : MUON_OK;
   }
 };
+
+AttnPrepLaunch prep_of(const muon_diff_attention_t& f) {
+  AttnPrepLaunch P{};
+  P.offsets = f.offsets;
+  P.sequences = (int32_t)f.sequences;
+  P.tokens = (int32_t)f.queries;
+  return P;
+}
+
+// Strides of an output, and whether it takes 16-byte stores.
+bool output_strides(int64_t s[3], const void* p, const Heads& h, size_t e) {
+  const int64_t v = 16 / (int64_t)e;
+  bool vec = (uintptr_t)p % 16 == 0 && h.dim % v == 0;
+  for (int i = 0; i < 3; ++i) {
+    s[i] = h.n[i] > 1 ? h.s[i] : 0;
+    vec = vec && s[i] % v == 0;
+  }
+  return vec;
+}
 
 AttnShape shape_of(const muon_diff_attention_t& f, const AttnLayout& l) {
   AttnShape s{};
@@ -468,13 +542,16 @@ muon_status_t muon_diff_attention_saved_size(const muon_diff_attention_t* f, siz
   });
 }
 
-muon_status_t muon_diff_attention_workspace_size(const muon_diff_attention_t* f, int32_t grad, size_t* bytes) {
+muon_status_t muon_diff_attention_workspace_size(const muon_diff_attention_t* f, const void* dout,
+                                                 const int64_t dout_strides[3], size_t* bytes) {
   return guarded([&]() -> muon_status_t {
     Args a;
     attn_sizes(a, f);
     if (!bytes) a.fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+    if (a.ok() && dout && !dout_strides) a.fail(MUON_ERR_INVALID_ARG, "dout_strides is NULL");
     if (!a.ok()) return a.report();
-    *bytes = grad ? 0 : attn_layout(*f).total;
+    const AttnLayout l = attn_layout(*f);
+    *bytes = dout ? attn_grad_layout(*f, l, dout, dout_strides).total : l.total;
     return MUON_OK;
   });
 }
@@ -511,28 +588,17 @@ muon_status_t muon_diff_attention(const muon_diff_attention_t* f, void* out, con
     if (s != MUON_OK) return s;
     const bool bf16 = call.bf16();
     if (f->sequences > 0) {
-      AttnPrepLaunch P{};
-      P.offsets = f->offsets;
-      P.sequences = (int32_t)f->sequences;
-      P.tokens = (int32_t)f->queries;
-      P.lists = 1;
-      P.list[0].count = (int32_t*)((char*)workspace + l.list[0]);
-      P.list[0].blocks = (AttnBlock*)((char*)workspace + l.list[0] + 256);
-      P.list[0].units = L.s.group;
-      P.list[0].per = attn_fwd_rows(bf16, l.dp, l.few);
+      AttnPrepLaunch P = prep_of(*f);
+      L.list = call.list(P, l.list[0], L.s.group, attn_fwd_rows(bf16, l.dp, l.few));
       s = launched("blocks of the packed batch", launch_attn_prep(P, st), st);
       if (s != MUON_OK) return s;
-      L.list.blocks = P.list[0].blocks;
-      L.list.count = P.list[0].count;
     }
     if (saved) {
       L.s.stat = (float*)((char*)saved + l.stat);
       L.s.o2 = (char*)saved + l.o2;
     }
     L.out = out;
-    for (int i = 0; i < 3; ++i) L.os[i] = t.out.n[i] > 1 ? t.out.s[i] : 0;
-    const int64_t v = 16 / (int64_t)e;
-    L.vec = (uintptr_t)out % 16 == 0 && L.os[0] % v == 0 && L.os[1] % v == 0 && L.os[2] % v == 0 && t.out.dim % v == 0;
+    L.vec = output_strides(L.os, out, t.out, e);
     L.rowBlocks = (int32_t)l.rowBlocks;
     L.splits = l.splits;
     L.splitKeys = l.splitKeys;
@@ -541,6 +607,107 @@ muon_status_t muon_diff_attention(const muon_diff_attention_t* f, void* out, con
     s = launched("differential attention", launch_attn_fwd(bf16, l.dp, l.few, L, st), st);
     if (s != MUON_OK || l.splits == 1) return s;
     return launched("sum of the key splits", launch_attn_join(bf16, l.dp, L, st), st);
+  });
+}
+
+muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const void* dout, const int64_t dout_strides[3],
+                                       const void* out, const int64_t out_strides[3], const void* saved,
+                                       size_t saved_bytes, const muon_diff_attention_grads_t* grads, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> muon_status_t {
+    HeadArgs a;
+    attn_sizes(a, f);
+    if (!grads) a.fail(MUON_ERR_INVALID_ARG, "grads is NULL");
+    if (a.ok() && (!dout_strides || !out_strides)) a.fail(MUON_ERR_INVALID_ARG, "dout_strides or out_strides is NULL");
+    if (!a.ok()) return a.report();
+    const AttnLayout l = attn_layout(*f);
+    const AttnGradLayout w = attn_grad_layout(*f, l, dout, dout_strides);
+    const AttnTensors t = attn_tensors(*f);
+    const size_t e = esize(f->dtype);
+    const Heads hd = heads_of(f->batch, f->queries, f->heads, 2 * f->dim, dout_strides);
+    const Heads ho = heads_of(f->batch, f->queries, f->heads, 2 * f->dim, out_strides);
+    Heads gq = t.q, gk = t.k, gv = t.v;
+    for (int i = 0; i < 3; ++i) {
+      gq.s[i] = grads->dq_strides[i];
+      gk.s[i] = grads->dk_strides[i];
+      gv.s[i] = grads->dv_strides[i];
+    }
+    attn_inputs(a, *f, t);
+    a.heads("dout", dout, hd, e, false);
+    a.heads("out", out, ho, e, false);
+    a.buffer("saved", saved, saved_bytes, l.saved, false);
+    if (grads->dq) a.heads("dq", grads->dq, gq, e, true);
+    if (!grads->dk != !grads->dv && t.k.count()) a.fail(MUON_ERR_INVALID_ARG, "dk and dv go together");
+    if (grads->dk) a.heads("dk", grads->dk, gk, e, true);
+    if (grads->dv) a.heads("dv", grads->dv, gv, e, true);
+    if (grads->dlambda) a.matrix("dlambda", grads->dlambda, 1, f->heads, f->heads, 4, true);
+    a.buffer("workspace", workspace, workspace_bytes, w.total, true);
+    a.size("workgroups", std::max(l.combos * w.keyBlocks * w.splits, l.combos * w.rowBlocks), 0, kMaxBlocks);
+    a.all_aliases([](const char*, const char*) { return false; });
+    if (!a.ok()) return a.report();
+    const bool wantK = grads->dk && t.k.count() > 0, wantQ = (grads->dq || grads->dlambda) && t.q.count() > 0;
+    if (!wantK && !wantQ && !grads->dlambda) return MUON_OK;
+    muon_status_t s = check_device();
+    if (s != MUON_OK) return s;
+    const hipStream_t st = (hipStream_t)stream;
+    char* ws = (char*)workspace;
+    AttnCall call{*f, ws, st};
+    const bool bf16 = call.bf16();
+    AttnGradLaunch L{};
+    L.s = shape_of(*f, l);
+    L.s.q = call.operand(f->q, t.q, w.q, L.s.qs);
+    L.s.k = call.operand(f->k, t.k, w.k, L.s.ks);
+    L.s.v = call.operand(f->v, t.v, w.v, L.s.vs);
+    L.dout = call.operand(dout, hd, w.dout, L.gs);
+    s = call.copy();
+    if (s != MUON_OK) return s;
+    if (f->sequences > 0 && f->queries > 0) {
+      AttnPrepLaunch P = prep_of(*f);
+      L.keyList = call.list(P, w.list[0], 1, kDkvKeys);
+      L.rowList = call.list(P, w.list[1], L.s.group, kDqRows);
+      s = launched("blocks of the packed batch", launch_attn_prep(P, st), st);
+      if (s != MUON_OK) return s;
+    }
+    L.s.stat = (float*)((char*)saved + l.stat);
+    L.s.o2 = (char*)saved + l.o2;
+    L.out = out;
+    L.outVec = output_strides(L.os, out, ho, e);
+    L.rec = (lf4*)(ws + w.rec);
+    L.recL = (lu4*)(ws + w.recL);
+    L.recD = (lu4*)(ws + w.recD);
+    L.rowLam = (float*)(ws + w.rowLam);
+    L.dq = grads->dq;
+    L.dqVec = output_strides(L.dqs, grads->dq, gq, e);
+    L.dk = grads->dk;
+    output_strides(L.dks, grads->dk, gk, e);
+    L.dv = grads->dv;
+    output_strides(L.dvs, grads->dv, gv, e);
+    L.dlam = grads->dlambda;
+    L.scale = f->scale;
+    L.batch = (int32_t)f->batch;
+    L.heads = (int32_t)f->heads;
+    L.keyBlocks = (int32_t)w.keyBlocks;
+    L.rowBlocks = (int32_t)w.rowBlocks;
+    L.splits = w.splits;
+    L.part = (float*)(ws + w.part);
+    if (hd.count() > 0) {
+      s = launched("row sums of the gradient", launch_attn_rows(bf16, L, st), st);
+      if (s != MUON_OK) return s;
+    }
+    if (wantK) {
+      s = launched("gradients of keys and values", launch_attn_dkv(bf16, l.dp, L, st), st);
+      if (s != MUON_OK) return s;
+      if (w.splits > 1) {
+        s = launched("sum of the row splits", launch_attn_dkv_join(bf16, l.dp, L, st), st);
+        if (s != MUON_OK) return s;
+      }
+    }
+    if (wantQ) {
+      s = launched("gradient of the queries", launch_attn_dq(bf16, l.dp, L, st), st);
+      if (s != MUON_OK) return s;
+    }
+    if (!grads->dlambda) return MUON_OK;
+    return launched("gradient of lambda", launch_attn_dlam(L, st), st);
   });
 }
 

@@ -1,0 +1,212 @@
+// Differential attention, gradient of the queries: for a row
+//   dS_1 = P_1·(dA − δ_1),  dS_2 = −λ·P_2·(dA − δ_2),  dA = dO·Vᵀ,
+//   dQ_m = scale·dS_m·K_m,
+// with P_m = exp2(c·S_m − L_m) recomputed from the saved log-sums.
+//
+// A wave has 32 rows (Q of both maps and dO in registers as operands) and runs
+// over the tiles of K_1, K_2 and V in LDS.  Everything is formed transposed, a
+// lane holding values of one row only: S_mᵀ = K_m·Q_mᵀ, dAᵀ = V·dOᵀ, and dS_mᵀ
+// serves as it lies in dQ_mᵀ = K_mᵀ·dS_mᵀ.  dA is formed once for both maps,
+// and −λ·scale is applied to the sums.
+//
+// λ's gradient is −Σ P_2·dA = −Σ_rows (δ_2 + Σ_j P_2·(dA − δ_2)): the second
+// sum, of the unrounded terms, takes out what δ_2 lacks (it came from a rounded
+// P_2·V), so the result is accurate to fp32.
+#include <hip/hip_runtime.h>
+
+#include "attention.hpp"
+#include "attn_tile.hpp"
+
+namespace muon {
+namespace {
+
+template <typename T, int DP> struct Dq {
+  static constexpr int kWaves = 4, kThreads = 256;
+  static constexpr int kBN = AT<T>::kBytes == 2 && DP == 64 ? 64 : 32;
+  static constexpr int kK = DP * AT<T>::kBytes, kV = 2 * kK;
+  static constexpr int kStage = kBN * (2 * kK + kV);
+  static constexpr int kWavesPerSimd = AT<T>::kBytes == 2 && DP == 64 ? 2 : 1;  // registers of the operands
+};
+
+// MAPS: bit 0 the first map, bit 1 the second (and λ's gradient).
+template <typename T, int DP, int MAPS>
+__global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const AttnGradLaunch L) {
+  using F = Dq<T, DP>;
+  constexpr bool k1st = MAPS & 1, k2nd = MAPS & 2;
+  constexpr int BN = F::kBN, E = AT<T>::kBytes;
+  constexpr int NC = DP / AT<T>::kStep, ND = DP / 32, SP = AT<T>::kSteps32;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * F::kStage];
+  const AttnShape& S = L.s;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  int id = blockIdx.x;
+  const int combo = id % S.combos;
+  id /= S.combos;
+  int tok0 = 0, nq = (int)S.nq, nk = (int)S.nk, at = 0;
+  if (L.rowList.blocks) {
+    const int n = *L.rowList.count;
+    if (id >= n) return;
+    const AttnBlock B = L.rowList.blocks[n - 1 - id];
+    tok0 = B.tok;
+    nq = B.n;
+    nk = B.nk;
+    at = B.at;
+  } else {
+    at = (L.rowBlocks - 1 - id) * kDqRows;
+  }
+  const int batch = combo / S.kv, hk = combo % S.kv, G = S.group;
+  const int rows = nq * G, shift = nk - nq + 1;
+  const int row = at + wave * 32 + (lane & 31);
+  const bool valid = row < rows;
+  const int t = row / G, g = row - t * G, head = hk * G + g;
+  const int lim = !valid ? 0 : S.causal ? min(max(t + shift, 0), nk) : nk;
+  const int64_t tok = tok0 + t;
+  const int last = min(at + kDqRows, rows) - 1;
+  const int kEnd = S.causal ? min(max(last / G + shift, 0), nk) : nk;
+  const int least = S.causal ? min(max(at / G + shift, 0), nk) : nk;
+
+  lu32x4 q[2][NC], d[2 * NC];
+  {
+    const char* p = (const char*)S.q + (batch * S.qs[0] + tok * S.qs[1] + 2 * head * S.qs[2]) * E;
+    const char* o = (const char*)L.dout + (batch * L.gs[0] + tok * L.gs[1] + head * L.gs[2]) * E;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        q[m][c] = lu32x4{0, 0, 0, 0};
+        if (valid && (2 * c + half) * 16 < S.dim * E)
+          q[m][c] = *(const lu32x4*)(p + m * S.qs[2] * E + (2 * c + half) * 16);
+      }
+#pragma unroll
+    for (int c = 0; c < 2 * NC; ++c) {
+      d[c] = lu32x4{0, 0, 0, 0};
+      if (valid && (2 * c + half) * 16 < 2 * S.dim * E) d[c] = *(const lu32x4*)(o + (2 * c + half) * 16);
+    }
+  }
+  const int64_t recAt = ((int64_t)batch * L.heads + head) * S.nq + tok;
+  float l1 = -kNegInf, l2 = -kNegInf, d1 = 0.f, d2 = 0.f;
+  if (valid) {
+    const lf4 r = L.rec[recAt];
+    l1 = r.v[0];
+    l2 = r.v[1];
+    d1 = r.v[2];
+    d2 = r.v[3];
+  }
+
+  TileLoader<F::kK, BN, F::kWaves> ldk;
+  TileLoader<F::kV, BN, F::kWaves> ldv;
+  ldk.init(lane, wave, S.ks[1] * E, S.dim * E);
+  ldv.init(lane, wave, S.vs[1] * E, 2 * S.dim * E);
+  const char* k1 = (const char*)S.k + (batch * S.ks[0] + tok0 * S.ks[1] + 2 * hk * S.ks[2]) * E;
+  const char* v0 = (const char*)S.v + (batch * S.vs[0] + tok0 * S.vs[1] + hk * S.vs[2]) * E;
+  const uint32_t base = a_lds(lds);
+  auto issue = [&](int key, uint32_t buf) __attribute__((always_inline)) {
+    const char* k = k1 + (int64_t)key * S.ks[1] * E;
+    ldk.issue(k, nk - key, buf);
+    ldk.issue(k + S.ks[2] * E, nk - key, buf + BN * F::kK);
+    ldv.issue(v0 + (int64_t)key * S.vs[1] * E, nk - key, buf + 2 * BN * F::kK);
+  };
+  const RowReader<F::kK> rk(lane);
+  const RowReader<F::kV> rv(lane);
+  const ColReader<T, F::kK> ck(lane);
+
+  af32x16 acc[2][ND];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < ND; ++n) acc[m][n] = af32x16{};
+  float sum = 0.f;
+
+  auto step = [&](uint32_t kt, uint32_t vt, int key, bool masked) __attribute__((always_inline)) {
+    af32x16 a{}, s1{}, s2{};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if constexpr (k1st) s1 = a_mma<T>(rk.get(kt, c), q[0][c], s1);
+      if constexpr (k2nd) s2 = a_mma<T>(rk.get(kt + BN * F::kK, c), q[1][c], s2);
+    }
+#pragma unroll
+    for (int c = 0; c < 2 * NC; ++c) a = a_mma<T>(rv.get(vt, c), d[c], a);
+    if (masked) {
+      const int n = lim - key - 4 * half;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool on = 8 * (i >> 2) + (i & 3) < n;
+        if constexpr (k1st) s1[i] = on ? s1[i] : kNegInf;
+        if constexpr (k2nd) s2[i] = on ? s2[i] : kNegInf;
+        a[i] = on ? a[i] : 0.f;
+      }
+    }
+    float e1[16], e2[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (k1st) e1[i] = a_exp2(s1[i] * S.c - l1) * (a[i] - d1);
+      if constexpr (k2nd) {
+        e2[i] = a_exp2(s2[i] * S.c - l2) * (a[i] - d2);
+        sum += e2[i];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < SP; ++u) {
+      const uint32_t kr = kt + u * AT<T>::kStep * F::kK;
+      lu32x4 b1, b2;
+      if constexpr (k1st) b1 = a_operand<T>(e1, u);
+      if constexpr (k2nd) b2 = a_operand<T>(e2, u);
+#pragma unroll
+      for (int n = 0; n < ND; ++n) {
+        if constexpr (k1st) acc[0][n] = a_mma<T>(ck.get(kr, n), b1, acc[0][n]);
+        if constexpr (k2nd) acc[1][n] = a_mma<T>(ck.get(kr + BN * F::kK, n), b2, acc[1][n]);
+      }
+    }
+  };
+
+  if (kEnd > 0) issue(0, base);
+  uint32_t buf = base;
+  for (int key = 0; key < kEnd; key += BN) {
+    a_landed();
+    const uint32_t other = 2 * base + F::kStage - buf;
+    if (key + BN < kEnd) issue(key + BN, other);
+#pragma unroll
+    for (int j = 0; j < BN; j += 32) {
+      if (key + j >= kEnd) break;
+      step(buf + j * F::kK, buf + 2 * BN * F::kK + j * F::kV, key + j, key + j + 32 > least);
+    }
+    buf = other;
+  }
+  if constexpr (k2nd) {
+    sum = a_half_sum(sum);
+    if (valid && half == 0) L.rowLam[recAt] = d2 + sum;
+  }
+  if (!L.dq) return;
+  // of a row that sees one key alone P = 1 whatever the scores: no gradient
+  const float f[2] = {L.scale, valid ? -S.lam[head] * L.scale : 0.f};
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    if (!(MAPS >> m & 1)) continue;
+    char* o = (char*)L.dq + (batch * L.dqs[0] + tok * L.dqs[1] + (2 * head + m) * L.dqs[2]) * E;
+#pragma unroll
+    for (int n = 0; n < ND; ++n) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = lim > 1 ? acc[m][n][i] * f[m] : 0.f;
+      a_store_row<T>(o, v, n * 32, S.dim, L.dqVec, valid, half);
+    }
+  }
+}
+
+template <typename T, int DP, int MAPS> hipError_t run(const AttnGradLaunch& L, hipStream_t st) {
+  attn_dq<T, DP, MAPS><<<dim3((unsigned)(L.s.combos * L.rowBlocks)), 256, 0, st>>>(L);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_dq(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {
+  if (bf16) return dp == 64 ? run<Bf16, 64, 3>(L, st) : run<Bf16, 128, 3>(L, st);
+  if (dp == 64) return run<float, 64, 3>(L, st);
+  // operands and sums of both maps are more than a wave's registers: a pass each
+  const hipError_t e = run<float, 128, 1>(L, st);
+  return e != hipSuccess ? e : run<float, 128, 2>(L, st);
+}
+
+}  // namespace muon
