@@ -30,6 +30,13 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (set HIPCC or install ROCm under /opt/rocm)")
 
 
+# The attention kernels keep more than 256 registers per lane: results that other
+# instructions read (scores) belong into VGPRs, sums into whichever file has room.
+# By default the compiler puts every MFMA result of such a kernel into AGPRs and
+# copies (dkv kernel: 320 copies and 5200 cycles per tile).
+EXTRA_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for src in ("attn_fwd.hip", "attn_dq.hip", "attn_dkv.hip")}
+
+
 def flags():
     return [
         "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-mcode-object-version=5",
@@ -43,7 +50,7 @@ def build(verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory(prefix="muon_build_") as tmp:
         def compile_one(src):
             obj = os.path.join(tmp, src + ".o")
-            cmd = [cc, *flags(), "-c", os.path.join(CSRC, src), "-o", obj]
+            cmd = [cc, *flags(), *EXTRA_FLAGS.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
             if verbose:
                 print(" ".join(cmd), flush=True)
             r = subprocess.run(cmd, capture_output=True, text=True)

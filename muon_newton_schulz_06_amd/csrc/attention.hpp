@@ -99,6 +99,7 @@ struct AttnFwdLaunch {
   // logarithms of their sums [split][combo][row][map]
   float *part, *partStat;
 };
+constexpr int kMaxSplits = 512;
 // Rows of a workgroup, keys of its tiles.
 int attn_fwd_rows(bool bf16, int dp, bool few);
 int attn_fwd_keys(bool bf16, int dp);
@@ -124,10 +125,15 @@ struct AttnGradLaunch {
   float* dlam;  // null: not wanted
   float scale;
   int32_t batch, heads;
-  // attn_dkv: blocks of keys, splits of the rows; attn_dq: blocks of rows
+  // attn_dkv: blocks of keys; attn_dq: blocks of rows
   AttnList keyList, rowList;
-  int32_t keyBlocks, rowBlocks, splits;
-  float* part;  // splits > 1: [split][combo][key][4·DP] sums of dk1, dk2, dv
+  int32_t keyBlocks, rowBlocks;
+  // attn_dkv in stretches of tiles (see there): their number (a multiple of 8;
+  // 0: a workgroup per block, no list), at least `least` tiles each; tiles of the
+  // list's blocks before each; [2·stretch][128 keys][4·DP] sums of dk1, dk2, dv
+  int32_t streams, least, packed;
+  const int64_t* cum;
+  float* part;
 };
 constexpr int kDkvKeys = 128, kDqRows = 128;
 hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, hipStream_t st);
@@ -136,8 +142,8 @@ hipError_t launch_attn_dkv_join(bool bf16, int dp, const AttnGradLaunch& L, hipS
 hipError_t launch_attn_dq(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
 hipError_t launch_attn_dlam(const AttnGradLaunch& L, hipStream_t st);
 
-// A packed batch's block lists: units·n rows of a sequence of n tokens are cut
-// into blocks of `per`.
+// Block lists: units·n rows of a sequence of n tokens are cut into blocks of
+// `per`.  Without offsets the tokens are one sequence.
 struct AttnPrepLaunch {
   const int32_t* offsets;
   int32_t sequences, tokens;
@@ -145,7 +151,12 @@ struct AttnPrepLaunch {
     AttnBlock* blocks;
     int32_t* count;
     int32_t units, per;
+    // null, or for blocks of keys: row tiles of 32 (one at least) of the blocks
+    // before each, of all at [count]
+    int64_t* cum;
   } list[2];
+  int32_t group, causal;
+  int64_t queries;  // of the one sequence
   int32_t lists;
 };
 hipError_t launch_attn_prep(const AttnPrepLaunch& L, hipStream_t st);

@@ -298,7 +298,7 @@ void plan_splits(AttnLayout& l, bool bf16, int64_t nk) {
   l.splits = 1;
   l.splitKeys = (int)((nk + bn - 1) / bn * bn);
   if (base >= 256 || nk < 4 * bn) return;
-  const int64_t want = std::min<int64_t>(std::max<int64_t>(1, 512 / base), blocks_of(nk, 2 * bn));
+  const int64_t want = std::min<int64_t>(std::max<int64_t>(1, kMaxSplits / base), blocks_of(nk, 2 * bn));
   const int64_t keys = blocks_of(blocks_of(nk, want), bn) * bn;
   l.splits = (int)blocks_of(nk, keys);
   l.splitKeys = (int)keys;
@@ -346,9 +346,9 @@ AttnLayout attn_layout(const muon_diff_attention_t& f) {
 }
 
 struct AttnGradLayout {
-  size_t list[2], q, k, v, dout, rec, recL, recD, rowLam, part, total;
+  size_t list[2], cum, q, k, v, dout, rec, recL, recD, rowLam, part, total;
   int64_t keyBlocks, rowBlocks;
-  int splits;
+  int streams, least;
 };
 
 AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout& l, const void* dout,
@@ -366,12 +366,24 @@ AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout
   };
   g.keyBlocks = blocks_of(f.keys, kDkvKeys);
   g.rowBlocks = blocks_of(l.rows, kDqRows);
-  const int64_t base = l.combos * g.keyBlocks;
-  if (f.sequences > 0) {
+  // attn_dkv runs a workgroup per block of keys where these fill the 256 CUs
+  // twice (the longer ones first, so that the sums of two come out alike); else
+  // equal stretches of all their tiles, one per CU, or fewer of `least` tiles.
+  // The sums of a block that stretches share are written and read once more.
+  const bool packed = f.sequences > 0;
+  g.least = bf16 && l.dp == 64 ? 6 : 3;
+  if (l.combos > 0 && f.keys > 0 && (packed || l.combos * g.keyBlocks < 512)) {
+    const double tiles = (double)l.combos * g.keyBlocks * (f.heads / f.kv_heads) * blocks_of(f.queries, 32);
+    g.streams = (int)std::min(256.0, std::max(8.0, std::ceil(tiles / g.least / 8) * 8));
+  }
+  if (packed) {
     g.keyBlocks = f.keys / kDkvKeys + f.sequences + 2;
     g.rowBlocks = l.rows / kDqRows + f.sequences + 2;
-    g.list[0] = take(256 + (size_t)g.keyBlocks * sizeof(AttnBlock));
     g.list[1] = take(256 + (size_t)g.rowBlocks * sizeof(AttnBlock));
+  }
+  if (g.streams) {
+    g.list[0] = take(256 + (size_t)g.keyBlocks * sizeof(AttnBlock));
+    g.cum = take((size_t)(g.keyBlocks + 1) * sizeof(int64_t));
   }
   g.q = take(direct(f.q, t.q, e) ? 0 : copy_bytes(t.q, e));
   g.k = take(direct(f.k, t.k, e) ? 0 : copy_bytes(t.k, e));
@@ -382,10 +394,7 @@ AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout
   g.recL = take(bf16 ? rows * 16 : 0);
   g.recD = take(bf16 ? rows * 16 : 0);
   g.rowLam = take(rows * 4);
-  // few blocks of keys: the rows that see them are split over several workgroups
-  const int64_t tiles = f.heads / f.kv_heads * blocks_of(f.queries, 32);
-  g.splits = base > 0 && base < 256 ? (int)std::max<int64_t>(1, std::min({blocks_of(512, base), tiles / 4, int64_t(16)})) : 1;
-  if (g.splits > 1) g.part = take((size_t)g.splits * l.combos * f.keys * 4 * l.dp * 4);
+  if (g.streams) g.part = take((size_t)g.streams * 2 * kDkvKeys * 4 * l.dp * 4);
   g.total = at;
   return g;
 }
@@ -459,6 +468,9 @@ AttnPrepLaunch prep_of(const muon_diff_attention_t& f) {
   P.offsets = f.offsets;
   P.sequences = (int32_t)f.sequences;
   P.tokens = (int32_t)f.queries;
+  P.group = (int32_t)(f.heads / f.kv_heads);
+  P.causal = f.causal != 0;
+  P.queries = f.queries;
   return P;
 }
 
@@ -642,7 +654,7 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     if (grads->dv) a.heads("dv", grads->dv, gv, e, true);
     if (grads->dlambda) a.matrix("dlambda", grads->dlambda, 1, f->heads, f->heads, 4, true);
     a.buffer("workspace", workspace, workspace_bytes, w.total, true);
-    a.size("workgroups", std::max(l.combos * w.keyBlocks * w.splits, l.combos * w.rowBlocks), 0, kMaxBlocks);
+    a.size("workgroups", std::max(l.combos * w.keyBlocks, l.combos * w.rowBlocks), 0, kMaxBlocks);
     a.all_aliases([](const char*, const char*) { return false; });
     if (!a.ok()) return a.report();
     const bool wantK = grads->dk && t.k.count() > 0, wantQ = (grads->dq || grads->dlambda) && t.q.count() > 0;
@@ -661,11 +673,16 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     L.dout = call.operand(dout, hd, w.dout, L.gs);
     s = call.copy();
     if (s != MUON_OK) return s;
-    if (f->sequences > 0 && f->queries > 0) {
+    if (w.streams || f->sequences > 0) {
       AttnPrepLaunch P = prep_of(*f);
-      L.keyList = call.list(P, w.list[0], 1, kDkvKeys);
-      L.rowList = call.list(P, w.list[1], L.s.group, kDqRows);
-      s = launched("blocks of the packed batch", launch_attn_prep(P, st), st);
+      P.tokens = (int32_t)f->keys;
+      if (w.streams) {
+        L.keyList = call.list(P, w.list[0], 1, kDkvKeys);
+        P.list[0].cum = (int64_t*)(ws + w.cum);
+        L.cum = P.list[0].cum;
+      }
+      if (f->sequences > 0) L.rowList = call.list(P, w.list[1], L.s.group, kDqRows);
+      s = launched("blocks of the batch", launch_attn_prep(P, st), st);
       if (s != MUON_OK) return s;
     }
     L.s.stat = (float*)((char*)saved + l.stat);
@@ -688,7 +705,9 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     L.heads = (int32_t)f->heads;
     L.keyBlocks = (int32_t)w.keyBlocks;
     L.rowBlocks = (int32_t)w.rowBlocks;
-    L.splits = w.splits;
+    L.streams = w.streams;
+    L.least = w.least;
+    L.packed = f->sequences > 0;
     L.part = (float*)(ws + w.part);
     if (hd.count() > 0) {
       s = launched("row sums of the gradient", launch_attn_rows(bf16, L, st), st);
@@ -697,8 +716,8 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     if (wantK) {
       s = launched("gradients of keys and values", launch_attn_dkv(bf16, l.dp, L, st), st);
       if (s != MUON_OK) return s;
-      if (w.splits > 1) {
-        s = launched("sum of the row splits", launch_attn_dkv_join(bf16, l.dp, L, st), st);
+      if (w.streams) {
+        s = launched("sums of shared blocks", launch_attn_dkv_join(bf16, l.dp, L, st), st);
         if (s != MUON_OK) return s;
       }
     }

@@ -16,8 +16,10 @@
 // That is 4 steps beside 32, instead of 16 reads of four values from LDS
 // beside 32 and 48 subtractions.  fp32 does the same with products of 2.
 //
-// No atomics: a workgroup owns its keys.  Where there are few, the row tiles
-// are split, and the splits' sums are joined in order.
+// No atomics: a workgroup owns its keys.  Where there are few of them or they are
+// seen by unequal numbers of rows (a packed batch), every workgroup takes an
+// equal stretch of tiles instead, and the sums of blocks that stretches share are
+// joined in order (8192 tokens in 11 documents: XXX).
 #include <hip/hip_runtime.h>
 
 #include "attention.hpp"
@@ -26,42 +28,101 @@
 namespace muon {
 namespace {
 
-// What a pass makes (PART): bit 0 dV, bit 1 dK_1, bit 2 dK_2.
+// The tiles of one block of keys that a workgroup runs: begin … end − 1.
+struct Piece {
+  int combo, tok, nq, nk, inside, at, begin, end;
+  int64_t slot;  // where its sums go to be joined; −1: the block is its own
+};
+
+// A workgroup's stretch of all combos' tiles, in the list's order, or (streams
+// = 0) the block of its number.
+struct Stretch {
+  int64_t each, total, per, pos, stop;  // tiles of a combo, all, of a stretch; this one
+  int64_t w;
+  int count;
+  __device__ __forceinline__ Stretch(const AttnGradLaunch& L, int64_t number) : w(number) {
+    if (!L.streams) {
+      pos = 0;
+      stop = 1;
+      return;
+    }
+    count = *L.keyList.count;
+    each = L.cum[count];
+    total = each * L.s.combos;
+    per = max((total + L.streams - 1) / L.streams, (int64_t)L.least);
+    pos = min(w * per, total);
+    stop = min(pos + per, total);
+  }
+  // the block of a combo's tile
+  __device__ __forceinline__ int find(const AttnGradLaunch& L, int64_t tile) const {
+    int lo = 0, hi = count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (L.cum[mid] <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ bool next(const AttnGradLaunch& L, Piece& p) {
+    if (pos >= stop) return false;
+    if (!L.streams) {  // the keys that most rows see first
+      p = Piece{(int)blockIdx.x % L.s.combos, 0, (int)L.s.nq, (int)L.s.nk, 1,
+                (int)blockIdx.x / L.s.combos * kDkvKeys, 0, 0x7fffffff, -1};
+      pos = stop;
+      return true;
+    }
+    p.combo = (int)(pos / each);
+    const int64_t tile = pos - p.combo * each;
+    const int b = find(L, tile);
+    const AttnBlock B = L.keyList.blocks[b];
+    p.tok = B.tok;
+    p.nq = L.packed ? B.n : (int)L.s.nq;
+    p.nk = B.n;
+    p.inside = B.nk > 0;
+    p.at = B.at;
+    const int64_t from = L.cum[b], to = L.cum[b + 1], n = min(stop - pos, to - tile);
+    p.begin = (int)(tile - from);
+    p.end = (int)(p.begin + n);
+    p.slot = n == to - from ? -1 : 2 * w + (p.begin == 0);
+    pos += n;
+    return true;
+  }
+};
+
+// What a pass makes (PART): bit 0 dV, bit 1 dK.
 template <typename T, int DP> struct Dkv {
   static constexpr int kWaves = 4, kThreads = 256, kRows = 32;
   static constexpr int kK = DP * AT<T>::kBytes, kVB = 2 * kK;
   static constexpr int kStage = kRows * (2 * kK + kVB) + (AT<T>::kBytes == 2 ? 2048 : 1024);
+  // Tiles come in groups with one wait and barrier each: three groups in LDS,
+  // one in use, one there, one on its way; two single tiles where there is no
+  // room for three.
+  static constexpr int kGroup = 6 * kStage <= 160 * 1024 ? 2 : 1;
+  static constexpr int kStages = 3 * kGroup * kStage <= 160 * 1024 ? 3 * kGroup : 2;
+  // operands read ahead of their product, as registers allow
+  static constexpr int kAhead = AT<T>::kBytes == 2 ? 6 : 2;
 };
 
 template <typename T, int DP, int PART>
 __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   using F = Dkv<T, DP>;
-  constexpr bool kV = PART & 1, kK1 = PART & 2, kK2 = PART & 4;  // what is made,
-  constexpr bool kS1 = kV || kK1, kS2 = kV || kK2;               // and from which scores
+  constexpr bool kV = PART & 1, kK = PART & 2;
+  constexpr int kRecs = AT<T>::kBytes == 2 ? 2 : 1;  // loads of the records
   constexpr int E = AT<T>::kBytes, NC = DP / AT<T>::kStep, ND = DP / 32, SP = AT<T>::kSteps32;
   constexpr int RQ = F::kRows * F::kK, RECS = 2 * RQ + F::kRows * F::kVB;  // bytes of a Q tile; where the records lie
-  __shared__ __attribute__((aligned(1024))) char lds[2 * F::kStage];
+  __shared__ __attribute__((aligned(1024))) char lds[F::kStages * F::kStage];
   const AttnShape& S = L.s;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  int id = blockIdx.x;
-  const int combo = id % S.combos;
-  id /= S.combos;
-  const int split = id % L.splits;
-  id /= L.splits;
-  int tok0 = 0, nq = (int)S.nq, nk = (int)S.nk, inside = 1, at = 0;
-  if (L.keyList.blocks) {
-    if (id >= *L.keyList.count) return;
-    const AttnBlock B = L.keyList.blocks[id];
-    tok0 = B.tok;
-    nq = nk = B.n;
-    inside = B.nk > 0;
-    at = B.at;
-  } else {  // the keys that most rows see first
-    at = id * kDkvKeys;
-  }
-  const int batch = combo / S.kv, hk = combo % S.kv, G = S.group;
+  // What this workgroup makes: one block of keys, all its row tiles; or, where
+  // the blocks are few or unequal, an equal stretch of all tiles of all blocks
+  // one after another, which may begin or end inside a block.
+  Stretch W(L, blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);  // neighbours on one XCD
+  Piece P;
+  while (W.next(L, P)) {
+  const int tok0 = P.tok, nq = P.nq, nk = P.nk, at = P.at;
+  const int batch = P.combo / S.kv, hk = P.combo % S.kv, G = S.group;
   const int shift = nk - nq + 1;
   const int key0 = at + wave * 32, key = key0 + (lane & 31);
   const bool valid = key < nk;
@@ -78,7 +139,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
         if (valid && (2 * c + half) * 16 < S.dim * E)
           k[m][c] = *(const lu32x4*)(p + m * S.ks[2] * E + (2 * c + half) * 16);
       }
-    if constexpr (PART & 6) {
+    if constexpr (kK) {
 #pragma unroll
       for (int c = 0; c < 2 * NC; ++c) {
         v[c] = lu32x4{0, 0, 0, 0};
@@ -89,10 +150,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
 
   // row tiles: tokens from the first that sees a key of the workgroup
   const int first = S.causal ? max(at - shift + 1, 0) & ~31 : 0;
-  const int perHead = inside && nq > first ? (nq - first + 31) / 32 : 0;
-  const int tiles = perHead * G;
-  const int share = (tiles + L.splits - 1) / L.splits;
-  const int begin = min(split * share, tiles), end = min(begin + share, tiles);
+  const int perHead = P.inside && nq > first ? (nq - first + 31) / 32 : 0;
+  const int begin = P.begin, end = (int)min((int64_t)P.end, (int64_t)perHead * G);
 
   TileLoader<F::kK, F::kRows, F::kWaves> ldq;
   TileLoader<F::kVB, F::kRows, F::kWaves> ldd;
@@ -102,25 +161,56 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   const char* d0 = (const char*)L.dout + (batch * L.gs[0] + tok0 * L.gs[1] + hk * G * L.gs[2]) * E;
   const int64_t rec0 = ((int64_t)batch * L.heads + hk * G) * S.nq + tok0;
   const uint32_t base = a_lds(lds);
-  // tile i: head i / perHead, tokens from first + 32·(i % perHead)
-  auto issue = [&](int g, int t, uint32_t buf) __attribute__((always_inline)) {
-    const char* q = q0 + (t * S.qs[1] + 2 * g * S.qs[2]) * E;
-    ldq.issue(q, nq - t, buf);
-    ldq.issue(q + S.qs[2] * E, nq - t, buf + RQ);
-    ldd.issue(d0 + (t * L.gs[1] + g * L.gs[2]) * E, nq - t, buf + 2 * RQ);
-    // the records: bf16 recL by wave 0, recD by wave 1; fp32 rec
-    const int64_t r = rec0 + g * S.nq + t;
-    if (wave < 2) {
-      const int i = lane & 31;
-      if constexpr (E == 2) {
-        // lanes past 31 deliver zeros behind the 32 records
-        if (wave == 0 || (PART & 6))
-          f_dma16(__builtin_amdgcn_readfirstlane(buf + RECS + wave * 1024), lane < 32 && i < nq - t ? (uint32_t)i * 16 : kFfnNowhere,
-                  f_buffer((uint64_t)((wave == 0 ? L.recL : L.recD) + r)));
-      } else if (wave == 0) {
-        f_dma16(__builtin_amdgcn_readfirstlane(buf + RECS), lane < 32 && i < nq - t ? (uint32_t)i * 16 : kFfnNowhere,
-                f_buffer((uint64_t)(L.rec + r)));
-      }
+  // The next tile to load: head g, tokens from t.  Past the last tile the loads
+  // deliver zeros.
+  struct Place {
+    int g, t;
+  };
+  auto next = [&](Place& p) __attribute__((always_inline)) {
+    p.t += 32;
+    if (p.t >= nq) {
+      p.t = first;
+      ++p.g;
+    }
+  };
+  Place now{0, first};
+  if (begin < end) now = Place{begin / perHead, first + 32 * (begin % perHead)};
+  Place load = now;
+  int filled = begin;
+  const int64_t qStep = 32 * S.qs[1] * E, dStep = 32 * L.gs[1] * E;
+  const char *q, *d, *rec;
+  auto locate = [&]() __attribute__((always_inline)) {
+    q = q0 + (load.t * S.qs[1] + 2 * load.g * S.qs[2]) * E;
+    d = d0 + (load.t * L.gs[1] + load.g * L.gs[2]) * E;
+    rec = (const char*)(E == 4 ? (const void*)L.rec : wave == 0 ? (const void*)L.recL : (const void*)L.recD) +
+          (rec0 + load.g * S.nq + load.t) * 16;
+  };
+  locate();
+  auto issue = [&](uint32_t buf) __attribute__((always_inline)) {
+    const int left = filled < end ? nq - load.t : 0;
+    if (left >= 32) {
+      ldq.issue(q, buf);
+      ldq.issue(q + S.qs[2] * E, buf + RQ);
+      ldd.issue(d, buf + 2 * RQ);
+    } else {
+      ldq.issue(q, left, buf);
+      ldq.issue(q + S.qs[2] * E, left, buf + RQ);
+      ldd.issue(d, left, buf + 2 * RQ);
+    }
+    // the records: bf16 recL by wave 0, recD by wave 1; fp32 rec by wave 0
+    // (lanes past 31 deliver zeros behind the 32 records)
+    if (wave < kRecs)
+      f_dma16(__builtin_amdgcn_readfirstlane(buf + RECS + wave * 1024),
+              lane < 32 && lane < left ? (uint32_t)lane * 16 : kFfnNowhere, f_buffer((uint64_t)rec));
+    ++filled;
+    const int g = load.g;
+    next(load);
+    if (load.g != g) {
+      locate();
+    } else {
+      q += qStep;
+      d += dStep;
+      rec += 512;
     }
   };
   const RowReader<F::kK> rq(lane);
@@ -140,101 +230,179 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
 #pragma unroll
   for (int n = 0; n < ND; ++n) dk[0][n] = dk[1][n] = dv[n] = dv[ND + n] = af32x16{};
 
-  auto step = [&](uint32_t buf, float lam, int t, bool masked) __attribute__((always_inline)) {
+  // A tile's products in the order they run, each with the LDS operand it
+  // reads: S_1, S_2 (their statistics last), dA and its statistics, dV, dK_1 and
+  // dK_2.  Operands are read kAhead products ahead, past the tile's end those
+  // of the next tile; element-wise work stands between the products, where it
+  // runs beside them.
+  constexpr int nS = NC + 1, nA = kK ? 2 * NC + 1 : 0, nV = kV ? SP * 2 * ND : 0, nK = kK ? SP * ND : 0;
+  constexpr int bS2 = nS, bA = bS2 + nS, bV = bA + nA, bK1 = bV + nV, bK2 = bK1 + nK;
+  constexpr int ALL = bK2 + nK, AHEAD = F::kAhead;
+  constexpr int PERIOD = (ALL + AHEAD - 1) / AHEAD * AHEAD;  // a tile's places in the ring of operands, some idle
+  constexpr bool kAcross = F::kStages >= 3;  // the next tile is there before this one ends
+  auto read = [&](auto stage, auto jc) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value;
+    const uint32_t buf = base + decltype(stage)::value * F::kStage;
     const uint32_t rec = buf + RECS + (lane & 31) * 16;
-    af32x16 s1{}, s2{}, a1{}, a2{};
-    const lu32x4 r = *(a_lds_u4)(uintptr_t)rec;
-    [[maybe_unused]] const float u = half ? 0.f : 1.f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if constexpr (kS1) s1 = a_mma<T>(rq.get(buf, c), k[0][c], s1);
-      if constexpr (kS2) s2 = a_mma<T>(rq.get(buf + RQ, c), k[1][c], s2);
-    }
-    // the statistics' steps come last: added first, each later sum would be
-    // rounded at their size
-    if constexpr (E == 2) {
-      if constexpr (kS1) s1 = a_mma<T>(r, one0, s1);
-      if constexpr (kS2) s2 = a_mma<T>(r, one3, s2);
+    if constexpr (j < bS2) {
+      if constexpr (j < NC) return rq.get(buf, j);
+      else return *(a_lds_u4)(uintptr_t)rec;
+    } else if constexpr (j < bA) {
+      if constexpr (j - bS2 < NC) return rq.get(buf + RQ, j - bS2);
+      else return *(a_lds_u4)(uintptr_t)rec;
+    } else if constexpr (j < bV) {
+      if constexpr (j - bA < 2 * NC) return rd.get(buf + 2 * RQ, j - bA);
+      else return *(a_lds_u4)(uintptr_t)(E == 2 ? rec + 1024 : rec);
+    } else if constexpr (j < bK1) {
+      constexpr int u = (j - bV) / (2 * ND), n = (j - bV) % (2 * ND);
+      return cd.get(buf + 2 * RQ, u, n);
     } else {
-      if constexpr (kS1)
-        s1 = __builtin_amdgcn_mfma_f32_32x32x2f32(fmaxf(__uint_as_float(r[0]) * invc, -1e30f), u, s1, 0, 0, 0);
-      if constexpr (kS2)
-        s2 = __builtin_amdgcn_mfma_f32_32x32x2f32(fmaxf(__uint_as_float(r[1]) * invc, -1e30f), u, s2, 0, 0, 0);
-    }
-    if constexpr (PART & 6) {  // a1 becomes dA − δ_1, a2 dA − δ_2
-#pragma unroll
-      for (int c = 0; c < 2 * NC; ++c) a1 = a_mma<T>(rd.get(buf + 2 * RQ, c), v[c], a1);
-      if constexpr (E == 2) {
-        const lu32x4 d = *(a_lds_u4)(uintptr_t)(rec + 1024);
-        if constexpr (kK2) a2 = a_mma<T>(d, one3, a1);
-        if constexpr (kK1) a1 = a_mma<T>(d, one0, a1);
-      } else {
-        if constexpr (kK2) a2 = __builtin_amdgcn_mfma_f32_32x32x2f32(-__uint_as_float(r[3]), u, a1, 0, 0, 0);
-        if constexpr (kK1) a1 = __builtin_amdgcn_mfma_f32_32x32x2f32(-__uint_as_float(r[2]), u, a1, 0, 0, 0);
-      }
-    }
-    // row t + i sees this lane's key if key < t + i + shift; of a row that sees
-    // one key alone P = 1 whatever the scores, and dS = 0
-    if (masked) {
-      const int n = S.causal ? key - shift - t - 4 * half : -1;
-      const int lone = (S.causal ? 1 - shift - t : -1) - 4 * half;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool on = 8 * (i >> 2) + (i & 3) > n;
-        const bool grad = on && nk > 1 && 8 * (i >> 2) + (i & 3) != lone;
-        if constexpr (kS1) s1[i] = on ? s1[i] : kNegInf;
-        if constexpr (kS2) s2[i] = on ? s2[i] : kNegInf;
-        if constexpr (kK1) a1[i] = grad ? a1[i] : 0.f;
-        if constexpr (kK2) a2[i] = grad ? a2[i] : 0.f;
-      }
-    }
-    float p1[16], p2[16], p[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if constexpr (kS1) p1[i] = a_exp2(s1[i] * S.c);
-      if constexpr (kS2) p2[i] = -lam * a_exp2(s2[i] * S.c);
-      if constexpr (kV) p[i] = p1[i] + p2[i];
-      if constexpr (kK1) p1[i] *= a1[i];
-      if constexpr (kK2) p2[i] *= a2[i];
-    }
-#pragma unroll
-    for (int u = 0; u < SP; ++u) {
-      if constexpr (kV) {
-        const lu32x4 a = a_operand<T>(p, u);
-#pragma unroll
-        for (int n = 0; n < 2 * ND; ++n)
-          dv[n] = a_mma<T>(a, cd.get(buf + 2 * RQ + u * AT<T>::kStep * F::kVB, n), dv[n]);
-      }
-      if constexpr (kK1) {
-        const lu32x4 a = a_operand<T>(p1, u);
-#pragma unroll
-        for (int n = 0; n < ND; ++n) dk[0][n] = a_mma<T>(a, cq.get(buf + u * AT<T>::kStep * F::kK, n), dk[0][n]);
-      }
-      if constexpr (kK2) {
-        const lu32x4 a = a_operand<T>(p2, u);
-#pragma unroll
-        for (int n = 0; n < ND; ++n) dk[1][n] = a_mma<T>(a, cq.get(buf + RQ + u * AT<T>::kStep * F::kK, n), dk[1][n]);
-      }
+      constexpr int m = j >= bK2, i = j - (m ? bK2 : bK1), u = i / ND, n = i % ND;
+      return cq.get(buf + m * RQ, u, n);
     }
   };
+  lu32x4 ring[AHEAD];
+  const float unit = half ? 0.f : 1.f;
+  // one statistics step: record values 0, 1, 2 (first) or 3, 4, 5 as three bf16, or fp32 value `at` times f
+  auto stat = [&](lu32x4 r, auto first, float value, af32x16 c) __attribute__((always_inline)) {
+    if constexpr (E == 2) return a_mma<T>(r, decltype(first)::value ? one0 : one3, c);
+    else return __builtin_amdgcn_mfma_f32_32x32x2f32(value, unit, c, 0, 0, 0);
+  };
+  auto tile = [&](auto stage, float lam, int t, int rows, bool masked, auto&& between) __attribute__((always_inline)) {
+    constexpr auto after = std::integral_constant<int, (decltype(stage)::value + 1) % F::kStages>{};
 
-  uint32_t buf = base;
-  int g = perHead ? begin / perHead : 0, i = begin - g * perHead;
-  if (begin < end) issue(g, first + 32 * i, base);
-  for (int tile = begin; tile < end; ++tile) {
+    af32x16 s1{}, s2{}, a1{}, a2{};
+    float p1[16], p2[16], p[16];
+    lu32x4 op{};
+    // elements [16·i/n, 16·(i+1)/n) of an element-wise step spread over n products
+    auto spread = [&](auto ic, auto nc, auto&& f) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value, n = decltype(nc)::value;
+      if constexpr (i >= 0 && i < n) {
+#pragma unroll
+        for (int e = 16 * i / n; e < 16 * (i + 1) / n; ++e) f(e);
+      }
+    };
+    auto first = [&](int e) __attribute__((always_inline)) { p1[e] = a_exp2(s1[e] * S.c); };
+    auto second = [&](int e) __attribute__((always_inline)) { p2[e] = -lam * a_exp2(s2[e] * S.c); };
+    auto grads = [&](int e) __attribute__((always_inline)) {
+      p1[e] *= a1[e];
+      p2[e] *= a2[e];
+    };
+    // row t + i sees this lane's key if key < t + i + shift; of a row that sees
+    // one key alone P = 1 whatever the scores, and dS = 0
+    const int n0 = S.causal ? key - shift - t - 4 * half : -1;
+    const int lone = (S.causal ? 1 - shift - t : -1) - 4 * half;
+    a_for<0, PERIOD>([&](auto jc) __attribute__((always_inline)) {
+      constexpr int j = decltype(jc)::value;
+      if constexpr (j == PERIOD - AHEAD) between();
+      const lu32x4 r = ring[j % AHEAD];
+      if constexpr (j + AHEAD < ALL) ring[j % AHEAD] = read(stage, std::integral_constant<int, j + AHEAD>{});
+      else if constexpr (kAcross && j + AHEAD >= PERIOD)
+        ring[j % AHEAD] = read(after, std::integral_constant<int, j + AHEAD - PERIOD>{});
+      if constexpr (j >= ALL) return;
+      if constexpr (j < bS2) {
+        if constexpr (j < NC) s1 = a_mma<T>(r, k[0][j], s1);
+        else s1 = stat(r, std::true_type{}, fmaxf(__uint_as_float(r[0]) * invc, -1e30f), s1);
+      } else if constexpr (j < bA) {
+        if constexpr (j - bS2 < NC) s2 = a_mma<T>(r, k[1][j - bS2], s2);
+        else s2 = stat(r, std::false_type{}, fmaxf(__uint_as_float(r[1]) * invc, -1e30f), s2);
+      } else if constexpr (j < bV) {
+        if constexpr (j - bA < 2 * NC) {
+          a1 = a_mma<T>(r, v[j - bA], a1);
+        } else {
+          a2 = stat(r, std::false_type{}, -__uint_as_float(r[3]), a1);
+          a1 = stat(r, std::true_type{}, -__uint_as_float(r[2]), a1);
+        }
+      } else if constexpr (j < bK1) {
+        constexpr int u = (j - bV) / (2 * ND), n = (j - bV) % (2 * ND);
+        if constexpr (n == 0) op = a_operand<T>(p, u);
+        dv[n] = a_mma<T>(op, r, dv[n]);
+      } else {
+        constexpr int m = j >= bK2, i = j - (m ? bK2 : bK1), u = i / ND, n = i % ND;
+        if constexpr (n == 0) op = m ? a_operand<T>(p2, u) : a_operand<T>(p1, u);
+        dk[m][n] = a_mma<T>(op, r, dk[m][n]);
+      }
+      // probabilities of the first map beside the second's scores, of the second
+      // beside dA
+      spread(std::integral_constant<int, j - bS2 - 1>{}, std::integral_constant<int, nS>{}, first);
+      if constexpr (kK) {
+        spread(std::integral_constant<int, j - bA - 1>{}, std::integral_constant<int, nA - 1>{}, second);
+      } else if constexpr (j == bA - 1) {
+        spread(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{}, first);
+        spread(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{}, second);
+      }
+      if constexpr (j == bV - 1) {
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int row = 8 * (i >> 2) + (i & 3);
+            const bool on = (row > n0) & (row < rows);
+            p1[i] = on ? p1[i] : 0.f;
+            p2[i] = on ? p2[i] : 0.f;
+            if constexpr (kK) {
+              const bool grad = on & (nk > 1) & (row != lone);
+              a1[i] = grad ? a1[i] : 0.f;
+              a2[i] = grad ? a2[i] : 0.f;
+            }
+          }
+        }
+        if constexpr (kV) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[i] = p1[i] + p2[i];
+        } else {
+          spread(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{}, grads);
+        }
+      }
+      if constexpr (kV && kK) spread(std::integral_constant<int, j - bV>{}, std::integral_constant<int, nV>{}, grads);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  auto prologue = [&](auto stage) __attribute__((always_inline)) {
+    a_for<0, AHEAD>([&](auto jc) __attribute__((always_inline)) { ring[decltype(jc)::value] = read(stage, jc); });
+  };
+  // read when the head changes and waited for there: a wait where it is used
+  // would be one for the loads into LDS too
+  auto lambda = [&](int g) __attribute__((always_inline)) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(S.lam[hk * G + g])));
+  };
+  float lam = begin < end ? lambda(now.g) : 0.f;
+  constexpr int NS = F::kStages;
+  __syncthreads();  // every wave has left the LDS of the piece before
+  if (begin < end) {
+    for (int i = 0; i < (kAcross ? 2 * F::kGroup : 1); ++i) issue(base + i * F::kStage);
     a_landed();
-    const uint32_t other = 2 * base + F::kStage - buf;
-    const int t = first + 32 * i;
-    const float lam = S.lam[hk * G + g];
-    if (++i == perHead) {
-      i = 0;
-      ++g;
-    }
-    if (tile + 1 < end) issue(g, first + 32 * i, other);
-    // no row of the tile sees a key of this wave: nothing to add
-    if (!S.causal || t + 31 + shift > key0) step(buf, lam, t, nk == 1 || (S.causal && t + shift < key0 + 32));
-    buf = other;
+    prologue(std::integral_constant<int, 0>{});
   }
+  // whole rounds of the stages: tiles past the last add nothing
+  for (int i = begin; i < end; i += NS) {
+    a_for<0, NS>([&](auto sc) __attribute__((always_inline)) {
+      constexpr int s = decltype(sc)::value, U = F::kGroup;
+      const int rows = i + s < end ? nq - now.t - 4 * half : 0;
+      const bool masked = nk == 1 || (S.causal && now.t + shift < key0 + 32) || i + s >= end || nq - now.t < 32;
+      if constexpr (kAcross) {
+        tile(sc, lam, now.t, rows, masked, [&]() __attribute__((always_inline)) {
+          if constexpr (s % U == U - 1) {
+            // the next group is there, and the one before this is free
+            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+            a_for<0, U>([&](auto uc) __attribute__((always_inline)) {
+              issue(base + (s + U + 1 + decltype(uc)::value) % NS * F::kStage);
+            });
+          }
+        });
+      } else {
+        issue(base + (s + 1) % NS * F::kStage);
+        tile(sc, lam, now.t, rows, masked, [] {});
+        a_landed();
+        prologue(std::integral_constant<int, (s + 1) % NS>{});
+      }
+      const int g = now.g;
+      next(now);
+      if (now.g != g) lam = lambda(min(now.g, G - 1));
+    });
+  }
+  // no load may still be on its way into LDS when the workgroup ends
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // registers run over keys here: lane l has column l % 32 of every sum
 #pragma unroll
@@ -242,12 +410,14 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
     const int kk = key0 + 8 * (r >> 2) + 4 * half + (r & 3);
     if (kk >= nk) continue;
     const int64_t tok = tok0 + kk;
-    if (L.splits > 1) {
-      float* o = L.part + (((int64_t)split * S.combos + combo) * S.nk + tok) * (4 * DP) + (lane & 31);
+    if (P.slot >= 0) {
+      float* o = L.part + (P.slot * kDkvKeys + kk - at) * (4 * DP) + (lane & 31);
 #pragma unroll
       for (int n = 0; n < ND; ++n) {
-        if constexpr (kK1) o[n * 32] = dk[0][n][r];
-        if constexpr (kK2) o[DP + n * 32] = dk[1][n][r];
+        if constexpr (kK) {
+          o[n * 32] = dk[0][n][r];
+          o[DP + n * 32] = dk[1][n][r];
+        }
         if constexpr (kV) {
           o[2 * DP + n * 32] = dv[n][r];
           o[2 * DP + (ND + n) * 32] = dv[ND + n][r];
@@ -260,9 +430,9 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
 #pragma unroll
     for (int n = 0; n < ND; ++n) {
       const int c = n * 32 + (lane & 31);
-      if (c < S.dim) {
-        if constexpr (kK1) LType<T>::put(ok, c, dk[0][n][r] * L.scale);
-        if constexpr (kK2) LType<T>::put(ok + L.dks[2] * E, c, dk[1][n][r] * L.scale);
+      if (kK && c < S.dim) {
+        LType<T>::put(ok, c, dk[0][n][r] * L.scale);
+        LType<T>::put(ok + L.dks[2] * E, c, dk[1][n][r] * L.scale);
       }
       if constexpr (kV) {
         if (c < 2 * S.dim) LType<T>::put(ov, c, dv[n][r]);
@@ -270,41 +440,53 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
       }
     }
   }
+  }
 }
 
-// The splits' sums added in order: a workgroup per key of a combo, four
-// columns a thread.
-template <typename T, int DP> __global__ __launch_bounds__(DP) void attn_dkv_join(const AttnGradLaunch L) {
-  constexpr int E = AT<T>::kBytes;
+// The sums of blocks that several stretches share, added in the stretches'
+// order by the workgroups of the one the block begins in: its part lies in that
+// one's second slot, the others in the next ones' first.
+template <typename T, int DP> __global__ __launch_bounds__(256) void attn_dkv_join(const AttnGradLaunch L) {
+  constexpr int E = AT<T>::kBytes, kKeys = 16;
   const AttnShape& S = L.s;
-  const int64_t combo = blockIdx.x / S.nk, key = blockIdx.x - combo * S.nk;
-  const int c0 = threadIdx.x * 4;
-  const int64_t all = S.combos * S.nk * (4 * DP);
-  const float* p = L.part + (combo * S.nk + key) * (4 * DP) + c0;
-  lf32x4 s = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < L.splits; ++i) s += *(const lf32x4*)(p + i * all);
+  const Stretch W(L, blockIdx.x);
+  if (W.stop >= W.total) return;
+  const int64_t combo = W.stop / W.each;  // of the next stretch's first tile
+  const int b = W.find(L, W.stop - combo * W.each);
+  const int64_t from = combo * W.each + L.cum[b], to = combo * W.each + L.cum[b + 1];
+  if (from >= W.stop || from < W.pos) return;  // not shared, or begun before
+  const AttnBlock B = L.keyList.blocks[b];
   const int64_t batch = combo / S.kv, hk = combo % S.kv;
-  if (c0 < 2 * DP) {
-    const int m = c0 >= DP, c = c0 - m * DP;
-    char* o = (char*)L.dk + (batch * L.dks[0] + key * L.dks[1] + (2 * hk + m) * L.dks[2]) * E;
-    for (int i = 0; i < 4; ++i)
-      if (c + i < S.dim) LType<T>::put(o, c + i, s[i] * L.scale);
-  } else {
-    const int c = c0 - 2 * DP;
-    char* o = (char*)L.dv + (batch * L.dvs[0] + key * L.dvs[1] + hk * L.dvs[2]) * E;
-    for (int i = 0; i < 4; ++i)
-      if (c + i < 2 * S.dim) LType<T>::put(o, c + i, s[i]);
+  constexpr int64_t kSlot = (int64_t)kDkvKeys * 4 * DP;
+  for (int i = threadIdx.x; i < kKeys * DP; i += 256) {
+    const int key = blockIdx.y * kKeys + i / DP, c0 = i % DP * 4;
+    if (B.at + key >= B.n) break;
+    const float* p = L.part + (int64_t)key * (4 * DP) + c0;
+    lf32x4 s = *(const lf32x4*)(p + (2 * (int64_t)blockIdx.x + 1) * kSlot);
+    for (int64_t w = blockIdx.x + 1; w * W.per < to; ++w) s += *(const lf32x4*)(p + 2 * w * kSlot);
+    const int64_t tok = B.tok + B.at + key;
+    if (c0 < 2 * DP) {
+      const int m = c0 >= DP, c = c0 - m * DP;
+      char* o = (char*)L.dk + (batch * L.dks[0] + tok * L.dks[1] + (2 * hk + m) * L.dks[2]) * E;
+      for (int j = 0; j < 4; ++j)
+        if (c + j < S.dim) LType<T>::put(o, c + j, s[j] * L.scale);
+    } else {
+      const int c = c0 - 2 * DP;
+      char* o = (char*)L.dv + (batch * L.dvs[0] + tok * L.dvs[1] + hk * L.dvs[2]) * E;
+      for (int j = 0; j < 4; ++j)
+        if (c + j < 2 * S.dim) LType<T>::put(o, c + j, s[j]);
+    }
   }
 }
 
 template <typename T, int DP, int PART, int... REST> hipError_t run(const AttnGradLaunch& L, hipStream_t st) {
-  attn_dkv<T, DP, PART><<<dim3((unsigned)(L.s.combos * L.keyBlocks * L.splits)), 256, 0, st>>>(L);
+  attn_dkv<T, DP, PART><<<dim3((unsigned)(L.streams ? L.streams : L.s.combos * L.keyBlocks)), 256, 0, st>>>(L);
   const hipError_t e = hipGetLastError();
   if constexpr (sizeof...(REST) > 0) return e != hipSuccess ? e : run<T, DP, REST...>(L, st);
   else return e;
 }
 template <typename T, int DP> hipError_t join(const AttnGradLaunch& L, hipStream_t st) {
-  attn_dkv_join<T, DP><<<dim3((unsigned)(L.s.combos * L.s.nk)), DP, 0, st>>>(L);
+  attn_dkv_join<T, DP><<<dim3(L.streams, kDkvKeys / 16), 256, 0, st>>>(L);
   return hipGetLastError();
 }
 
@@ -312,8 +494,8 @@ template <typename T, int DP> hipError_t join(const AttnGradLaunch& L, hipStream
 
 hipError_t launch_attn_dkv(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {
   // operands and sums of 32 wide keys are more than a wave's registers: more passes
-  if (bf16) return dp == 64 ? run<Bf16, 64, 7>(L, st) : run<Bf16, 128, 1, 6>(L, st);
-  return dp == 64 ? run<float, 64, 7>(L, st) : run<float, 128, 1, 2, 4>(L, st);
+  if (bf16) return dp == 64 ? run<Bf16, 64, 3>(L, st) : run<Bf16, 128, 1, 2>(L, st);
+  return dp == 64 ? run<float, 64, 3>(L, st) : run<float, 128, 1, 2>(L, st);
 }
 hipError_t launch_attn_dkv_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {
   if (bf16) return dp == 64 ? join<Bf16, 64>(L, st) : join<Bf16, 128>(L, st);

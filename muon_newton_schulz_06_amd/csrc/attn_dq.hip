@@ -148,14 +148,13 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
     }
 #pragma unroll
     for (int u = 0; u < SP; ++u) {
-      const uint32_t kr = kt + u * AT<T>::kStep * F::kK;
       lu32x4 b1, b2;
       if constexpr (k1st) b1 = a_operand<T>(e1, u);
       if constexpr (k2nd) b2 = a_operand<T>(e2, u);
 #pragma unroll
       for (int n = 0; n < ND; ++n) {
-        if constexpr (k1st) acc[0][n] = a_mma<T>(ck.get(kr, n), b1, acc[0][n]);
-        if constexpr (k2nd) acc[1][n] = a_mma<T>(ck.get(kr + BN * F::kK, n), b2, acc[1][n]);
+        if constexpr (k1st) acc[0][n] = a_mma<T>(ck.get(kt, u, n), b1, acc[0][n]);
+        if constexpr (k2nd) acc[1][n] = a_mma<T>(ck.get(kt + BN * F::kK, u, n), b2, acc[1][n]);
       }
     }
   };

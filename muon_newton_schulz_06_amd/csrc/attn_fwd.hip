@@ -188,7 +188,7 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
     for (int t = 0; t < SP; ++t)
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
-        const lu32x4 a = cd.get(vt + t * AT<T>::kStep * F::kV, n);
+        const lu32x4 a = cd.get(vt, t, n);
 #pragma unroll
         for (int r = 0; r < RS; ++r) o[r][n] = a_mma<T>(a, p[r][t], o[r][n]);
       }
@@ -282,64 +282,77 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
   }
 }
 
-// The splits' results of a row joined, a wave per row: weights from the
-// logarithms of their sums, in split order.
+// The splits' results of a row joined, a workgroup per row: the splits' weights
+// from the logarithms of their sums, then both maps' columns, four a thread,
+// the splits dealt out to as many groups of threads as there are and the groups
+// added in order.
 template <typename T, int DP> __global__ __launch_bounds__(256) void attn_join(const AttnFwdLaunch L) {
-  constexpr int E = AT<T>::kBytes, PER = 2 * DP / 64;
+  constexpr int E = AT<T>::kBytes, COLS = DP, GROUPS = 256 / COLS;  // threads for 2 · 2·DP columns
+  __shared__ float weight[2][kMaxSplits], top[2], sums[2];
+  __shared__ lf32x4 part[GROUPS][COLS];
   const AttnShape& S = L.s;
-  const int lane = threadIdx.x & 63;
-  const int64_t rows = S.nq * S.group, all = rows * S.combos;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (id >= all) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t rows = S.nq * S.group, all = rows * S.combos, id = blockIdx.x;
   const int combo = (int)(id / rows);
   const int64_t row = id - combo * rows;
   const int64_t tok = row / S.group;
   const int batch = combo / S.kv, head = (combo % S.kv) * S.group + (int)(row - tok * S.group);
-  float res[2][PER], top[2], sum[2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    top[m] = kNegInf;
+  if (wave < 2) {  // a wave per map
+    float m = kNegInf, l = 0.f;
     for (int s = lane; s < L.splits; s += 64) {
-      const float v = L.partStat[(s * all + id) * 2 + m];
-      top[m] = v != v || v > top[m] ? v : top[m];
+      const float v = L.partStat[(s * all + id) * 2 + wave];
+      weight[wave][s] = v;
+      m = v != v || v > m ? v : m;
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
-      const float v = __shfl_xor(top[m], o, 64);
-      top[m] = v != v || v > top[m] ? v : top[m];
+      const float v = __shfl_xor(m, o, 64);
+      m = v != v || v > m ? v : m;
     }
-    sum[m] = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) res[m][i] = 0.f;
+    for (int s = lane; s < L.splits; s += 64) {
+      const float w = m == kNegInf ? 0.f : a_exp2(weight[wave][s] - m);
+      weight[wave][s] = w;
+      l += w;
+    }
+    l = l_wave_sum(l);
+    if (lane == 0) {
+      top[wave] = m;
+      sums[wave] = l;
+      if (S.stat) S.stat[((int64_t)combo * 2 + wave) * rows + row] = m == kNegInf ? -kNegInf : m + a_log2(l);
+    }
   }
-  for (int s = 0; s < L.splits; ++s) {
-    const float* d = L.part + (s * all + id) * (4 * DP) + lane * PER;
+  __syncthreads();
+  const int col = tid % COLS, group = tid / COLS, map = col / (COLS / 2);
+  const float* d = L.part + id * (4 * DP) + col * 4;
+  lf32x4 res = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = group; s < L.splits; s += GROUPS) {
+    const float w = weight[map][s];
+    const lf32x4 v = *(const lf32x4*)(d + s * all * (4 * DP));
+    // a split whose keys the row does not see left zeros
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const float v = L.partStat[(s * all + id) * 2 + m];
-      if (v == kNegInf) continue;
-      const float w = a_exp2(v - top[m]);
-      sum[m] += w;
+    for (int i = 0; i < 4; ++i) res[i] += w * v[i];
+  }
+  part[group][col] = res;
+  __syncthreads();
+  if (tid >= COLS / 2) return;
+  lf32x4 r[2];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) res[m][i] += w * d[m * 2 * DP + i];
-    }
+  for (int m = 0; m < 2; ++m) {
+    lf32x4 s = part[0][m * (COLS / 2) + tid];
+    for (int g = 1; g < GROUPS; ++g) s += part[g][m * (COLS / 2) + tid];
+    const float inv = top[m] == kNegInf ? 0.f : 1.f / sums[m];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[m][i] = s[i] * inv;
   }
   const float lam = S.lam[head];
   char* o = (char*)L.out + (batch * L.os[0] + tok * L.os[1] + head * L.os[2]) * E;
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const float inv = top[m] == kNegInf ? 0.f : 1.f / sum[m];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) res[m][i] *= inv;
-    if (S.stat && lane == 0)
-      S.stat[((int64_t)combo * 2 + m) * rows + row] = top[m] == kNegInf ? -kNegInf : top[m] + a_log2(sum[m]);
-  }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = lane * PER + i;
+  for (int i = 0; i < 4; ++i) {
+    const int c = tid * 4 + i;
     if (c >= 2 * S.dim) continue;
-    LType<T>::put(o, c, res[0][i] - lam * res[1][i]);
-    if (S.o2) LType<T>::put((char*)S.o2 + (id * S.pitch) * E, c, res[1][i]);
+    LType<T>::put(o, c, r[0][i] - lam * r[1][i]);
+    if (S.o2) LType<T>::put((char*)S.o2 + (id * S.pitch) * E, c, r[1][i]);
   }
 }
 
@@ -349,7 +362,7 @@ template <typename T, int DP, bool FEW> hipError_t run(const AttnFwdLaunch& L, h
 }
 template <typename T, int DP> hipError_t join(const AttnFwdLaunch& L, hipStream_t st) {
   const int64_t rows = L.s.nq * L.s.group * L.s.combos;
-  attn_join<T, DP><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, st>>>(L);
+  attn_join<T, DP><<<dim3((unsigned)rows), 256, 0, st>>>(L);
   return hipGetLastError();
 }
 

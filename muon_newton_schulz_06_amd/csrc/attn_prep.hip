@@ -1,5 +1,5 @@
-// What precedes the attention products: a packed batch's block lists, and
-// aligned copies of tensors that the 16-byte loads into LDS cannot read.
+// What precedes the attention products: the block lists, and aligned copies
+// of tensors that the 16-byte loads into LDS cannot read.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -27,7 +27,7 @@ template <typename F> __device__ __forceinline__ int64_t scan(int64_t v, int64_t
   return v;
 }
 
-// The block lists of a packed batch, one workgroup per list.  The spans are the
+// The block lists of a batch, one workgroup per list.  The spans are the
 // rows before the first offset, each sequence, and the rows after the last one;
 // the first and last of these have no keys.  Offsets are cut to [0, tokens] and
 // one below its predecessor is raised to it, so whatever they hold, every row
@@ -36,7 +36,7 @@ __global__ __launch_bounds__(kPrep) void attn_prep(const AttnPrepLaunch L) {
   __shared__ int64_t red[kPrep / 64];
   __shared__ int begin[kPrep], size[kPrep], first[kPrep];  // a chunk of spans: tokens, blocks before
   const auto& D = L.list[blockIdx.x];
-  const int tid = threadIdx.x, spans = L.sequences + 2;
+  const int tid = threadIdx.x, spans = L.offsets ? L.sequences + 2 : 1;
   auto larger = [](int64_t a, int64_t b) { return a > b ? a : b; };
   auto sum = [](int64_t a, int64_t b) { return a + b; };
   int64_t edge = 0;  // where the chunk's first span begins
@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kPrep) void attn_prep(const AttnPrepLaunch L) {
   for (int s0 = 0; s0 < spans; s0 += kPrep) {
     const int s = s0 + tid;
     int64_t end = L.tokens;  // of span s
-    if (s <= L.sequences) end = min(max(L.offsets[s], 0), L.tokens);
+    if (L.offsets && s <= L.sequences) end = min(max(L.offsets[s], 0), L.tokens);
     end = scan(larger(end, edge), red, larger);
     size[tid] = (int)end;  // for the neighbour
     __syncthreads();
@@ -66,13 +66,31 @@ __global__ __launch_bounds__(kPrep) void attn_prep(const AttnPrepLaunch L) {
         if (first[mid] <= b) lo = mid;
         else hi = mid - 1;
       }
-      const bool inside = s0 + lo > 0 && s0 + lo <= L.sequences;
+      const bool inside = !L.offsets || (s0 + lo > 0 && s0 + lo <= L.sequences);
       D.blocks[done + b] = AttnBlock{begin[lo], size[lo], inside ? size[lo] : 0, (b - first[lo]) * D.per};
     }
     done += total;
     __syncthreads();
   }
   if (tid == 0) *D.count = done;
+  if (!D.cum) return;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < done; b0 += kPrep) {
+    int64_t n = 0;
+    if (b0 + tid < done) {
+      const AttnBlock B = D.blocks[b0 + tid];
+      const int64_t nq = L.offsets ? B.n : L.queries, shift = B.n - nq + 1;
+      const int64_t first = L.causal ? max(B.at - shift + 1, (int64_t)0) & ~(int64_t)31 : 0;
+      n = B.nk > 0 && nq > first ? (nq - first + 31) / 32 * L.group : 1;
+    }
+    const int64_t upto = scan(n, red, sum);
+    if (b0 + tid < done) D.cum[b0 + tid] = before + upto - n;
+    if (tid == kPrep - 1) red[0] = upto;
+    __syncthreads();
+    before += red[0];
+    __syncthreads();
+  }
+  if (tid == 0) D.cum[done] = before;
 }
 
 // One workgroup per 256 chunks of a tensor's copy; the pitch's end holds zeros.

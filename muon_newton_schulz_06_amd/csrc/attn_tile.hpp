@@ -11,6 +11,8 @@
 // 16·s + 4·half + {0…3, 8…11} (bf16) or 8·s + 4·half + {0…3} (fp32).
 #pragma once
 
+#include <type_traits>
+
 #include "dma.hpp"
 #include "layers.hpp"
 
@@ -22,12 +24,20 @@ typedef short as16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) as16x4* a_lds_s4;
 typedef __attribute__((address_space(3))) const lu32x4* a_lds_u4;
 typedef __attribute__((address_space(3))) const uint32_t* a_lds_u1;
+typedef __attribute__((address_space(3))) lf32x4* a_lds_f4;
 
 template <typename T> struct AT {
   static constexpr int kBytes = 16 / LType<T>::kVec;
   static constexpr int kStep = 2 * LType<T>::kVec;  // contraction of a step
   static constexpr int kSteps32 = 32 / kStep;       // steps over the rows of a result
 };
+
+template <int B, int E, typename F> __device__ __forceinline__ void a_for(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    a_for<B + 1, E>(f);
+  }
+}
 
 __device__ __forceinline__ uint32_t a_lds(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
@@ -59,12 +69,15 @@ template <typename T> __device__ __forceinline__ lu32x4 a_operand(const float (&
 }
 
 // LDS tiles of rows of RB bytes; 16-byte chunk c of row r lies at c ^ a_swz(r).
-// Row reads take the same chunk of 32 rows: eight consecutive rows differ in
-// the chunk's low three bits.  Column reads take 64 (bf16) bytes of four
+// LDS has 64 banks, 256 bytes; 16 lanes of a 16-byte read are served at a time.
+// Row reads take the same chunk of 32 rows: sixteen rows that differ in their
+// low four bits (whichever of bits 2 to 4 the hardware's groups vary) fall into
+// different chunks of 256 bytes.  Column reads take 64 bytes (bf16) of four
 // consecutive rows: those differ in which 64 bytes of 256 they fall into.
+// (Measured: without bit 3 a row read took 8 cycles, not 4.)
 template <int RB> __device__ __forceinline__ int a_swz(int r) {
-  if constexpr (RB == 128) return (r >> 1 & 1) << 2 | (r & 1) << 1 | (r >> 2 & 1);
-  else return (r & 1) << 2 | (r >> 1 & 1) * 10 | (r >> 2 & 1);
+  if constexpr (RB == 128) return (r >> 1 & 1) << 2 | (r >> 2 & 1) << 1 | (r >> 3 & 1);
+  else return (r & 1) << 2 | (r >> 1 & 1) << 3 | (r >> 2 & 1) | (r >> 3 & 1) << 1;
 }
 
 // A lane's reads of row operands: rows 32·n + lane % 32, step c.
@@ -95,18 +108,19 @@ template <typename T, int RB> struct ColReader {
       at = r * RB + ((((lane & 31) >> 2) ^ a_swz<RB>(r)) << 4) + (lane & 3) * 4;
     }
   }
-  // tile: LDS address of the step's first row; n a constant
-  __device__ __forceinline__ lu32x4 get(uint32_t tile, int n) const {
+  // tile: LDS address of the tile's first row; step s of its rows; n a constant
+  __device__ __forceinline__ lu32x4 get(uint32_t tile, int s, int n) const {
     if constexpr (AT<T>::kBytes == 2) {
-      const uint32_t a = (at ^ (n << 6)) + tile;
+      const uint32_t a = (at ^ (n << 6)) + s * (16 * RB) + tile;
+      const uint32_t b = (at ^ (n << 6) ^ (a_swz<RB>(8) << 4)) + (s * 16 + 8) * RB + tile;
       const as16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((a_lds_s4)(uintptr_t)a);
-      const as16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((a_lds_s4)(uintptr_t)(a + 8 * RB));
+      const as16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((a_lds_s4)(uintptr_t)b);
       return __builtin_bit_cast(lu32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
       lu32x4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        v[i] = *(a_lds_u1)(uintptr_t)((at ^ (n << 7) ^ (a_swz<RB>(i) << 4)) + i * RB + tile);
+        v[i] = *(a_lds_u1)(uintptr_t)((at ^ (n << 7) ^ (a_swz<RB>((s & 1) * 8 + i) << 4)) + (s * 8 + i) * RB + tile);
       return v;
     }
   }
@@ -127,6 +141,12 @@ template <int RB, int ROWS, int NW> struct TileLoader {
       const int r = row0 + p * kRowsPer, c = (lane % kChunks) ^ a_swz<RB>(r);
       off[p] = c * 16 < bytes ? (uint32_t)(r * ldBytes) + c * 16 : kFfnNowhere;
     }
+  }
+  // a tile of which every row is there
+  __device__ __forceinline__ void issue(const char* base, uint32_t dst) const {
+    const fi32x4 buf = f_buffer((uint64_t)base);
+#pragma unroll
+    for (int p = 0; p < N; ++p) f_dma16(__builtin_amdgcn_readfirstlane(dst + (wave * N + p) * 1024), off[p], buf);
   }
   __device__ __forceinline__ void issue(const char* base, int64_t left, uint32_t dst) const {
     const fi32x4 buf = f_buffer((uint64_t)base);
