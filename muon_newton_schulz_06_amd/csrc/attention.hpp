@@ -109,6 +109,16 @@ hipError_t launch_attn_join(bool bf16, int dp, const AttnFwdLaunch& L, hipStream
 // What the backward products need of a row: {L1, L2, δ1, δ2}, and for bf16 the
 // same as operands of a product (see attn_dkv), two 16-byte records per row.
 // All are [batch][head][token].
+// How the blocks (of rows or keys) of all combos are dealt out: a workgroup per
+// block (streams = 0), or equal stretches of the tiles of all blocks, at least
+// `least` tiles each.
+struct AttnRuns {
+  AttnList list;
+  const int64_t* cum;  // tiles of the list's blocks before each, of all at [count]
+  int32_t blocks;      // of a combo, without a list or as an upper bound
+  int32_t streams, least;
+};
+
 struct AttnGradLaunch {
   AttnShape s;
   const void* dout;  // whole aligned chunks
@@ -125,38 +135,38 @@ struct AttnGradLaunch {
   float* dlam;  // null: not wanted
   float scale;
   int32_t batch, heads;
-  // attn_dkv: blocks of keys; attn_dq: blocks of rows
-  AttnList keyList, rowList;
-  int32_t keyBlocks, rowBlocks;
-  // attn_dkv in stretches of tiles (see there): their number (a multiple of 8;
-  // 0: a workgroup per block, no list), at least `least` tiles each; tiles of the
-  // list's blocks before each; [2·stretch][128 keys][4·DP] sums of dk1, dk2, dv
-  int32_t streams, least, packed;
-  const int64_t* cum;
+  AttnRuns keyRuns, rowRuns;  // of attn_dkv, attn_dq
+  int32_t packed;
+  // sums of blocks that stretches share: attn_dkv [2·stretch][128 keys][4·DP] of
+  // dk1, dk2, dv; attn_dq [2·stretch][128 rows][2·DP + 1] of dq1, dq2 and λ's
   float* part;
 };
 constexpr int kDkvKeys = 128, kDqRows = 128;
 hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, hipStream_t st);
 hipError_t launch_attn_dkv(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
 hipError_t launch_attn_dkv_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
+int attn_dq_keys(bool bf16, int dp);  // of a tile
 hipError_t launch_attn_dq(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
+hipError_t launch_attn_dq_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
 hipError_t launch_attn_dlam(const AttnGradLaunch& L, hipStream_t st);
 
 // Block lists: units·n rows of a sequence of n tokens are cut into blocks of
 // `per`.  Without offsets the tokens are one sequence.
 struct AttnPrepLaunch {
   const int32_t* offsets;
-  int32_t sequences, tokens;
+  int32_t sequences;
   struct {
     AttnBlock* blocks;
     int32_t* count;
-    int32_t units, per;
-    // null, or for blocks of keys: row tiles of 32 (one at least) of the blocks
-    // before each, of all at [count]
+    int32_t tokens, units, per;
+    // null, or tiles (one at least) of the blocks before each, of all at [count]:
+    // of blocks of keys (units 1) tiles of 32 rows, of blocks of rows tiles of
+    // `tile` keys
     int64_t* cum;
+    int32_t tile;
   } list[2];
   int32_t group, causal;
-  int64_t queries;  // of the one sequence
+  int64_t queries, keys;  // of the one sequence
   int32_t lists;
 };
 hipError_t launch_attn_prep(const AttnPrepLaunch& L, hipStream_t st);

@@ -345,10 +345,16 @@ AttnLayout attn_layout(const muon_diff_attention_t& f) {
   return l;
 }
 
-struct AttnGradLayout {
-  size_t list[2], cum, q, k, v, dout, rec, recL, recD, rowLam, part, total;
-  int64_t keyBlocks, rowBlocks;
+// How the blocks of a pass are dealt out (see AttnRuns), and where its list lies.
+struct RunsPlan {
+  int64_t blocks;
   int streams, least;
+  size_t list, cum;
+};
+
+struct AttnGradLayout {
+  size_t q, k, v, dout, rec, recL, recD, rowLam, part, total;
+  RunsPlan keys, rows;
 };
 
 AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout& l, const void* dout,
@@ -364,27 +370,27 @@ AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout
     at += align256(n);
     return o;
   };
-  g.keyBlocks = blocks_of(f.keys, kDkvKeys);
-  g.rowBlocks = blocks_of(l.rows, kDqRows);
-  // attn_dkv runs a workgroup per block of keys where these fill the 256 CUs
-  // twice (the longer ones first, so that the sums of two come out alike); else
-  // equal stretches of all their tiles, one per CU, or fewer of `least` tiles.
-  // The sums of a block that stretches share are written and read once more.
-  const bool packed = f.sequences > 0;
-  g.least = bf16 && l.dp == 64 ? 6 : 3;
-  if (l.combos > 0 && f.keys > 0 && (packed || l.combos * g.keyBlocks < 512)) {
-    const double tiles = (double)l.combos * g.keyBlocks * (f.heads / f.kv_heads) * blocks_of(f.queries, 32);
-    g.streams = (int)std::min(256.0, std::max(8.0, std::ceil(tiles / g.least / 8) * 8));
-  }
-  if (packed) {
-    g.keyBlocks = f.keys / kDkvKeys + f.sequences + 2;
-    g.rowBlocks = l.rows / kDqRows + f.sequences + 2;
-    g.list[1] = take(256 + (size_t)g.rowBlocks * sizeof(AttnBlock));
-  }
-  if (g.streams) {
-    g.list[0] = take(256 + (size_t)g.keyBlocks * sizeof(AttnBlock));
-    g.cum = take((size_t)(g.keyBlocks + 1) * sizeof(int64_t));
-  }
+  // A workgroup per block where these fill the CUs' places twice (the longer
+  // ones first, so that the sums of two come out alike); else equal stretches of
+  // all tiles, one per place, or fewer of `least` tiles.  The sums of a block that
+  // stretches share are written and read once more.  Blocks of keys of a packed
+  // batch go in stretches too: one of a long sequence is seen by the group's whole
+  // rows, many times the mean (8192 tokens in 11 documents, 28 heads of 64: 744 µs
+  // by blocks, 483 in stretches); blocks of rows are smaller (232 / 349 µs).
+  const bool packed = f.sequences > 0, light = bf16 && l.dp == 64;
+  auto runs = [&](RunsPlan& r, bool unequal, int64_t n, int per, double tilesOfBlock, int places, int least) {
+    r.blocks = blocks_of(n, per);
+    r.least = least;
+    if (l.combos > 0 && n > 0 && (unequal || l.combos * r.blocks < 2 * places)) {
+      const double tiles = (double)l.combos * r.blocks * tilesOfBlock;
+      r.streams = (int)std::min<double>(places, std::max(8.0, std::ceil(tiles / least / 8) * 8));
+    }
+    if (packed) r.blocks = n / per + f.sequences + 2;
+    if (packed || r.streams) r.list = take(256 + (size_t)r.blocks * sizeof(AttnBlock));
+    if (r.streams) r.cum = take((size_t)(r.blocks + 1) * sizeof(int64_t));
+  };
+  runs(g.keys, packed, f.keys, kDkvKeys, (double)(f.heads / f.kv_heads) * blocks_of(f.queries, 32), 256, light ? 6 : 3);
+  runs(g.rows, false, l.rows, kDqRows, blocks_of(f.keys, attn_dq_keys(bf16, l.dp)), light ? 512 : 256, 2);
   g.q = take(direct(f.q, t.q, e) ? 0 : copy_bytes(t.q, e));
   g.k = take(direct(f.k, t.k, e) ? 0 : copy_bytes(t.k, e));
   g.v = take(direct(f.v, t.v, e) ? 0 : copy_bytes(t.v, e));
@@ -394,7 +400,7 @@ AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout
   g.recL = take(bf16 ? rows * 16 : 0);
   g.recD = take(bf16 ? rows * 16 : 0);
   g.rowLam = take(rows * 4);
-  if (g.streams) g.part = take((size_t)g.streams * 2 * kDkvKeys * 4 * l.dp * 4);
+  g.part = take(std::max((size_t)g.keys.streams * 2 * kDkvKeys * 4 * l.dp, (size_t)g.rows.streams * 2 * kDqRows * (2 * l.dp + 4)) * 4);
   g.total = at;
   return g;
 }
@@ -450,10 +456,11 @@ struct AttnCall {
     return ws + at;
   }
   // Adds a list to the launch that makes them.
-  AttnList list(AttnPrepLaunch& P, size_t at, int32_t units, int32_t per) const {
+  AttnList list(AttnPrepLaunch& P, size_t at, int32_t tokens, int32_t units, int32_t per) const {
     auto& l = P.list[P.lists++];
     l.count = (int32_t*)(ws + at);
     l.blocks = (AttnBlock*)(ws + at + 256);
+    l.tokens = tokens;
     l.units = units;
     l.per = per;
     return {l.blocks, l.count};
@@ -467,10 +474,10 @@ AttnPrepLaunch prep_of(const muon_diff_attention_t& f) {
   AttnPrepLaunch P{};
   P.offsets = f.offsets;
   P.sequences = (int32_t)f.sequences;
-  P.tokens = (int32_t)f.queries;
   P.group = (int32_t)(f.heads / f.kv_heads);
   P.causal = f.causal != 0;
   P.queries = f.queries;
+  P.keys = f.keys;
   return P;
 }
 
@@ -601,8 +608,8 @@ muon_status_t muon_diff_attention(const muon_diff_attention_t* f, void* out, con
     const bool bf16 = call.bf16();
     if (f->sequences > 0) {
       AttnPrepLaunch P = prep_of(*f);
-      L.list = call.list(P, l.list[0], L.s.group, attn_fwd_rows(bf16, l.dp, l.few));
-      s = launched("blocks of the packed batch", launch_attn_prep(P, st), st);
+      L.list = call.list(P, l.list[0], (int32_t)f->queries, L.s.group, attn_fwd_rows(bf16, l.dp, l.few));
+      s = launched("blocks of the batch", launch_attn_prep(P, st), st);
       if (s != MUON_OK) return s;
     }
     if (saved) {
@@ -654,7 +661,7 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     if (grads->dv) a.heads("dv", grads->dv, gv, e, true);
     if (grads->dlambda) a.matrix("dlambda", grads->dlambda, 1, f->heads, f->heads, 4, true);
     a.buffer("workspace", workspace, workspace_bytes, w.total, true);
-    a.size("workgroups", std::max(l.combos * w.keyBlocks, l.combos * w.rowBlocks), 0, kMaxBlocks);
+    a.size("workgroups", l.combos * std::max(w.keys.blocks, w.rows.blocks), 0, kMaxBlocks);
     a.all_aliases([](const char*, const char*) { return false; });
     if (!a.ok()) return a.report();
     const bool wantK = grads->dk && t.k.count() > 0, wantQ = (grads->dq || grads->dlambda) && t.q.count() > 0;
@@ -673,15 +680,23 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     L.dout = call.operand(dout, hd, w.dout, L.gs);
     s = call.copy();
     if (s != MUON_OK) return s;
-    if (w.streams || f->sequences > 0) {
-      AttnPrepLaunch P = prep_of(*f);
-      P.tokens = (int32_t)f->keys;
-      if (w.streams) {
-        L.keyList = call.list(P, w.list[0], 1, kDkvKeys);
-        P.list[0].cum = (int64_t*)(ws + w.cum);
-        L.cum = P.list[0].cum;
+    AttnPrepLaunch P = prep_of(*f);
+    auto runs = [&](const RunsPlan& r, int32_t tokens, int32_t units, int32_t per, int32_t tile) {
+      AttnRuns R{};
+      R.blocks = (int32_t)r.blocks;
+      R.streams = r.streams;
+      R.least = r.least;
+      if (r.streams || f->sequences > 0) R.list = call.list(P, r.list, tokens, units, per);
+      if (r.streams) {
+        P.list[P.lists - 1].tile = tile;
+        P.list[P.lists - 1].cum = (int64_t*)(ws + r.cum);
+        R.cum = P.list[P.lists - 1].cum;
       }
-      if (f->sequences > 0) L.rowList = call.list(P, w.list[1], L.s.group, kDqRows);
+      return R;
+    };
+    L.keyRuns = runs(w.keys, (int32_t)f->keys, 1, kDkvKeys, 0);
+    L.rowRuns = runs(w.rows, (int32_t)f->queries, L.s.group, kDqRows, attn_dq_keys(bf16, l.dp));
+    if (P.lists) {
       s = launched("blocks of the batch", launch_attn_prep(P, st), st);
       if (s != MUON_OK) return s;
     }
@@ -703,10 +718,6 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     L.scale = f->scale;
     L.batch = (int32_t)f->batch;
     L.heads = (int32_t)f->heads;
-    L.keyBlocks = (int32_t)w.keyBlocks;
-    L.rowBlocks = (int32_t)w.rowBlocks;
-    L.streams = w.streams;
-    L.least = w.least;
     L.packed = f->sequences > 0;
     L.part = (float*)(ws + w.part);
     if (hd.count() > 0) {
@@ -716,14 +727,18 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     if (wantK) {
       s = launched("gradients of keys and values", launch_attn_dkv(bf16, l.dp, L, st), st);
       if (s != MUON_OK) return s;
-      if (w.streams) {
-        s = launched("sums of shared blocks", launch_attn_dkv_join(bf16, l.dp, L, st), st);
+      if (w.keys.streams) {
+        s = launched("sums of shared blocks of keys", launch_attn_dkv_join(bf16, l.dp, L, st), st);
         if (s != MUON_OK) return s;
       }
     }
     if (wantQ) {
       s = launched("gradient of the queries", launch_attn_dq(bf16, l.dp, L, st), st);
       if (s != MUON_OK) return s;
+      if (w.rows.streams) {
+        s = launched("sums of shared blocks of rows", launch_attn_dq_join(bf16, l.dp, L, st), st);
+        if (s != MUON_OK) return s;
+      }
     }
     if (!grads->dlambda) return MUON_OK;
     return launched("gradient of lambda", launch_attn_dlam(L, st), st);

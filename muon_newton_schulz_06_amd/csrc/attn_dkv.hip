@@ -28,67 +28,6 @@
 namespace muon {
 namespace {
 
-// The tiles of one block of keys that a workgroup runs: begin … end − 1.
-struct Piece {
-  int combo, tok, nq, nk, inside, at, begin, end;
-  int64_t slot;  // where its sums go to be joined; −1: the block is its own
-};
-
-// A workgroup's stretch of all combos' tiles, in the list's order, or (streams
-// = 0) the block of its number.
-struct Stretch {
-  int64_t each, total, per, pos, stop;  // tiles of a combo, all, of a stretch; this one
-  int64_t w;
-  int count;
-  __device__ __forceinline__ Stretch(const AttnGradLaunch& L, int64_t number) : w(number) {
-    if (!L.streams) {
-      pos = 0;
-      stop = 1;
-      return;
-    }
-    count = *L.keyList.count;
-    each = L.cum[count];
-    total = each * L.s.combos;
-    per = max((total + L.streams - 1) / L.streams, (int64_t)L.least);
-    pos = min(w * per, total);
-    stop = min(pos + per, total);
-  }
-  // the block of a combo's tile
-  __device__ __forceinline__ int find(const AttnGradLaunch& L, int64_t tile) const {
-    int lo = 0, hi = count - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (L.cum[mid] <= tile) lo = mid;
-      else hi = mid - 1;
-    }
-    return lo;
-  }
-  __device__ __forceinline__ bool next(const AttnGradLaunch& L, Piece& p) {
-    if (pos >= stop) return false;
-    if (!L.streams) {  // the keys that most rows see first
-      p = Piece{(int)blockIdx.x % L.s.combos, 0, (int)L.s.nq, (int)L.s.nk, 1,
-                (int)blockIdx.x / L.s.combos * kDkvKeys, 0, 0x7fffffff, -1};
-      pos = stop;
-      return true;
-    }
-    p.combo = (int)(pos / each);
-    const int64_t tile = pos - p.combo * each;
-    const int b = find(L, tile);
-    const AttnBlock B = L.keyList.blocks[b];
-    p.tok = B.tok;
-    p.nq = L.packed ? B.n : (int)L.s.nq;
-    p.nk = B.n;
-    p.inside = B.nk > 0;
-    p.at = B.at;
-    const int64_t from = L.cum[b], to = L.cum[b + 1], n = min(stop - pos, to - tile);
-    p.begin = (int)(tile - from);
-    p.end = (int)(p.begin + n);
-    p.slot = n == to - from ? -1 : 2 * w + (p.begin == 0);
-    pos += n;
-    return true;
-  }
-};
-
 // What a pass makes (PART): bit 0 dV, bit 1 dK.
 template <typename T, int DP> struct Dkv {
   static constexpr int kWaves = 4, kThreads = 256, kRows = 32;
@@ -118,10 +57,11 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   // What this workgroup makes: one block of keys, all its row tiles; or, where
   // the blocks are few or unequal, an equal stretch of all tiles of all blocks
   // one after another, which may begin or end inside a block.
-  Stretch W(L, blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);  // neighbours on one XCD
+  Stretch W(L.keyRuns, S.combos, blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);  // neighbours on one XCD
   Piece P;
-  while (W.next(L, P)) {
-  const int tok0 = P.tok, nq = P.nq, nk = P.nk, at = P.at;
+  // (dense: the keys that most rows see first)
+  while (W.next(L.keyRuns, S.combos, blockIdx.x / S.combos * kDkvKeys, P)) {
+  const int tok0 = P.tok, nq = L.packed ? P.n : (int)S.nq, nk = L.packed ? P.n : (int)S.nk, at = P.at;
   const int batch = P.combo / S.kv, hk = P.combo % S.kv, G = S.group;
   const int shift = nk - nq + 1;
   const int key0 = at + wave * 32, key = key0 + (lane & 31);
@@ -151,7 +91,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   // row tiles: tokens from the first that sees a key of the workgroup
   const int first = S.causal ? max(at - shift + 1, 0) & ~31 : 0;
   const int perHead = P.inside && nq > first ? (nq - first + 31) / 32 : 0;
-  const int begin = P.begin, end = (int)min((int64_t)P.end, (int64_t)perHead * G);
+  const int begin = (int)P.begin, end = (int)min(P.end, (int64_t)perHead * G);
 
   TileLoader<F::kK, F::kRows, F::kWaves> ldq;
   TileLoader<F::kVB, F::kRows, F::kWaves> ldd;
@@ -447,15 +387,15 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
 // order by the workgroups of the one the block begins in: its part lies in that
 // one's second slot, the others in the next ones' first.
 template <typename T, int DP> __global__ __launch_bounds__(256) void attn_dkv_join(const AttnGradLaunch L) {
-  constexpr int E = AT<T>::kBytes, kKeys = 16;
+  constexpr int E = AT<T>::kBytes, kKeys = 8;
   const AttnShape& S = L.s;
-  const Stretch W(L, blockIdx.x);
+  const Stretch W(L.keyRuns, S.combos, blockIdx.x);
   if (W.stop >= W.total) return;
   const int64_t combo = W.stop / W.each;  // of the next stretch's first tile
-  const int b = W.find(L, W.stop - combo * W.each);
-  const int64_t from = combo * W.each + L.cum[b], to = combo * W.each + L.cum[b + 1];
+  const int b = W.find(L.keyRuns, W.stop - combo * W.each);
+  const int64_t from = combo * W.each + L.keyRuns.cum[b], to = combo * W.each + L.keyRuns.cum[b + 1];
   if (from >= W.stop || from < W.pos) return;  // not shared, or begun before
-  const AttnBlock B = L.keyList.blocks[b];
+  const AttnBlock B = L.keyRuns.list.blocks[b];
   const int64_t batch = combo / S.kv, hk = combo % S.kv;
   constexpr int64_t kSlot = (int64_t)kDkvKeys * 4 * DP;
   for (int i = threadIdx.x; i < kKeys * DP; i += 256) {
@@ -463,6 +403,7 @@ template <typename T, int DP> __global__ __launch_bounds__(256) void attn_dkv_jo
     if (B.at + key >= B.n) break;
     const float* p = L.part + (int64_t)key * (4 * DP) + c0;
     lf32x4 s = *(const lf32x4*)(p + (2 * (int64_t)blockIdx.x + 1) * kSlot);
+#pragma unroll 4
     for (int64_t w = blockIdx.x + 1; w * W.per < to; ++w) s += *(const lf32x4*)(p + 2 * w * kSlot);
     const int64_t tok = B.tok + B.at + key;
     if (c0 < 2 * DP) {
@@ -480,13 +421,13 @@ template <typename T, int DP> __global__ __launch_bounds__(256) void attn_dkv_jo
 }
 
 template <typename T, int DP, int PART, int... REST> hipError_t run(const AttnGradLaunch& L, hipStream_t st) {
-  attn_dkv<T, DP, PART><<<dim3((unsigned)(L.streams ? L.streams : L.s.combos * L.keyBlocks)), 256, 0, st>>>(L);
+  attn_dkv<T, DP, PART><<<dim3((unsigned)(L.keyRuns.streams ? L.keyRuns.streams : L.s.combos * L.keyRuns.blocks)), 256, 0, st>>>(L);
   const hipError_t e = hipGetLastError();
   if constexpr (sizeof...(REST) > 0) return e != hipSuccess ? e : run<T, DP, REST...>(L, st);
   else return e;
 }
 template <typename T, int DP> hipError_t join(const AttnGradLaunch& L, hipStream_t st) {
-  attn_dkv_join<T, DP><<<dim3(L.streams, kDkvKeys / 16), 256, 0, st>>>(L);
+  attn_dkv_join<T, DP><<<dim3(L.keyRuns.streams, kDkvKeys / 8), 256, 0, st>>>(L);
   return hipGetLastError();
 }
 

@@ -40,22 +40,14 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  int id = blockIdx.x;
-  const int combo = id % S.combos;
-  id /= S.combos;
-  int tok0 = 0, nq = (int)S.nq, nk = (int)S.nk, at = 0;
-  if (L.rowList.blocks) {
-    const int n = *L.rowList.count;
-    if (id >= n) return;
-    const AttnBlock B = L.rowList.blocks[n - 1 - id];
-    tok0 = B.tok;
-    nq = B.n;
-    nk = B.nk;
-    at = B.at;
-  } else {
-    at = (L.rowBlocks - 1 - id) * kDqRows;
-  }
-  const int batch = combo / S.kv, hk = combo % S.kv, G = S.group;
+  // one block of rows, all its key tiles, or an equal stretch of the tiles of
+  // all blocks (dense: the rows that see most keys first)
+  Stretch W(L.rowRuns, S.combos, blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8);  // neighbours on one XCD
+  Piece P;
+  while (W.next(L.rowRuns, S.combos, (L.rowRuns.blocks - 1 - (int)blockIdx.x / S.combos) * kDqRows, P)) {
+  const int tok0 = P.tok, at = P.at;
+  const int nq = L.packed ? P.n : (int)S.nq, nk = L.packed ? (P.inside ? P.n : 0) : (int)S.nk;
+  const int batch = P.combo / S.kv, hk = P.combo % S.kv, G = S.group;
   const int rows = nq * G, shift = nk - nq + 1;
   const int row = at + wave * 32 + (lane & 31);
   const bool valid = row < rows;
@@ -63,7 +55,8 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
   const int lim = !valid ? 0 : S.causal ? min(max(t + shift, 0), nk) : nk;
   const int64_t tok = tok0 + t;
   const int last = min(at + kDqRows, rows) - 1;
-  const int kEnd = S.causal ? min(max(last / G + shift, 0), nk) : nk;
+  const int kSee = S.causal ? min(max(last / G + shift, 0), nk) : nk;
+  const int kBegin = (int)P.begin * BN, kEnd = (int)min(P.end * BN, (int64_t)kSee);
   const int least = S.causal ? min(max(at / G + shift, 0), nk) : nk;
 
   lu32x4 q[2][NC], d[2 * NC];
@@ -159,9 +152,10 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
     }
   };
 
-  if (kEnd > 0) issue(0, base);
+  __syncthreads();  // every wave has left the LDS of the piece before
+  if (kBegin < kEnd) issue(kBegin, base);
   uint32_t buf = base;
-  for (int key = 0; key < kEnd; key += BN) {
+  for (int key = kBegin; key < kEnd; key += BN) {
     a_landed();
     const uint32_t other = 2 * base + F::kStage - buf;
     if (key + BN < kEnd) issue(key + BN, other);
@@ -172,11 +166,24 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
     }
     buf = other;
   }
-  if constexpr (k2nd) {
-    sum = a_half_sum(sum);
-    if (valid && half == 0) L.rowLam[recAt] = d2 + sum;
+  if constexpr (k2nd) sum = a_half_sum(sum);
+  if (P.slot >= 0) {
+    float* o = L.part + (P.slot * kDqRows + wave * 32 + (lane & 31)) * (2 * DP + 4);
+    if (k2nd && valid && half == 0) o[2 * DP] = sum;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (!(MAPS >> m & 1)) continue;
+#pragma unroll
+      for (int n = 0; n < ND; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // rows that do not exist have a place too
+          *(lf32x4*)(o + m * DP + n * 32 + 8 * i + 4 * half) =
+              lf32x4{acc[m][n][4 * i], acc[m][n][4 * i + 1], acc[m][n][4 * i + 2], acc[m][n][4 * i + 3]};
+    }
+    continue;
   }
-  if (!L.dq) return;
+  if (k2nd && valid && half == 0) L.rowLam[recAt] = d2 + sum;
+  if (!L.dq) continue;
   // of a row that sees one key alone P = 1 whatever the scores: no gradient
   const float f[2] = {L.scale, valid ? -S.lam[head] * L.scale : 0.f};
 #pragma unroll
@@ -191,15 +198,69 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
       a_store_row<T>(o, v, n * 32, S.dim, L.dqVec, valid, half);
     }
   }
+  }
+}
+
+// The sums of blocks that several stretches share, added in the stretches'
+// order (see attn_dkv.hip).
+template <typename T, int DP> __global__ __launch_bounds__(256) void attn_dq_join(const AttnGradLaunch L) {
+  constexpr int E = AT<T>::kBytes, kRows = 8, kLd = 2 * DP + 4, kCols = 2 * DP / 4 + 1;
+  const AttnShape& S = L.s;
+  const Stretch W(L.rowRuns, S.combos, blockIdx.x);
+  if (W.stop >= W.total) return;
+  const int64_t combo = W.stop / W.each;  // of the next stretch's first tile
+  const int b = W.find(L.rowRuns, W.stop - combo * W.each);
+  const int64_t from = combo * W.each + L.rowRuns.cum[b], to = combo * W.each + L.rowRuns.cum[b + 1];
+  if (from >= W.stop || from < W.pos) return;  // not shared, or begun before
+  const AttnBlock B = L.rowRuns.list.blocks[b];
+  const int nq = L.packed ? B.n : (int)S.nq, nk = L.packed ? B.nk : (int)S.nk;
+  const int batch = (int)combo / S.kv, hk = (int)combo % S.kv, G = S.group;
+  constexpr int64_t kSlot = (int64_t)kDqRows * kLd;
+  for (int i = threadIdx.x; i < kRows * kCols; i += 256) {
+    const int r = blockIdx.y * kRows + i / kCols, c0 = i % kCols * 4;
+    const int row = B.at + r;
+    if (row >= nq * G) break;
+    const float* p = L.part + r * kLd + c0;
+    lf32x4 s = *(const lf32x4*)(p + (2 * (int64_t)blockIdx.x + 1) * kSlot);
+#pragma unroll 4
+    for (int64_t w = blockIdx.x + 1; w * W.per < to; ++w) s += *(const lf32x4*)(p + 2 * w * kSlot);
+    const int t = row / G, head = hk * G + row - t * G;
+    const int64_t tok = B.tok + t;
+    if (c0 == 2 * DP) {
+      const int64_t at = ((int64_t)batch * L.heads + head) * S.nq + tok;
+      L.rowLam[at] = L.rec[at].v[3] + s[0];
+      continue;
+    }
+    if (!L.dq) continue;
+    const int lim = S.causal ? min(t + nk - nq + 1, nk) : nk;
+    const int m = c0 >= DP, c = c0 - m * DP;
+    const float f = lim > 1 ? m ? -S.lam[head] * L.scale : L.scale : 0.f;
+    char* o = (char*)L.dq + (batch * L.dqs[0] + tok * L.dqs[1] + (2 * head + m) * L.dqs[2]) * E;
+    for (int j = 0; j < 4; ++j)
+      if (c + j < S.dim) LType<T>::put(o, c + j, lim > 1 ? s[j] * f : 0.f);
+  }
 }
 
 template <typename T, int DP, int MAPS> hipError_t run(const AttnGradLaunch& L, hipStream_t st) {
-  attn_dq<T, DP, MAPS><<<dim3((unsigned)(L.s.combos * L.rowBlocks)), 256, 0, st>>>(L);
+  attn_dq<T, DP, MAPS><<<dim3((unsigned)(L.rowRuns.streams ? L.rowRuns.streams : L.s.combos * L.rowRuns.blocks)), 256, 0, st>>>(L);
+  return hipGetLastError();
+}
+
+template <typename T, int DP> hipError_t join(const AttnGradLaunch& L, hipStream_t st) {
+  attn_dq_join<T, DP><<<dim3(L.rowRuns.streams, kDqRows / 8), 256, 0, st>>>(L);
   return hipGetLastError();
 }
 
 }  // namespace
 
+int attn_dq_keys(bool bf16, int dp) { return bf16 && dp == 64 ? 64 : 32; }
+static_assert(Dq<Bf16, 64>::kBN == 64 && Dq<Bf16, 128>::kBN == 32 && Dq<float, 64>::kBN == 32 && Dq<float, 128>::kBN == 32,
+              "attn_dq_keys");
+
+hipError_t launch_attn_dq_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {
+  if (bf16) return dp == 64 ? join<Bf16, 64>(L, st) : join<Bf16, 128>(L, st);
+  return dp == 64 ? join<float, 64>(L, st) : join<float, 128>(L, st);
+}
 hipError_t launch_attn_dq(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {
   if (bf16) return dp == 64 ? run<Bf16, 64, 3>(L, st) : run<Bf16, 128, 3>(L, st);
   if (dp == 64) return run<float, 64, 3>(L, st);

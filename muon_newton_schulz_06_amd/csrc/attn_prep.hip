@@ -39,12 +39,13 @@ __global__ __launch_bounds__(kPrep) void attn_prep(const AttnPrepLaunch L) {
   const int tid = threadIdx.x, spans = L.offsets ? L.sequences + 2 : 1;
   auto larger = [](int64_t a, int64_t b) { return a > b ? a : b; };
   auto sum = [](int64_t a, int64_t b) { return a + b; };
+  const int64_t tokens = D.tokens;
   int64_t edge = 0;  // where the chunk's first span begins
   int done = 0;      // blocks of the chunks before
   for (int s0 = 0; s0 < spans; s0 += kPrep) {
     const int s = s0 + tid;
-    int64_t end = L.tokens;  // of span s
-    if (L.offsets && s <= L.sequences) end = min(max(L.offsets[s], 0), L.tokens);
+    int64_t end = tokens;  // of span s
+    if (L.offsets && s <= L.sequences) end = min(max((int64_t)L.offsets[s], (int64_t)0), tokens);
     end = scan(larger(end, edge), red, larger);
     size[tid] = (int)end;  // for the neighbour
     __syncthreads();
@@ -79,9 +80,15 @@ __global__ __launch_bounds__(kPrep) void attn_prep(const AttnPrepLaunch L) {
     int64_t n = 0;
     if (b0 + tid < done) {
       const AttnBlock B = D.blocks[b0 + tid];
-      const int64_t nq = L.offsets ? B.n : L.queries, shift = B.n - nq + 1;
-      const int64_t first = L.causal ? max(B.at - shift + 1, (int64_t)0) & ~(int64_t)31 : 0;
-      n = B.nk > 0 && nq > first ? (nq - first + 31) / 32 * L.group : 1;
+      const int64_t nq = L.offsets ? B.n : L.queries, nk = L.offsets ? B.nk : L.keys;
+      if (D.units == 1 && D.tile == 0) {
+        const int64_t first = L.causal ? max(B.at - (B.n - nq), (int64_t)0) & ~(int64_t)31 : 0;
+        n = B.nk > 0 && nq > first ? (nq - first + 31) / 32 * L.group : 1;
+      } else {
+        const int64_t last = min((int64_t)B.at + D.per, nq * D.units) - 1;
+        const int64_t see = L.causal ? min(max(last / D.units + nk - nq + 1, (int64_t)0), nk) : nk;
+        n = max((see + D.tile - 1) / D.tile, (int64_t)1);
+      }
     }
     const int64_t upto = scan(n, red, sum);
     if (b0 + tid < done) D.cum[b0 + tid] = before + upto - n;

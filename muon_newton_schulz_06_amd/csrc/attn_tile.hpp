@@ -13,6 +13,7 @@
 
 #include <type_traits>
 
+#include "attention.hpp"
 #include "dma.hpp"
 #include "layers.hpp"
 
@@ -154,6 +155,74 @@ template <int RB, int ROWS, int NW> struct TileLoader {
     for (int p = 0; p < N; ++p)
       f_dma16(__builtin_amdgcn_readfirstlane(dst + (wave * N + p) * 1024),
               row0 + p * kRowsPer < left ? off[p] : kFfnNowhere, buf);
+  }
+};
+
+// The tiles of one block that a workgroup runs: begin … end − 1.
+struct Piece {
+  int combo, tok, n, inside, at;
+  int64_t begin, end;
+  int64_t slot;  // where its sums go to be joined; −1: the block is its own
+};
+
+// A workgroup's stretch of all combos' tiles, in the list's order, or (streams
+// = 0) the block of its number.
+struct Stretch {
+  int64_t each, total, per, pos, stop;  // tiles of a combo, all, of a stretch; this one
+  int64_t w;
+  int count;
+  __device__ __forceinline__ Stretch(const AttnRuns& R, int combos, int64_t number) : w(number) {
+    pos = 0;
+    stop = 1;
+    if (!R.streams) return;
+    count = *R.list.count;
+    each = R.cum[count];
+    total = each * combos;
+    per = max((total + R.streams - 1) / R.streams, (int64_t)R.least);
+    pos = min(w * per, total);
+    stop = min(pos + per, total);
+  }
+  // the block of a combo's tile
+  __device__ __forceinline__ int find(const AttnRuns& R, int64_t tile) const {
+    int lo = 0, hi = count - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (R.cum[mid] <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
+  // at: the row or key the workgroup's block begins at, without a list
+  __device__ __forceinline__ bool next(const AttnRuns& R, int combos, int at, Piece& p) {
+    if (pos >= stop) return false;
+    if (!R.streams) {
+      p = Piece{(int)blockIdx.x % combos, 0, 0, 1, at, 0, int64_t(1) << 40, -1};
+      if (R.list.blocks) {  // from the last one: in every sequence the rows that see most keys first
+        const int id = *R.list.count - 1 - (int)blockIdx.x / combos;
+        if (id < 0) return false;
+        const AttnBlock B = R.list.blocks[id];
+        p.tok = B.tok;
+        p.n = B.n;
+        p.inside = B.nk > 0;
+        p.at = B.at;
+      }
+      pos = stop;
+      return true;
+    }
+    p.combo = (int)(pos / each);
+    const int64_t tile = pos - p.combo * each;
+    const int b = find(R, tile);
+    const AttnBlock B = R.list.blocks[b];
+    p.tok = B.tok;
+    p.n = B.n;
+    p.inside = B.nk > 0;
+    p.at = B.at;
+    const int64_t from = R.cum[b], to = R.cum[b + 1], n = min(stop - pos, to - tile);
+    p.begin = tile - from;
+    p.end = p.begin + n;
+    p.slot = n == to - from ? -1 : 2 * w + (p.begin == 0);
+    pos += n;
+    return true;
   }
 };
 
