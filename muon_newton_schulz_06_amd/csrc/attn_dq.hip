@@ -154,17 +154,21 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
 
   __syncthreads();  // every wave has left the LDS of the piece before
   if (kBegin < kEnd) issue(kBegin, base);
-  uint32_t buf = base;
-  for (int key = kBegin; key < kEnd; key += BN) {
-    a_landed();
-    const uint32_t other = 2 * base + F::kStage - buf;
-    if (key + BN < kEnd) issue(key + BN, other);
+  // the two buffers by turns, their addresses constants
+  for (int key = kBegin; key < kEnd; key += 2 * BN) {
+    a_for<0, 2>([&](auto bc) __attribute__((always_inline)) {
+      constexpr int b = decltype(bc)::value;
+      const int k0 = key + b * BN;
+      if (k0 >= kEnd) return;
+      a_landed();  // this tile; the other buffer is free
+      if (k0 + BN < kEnd) issue(k0 + BN, base + (1 - b) * F::kStage);
 #pragma unroll
-    for (int j = 0; j < BN; j += 32) {
-      if (key + j >= kEnd) break;
-      step(buf + j * F::kK, buf + 2 * BN * F::kK + j * F::kV, key + j, key + j + 32 > least);
-    }
-    buf = other;
+      for (int j = 0; j < BN; j += 32) {
+        if (k0 + j >= kEnd) break;
+        const uint32_t buf = base + b * F::kStage;
+        step(buf + j * F::kK, buf + 2 * BN * F::kK + j * F::kV, k0 + j, k0 + j + 32 > least);
+      }
+    });
   }
   if constexpr (k2nd) sum = a_half_sum(sum);
   if (P.slot >= 0) {

@@ -125,20 +125,23 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
     ldk.issue(k + S.ks[2] * E, nk - key, buf + BN * F::kK);
     ldv.issue(v0 + (int64_t)key * S.vs[1] * E, nk - key, buf + 2 * BN * F::kK);
   };
-  const RowReader<F::kK> rd(lane);
+  const RowReader<F::kK> rd(lane, map * (BN * F::kK));  // in the map's own keys
   const ColReader<T, F::kV> cd(lane);
 
   af32x16 o[RS][NV];
-  float m[RS], l[RS];
+  float m[RS], l[RS], lag[RS];
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
-    m[r] = kNegInf;
-    l[r] = 0.f;
+    m[r] = l[r] = 0.f;
+    lag[r] = -1.f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) o[r][n] = af32x16{};
   }
 
-  // 32 keys of a tile
+  // 32 keys of a tile.  Exponents refer to m, a maximum of keys gone by that may
+  // lag behind the true one: as long as no 16 probabilities of a lane sum to more
+  // than kLag, nothing is compared and nothing rescaled.
+  constexpr float kLag = 1024.f;
   auto step = [&](uint32_t kt, uint32_t vt, int key, bool masked) __attribute__((always_inline)) {
     af32x16 s[RS];
 #pragma unroll
@@ -157,28 +160,34 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[r][i] = 8 * (i >> 2) + (i & 3) < n ? s[r][i] : kNegInf;
       }
-      float mx = fmaxf(s[r][0], s[r][1]);
+      float e[16], sum = 0.f;
 #pragma unroll
-      for (int i = 2; i < 16; ++i) mx = fmaxf(mx, s[r][i]);
-      mx = a_half_max(mx) * S.c;
-      // the maximum that the exponents refer to lags behind the true one by at
-      // most 8: the results are rescaled seldom
-      if (__any(mx > m[r] + 8.f)) {
-        const float mn = fmaxf(m[r], mx);
-        const float f = mn == kNegInf ? 1.f : a_exp2(m[r] - mn);
-        m[r] = mn;
+      for (int i = 0; i < 16; ++i) {
+        e[i] = a_exp2(s[r][i] * S.c - m[r]);
+        sum += e[i];
+      }
+      if (__any(sum > lag[r])) {
+        float mx = s[r][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[r][i]);
+        mx = a_half_max(mx) * S.c;
+        // a row that has seen no key has m = 0, sums of 0 and no lag allowed
+        const float mn = lag[r] < 0.f ? mx : fmaxf(m[r], mx);
+        const bool seen = mn != kNegInf;
+        const float f = lag[r] < 0.f ? 0.f : a_exp2(m[r] - mn);
+        m[r] = seen ? mn : 0.f;
+        lag[r] = seen ? kLag : -1.f;
         l[r] *= f;
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[r][n][i] *= f;
-      }
-      const float mu = m[r] == kNegInf ? 0.f : m[r];
-      float e[16], sum = 0.f;
+        sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        e[i] = a_exp2(s[r][i] * S.c - mu);
-        sum += e[i];
+        for (int i = 0; i < 16; ++i) {
+          e[i] = a_exp2(s[r][i] * S.c - m[r]);
+          sum += e[i];
+        }
       }
       l[r] += sum;
 #pragma unroll
@@ -195,18 +204,21 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
   };
 
   if (kBegin < kEnd) issue(kBegin, base);
-  uint32_t buf = base;
-  for (int key = kBegin; key < kEnd; key += BN) {
-    a_landed();  // this tile; the other buffer is free
-    const uint32_t other = 2 * base + F::kStage - buf;
-    if (key + BN < kEnd) issue(key + BN, other);
+  // the two buffers by turns, their addresses constants
+  for (int key = kBegin; key < kEnd; key += 2 * BN) {
+    a_for<0, 2>([&](auto bc) __attribute__((always_inline)) {
+      constexpr int b = decltype(bc)::value;
+      const int k0 = key + b * BN;
+      if (k0 >= kEnd) return;
+      a_landed();  // this tile; the other buffer is free
+      if (k0 + BN < kEnd) issue(k0 + BN, base + (1 - b) * F::kStage);
 #pragma unroll
-    for (int j = 0; j < BN; j += 32) {
-      if (key + j >= kEnd) break;
-      const uint32_t kt = buf + map * (BN * F::kK) + j * F::kK, vt = buf + 2 * BN * F::kK + j * F::kV;
-      step(kt, vt, key + j, key + j + 32 > least);
-    }
-    buf = other;
+      for (int j = 0; j < BN; j += 32) {
+        if (k0 + j >= kEnd) break;
+        const uint32_t buf = base + b * F::kStage;
+        step(buf + j * F::kK, buf + 2 * BN * F::kK + j * F::kV, k0 + j, k0 + j + 32 > least);
+      }
+    });
   }
   __syncthreads();
 

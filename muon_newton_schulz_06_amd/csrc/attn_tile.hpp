@@ -84,9 +84,10 @@ template <int RB> __device__ __forceinline__ int a_swz(int r) {
 // A lane's reads of row operands: rows 32·n + lane % 32, step c.
 template <int RB> struct RowReader {
   uint32_t at;
-  __device__ __forceinline__ RowReader(int lane) {
+  // offset: bytes added to every tile's address, a multiple of RB
+  __device__ __forceinline__ RowReader(int lane, uint32_t offset = 0) {
     const int r = lane & 31;
-    at = r * RB + (((lane >> 5) ^ a_swz<RB>(r)) << 4);
+    at = r * RB + (((lane >> 5) ^ a_swz<RB>(r)) << 4) + offset;
   }
   // tile: LDS address of row 32·n (a multiple of RB); c a constant
   __device__ __forceinline__ lu32x4 get(uint32_t tile, int c) const {
