@@ -22,10 +22,15 @@ namespace {
 
 template <typename T, int DP> struct Dq {
   static constexpr int kWaves = 4, kThreads = 256;
-  static constexpr int kBN = AT<T>::kBytes == 2 && DP == 64 ? 64 : 32;
+  static constexpr int kBN = 32;
   static constexpr int kK = DP * AT<T>::kBytes, kV = 2 * kK;
   static constexpr int kStage = kBN * (2 * kK + kV);
-  static constexpr int kWavesPerSimd = AT<T>::kBytes == 2 && DP == 64 ? 2 : 1;  // registers of the operands
+  // 64-wide bf16: dO is an operand in LDS, not in registers, which leaves room
+  // for operands read ahead at two waves per SIMD
+  static constexpr bool kInLds = AT<T>::kBytes == 2 && DP == 64;
+  static constexpr int kWavesPerSimd = kInLds ? 2 : 1;
+  static constexpr int kAhead = 8;
+  static constexpr int kOut = kInLds ? kDqRows * kV : 0;  // bytes of dO
 };
 
 // MAPS: bit 0 the first map, bit 1 the second (and λ's gradient).
@@ -35,7 +40,7 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
   constexpr bool k1st = MAPS & 1, k2nd = MAPS & 2;
   constexpr int BN = F::kBN, E = AT<T>::kBytes;
   constexpr int NC = DP / AT<T>::kStep, ND = DP / 32, SP = AT<T>::kSteps32;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * F::kStage];
+  __shared__ __attribute__((aligned(1024))) char lds[2 * F::kStage + F::kOut];
   const AttnShape& S = L.s;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -59,7 +64,7 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
   const int kBegin = (int)P.begin * BN, kEnd = (int)min(P.end * BN, (int64_t)kSee);
   const int least = S.causal ? min(max(at / G + shift, 0), nk) : nk;
 
-  lu32x4 q[2][NC], d[2 * NC];
+  lu32x4 q[2][NC], d[F::kInLds ? 1 : 2 * NC];
   {
     const char* p = (const char*)S.q + (batch * S.qs[0] + tok * S.qs[1] + 2 * head * S.qs[2]) * E;
     const char* o = (const char*)L.dout + (batch * L.gs[0] + tok * L.gs[1] + head * L.gs[2]) * E;
@@ -71,10 +76,19 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
         if (valid && (2 * c + half) * 16 < S.dim * E)
           q[m][c] = *(const lu32x4*)(p + m * S.qs[2] * E + (2 * c + half) * 16);
       }
+    if constexpr (!F::kInLds) {
 #pragma unroll
-    for (int c = 0; c < 2 * NC; ++c) {
-      d[c] = lu32x4{0, 0, 0, 0};
-      if (valid && (2 * c + half) * 16 < 2 * S.dim * E) d[c] = *(const lu32x4*)(o + (2 * c + half) * 16);
+      for (int c = 0; c < 2 * NC; ++c) {
+        d[c] = lu32x4{0, 0, 0, 0};
+        if (valid && (2 * c + half) * 16 < 2 * S.dim * E) d[c] = *(const lu32x4*)(o + (2 * c + half) * 16);
+      }
+    } else {  // this wave's rows of dO, into its own part of LDS
+#pragma unroll
+      for (int c = 0; c < 2 * NC; ++c) {
+        lu32x4 x = {0, 0, 0, 0};
+        if (valid && (2 * c + half) * 16 < 2 * S.dim * E) x = *(const lu32x4*)(o + (2 * c + half) * 16);
+        RowReader<F::kV>(lane).put(a_lds(lds) + 2 * F::kStage + wave * 32 * F::kV, c, x);
+      }
     }
   }
   const int64_t recAt = ((int64_t)batch * L.heads + head) * S.nq + tok;
@@ -111,63 +125,95 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
     for (int n = 0; n < ND; ++n) acc[m][n] = af32x16{};
   float sum = 0.f;
 
-  auto step = [&](uint32_t kt, uint32_t vt, int key, bool masked) __attribute__((always_inline)) {
-    af32x16 a{}, s1{}, s2{};
+  // The products of 32 keys in the order they run, each with the LDS operand it
+  // reads: dA, S_1, S_2, dQ_1, dQ_2.  Operands are read AHEAD products ahead, past
+  // the end those of the next 32 keys.
+  // (where dO lies in LDS, its operand before each of V's)
+  constexpr int AHEAD = F::kAhead, bS1 = (F::kInLds ? 4 : 2) * NC, bS2 = bS1 + (k1st ? NC : 0), bQ1 = bS2 + (k2nd ? NC : 0);
+  constexpr int bQ2 = bQ1 + (k1st ? SP * ND : 0), ALL = bQ2 + (k2nd ? SP * ND : 0);
+  static_assert(ALL % AHEAD == 0, "a step takes whole rounds of the ring");
+  lu32x4 ring[AHEAD];
+  auto read = [&](auto bc, auto stepc, auto jc) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value, at0 = decltype(bc)::value * F::kStage, s0 = decltype(stepc)::value * 32;
+    const uint32_t kt = base + at0 + s0 * F::kK, vt = base + at0 + 2 * BN * F::kK + s0 * F::kV;
+    if constexpr (F::kInLds && j < bS1) return rv.get(j % 2 ? vt : base + 2 * F::kStage + wave * 32 * F::kV, j / 2);
+    else if constexpr (j < bS1) return rv.get(vt, j);
+    else if constexpr (j < bS2) return rk.get(kt, j - bS1);
+    else if constexpr (j < bQ1) return rk.get(kt + BN * F::kK, j - bS2);
+    else if constexpr (j < bQ2) return ck.get(kt, (j - bQ1) / ND, (j - bQ1) % ND);
+    else return ck.get(kt + BN * F::kK, (j - bQ2) / ND, (j - bQ2) % ND);
+  };
+  constexpr int STEPS = BN / 32;
+  // step s of the tile in buffer b; `between` runs before the next tile's first read
+  auto step = [&](auto bc, auto stepc, int key, bool masked, auto&& between) __attribute__((always_inline)) {
+    constexpr int s = decltype(stepc)::value, b = decltype(bc)::value;
+    constexpr auto nextB = std::integral_constant<int, s + 1 < STEPS ? b : 1 - b>{};
+    constexpr auto nextS = std::integral_constant<int, (s + 1) % STEPS>{};
+    af32x16 a{}, v{};
+    lu32x4 op[2][SP], cur{};
+    float e[16];
+    const int on = lim - key - 4 * half;
+    a_for<0, ALL>([&](auto jc) __attribute__((always_inline)) {
+      constexpr int j = decltype(jc)::value;
+      if constexpr (j == ALL - AHEAD) between();
+      const lu32x4 r = ring[j % AHEAD];
+      if constexpr (j + AHEAD < ALL) ring[j % AHEAD] = read(bc, stepc, std::integral_constant<int, j + AHEAD>{});
+      else ring[j % AHEAD] = read(nextB, nextS, std::integral_constant<int, j + AHEAD - ALL>{});
+      if constexpr (j < bS1) {
+        if constexpr (!F::kInLds) a = a_mma<T>(r, d[j], a);
+        else if constexpr (j % 2) a = a_mma<T>(r, cur, a);
+        else cur = r;
+      } else if constexpr (j < bQ1) {
+        constexpr int m = j >= bS2, c = j - (m ? bS2 : bS1);
+        if constexpr (c == 0) v = af32x16{};
+        v = a_mma<T>(r, q[m][c], v);
+        if constexpr (c == NC - 1) {
+          const float l = m ? l2 : l1, dd = m ? d2 : d1;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if constexpr (k1st) s1 = a_mma<T>(rk.get(kt, c), q[0][c], s1);
-      if constexpr (k2nd) s2 = a_mma<T>(rk.get(kt + BN * F::kK, c), q[1][c], s2);
-    }
+          for (int i = 0; i < 16; ++i) e[i] = a_exp2(v[i] * S.c - l) * (a[i] - dd);
+          if (masked) {
 #pragma unroll
-    for (int c = 0; c < 2 * NC; ++c) a = a_mma<T>(rv.get(vt, c), d[c], a);
-    if (masked) {
-      const int n = lim - key - 4 * half;
+            for (int i = 0; i < 16; ++i) e[i] = 8 * (i >> 2) + (i & 3) < on ? e[i] : 0.f;
+          }
+          if constexpr (m) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool on = 8 * (i >> 2) + (i & 3) < n;
-        if constexpr (k1st) s1[i] = on ? s1[i] : kNegInf;
-        if constexpr (k2nd) s2[i] = on ? s2[i] : kNegInf;
-        a[i] = on ? a[i] : 0.f;
+            for (int i = 0; i < 16; ++i) sum += e[i];
+          }
+#pragma unroll
+          for (int u = 0; u < SP; ++u) op[m][u] = a_operand<T>(e, u);
+        }
+      } else {
+        constexpr int m = j >= bQ2, i = j - (m ? bQ2 : bQ1), u = i / ND, n = i % ND;
+        acc[m][n] = a_mma<T>(r, op[m][u], acc[m][n]);
       }
-    }
-    float e1[16], e2[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if constexpr (k1st) e1[i] = a_exp2(s1[i] * S.c - l1) * (a[i] - d1);
-      if constexpr (k2nd) {
-        e2[i] = a_exp2(s2[i] * S.c - l2) * (a[i] - d2);
-        sum += e2[i];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < SP; ++u) {
-      lu32x4 b1, b2;
-      if constexpr (k1st) b1 = a_operand<T>(e1, u);
-      if constexpr (k2nd) b2 = a_operand<T>(e2, u);
-#pragma unroll
-      for (int n = 0; n < ND; ++n) {
-        if constexpr (k1st) acc[0][n] = a_mma<T>(ck.get(kt, u, n), b1, acc[0][n]);
-        if constexpr (k2nd) acc[1][n] = a_mma<T>(ck.get(kt + BN * F::kK, u, n), b2, acc[1][n]);
-      }
-    }
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
 
   __syncthreads();  // every wave has left the LDS of the piece before
-  if (kBegin < kEnd) issue(kBegin, base);
+  if (kBegin < kEnd) {
+    issue(kBegin, base);
+    a_landed();
+    if (kBegin + BN < kEnd) issue(kBegin + BN, base + F::kStage);
+    a_for<0, AHEAD>([&](auto jc) __attribute__((always_inline)) {
+      ring[decltype(jc)::value] = read(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, jc);
+    });
+  }
   // the two buffers by turns, their addresses constants
   for (int key = kBegin; key < kEnd; key += 2 * BN) {
     a_for<0, 2>([&](auto bc) __attribute__((always_inline)) {
       constexpr int b = decltype(bc)::value;
       const int k0 = key + b * BN;
       if (k0 >= kEnd) return;
-      a_landed();  // this tile; the other buffer is free
-      if (k0 + BN < kEnd) issue(k0 + BN, base + (1 - b) * F::kStage);
-#pragma unroll
-      for (int j = 0; j < BN; j += 32) {
-        if (k0 + j >= kEnd) break;
-        const uint32_t buf = base + b * F::kStage;
-        step(buf + j * F::kK, buf + 2 * BN * F::kK + j * F::kV, k0 + j, k0 + j + 32 > least);
-      }
+      a_for<0, STEPS>([&](auto sc) __attribute__((always_inline)) {
+        constexpr int s = decltype(sc)::value;
+        step(bc, sc, k0 + 32 * s, k0 + 32 * s + 32 > least, [&]() __attribute__((always_inline)) {
+          if constexpr (s == STEPS - 1) {
+            a_landed();  // the next tile is there, this one has been read by every wave
+            if (k0 + 2 * BN < kEnd) issue(k0 + 2 * BN, base + b * F::kStage);
+          }
+        });
+      });
     });
   }
   if constexpr (k2nd) sum = a_half_sum(sum);
@@ -257,8 +303,8 @@ template <typename T, int DP> hipError_t join(const AttnGradLaunch& L, hipStream
 
 }  // namespace
 
-int attn_dq_keys(bool bf16, int dp) { return bf16 && dp == 64 ? 64 : 32; }
-static_assert(Dq<Bf16, 64>::kBN == 64 && Dq<Bf16, 128>::kBN == 32 && Dq<float, 64>::kBN == 32 && Dq<float, 128>::kBN == 32,
+int attn_dq_keys(bool, int) { return 32; }
+static_assert(Dq<Bf16, 64>::kBN == 32 && Dq<Bf16, 128>::kBN == 32 && Dq<float, 64>::kBN == 32 && Dq<float, 128>::kBN == 32,
               "attn_dq_keys");
 
 hipError_t launch_attn_dq_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {

@@ -93,6 +93,9 @@ template <int RB> struct RowReader {
   __device__ __forceinline__ lu32x4 get(uint32_t tile, int c) const {
     return *(a_lds_u4)(uintptr_t)((at ^ (c << 5)) + tile);
   }
+  __device__ __forceinline__ void put(uint32_t tile, int c, lu32x4 v) const {
+    *(__attribute__((address_space(3))) lu32x4*)(uintptr_t)((at ^ (c << 5)) + tile) = v;
+  }
 };
 
 // A lane's reads of column operands: columns 32·n + lane % 32, the step's rows.
