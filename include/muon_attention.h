@@ -114,9 +114,10 @@ muon_status_t muon_dropout_grad(const void* dy, int64_t ld_dy, double p, uint64_
  *     the device) and sees itself alone.  Tokens before the first and from the
  *     last offset on give zeros.  Offsets outside [0, tokens] are cut to it, one
  *     below its predecessor is raised to it.
- *   1 ≤ dim ≤ 128; kv_heads divides heads; scale finite and > 0;
+ *   1 ≤ dim ≤ 128; kv_heads divides heads; 0 < scale ≤ 1e30;
  *   batch · queries, batch · keys ≤ 2^24; queries · group < 2^30;
- *   batch · queries · heads ≤ 2^28.
+ *   batch · queries · heads ≤ 2^28; at most 2^23 workgroups (per batch entry and
+ *   key/value head one for 32 to 128 rows of queries · group, or 128 keys).
  * Keys behind the end of a sequence are never read.  Keys of the same sequence
  * that only the causal rule hides enter with probability 0: an infinite or NaN
  * value of v there reaches the row as 0 · v does.
@@ -137,14 +138,15 @@ typedef struct muon_diff_attention {
 } muon_diff_attention_t;
 
 /* saved: NULL, or muon_diff_attention_saved_size bytes (256-byte aligned) that
- * receive what muon_diff_attention_grad reads: the maps' log-sums (fp32) and
- * P_2 · v (dtype). */
+ * receive what muon_diff_attention_grad reads: the maps' log-sums (fp32) and,
+ * for MUON_DTYPE_F32, P_2 · v (fp32), for MUON_DTYPE_BF16 P_1 · v and P_2 · v
+ * (16 bits a value with a scale per row: 2^-15 of the row's largest value). */
 muon_status_t muon_diff_attention(const muon_diff_attention_t* attention, void* out,
                                   const int64_t out_strides[3], void* saved, size_t saved_bytes,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
-/* Gradients of muon_diff_attention from the gradient of out, out itself and
- * `saved`.  With dA = dout·vᵀ, δ_m = Σ_j P_m · dA:
+/* Gradients of muon_diff_attention from the gradient of out, out itself (read
+ * for MUON_DTYPE_F32 only) and `saved`.  With dA = dout·vᵀ, δ_m = Σ_j P_m · dA:
  *   dS_1 = P_1·(dA − δ_1), dS_2 = −lambda·P_2·(dA − δ_2),
  *   dq_m = scale·dS_m·k_m, dk_m = scale·Σ dS_mᵀ·q_m over the group's heads,
  *   dv = Σ (P_1 − lambda·P_2)ᵀ·dout over them, dlambda[h] = −Σ P_2·dA.

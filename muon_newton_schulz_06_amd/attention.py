@@ -51,6 +51,9 @@ class MuonRotaryHeads(ctypes.Structure):
                 ("in_strides", _i64x3), ("out_strides", _i64x3)]
 
 
+_two_heads = MuonRotaryHeads * 2  # kept: ctypes makes the type anew, in 20 us, where nothing else holds it
+
+
 class MuonDiffAttention(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("queries", ctypes.c_int64), ("keys", ctypes.c_int64),
                 ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64), ("dim", ctypes.c_int64),
@@ -110,7 +113,7 @@ def _contiguous_values(t):
 
 def _input_heads(t, name):
     t = _heads(t, name)
-    return t if _contiguous_values(t) else t.contiguous()
+    return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
 
 
 def _strides(t):
@@ -196,14 +199,14 @@ def _rotary(entry, q, k, freqs, positions, start, interleaved, scale, q_out, k_o
                 positions = positions.contiguous()
             r.positions, r.position_bytes = _ptr(positions), positions.element_size()
             r.position_stride = positions.stride(0) if many else 0
-        outs, arr, kept = [], (MuonRotaryHeads * 2)(), []
+        outs, arr, kept = [], _two_heads(), []
         n = 1 if k is None else 2
         for i, (t, out, name) in enumerate(((q, q_out, "q"), (k, k_out, "k"))[:n]):
-            t4 = _input_heads(t, name)
+            t4 = _input_heads(t, name) if i else q4
             if t4.shape[:2] != q4.shape[:2] or t4.shape[3] != dim or t.dim() != q.dim():
                 raise ValueError(f"k has shape {tuple(t.shape)}, q {tuple(q.shape)}: only their heads may differ")
             o = _output(out, t.shape, t.dtype, dev, name + "_out")
-            o4 = _heads(o, name + "_out")
+            o4 = o if o.dim() == 4 else o.unsqueeze(0)
             arr[i] = MuonRotaryHeads(_ptr(t4), _ptr(o4), t4.shape[2], _strides(t4), _strides(o4))
             outs.append(o)
             kept.append(t4)

@@ -80,15 +80,18 @@ struct AttnShape {
   const void *q, *k, *v;
   int64_t qs[3], ks[3], vs[3];  // batch, token, head strides, elements
   const float* lam;             // per head
-  // saved: log2 of the maps' sums, [combo][map][row], and the second map's
-  // result, [combo][row][pitch] in the tensors' type
+  // saved: log2 of the maps' sums, [combo][map][row], and their results P_m·V
+  // for the row sums of the backward pass (see attn_rows): fp32 the second map's,
+  // [combo][row][pitch]; bf16 both, [combo][map][row][pitch], 16-bit whole
+  // multiples of the row's unit, [combo][map][row]
   float* stat;
-  void* o2;
+  float* unit;
+  void* kept;
   int64_t pitch;
 };
 
 struct AttnFwdLaunch {
-  AttnShape s;  // o2, stat null: not wanted
+  AttnShape s;  // kept, stat null: not wanted
   void* out;
   int64_t os[3];
   int32_t vec;  // out rows take aligned 16-byte stores
@@ -123,7 +126,7 @@ struct AttnGradLaunch {
   AttnShape s;
   const void* dout;  // whole aligned chunks
   int64_t gs[3];
-  const void* out;  // any alignment
+  const void* out;  // any alignment; read for fp32 only
   int64_t os[3];
   int32_t outVec;  // out is whole aligned chunks too
   lf4* rec;

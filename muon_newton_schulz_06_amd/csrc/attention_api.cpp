@@ -280,7 +280,7 @@ void dense(int64_t s[3], const Heads& h, int64_t pitch) {
 }
 
 struct AttnLayout {
-  size_t stat, o2, saved;  // in `saved`
+  size_t stat, unit, kept, saved;  // in `saved`
   size_t list[2], q, k, v, part, partStat, total;
   int64_t rows;            // of a combo
   int64_t combos, pitch;
@@ -315,8 +315,9 @@ AttnLayout attn_layout(const muon_diff_attention_t& f) {
   l.dp = f.dim <= 64 ? 64 : 128;
   l.pitch = pitch_of(2 * f.dim, e);
   l.stat = 0;
-  l.o2 = align256((size_t)l.combos * 2 * l.rows * 4);
-  l.saved = l.o2 + align256((size_t)l.combos * l.rows * l.pitch * e);
+  l.unit = align256((size_t)l.combos * 2 * l.rows * 4);
+  l.kept = l.unit + (bf16 ? l.unit : 0);
+  l.saved = l.kept + align256((size_t)l.combos * (bf16 ? 2 : 1) * l.rows * l.pitch * e);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t o = at;
@@ -509,7 +510,7 @@ AttnShape shape_of(const muon_diff_attention_t& f, const AttnLayout& l) {
 
 void attn_inputs(HeadArgs& a, const muon_diff_attention_t& f, const AttnTensors& t) {
   const size_t e = esize(f.dtype);
-  if (!(f.scale > 0) || !std::isfinite(f.scale)) a.fail(MUON_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!(f.scale > 0 && f.scale <= 1e30f)) a.fail(MUON_ERR_INVALID_ARG, "scale must be > 0 and at most 1e30");
   a.heads("q", f.q, t.q, e, false);
   a.heads("k", f.k, t.k, e, false);
   a.heads("v", f.v, t.v, e, false);
@@ -614,7 +615,8 @@ muon_status_t muon_diff_attention(const muon_diff_attention_t* f, void* out, con
     }
     if (saved) {
       L.s.stat = (float*)((char*)saved + l.stat);
-      L.s.o2 = (char*)saved + l.o2;
+      L.s.unit = (float*)((char*)saved + l.unit);
+      L.s.kept = (char*)saved + l.kept;
     }
     L.out = out;
     L.vec = output_strides(L.os, out, t.out, e);
@@ -701,7 +703,8 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
       if (s != MUON_OK) return s;
     }
     L.s.stat = (float*)((char*)saved + l.stat);
-    L.s.o2 = (char*)saved + l.o2;
+    L.s.unit = (float*)((char*)saved + l.unit);
+    L.s.kept = (char*)saved + l.kept;
     L.out = out;
     L.outVec = output_strides(L.os, out, ho, e);
     L.rec = (lf4*)(ws + w.rec);

@@ -16,8 +16,20 @@
 // end the second map's wave hands λ·P_2·V over through LDS.
 //
 // Rounding: scores, maxima, sums and results are fp32; for bf16 tensors the
-// probabilities, relative to a maximum that lags by at most 2^8, are rounded
-// to bf16 as operands of the second product (their sum is of the unrounded).
+// probabilities are rounded to bf16 as operands of the second product.  Two sums
+// of them run along: of the unrounded ones, for the log-sums that the backward
+// pass recomputes probabilities from, and of the rounded ones, by which a result
+// is divided.  Where one key has most of a row, the rounding of its probability
+// then drops out; divided by the other sum, it would be an error of the whole
+// result, much larger than the gradients of such a row's scores,
+// P·(dA − δ), that the backward pass takes from it.
+//
+// Bound by the matrix unit and the exponentials beside it: a wave issues 24
+// products of 32×32×16 for 2048 probabilities, two waves per SIMD.  4 × 4096
+// tokens, 28 heads of 64 on 4, bf16, causal: 700 to 720 µs (1000 TFLOP/s of the
+// four products) without the second sum and with the second map's result kept
+// alone, 790 with both; comparing every maximum: 800 and more.  One token of
+// 16384 keys, split over 512 workgroups: 11 µs, 3 TB/s, and 7.6 for the join.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -129,10 +141,10 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
   const ColReader<T, F::kV> cd(lane);
 
   af32x16 o[RS][NV];
-  float m[RS], l[RS], lag[RS];
+  float m[RS], l[RS], lr[RS], lag[RS];
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
-    m[r] = l[r] = 0.f;
+    m[r] = l[r] = lr[r] = 0.f;
     lag[r] = -1.f;
 #pragma unroll
     for (int n = 0; n < NV; ++n) o[r][n] = af32x16{};
@@ -178,6 +190,7 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
         m[r] = seen ? mn : 0.f;
         lag[r] = seen ? kLag : -1.f;
         l[r] *= f;
+        lr[r] *= f;
 #pragma unroll
         for (int n = 0; n < NV; ++n)
 #pragma unroll
@@ -191,7 +204,10 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
       }
       l[r] += sum;
 #pragma unroll
-      for (int t = 0; t < SP; ++t) p[r][t] = a_operand<T>(e, t);
+      for (int t = 0; t < SP; ++t) {
+        p[r][t] = a_operand<T>(e, t);
+        if constexpr (E == 2) lr[r] = a_operand_sum(p[r][t], lr[r]);
+      }
     }
 #pragma unroll
     for (int t = 0; t < SP; ++t)
@@ -225,7 +241,8 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
     l[r] = a_half_sum(l[r]);
-    const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;  // a row that sees no key: zeros
+    const float sum = E == 2 ? a_half_sum(lr[r]) : l[r];
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees no key: zeros
 #pragma unroll
     for (int n = 0; n < NV; ++n)
 #pragma unroll
@@ -259,19 +276,35 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
     const int64_t row = (int64_t)tok[r] * G + head[r] - hk * G, rowsAll = S.nq * G;
     if (S.stat && half == 0 && valid[r])  // a row that sees no key: +∞, so that its probabilities are 0
       S.stat[((int64_t)combo * 2 + map) * rowsAll + row] = l[r] == 0.f ? -kNegInf : m[r] + a_log2(l[r]);
-    if (map == 1) {
-      const float lam = valid[r] ? S.lam[head[r]] : 0.f;
+    if (S.kept && (E == 2 || map == 1)) {
+      const int64_t at = ((int64_t)combo * (E == 2 ? 2 : 1) + (E == 2 ? map : 0)) * rowsAll + row;
+      float inv = 1.f;
+      if constexpr (E == 2) {
+        uint32_t top = 0;  // as whole numbers infinities and NaN are above all else
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(o[r][n][i]) & 0x7fffffffu);
+        const Whole w(a_half_max(top));
+        inv = w.inv;
+        if (half == 0 && valid[r]) S.unit[at] = w.unit;
+      }
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = o[r][n][i];
-        if (S.o2)
-          a_store_row<T>((char*)S.o2 + ((int64_t)combo * rowsAll + row) * S.pitch * E, v, n * 32, 2 * S.dim,
-                         true, valid[r], half);
+        for (int i = 0; i < 16; ++i) v[i] = E == 2 ? o[r][n][i] * inv : o[r][n][i];
+        a_store_row<T, true>((char*)S.kept + at * S.pitch * E, v, n * 32, 2 * S.dim, true, valid[r], half);
+      }
+    }
+    if (map == 1) {
+      const float lam = valid[r] ? S.lam[head[r]] : 0.f;
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          x[((r * NV + n) * 4 + g) * 64] = lf32x4{v[4 * g] * lam, v[4 * g + 1] * lam, v[4 * g + 2] * lam, v[4 * g + 3] * lam};
+          x[((r * NV + n) * 4 + g) * 64] = lf32x4{o[r][n][4 * g] * lam, o[r][n][4 * g + 1] * lam,
+                                                  o[r][n][4 * g + 2] * lam, o[r][n][4 * g + 3] * lam};
       }
     }
   }
@@ -301,6 +334,7 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
 template <typename T, int DP> __global__ __launch_bounds__(256) void attn_join(const AttnFwdLaunch L) {
   constexpr int E = AT<T>::kBytes, COLS = DP, GROUPS = 256 / COLS;  // threads for 2 · 2·DP columns
   __shared__ float weight[2][kMaxSplits], top[2], sums[2];
+  __shared__ uint32_t most[2];  // the largest magnitude of a map's results
   __shared__ lf32x4 part[GROUPS][COLS];
   const AttnShape& S = L.s;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -309,6 +343,7 @@ template <typename T, int DP> __global__ __launch_bounds__(256) void attn_join(c
   const int64_t row = id - combo * rows;
   const int64_t tok = row / S.group;
   const int batch = combo / S.kv, head = (combo % S.kv) * S.group + (int)(row - tok * S.group);
+  if (tid < 2) most[tid] = 0;
   if (wave < 2) {  // a wave per map
     float m = kNegInf, l = 0.f;
     for (int s = lane; s < L.splits; s += 64) {
@@ -347,24 +382,42 @@ template <typename T, int DP> __global__ __launch_bounds__(256) void attn_join(c
   }
   part[group][col] = res;
   __syncthreads();
-  if (tid >= COLS / 2) return;
+  const bool mine = tid < COLS / 2;
   lf32x4 r[2];
+  if (mine) {
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    lf32x4 s = part[0][m * (COLS / 2) + tid];
-    for (int g = 1; g < GROUPS; ++g) s += part[g][m * (COLS / 2) + tid];
-    const float inv = top[m] == kNegInf ? 0.f : 1.f / sums[m];
+    for (int m = 0; m < 2; ++m) {
+      lf32x4 s = part[0][m * (COLS / 2) + tid];
+      for (int g = 1; g < GROUPS; ++g) s += part[g][m * (COLS / 2) + tid];
+      const float inv = top[m] == kNegInf ? 0.f : 1.f / sums[m];
+      uint32_t largest = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[m][i] = s[i] * inv;
+      for (int i = 0; i < 4; ++i) {
+        r[m][i] = s[i] * inv;
+        largest = max(largest, __float_as_uint(r[m][i]) & 0x7fffffffu);
+      }
+      if (E == 2 && S.kept) atomicMax(&most[m], largest);  // (a maximum: in any order)
+    }
+    const float lam = S.lam[head];
+    char* o = (char*)L.out + (batch * L.os[0] + tok * L.os[1] + head * L.os[2]) * E;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (tid * 4 + i < 2 * S.dim) LType<T>::put(o, tid * 4 + i, r[0][i] - lam * r[1][i]);
   }
-  const float lam = S.lam[head];
-  char* o = (char*)L.out + (batch * L.os[0] + tok * L.os[1] + head * L.os[2]) * E;
+  if (!S.kept) return;
+  __syncthreads();
+  if (!mine || tid * 4 >= S.pitch) return;
+  if constexpr (E == 2) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = tid * 4 + i;
-    if (c >= 2 * S.dim) continue;
-    LType<T>::put(o, c, r[0][i] - lam * r[1][i]);
-    if (S.o2) LType<T>::put((char*)S.o2 + (id * S.pitch) * E, c, r[1][i]);
+    for (int m = 0; m < 2; ++m) {
+      const int64_t at = ((int64_t)combo * 2 + m) * rows + row;
+      const Whole w(most[m]);
+      if (tid == 0) S.unit[at] = w.unit;
+      *(lu32x2*)((char*)S.kept + (at * S.pitch + tid * 4) * E) =
+          lu32x2{a_pair_whole(r[m][0] * w.inv, r[m][1] * w.inv), a_pair_whole(r[m][2] * w.inv, r[m][3] * w.inv)};
+    }
+  } else {
+    *(lf32x4*)((char*)S.kept + (id * S.pitch + tid * 4) * E) = r[1];
   }
 }
 

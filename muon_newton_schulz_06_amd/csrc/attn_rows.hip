@@ -1,8 +1,14 @@
 // The row sums of the attention's backward pass, and the sum of λ's gradient.
 //
-// With O = O_1 − λ·O_2, O_m = P_m·V:  δ_2 = Σ_j P_2·dA = dO·O_2 and
-// δ_1 = dO·O_1 = dO·O + λ·δ_2.  One pass over dO, O and the saved O_2, bound by
-// HBM; 16 lanes share a row.
+// With O = O_1 − λ·O_2, O_m = P_m·V:  δ_m = Σ_j P_m·dA = dO·O_m.  One pass over dO
+// and what the forward pass kept, bound by HBM; 16 lanes share a row.
+//
+// fp32: δ_1 = dO·O + λ·δ_2 from O and the kept O_2.  bf16: from O_1 and O_2,
+// kept as 16-bit whole multiples of a unit of the row, 2^-15 of its largest
+// value: rounded to bf16 they would be off by 2^-8 of themselves, and δ with
+// them, where a row sees few keys by several times the rounding of the
+// dS = P·(dA − δ) that it goes into (of dK of two keys, 40 values a head:
+// 6.6·10^-3 instead of 2.5·10^-3).
 #include <hip/hip_runtime.h>
 
 #include "attention.hpp"
@@ -20,6 +26,15 @@ __device__ __forceinline__ void split3(float x, uint32_t (&h)[3]) {
   }
 }
 
+// Whole multiples of a unit.
+__device__ __forceinline__ void widen_whole(const lu32x4& v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = (float)(int16_t)v[i];
+    f[2 * i + 1] = (float)((int32_t)v[i] >> 16);
+  }
+}
+
 template <typename T, bool VEC> __global__ __launch_bounds__(256) void attn_rows(const AttnGradLaunch L) {
   constexpr int V = LType<T>::kVec, E = AT<T>::kBytes;
   const AttnShape& S = L.s;
@@ -34,28 +49,41 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void attn_rows
   const int64_t combo = b * S.kv + hk, row = t * S.group + g, all = S.nq * S.group;
   const char* d = (const char*)L.dout + (b * L.gs[0] + t * L.gs[1] + h * L.gs[2]) * E;
   const char* o = (const char*)L.out + (b * L.os[0] + t * L.os[1] + h * L.os[2]) * E;
-  const char* o2 = (const char*)S.o2 + (combo * all + row) * S.pitch * E;
+  const int64_t at1 = E == 2 ? combo * 2 * all + row : 0, at2 = E == 2 ? at1 + all : combo * all + row;
+  const char* o1 = E == 2 ? (const char*)S.kept + at1 * S.pitch * E : o;
+  const char* o2 = (const char*)S.kept + at2 * S.pitch * E;
   const int width = 2 * S.dim;
-  float s = 0.f, s2 = 0.f;
+  float s1 = 0.f, s2 = 0.f;
   for (int c = lane * V; c < width; c += 16 * V) {
     float x[V], y[V], z[V];
-    l_widen<T>(*(const lu32x4*)(d + c * E), x);  // zeros past the width
-    l_widen<T>(l_load<T, VEC>(o, c, width), y);
-    l_widen<T>(*(const lu32x4*)(o2 + c * E), z);
+    l_widen<T>(*(const lu32x4*)(d + c * E), x);  // zeros past the width, as in the kept rows
+    if constexpr (E == 2) {
+      widen_whole(*(const lu32x4*)(o1 + c * E), y);
+      widen_whole(*(const lu32x4*)(o2 + c * E), z);
+    } else {
+      l_widen<T>(l_load<T, VEC>(o1, c, width), y);
+      l_widen<T>(*(const lu32x4*)(o2 + c * E), z);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      s += x[i] * y[i];
+      s1 += x[i] * y[i];
       s2 += x[i] * z[i];
     }
   }
 #pragma unroll
   for (int w = 8; w > 0; w >>= 1) {
-    s += __shfl_xor(s, w, 64);
+    s1 += __shfl_xor(s1, w, 64);
     s2 += __shfl_xor(s2, w, 64);
   }
   if (lane) return;
-  const float s1 = s + S.lam[h] * s2;
+  if constexpr (E == 2) {
+    s1 *= S.unit[at1];
+    s2 *= S.unit[at2];
+  } else {
+    s1 += S.lam[h] * s2;
+  }
   const float l1 = S.stat[(combo * 2) * all + row], l2 = S.stat[(combo * 2 + 1) * all + row];
+  if (l2 == -kNegInf) s1 = s2 = 0.f;  // a row that sees no key, whatever its dO holds
   const int64_t at = (b * L.heads + h) * S.nq + t;
   L.rec[at] = lf4{{l1, l2, s1, s2}};
   if constexpr (E == 2) {
@@ -71,18 +99,28 @@ template <typename T, bool VEC> __global__ __launch_bounds__(256) void attn_rows
 }
 
 // dλ of a head: minus the sum of its rows' δ_2, in an order fixed by the sizes.
-__global__ __launch_bounds__(256) void attn_dlam(const AttnGradLaunch L) {
-  __shared__ float red[4];
+// A workgroup per head, bound by the latency of its loads: 16 waves with four
+// loads in flight each (4x4096 rows: 23 µs with four waves of one load, 5.4 now).
+constexpr int kLamThreads = 1024, kLamLoads = 4;
+__global__ __launch_bounds__(kLamThreads) void attn_dlam(const AttnGradLaunch L) {
+  __shared__ float red[kLamThreads / 64];
   const int h = blockIdx.x;
-  float s = 0.f;
+  float s[kLamLoads] = {};
   for (int b = 0; b < L.batch; ++b) {
     const float* p = L.rowLam + ((int64_t)b * L.heads + h) * L.s.nq;
-    for (int64_t t = threadIdx.x; t < L.s.nq; t += 256) s += p[t];
+    for (int64_t t0 = threadIdx.x; t0 < L.s.nq; t0 += kLamThreads * kLamLoads)
+#pragma unroll
+      for (int i = 0; i < kLamLoads; ++i) {
+        const int64_t t = t0 + i * kLamThreads;
+        s[i] += t < L.s.nq ? p[t] : 0.f;
+      }
   }
-  s = l_wave_sum(s);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  float sum = l_wave_sum((s[0] + s[1]) + (s[2] + s[3]));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) L.dlam[h] = -(red[0] + red[1] + red[2] + red[3]);
+  if (threadIdx.x >= 64) return;
+  sum = l_wave_sum(threadIdx.x < kLamThreads / 64 ? red[threadIdx.x] : 0.f);
+  if (threadIdx.x == 0) L.dlam[h] = -sum;
 }
 
 }  // namespace
@@ -91,8 +129,7 @@ hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, hipStream_t st) 
   const int64_t rows = (int64_t)L.batch * L.s.nq * L.heads;
   const dim3 grid((unsigned)((rows + 15) / 16));
   if (bf16) {
-    if (L.outVec) attn_rows<Bf16, true><<<grid, 256, 0, st>>>(L);
-    else attn_rows<Bf16, false><<<grid, 256, 0, st>>>(L);
+    attn_rows<Bf16, true><<<grid, 256, 0, st>>>(L);
   } else {
     if (L.outVec) attn_rows<float, true><<<grid, 256, 0, st>>>(L);
     else attn_rows<float, false><<<grid, 256, 0, st>>>(L);
@@ -101,7 +138,7 @@ hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, hipStream_t st) 
 }
 
 hipError_t launch_attn_dlam(const AttnGradLaunch& L, hipStream_t st) {
-  attn_dlam<<<dim3(L.heads), 256, 0, st>>>(L);
+  attn_dlam<<<dim3(L.heads), kLamThreads, 0, st>>>(L);
   return hipGetLastError();
 }
 

@@ -56,6 +56,18 @@ template <typename T> __device__ __forceinline__ af32x16 a_mma(lu32x4 a, lu32x4 
   }
 }
 
+// sum + the eight bf16 of an operand.
+__device__ __forceinline__ float a_operand_sum(const lu32x4& op, float sum) {
+  typedef __bf16 Two __attribute__((ext_vector_type(2)));
+  const Two one = {(__bf16)1.f, (__bf16)1.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t two = op[i];  // (a bit_cast of a vector's element itself takes the vector's first)
+    sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(Two, two), one, sum, false);
+  }
+  return sum;
+}
+
 // Step s of a result as an operand.
 template <typename T> __device__ __forceinline__ lu32x4 a_operand(const float (&p)[16], int s) {
   lu32x4 r;
@@ -238,6 +250,10 @@ __device__ __forceinline__ float a_half_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
+__device__ __forceinline__ uint32_t a_half_max(uint32_t v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(r[0], r[1]);
+}
 __device__ __forceinline__ float a_half_sum(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
@@ -248,11 +264,32 @@ __device__ __forceinline__ float a_log2(float v) { return __builtin_amdgcn_logf(
 
 constexpr float kNegInf = -__builtin_inff();
 
+typedef uint32_t lu32x2 __attribute__((ext_vector_type(2)));
+
+// Values as 16-bit whole multiples of a unit, their largest magnitude / 32767
+// (given as the bits of that magnitude): off by at most one unit.  Rows with an
+// infinity or NaN have the unit NaN, all but vanishing ones the unit 0.
+struct Whole {
+  float unit, inv;  // inv: to [−1, 1]
+  __device__ __forceinline__ explicit Whole(uint32_t top) {
+    const float f = __uint_as_float(top);
+    const bool some = f > 1e-30f, finite = top < 0x7f800000u;
+    inv = some && finite ? 1.f / f : 0.f;
+    unit = !finite ? __builtin_nanf("") : some ? f / 32767.f : 0.f;
+  }
+};
+__device__ __forceinline__ uint32_t a_pair_whole(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pknorm_i16(a, b));
+}
+
 // Values of one row and the 32 columns of a result's transpose (lane: row
 // l % 32, registers: columns 8·(i / 4) + 4·half + i % 4) as stores of four,
 // or, for bf16 with 16-byte stores, of eight columns.
-template <typename T> __device__ __forceinline__ void a_store_row(char* row, const float (&v)[16], int col0, int width,
-                                                                  bool vec, bool valid, int half) {
+// WHOLE (bf16): of values in [−1, 1] the multiples of 1/32767 instead.
+template <typename T, bool WHOLE = false>
+__device__ __forceinline__ void a_store_row(char* row, const float (&v)[16], int col0, int width, bool vec, bool valid,
+                                            int half) {
+  auto pair = [](float a, float b) { return WHOLE ? a_pair_whole(a, b) : l_f32_bf16x2(a, b); };
   if constexpr (AT<T>::kBytes == 2) {
     if (vec) {  // the halves exchange groups of four columns, so that each lane has eight in a row
 #pragma unroll
@@ -260,9 +297,8 @@ template <typename T> __device__ __forceinline__ void a_store_row(char* row, con
         uint32_t x[2], y[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const auto s = __builtin_amdgcn_permlane32_swap(l_f32_bf16x2(v[4 * g + 2 * i], v[4 * g + 2 * i + 1]),
-                                                          l_f32_bf16x2(v[4 * g + 4 + 2 * i], v[4 * g + 5 + 2 * i]),
-                                                          false, false);
+          const auto s = __builtin_amdgcn_permlane32_swap(pair(v[4 * g + 2 * i], v[4 * g + 2 * i + 1]),
+                                                          pair(v[4 * g + 4 + 2 * i], v[4 * g + 5 + 2 * i]), false, false);
           x[i] = s[0];
           y[i] = s[1];
         }
