@@ -117,7 +117,8 @@ def _input_heads(t, name):
 
 
 def _strides(t):
-    return _i64x3(*t.stride()[:3])
+    b, n, h, _ = t.stride()
+    return _i64x3(b, n, h)
 
 
 def _output(out, shape, dtype, dev, name):
@@ -173,11 +174,12 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
 
 
 def _rotary(entry, q, k, freqs, positions, start, interleaved, scale, q_out, k_out, stream):
-    L = _lib()
     dev = _device(q, "q")
     code = _code(q, "q")
-    _same(dev, q.dtype, k=k)
-    _same(dev, torch.float64, freqs=freqs)
+    if k is not None and (k.device != dev or k.dtype != q.dtype):
+        _same(dev, q.dtype, k=k)
+    if freqs.device != dev or freqs.dtype != torch.float64:
+        _same(dev, torch.float64, freqs=freqs)
     if freqs.dim() != 1 or not freqs.is_contiguous():
         raise ValueError(f"freqs must be a contiguous vector, got shape {tuple(freqs.shape)}")
     with _on(dev, stream):
@@ -186,32 +188,43 @@ def _rotary(entry, q, k, freqs, positions, start, interleaved, scale, q_out, k_o
         r = MuonRotary(batch, tokens, dim, 2 * freqs.numel(), _ptr(freqs), None, 0, int(start), 0,
                        int(bool(interleaved)), scale, code)
         if positions is not None:
-            _same(dev, None, positions=positions)
-            if positions.dtype not in (torch.int32, torch.int64):
-                raise TypeError(f"positions have dtype {positions.dtype}; use int32 or int64")
-            if tuple(positions.shape) not in ((tokens,), (1, tokens), (batch, tokens)):
-                raise ValueError(f"positions have shape {tuple(positions.shape)}, expected ({tokens},) or "
-                                 f"({batch}, {tokens})")
-            if tokens > 1 and positions.stride(-1) != 1:
-                positions = positions.contiguous()
-            many = positions.dim() == 2 and positions.shape[0] > 1
-            if many and 0 < positions.stride(0) < tokens:
-                positions = positions.contiguous()
-            r.positions, r.position_bytes = _ptr(positions), positions.element_size()
-            r.position_stride = positions.stride(0) if many else 0
-        outs, arr, kept = [], _two_heads(), []
-        n = 1 if k is None else 2
-        for i, (t, out, name) in enumerate(((q, q_out, "q"), (k, k_out, "k"))[:n]):
-            t4 = _input_heads(t, name) if i else q4
-            if t4.shape[:2] != q4.shape[:2] or t4.shape[3] != dim or t.dim() != q.dim():
-                raise ValueError(f"k has shape {tuple(t.shape)}, q {tuple(q.shape)}: only their heads may differ")
-            o = _output(out, t.shape, t.dtype, dev, name + "_out")
-            o4 = o if o.dim() == 4 else o.unsqueeze(0)
-            arr[i] = MuonRotaryHeads(_ptr(t4), _ptr(o4), t4.shape[2], _strides(t4), _strides(o4))
-            outs.append(o)
-            kept.append(t4)
-        _check(entry(L)(ctypes.byref(r), arr, n, _raw_stream(dev.index)))
-    return (outs[0], outs[1] if n == 2 else None)
+            positions = _positions(r, positions, dev)
+        arr = _two_heads()
+        qo, kept = _turn(arr, 0, q, q4, q_out, "q")
+        ko, n = None, 1
+        if k is not None:
+            k4 = _input_heads(k, "k")
+            if k4.shape[0] != batch or k4.shape[1] != tokens or k4.shape[3] != dim or k.dim() != q.dim():
+                raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}: only their heads may differ")
+            (ko, kept2), n = _turn(arr, 1, k, k4, k_out, "k"), 2
+        _check(entry(ctypes.byref(r), arr, n, _raw_stream(dev.index)))
+    return qo, ko
+
+
+def _positions(r, positions, dev):
+    """Sets them in r; the tensor r then points into."""
+    if positions.device != dev or positions.dtype not in (torch.int32, torch.int64):
+        _same(dev, None, positions=positions)
+        raise TypeError(f"positions have dtype {positions.dtype}; use int32 or int64")
+    shape, tokens = tuple(positions.shape), r.tokens
+    if shape not in ((tokens,), (1, tokens), (r.batch, tokens)):
+        raise ValueError(f"positions have shape {shape}, expected ({tokens},) or ({r.batch}, {tokens})")
+    if tokens > 1 and positions.stride(-1) != 1:
+        positions = positions.contiguous()
+    if len(shape) == 2 and shape[0] > 1:
+        if 0 < positions.stride(0) < tokens:
+            positions = positions.contiguous()
+        r.position_stride = positions.stride(0)
+    r.positions, r.position_bytes = _ptr(positions), positions.element_size()
+    return positions
+
+
+def _turn(arr, i, t, t4, out, name):
+    """Sets tensor i of a call: (its output, what arr points into)."""
+    o = _output(out, t.shape, t.dtype, t.device, name + "_out")
+    o4 = o if o.dim() == 4 else o.unsqueeze(0)
+    arr[i] = MuonRotaryHeads(_ptr(t4), _ptr(o4), t4.shape[2], _strides(t4), _strides(o4))
+    return o, t4
 
 
 def muon_rotary(q, k, freqs, positions=None, start: int = 0, interleaved: bool = False, scale: float = 1.0,
@@ -222,14 +235,14 @@ def muon_rotary(q, k, freqs, positions=None, start: int = 0, interleaved: bool =
     alone): (batch, tokens, heads, dim) or (tokens, heads, dim); freqs:
     float64; positions: int32 or int64, (tokens,) or (batch, tokens), by
     default start, start + 1, …  q_out and k_out may be q and k (in place)."""
-    return _rotary(lambda L: L.muon_rotary, q, k, freqs, positions, start, interleaved, scale, q_out, k_out, stream)
+    return _rotary(_lib().muon_rotary, q, k, freqs, positions, start, interleaved, scale, q_out, k_out, stream)
 
 
 def muon_rotary_grad(dq, dk, freqs, positions=None, start: int = 0, interleaved: bool = False, scale: float = 1.0,
                      q_out=None, k_out=None, stream=None):
     """Gradients of muon_rotary's q and k from those of its results: the
     rotation by the opposite angles.  Arguments as there."""
-    return _rotary(lambda L: L.muon_rotary_grad, dq, dk, freqs, positions, start, interleaved, scale, q_out, k_out,
+    return _rotary(_lib().muon_rotary_grad, dq, dk, freqs, positions, start, interleaved, scale, q_out, k_out,
                    stream)
 
 
