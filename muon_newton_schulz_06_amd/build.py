@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libmuon_ns.so")
 SOURCES = ["gemm_axpy.hip", "gemm_sq.hip", "gemm_final.hip", "gemm_syrk.hip", "elementwise.hip",
            "select.hip", "noalloc.hip", "embedding.hip", "rmsnorm.hip", "ffn_tile32.hip", "ffn_tile16_glu.hip",
            "ffn_tile16_store.hip", "ffn_few.hip", "ffn_join.hip", "rotary.hip", "dropout.hip", "attn_prep.hip", "attn_fwd.hip",
-           "attn_rows.hip", "attn_dq.hip", "attn_dkv.hip", "plan.cpp", "api.cpp", "layers_api.cpp", "attention_api.cpp"]
+           "attn_rows.hip", "attn_dq.hip", "attn_dkv.hip", "attn_join.hip", "plan.cpp", "api.cpp", "layers_api.cpp",
+           "attention_api.cpp"]
 
 
 def hipcc() -> str:

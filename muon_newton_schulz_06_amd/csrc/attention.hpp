@@ -141,16 +141,15 @@ struct AttnGradLaunch {
   AttnRuns keyRuns, rowRuns;  // of attn_dkv, attn_dq
   int32_t packed;
   // sums of blocks that stretches share: attn_dkv [2·stretch][128 keys][4·DP] of
-  // dk1, dk2, dv; attn_dq [2·stretch][128 rows][2·DP + 1] of dq1, dq2 and λ's
-  float* part;
+  // dk1, dk2, dv; attn_dq [2·stretch][128 rows][2·DP + 4] of dq1, dq2 and λ's
+  float *part, *rowPart;
+  int32_t joinKeys, joinRows;  // which of them there are
 };
 constexpr int kDkvKeys = 128, kDqRows = 128;
-hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, hipStream_t st);
 hipError_t launch_attn_dkv(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
-hipError_t launch_attn_dkv_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
 int attn_dq_keys(bool bf16, int dp);  // of a tile
 hipError_t launch_attn_dq(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
-hipError_t launch_attn_dq_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
+hipError_t launch_attn_grad_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st);
 hipError_t launch_attn_dlam(const AttnGradLaunch& L, hipStream_t st);
 
 // Block lists: units·n rows of a sequence of n tokens are cut into blocks of
@@ -173,6 +172,8 @@ struct AttnPrepLaunch {
   int32_t lists;
 };
 hipError_t launch_attn_prep(const AttnPrepLaunch& L, hipStream_t st);
+// The row sums of the backward pass, and its lists beside them.
+hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, const AttnPrepLaunch& P, hipStream_t st);
 
 // Aligned copies [batch][token][head][pitch] of tensors whose rows are not
 // whole aligned 16-byte chunks.

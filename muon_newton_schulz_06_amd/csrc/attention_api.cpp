@@ -354,7 +354,7 @@ struct RunsPlan {
 };
 
 struct AttnGradLayout {
-  size_t q, k, v, dout, rec, recL, recD, rowLam, part, total;
+  size_t q, k, v, dout, rec, recL, recD, rowLam, part, rowPart, total;
   RunsPlan keys, rows;
 };
 
@@ -401,7 +401,8 @@ AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout
   g.recL = take(bf16 ? rows * 16 : 0);
   g.recD = take(bf16 ? rows * 16 : 0);
   g.rowLam = take(rows * 4);
-  g.part = take(std::max((size_t)g.keys.streams * 2 * kDkvKeys * 4 * l.dp, (size_t)g.rows.streams * 2 * kDqRows * (2 * l.dp + 4)) * 4);
+  g.part = take((size_t)g.keys.streams * 2 * kDkvKeys * 4 * l.dp * 4);
+  g.rowPart = take((size_t)g.rows.streams * 2 * kDqRows * (2 * l.dp + 4) * 4);
   g.total = at;
   return g;
 }
@@ -698,10 +699,6 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     };
     L.keyRuns = runs(w.keys, (int32_t)f->keys, 1, kDkvKeys, 0);
     L.rowRuns = runs(w.rows, (int32_t)f->queries, L.s.group, kDqRows, attn_dq_keys(bf16, l.dp));
-    if (P.lists) {
-      s = launched("blocks of the batch", launch_attn_prep(P, st), st);
-      if (s != MUON_OK) return s;
-    }
     L.s.stat = (float*)((char*)saved + l.stat);
     L.s.unit = (float*)((char*)saved + l.unit);
     L.s.kept = (char*)saved + l.kept;
@@ -723,25 +720,24 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     L.heads = (int32_t)f->heads;
     L.packed = f->sequences > 0;
     L.part = (float*)(ws + w.part);
-    if (hd.count() > 0) {
-      s = launched("row sums of the gradient", launch_attn_rows(bf16, L, st), st);
+    L.rowPart = (float*)(ws + w.rowPart);
+    L.joinKeys = wantK && w.keys.streams;
+    L.joinRows = wantQ && w.rows.streams;
+    if (hd.count() > 0 || P.lists) {
+      s = launched("row sums of the gradient", launch_attn_rows(bf16, L, P, st), st);
       if (s != MUON_OK) return s;
     }
     if (wantK) {
       s = launched("gradients of keys and values", launch_attn_dkv(bf16, l.dp, L, st), st);
       if (s != MUON_OK) return s;
-      if (w.keys.streams) {
-        s = launched("sums of shared blocks of keys", launch_attn_dkv_join(bf16, l.dp, L, st), st);
-        if (s != MUON_OK) return s;
-      }
     }
     if (wantQ) {
       s = launched("gradient of the queries", launch_attn_dq(bf16, l.dp, L, st), st);
       if (s != MUON_OK) return s;
-      if (w.rows.streams) {
-        s = launched("sums of shared blocks of rows", launch_attn_dq_join(bf16, l.dp, L, st), st);
-        if (s != MUON_OK) return s;
-      }
+    }
+    if (L.joinKeys || L.joinRows) {
+      s = launched("sums of shared blocks", launch_attn_grad_join(bf16, l.dp, L, st), st);
+      if (s != MUON_OK) return s;
     }
     if (!grads->dlambda) return MUON_OK;
     return launched("gradient of lambda", launch_attn_dlam(L, st), st);

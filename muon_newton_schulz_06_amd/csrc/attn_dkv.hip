@@ -394,52 +394,11 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   }
 }
 
-// The sums of blocks that several stretches share, added in the stretches'
-// order by the workgroups of the one the block begins in: its part lies in that
-// one's second slot, the others in the next ones' first.
-template <typename T, int DP> __global__ __launch_bounds__(256) void attn_dkv_join(const AttnGradLaunch L) {
-  constexpr int E = AT<T>::kBytes, kKeys = 8;
-  const AttnShape& S = L.s;
-  const Stretch W(L.keyRuns, S.combos, blockIdx.x);
-  if (W.stop >= W.total) return;
-  const int64_t combo = W.stop / W.each;  // of the next stretch's first tile
-  const int b = W.find(L.keyRuns, W.stop - combo * W.each);
-  const int64_t from = combo * W.each + L.keyRuns.cum[b], to = combo * W.each + L.keyRuns.cum[b + 1];
-  if (from >= W.stop || from < W.pos) return;  // not shared, or begun before
-  const AttnBlock B = L.keyRuns.list.blocks[b];
-  const int64_t batch = combo / S.kv, hk = combo % S.kv;
-  constexpr int64_t kSlot = (int64_t)kDkvKeys * 4 * DP;
-  for (int i = threadIdx.x; i < kKeys * DP; i += 256) {
-    const int key = blockIdx.y * kKeys + i / DP, c0 = i % DP * 4;
-    if (B.at + key >= B.n) break;
-    const float* p = L.part + (int64_t)key * (4 * DP) + c0;
-    lf32x4 s = *(const lf32x4*)(p + (2 * (int64_t)blockIdx.x + 1) * kSlot);
-#pragma unroll 4
-    for (int64_t w = blockIdx.x + 1; w * W.per < to; ++w) s += *(const lf32x4*)(p + 2 * w * kSlot);
-    const int64_t tok = B.tok + B.at + key;
-    if (c0 < 2 * DP) {
-      const int m = c0 >= DP, c = c0 - m * DP;
-      char* o = (char*)L.dk + (batch * L.dks[0] + tok * L.dks[1] + (2 * hk + m) * L.dks[2]) * E;
-      for (int j = 0; j < 4; ++j)
-        if (c + j < S.dim) LType<T>::put(o, c + j, s[j] * L.scale);
-    } else {
-      const int c = c0 - 2 * DP;
-      char* o = (char*)L.dv + (batch * L.dvs[0] + tok * L.dvs[1] + hk * L.dvs[2]) * E;
-      for (int j = 0; j < 4; ++j)
-        if (c + j < 2 * S.dim) LType<T>::put(o, c + j, s[j]);
-    }
-  }
-}
-
 template <typename T, int DP, int PART, int... REST> hipError_t run(const AttnGradLaunch& L, hipStream_t st) {
   attn_dkv<T, DP, PART><<<dim3((unsigned)(L.keyRuns.streams ? L.keyRuns.streams : L.s.combos * L.keyRuns.blocks)), 256, 0, st>>>(L);
   const hipError_t e = hipGetLastError();
   if constexpr (sizeof...(REST) > 0) return e != hipSuccess ? e : run<T, DP, REST...>(L, st);
   else return e;
-}
-template <typename T, int DP> hipError_t join(const AttnGradLaunch& L, hipStream_t st) {
-  attn_dkv_join<T, DP><<<dim3(L.keyRuns.streams, kDkvKeys / 8), 256, 0, st>>>(L);
-  return hipGetLastError();
 }
 
 }  // namespace
@@ -448,10 +407,6 @@ hipError_t launch_attn_dkv(bool bf16, int dp, const AttnGradLaunch& L, hipStream
   // operands and sums of 32 wide keys are more than a wave's registers: more passes
   if (bf16) return dp == 64 ? run<Bf16, 64, 3>(L, st) : run<Bf16, 128, 1, 2>(L, st);
   return dp == 64 ? run<float, 64, 3>(L, st) : run<float, 128, 1, 2>(L, st);
-}
-hipError_t launch_attn_dkv_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {
-  if (bf16) return dp == 64 ? join<Bf16, 64>(L, st) : join<Bf16, 128>(L, st);
-  return dp == 64 ? join<float, 64>(L, st) : join<float, 128>(L, st);
 }
 
 }  // namespace muon

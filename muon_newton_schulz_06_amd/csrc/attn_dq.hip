@@ -226,7 +226,7 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
   }
   if constexpr (k2nd) sum = a_half_sum(sum);
   if (P.slot >= 0) {
-    float* o = L.part + (P.slot * kDqRows + wave * 32 + (lane & 31)) * (2 * DP + 4);
+    float* o = L.rowPart + (P.slot * kDqRows + wave * 32 + (lane & 31)) * (2 * DP + 4);
     if (k2nd && valid && half == 0) o[2 * DP] = sum;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -259,53 +259,8 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
   }
 }
 
-// The sums of blocks that several stretches share, added in the stretches'
-// order (see attn_dkv.hip).
-template <typename T, int DP> __global__ __launch_bounds__(256) void attn_dq_join(const AttnGradLaunch L) {
-  constexpr int E = AT<T>::kBytes, kRows = 8, kLd = 2 * DP + 4, kCols = 2 * DP / 4 + 1;
-  const AttnShape& S = L.s;
-  const Stretch W(L.rowRuns, S.combos, blockIdx.x);
-  if (W.stop >= W.total) return;
-  const int64_t combo = W.stop / W.each;  // of the next stretch's first tile
-  const int b = W.find(L.rowRuns, W.stop - combo * W.each);
-  const int64_t from = combo * W.each + L.rowRuns.cum[b], to = combo * W.each + L.rowRuns.cum[b + 1];
-  if (from >= W.stop || from < W.pos) return;  // not shared, or begun before
-  const AttnBlock B = L.rowRuns.list.blocks[b];
-  const int nq = L.packed ? B.n : (int)S.nq, nk = L.packed ? B.nk : (int)S.nk;
-  const int batch = (int)combo / S.kv, hk = (int)combo % S.kv, G = S.group;
-  constexpr int64_t kSlot = (int64_t)kDqRows * kLd;
-  for (int i = threadIdx.x; i < kRows * kCols; i += 256) {
-    const int r = blockIdx.y * kRows + i / kCols, c0 = i % kCols * 4;
-    const int row = B.at + r;
-    if (row >= nq * G) break;
-    const float* p = L.part + r * kLd + c0;
-    lf32x4 s = *(const lf32x4*)(p + (2 * (int64_t)blockIdx.x + 1) * kSlot);
-#pragma unroll 4
-    for (int64_t w = blockIdx.x + 1; w * W.per < to; ++w) s += *(const lf32x4*)(p + 2 * w * kSlot);
-    const int t = row / G, head = hk * G + row - t * G;
-    const int64_t tok = B.tok + t;
-    if (c0 == 2 * DP) {
-      const int64_t at = ((int64_t)batch * L.heads + head) * S.nq + tok;
-      L.rowLam[at] = L.rec[at].v[3] + s[0];
-      continue;
-    }
-    if (!L.dq) continue;
-    const int lim = S.causal ? min(t + nk - nq + 1, nk) : nk;
-    const int m = c0 >= DP, c = c0 - m * DP;
-    const float f = lim > 1 ? m ? -S.lam[head] * L.scale : L.scale : 0.f;
-    char* o = (char*)L.dq + (batch * L.dqs[0] + tok * L.dqs[1] + (2 * head + m) * L.dqs[2]) * E;
-    for (int j = 0; j < 4; ++j)
-      if (c + j < S.dim) LType<T>::put(o, c + j, lim > 1 ? s[j] * f : 0.f);
-  }
-}
-
 template <typename T, int DP, int MAPS> hipError_t run(const AttnGradLaunch& L, hipStream_t st) {
   attn_dq<T, DP, MAPS><<<dim3((unsigned)(L.rowRuns.streams ? L.rowRuns.streams : L.s.combos * L.rowRuns.blocks)), 256, 0, st>>>(L);
-  return hipGetLastError();
-}
-
-template <typename T, int DP> hipError_t join(const AttnGradLaunch& L, hipStream_t st) {
-  attn_dq_join<T, DP><<<dim3(L.rowRuns.streams, kDqRows / 8), 256, 0, st>>>(L);
   return hipGetLastError();
 }
 
@@ -315,10 +270,6 @@ int attn_dq_keys(bool, int) { return 32; }
 static_assert(Dq<Bf16, 64>::kBN == 32 && Dq<Bf16, 128>::kBN == 32 && Dq<float, 64>::kBN == 32 && Dq<float, 128>::kBN == 32,
               "attn_dq_keys");
 
-hipError_t launch_attn_dq_join(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {
-  if (bf16) return dp == 64 ? join<Bf16, 64>(L, st) : join<Bf16, 128>(L, st);
-  return dp == 64 ? join<float, 64>(L, st) : join<float, 128>(L, st);
-}
 hipError_t launch_attn_dq(bool bf16, int dp, const AttnGradLaunch& L, hipStream_t st) {
   if (bf16) return dp == 64 ? run<Bf16, 64, 3>(L, st) : run<Bf16, 128, 3>(L, st);
   if (dp == 64) return run<float, 64, 3>(L, st);

@@ -11,7 +11,10 @@
 // 6.6·10^-3 instead of 2.5·10^-3).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "attention.hpp"
+#include "attn_lists.hpp"
 #include "attn_tile.hpp"
 
 namespace muon {
@@ -35,66 +38,71 @@ __device__ __forceinline__ void widen_whole(const lu32x4& v, float (&f)[8]) {
   }
 }
 
-template <typename T, bool VEC> __global__ __launch_bounds__(256) void attn_rows(const AttnGradLaunch L) {
+// The first workgroups make the lists of the products that follow, which take as
+// long (7 µs: scans and searches by one workgroup) as the sums of few rows.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(kPrep) void attn_rows(const AttnGradLaunch L, const AttnPrepLaunch P) {
+  if ((int)blockIdx.x < P.lists) return attn_lists(P, blockIdx.x);
   constexpr int V = LType<T>::kVec, E = AT<T>::kBytes;
   const AttnShape& S = L.s;
   const int64_t rows = (int64_t)L.batch * S.nq * L.heads;
-  const int64_t id = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  if (id >= rows) return;
-  const int lane = threadIdx.x & 15;
-  const int64_t bt = id / L.heads;
-  const int h = (int)(id - bt * L.heads);
-  const int64_t b = bt / S.nq, t = bt - b * S.nq;
-  const int hk = h / S.group, g = h - hk * S.group;
-  const int64_t combo = b * S.kv + hk, row = t * S.group + g, all = S.nq * S.group;
-  const char* d = (const char*)L.dout + (b * L.gs[0] + t * L.gs[1] + h * L.gs[2]) * E;
-  const char* o = (const char*)L.out + (b * L.os[0] + t * L.os[1] + h * L.os[2]) * E;
-  const int64_t at1 = E == 2 ? combo * 2 * all + row : 0, at2 = E == 2 ? at1 + all : combo * all + row;
-  const char* o1 = E == 2 ? (const char*)S.kept + at1 * S.pitch * E : o;
-  const char* o2 = (const char*)S.kept + at2 * S.pitch * E;
-  const int width = 2 * S.dim;
-  float s1 = 0.f, s2 = 0.f;
-  for (int c = lane * V; c < width; c += 16 * V) {
-    float x[V], y[V], z[V];
-    l_widen<T>(*(const lu32x4*)(d + c * E), x);  // zeros past the width, as in the kept rows
+  const int64_t each = (int64_t)(gridDim.x - P.lists) * (kPrep / 16);
+  for (int64_t id = (int64_t)(blockIdx.x - P.lists) * (kPrep / 16) + (threadIdx.x >> 4); id < rows; id += each) {
+    const int lane = threadIdx.x & 15;
+    const int64_t bt = id / L.heads;
+    const int h = (int)(id - bt * L.heads);
+    const int64_t b = bt / S.nq, t = bt - b * S.nq;
+    const int hk = h / S.group, g = h - hk * S.group;
+    const int64_t combo = b * S.kv + hk, row = t * S.group + g, all = S.nq * S.group;
+    const char* d = (const char*)L.dout + (b * L.gs[0] + t * L.gs[1] + h * L.gs[2]) * E;
+    const char* o = (const char*)L.out + (b * L.os[0] + t * L.os[1] + h * L.os[2]) * E;
+    const int64_t at1 = E == 2 ? combo * 2 * all + row : 0, at2 = E == 2 ? at1 + all : combo * all + row;
+    const char* o1 = E == 2 ? (const char*)S.kept + at1 * S.pitch * E : o;
+    const char* o2 = (const char*)S.kept + at2 * S.pitch * E;
+    const int width = 2 * S.dim;
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = lane * V; c < width; c += 16 * V) {
+      float x[V], y[V], z[V];
+      l_widen<T>(*(const lu32x4*)(d + c * E), x);  // zeros past the width, as in the kept rows
+      if constexpr (E == 2) {
+        widen_whole(*(const lu32x4*)(o1 + c * E), y);
+        widen_whole(*(const lu32x4*)(o2 + c * E), z);
+      } else {
+        l_widen<T>(l_load<T, VEC>(o1, c, width), y);
+        l_widen<T>(*(const lu32x4*)(o2 + c * E), z);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s1 += x[i] * y[i];
+        s2 += x[i] * z[i];
+      }
+    }
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) {
+      s1 += __shfl_xor(s1, w, 64);
+      s2 += __shfl_xor(s2, w, 64);
+    }
+    if (lane) continue;
     if constexpr (E == 2) {
-      widen_whole(*(const lu32x4*)(o1 + c * E), y);
-      widen_whole(*(const lu32x4*)(o2 + c * E), z);
+      s1 *= S.unit[at1];
+      s2 *= S.unit[at2];
     } else {
-      l_widen<T>(l_load<T, VEC>(o1, c, width), y);
-      l_widen<T>(*(const lu32x4*)(o2 + c * E), z);
+      s1 += S.lam[h] * s2;
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      s1 += x[i] * y[i];
-      s2 += x[i] * z[i];
+    const float l1 = S.stat[(combo * 2) * all + row], l2 = S.stat[(combo * 2 + 1) * all + row];
+    if (l2 == -kNegInf) s1 = s2 = 0.f;  // a row that sees no key, whatever its dO holds
+    const int64_t at = (b * L.heads + h) * S.nq + t;
+    L.rec[at] = lf4{{l1, l2, s1, s2}};
+    if constexpr (E == 2) {
+      // −L/c is finite: an infinity would meet zeros in the product
+      uint32_t a[3], e[3];
+      split3(fmaxf(fminf(-l1 / S.c, 1e30f), -1e30f), a);
+      split3(fmaxf(fminf(-l2 / S.c, 1e30f), -1e30f), e);
+      L.recL[at] = lu4{{a[0] | a[1] << 16, a[2] | e[0] << 16, e[1] | e[2] << 16, 0u}};
+      split3(-s1, a);
+      split3(-s2, e);
+      L.recD[at] = lu4{{a[0] | a[1] << 16, a[2] | e[0] << 16, e[1] | e[2] << 16, 0u}};
     }
-  }
-#pragma unroll
-  for (int w = 8; w > 0; w >>= 1) {
-    s1 += __shfl_xor(s1, w, 64);
-    s2 += __shfl_xor(s2, w, 64);
-  }
-  if (lane) return;
-  if constexpr (E == 2) {
-    s1 *= S.unit[at1];
-    s2 *= S.unit[at2];
-  } else {
-    s1 += S.lam[h] * s2;
-  }
-  const float l1 = S.stat[(combo * 2) * all + row], l2 = S.stat[(combo * 2 + 1) * all + row];
-  if (l2 == -kNegInf) s1 = s2 = 0.f;  // a row that sees no key, whatever its dO holds
-  const int64_t at = (b * L.heads + h) * S.nq + t;
-  L.rec[at] = lf4{{l1, l2, s1, s2}};
-  if constexpr (E == 2) {
-    // −L/c is finite: an infinity would meet zeros in the product
-    uint32_t a[3], e[3];
-    split3(fmaxf(fminf(-l1 / S.c, 1e30f), -1e30f), a);
-    split3(fmaxf(fminf(-l2 / S.c, 1e30f), -1e30f), e);
-    L.recL[at] = lu4{{a[0] | a[1] << 16, a[2] | e[0] << 16, e[1] | e[2] << 16, 0u}};
-    split3(-s1, a);
-    split3(-s2, e);
-    L.recD[at] = lu4{{a[0] | a[1] << 16, a[2] | e[0] << 16, e[1] | e[2] << 16, 0u}};
   }
 }
 
@@ -125,15 +133,12 @@ __global__ __launch_bounds__(kLamThreads) void attn_dlam(const AttnGradLaunch L)
 
 }  // namespace
 
-hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, hipStream_t st) {
-  const int64_t rows = (int64_t)L.batch * L.s.nq * L.heads;
-  const dim3 grid((unsigned)((rows + 15) / 16));
-  if (bf16) {
-    attn_rows<Bf16, true><<<grid, 256, 0, st>>>(L);
-  } else {
-    if (L.outVec) attn_rows<float, true><<<grid, 256, 0, st>>>(L);
-    else attn_rows<float, false><<<grid, 256, 0, st>>>(L);
-  }
+hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, const AttnPrepLaunch& P, hipStream_t st) {
+  const int64_t rows = (int64_t)L.batch * L.s.nq * L.heads, per = kPrep / 16;
+  const dim3 grid((unsigned)(P.lists + std::min<int64_t>((rows + per - 1) / per, 1 << 20)));
+  if (bf16) attn_rows<Bf16, true><<<grid, kPrep, 0, st>>>(L, P);
+  else if (L.outVec) attn_rows<float, true><<<grid, kPrep, 0, st>>>(L, P);
+  else attn_rows<float, false><<<grid, kPrep, 0, st>>>(L, P);
   return hipGetLastError();
 }
 

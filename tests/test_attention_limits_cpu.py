@@ -101,7 +101,8 @@ def test_attention(launches):
                 for b, q, k, h, kv, seqs in ((1, 1, 1, 1, 1, 0), (1, 1, 0, 4, 2, 0), (1, 1, 1 << 20, 28, 4, 0), (8, 1, 65536, 28, 4, 0),
                                              (1, 1, 1 << 24, 1, 1, 0), (2, 333, 333, 6, 2, 0), (1, 1 << 20, 1 << 20, 2, 1, 0),
                                              (1 << 20, 1, 1, 4, 4, 0), (1, 1 << 24, 5, 1, 1, 0), (64, 1, 333, 1 << 10, 1, 0),
-                                             (1, 8192, 8192, 28, 4, 11), (1, 1 << 20, 1 << 20, 8, 1, 1 << 20), (1, 5, 5, 2, 2, 1)):
+                                             (1, 8192, 8192, 28, 4, 11), (1, 1 << 20, 1 << 20, 8, 1, 1 << 20), (1, 5, 5, 2, 2, 1),
+                                             (1, 1 << 24, 1, 16, 16, 0), (1 << 20, 16, 1, 16, 1, 0), (1, 1 << 24, 1 << 24, 16, 16, 7)):
                     calls.append(["attention", b, q, k, h, kv, dim, seqs, causal, dt])
     found = launches(calls)
     check({c: ls for c, (ls, _) in found.items()}, least=3)
