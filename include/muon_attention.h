@@ -25,8 +25,8 @@
  *
  * An output may not overlap an input or another output unless the entry point
  * says so (MUON_ERR_ALIAS).  Overlap is judged by address ranges, except that
- * tensors of one token stride whose tokens interleave (queries and keys of one
- * fused projection) count as apart.
+ * tensors of one token stride (of one token each: batch stride) that interleave,
+ * as queries and keys of one fused projection do, count as apart.
  */
 #ifndef MUON_ATTENTION_H
 #define MUON_ATTENTION_H

@@ -16,7 +16,9 @@ values), with any strides; inputs whose values are not contiguous
 are those of the layers: float32 or bfloat16 on one CUDA/HIP device, work on the
 current stream, or on ``stream``, a cached workspace unless one is passed; the
 functions record nothing for autograd, the modules have a backward pass and
-refuse forward-mode tangents.
+refuse forward-mode tangents.  Before a backward pass is captured into a graph,
+drop the graphs that eager passes built of the same parameters: torch ties a
+parameter to the stream of the first graph that is alive.
 """
 from __future__ import annotations
 
@@ -151,7 +153,7 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
         raise ValueError(f"dim must be even and at least 2, got {dim}")
     if not base > 0 or not factor > 0:
         raise ValueError("base and factor must be positive")
-    i = torch.arange(dim // 2, dtype=torch.float64)
+    i = torch.arange(dim // 2, dtype=torch.float64, device="cpu")
     if scaling == "base":
         if dim == 2:
             raise ValueError('scaling "base" needs dim > 2')
@@ -490,7 +492,8 @@ class _DiffAttentionFn(torch.autograd.Function):
 class Rotary(torch.nn.Module):
     """Rotates queries and keys by their positions.  rotated: the values of a
     head that take part (by default all ``dim``); the scalings for long contexts
-    are rotary_frequencies'."""
+    are rotary_frequencies'.  The first call on a device copies the frequencies
+    there, so it cannot be one that is captured into a graph."""
 
     def __init__(self, dim: int, rotated: int | None = None, base: float = 10000.0, interleaved: bool = False,
                  scaling: str | None = None, factor: float = 1.0, original_length: int = 0):
@@ -498,7 +501,8 @@ class Rotary(torch.nn.Module):
         rotated = dim if rotated is None else rotated
         if rotated > dim:
             raise ValueError(f"rotated ({rotated}) above dim ({dim})")
-        self.freqs, self.scale = rotary_frequencies(rotated, base, scaling, factor, original_length)
+        with torch.inference_mode(False):
+            self.freqs, self.scale = rotary_frequencies(rotated, base, scaling, factor, original_length)
         self.dim, self.interleaved = dim, bool(interleaved)
         self._here = {}  # the frequencies per device: fp64 whatever dtype the module is cast to
 
@@ -508,7 +512,8 @@ class Rotary(torch.nn.Module):
             raise ValueError(f"heads of {q.shape[-1]} values, expected {self.dim}")
         freqs = self._here.get(q.device)
         if freqs is None:
-            freqs = self._here[q.device] = self.freqs.to(q.device)
+            with torch.inference_mode(False):  # (a later backward pass may save them)
+                freqs = self._here[q.device] = self.freqs.to(q.device, copy=True)
         q, k = _RotaryFn.apply(q, k, freqs, positions, start, self.interleaved, self.scale)
         return q if k is None else (q, k)
 
@@ -517,14 +522,24 @@ class Dropout(torch.nn.Module):
     """residual + dropout(x): each call of the training mode draws anew, from
     the seed and a counter of the calls on the device (so that replays of a
     captured graph draw anew too).  In evaluation mode, or with p = 0, the
-    addition alone."""
+    addition alone.
 
-    def __init__(self, p: float, seed: int = 0, device=None):
+    seed: by default drawn from torch's CPU generator; it is part of the state.
+    Modules (and ranks) with equal seeds drop the same elements.  The counter
+    goes by calls: a forward pass repeated to save memory would draw again."""
+
+    def __init__(self, p: float, seed: int | None = None, device=None):
         super().__init__()
         if not 0.0 <= p <= 1.0:
             raise ValueError(f"p must be in [0, 1], got {p}")
-        self.p, self.seed = float(p), int(seed)
+        self.p, self.seed = float(p), int(torch.randint(1 << 62, (), device="cpu")) if seed is None else int(seed)
         self.register_buffer("calls", torch.zeros(1, dtype=torch.int64, device=device))
+
+    def get_extra_state(self):
+        return self.seed
+
+    def set_extra_state(self, seed):
+        self.seed = int(seed)
 
     def forward(self, x, residual=None):
         if not self.training or self.p == 0.0:

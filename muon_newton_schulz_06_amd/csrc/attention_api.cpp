@@ -66,17 +66,20 @@ struct HeadArgs : Args {
     tensors.push_back({{lo, lo + (uintptr_t)k.last() * esz, name, 0, written}, k, (int64_t)esz});
   }
 
-  // Tokens of both lie one stride apart, and what one holds of a token ends
-  // before the other's begins.
+  // Tokens (or, of one token, batch entries) of both lie whole multiples of one
+  // stride apart, and what one holds of a token ends before the other's begins.
   static bool apart(const Tensor& a, const Tensor& b) {
-    const int64_t s = (a.h.n[1] > 1 ? a.h.s[1] : b.h.s[1]) * a.esz;
-    if (a.esz != b.esz || s == 0) return false;
-    int64_t ext[2];
+    if (a.esz != b.esz) return false;
     const Tensor* t[2] = {&a, &b};
+    int64_t s = 0, ext[2];
+    for (int i = 1; i >= 0; --i)
+      for (const Tensor* x : t)
+        if (s == 0 && x->h.n[i] > 1) s = x->h.s[i] * a.esz;
+    if (s == 0) return false;
     for (int i = 0; i < 2; ++i) {
       const Heads& h = t[i]->h;
-      if (h.n[1] > 1 && h.s[1] * a.esz != s) return false;
-      if (h.n[0] > 1 && h.s[0] * a.esz % s) return false;
+      for (int j = 0; j < 2; ++j)
+        if (h.n[j] > 1 && h.s[j] * a.esz % s) return false;
       ext[i] = ((h.n[2] - 1) * h.s[2] + h.dim) * a.esz;
     }
     const int64_t d = (((int64_t)(b.r.lo - a.r.lo)) % s + s) % s;

@@ -268,12 +268,12 @@ typedef uint32_t lu32x2 __attribute__((ext_vector_type(2)));
 
 // Values as 16-bit whole multiples of a unit, their largest magnitude / 32767
 // (given as the bits of that magnitude): off by at most one unit.  Rows with an
-// infinity or NaN have the unit NaN, all but vanishing ones the unit 0.
+// infinity or NaN have the unit NaN, rows of zeros (or subnormal values) the unit 0.
 struct Whole {
   float unit, inv;  // inv: to [−1, 1]
   __device__ __forceinline__ explicit Whole(uint32_t top) {
     const float f = __uint_as_float(top);
-    const bool some = f > 1e-30f, finite = top < 0x7f800000u;
+    const bool some = f > 2e-38f, finite = top < 0x7f800000u;
     inv = some && finite ? 1.f / f : 0.f;
     unit = !finite ? __builtin_nanf("") : some ? f / 32767.f : 0.f;
   }

@@ -144,6 +144,21 @@ def test_diff_attention_grad_refusals(L, kw, status):
     assert L.muon_last_error().decode()
 
 
+@pytest.mark.parametrize("kw,overlap", [
+    # q and k of one projection in place: of several tokens, and of one token of several batch entries
+    (dict(batch=2, tokens=4, q=A, qo=A, qs=(2048, 512, 64), qos=(2048, 512, 64), k=A + 512, ko=A + 512,
+          ks=(2048, 512, 64), kos=(2048, 512, 64)), False),
+    (dict(batch=3, tokens=1, q=A, qo=A, qs=(512, 512, 64), qos=(512, 512, 64), k=A + 512, ko=A + 512,
+          ks=(512, 512, 64), kos=(512, 512, 64)), False),
+    (dict(batch=3, tokens=1, q=A, qo=A, qs=(512, 7, 64), qos=(512, 7, 64), k=A + 510, ko=A + 510,
+          ks=(512, 9, 64), kos=(512, 9, 64)), True),
+    (dict(batch=3, tokens=1, q=A, qo=A, qs=(512, 7, 64), qos=(512, 7, 64), k=A + 512, ko=A + 512,
+          ks=(500, 9, 64), kos=(500, 9, 64)), True)])
+def test_interleaved_tensors(L, kw, overlap):
+    """(heads 4 and 2 of 64 bf16; what is taken gets as far as the device)"""
+    assert (rotary(L, **kw) == ALIAS) == overlap
+
+
 def test_nothing_to_do_needs_no_device(L):
     """Calls without work return before any HIP call, whatever the pointers."""
     assert rotary(L, tokens=0, q=None, qo=None, k=None, ko=None, freqs=None, pos=None) == 0
@@ -384,6 +399,27 @@ def test_dropout_module_without_dropping():
     x, r = torch.randn(3, 4), torch.randn(3, 4)
     for m in (mns.Dropout(0.0), mns.Dropout(0.7).eval()):
         assert m(x) is x and torch.equal(m(x, r), x + r) and int(m.calls) == 0
+
+
+def test_dropout_module_seeds():
+    """Drawn apart, repeatable by torch's seed, restored with the state."""
+    torch.manual_seed(5)
+    a, b = mns.Dropout(0.5), mns.Dropout(0.5)
+    torch.manual_seed(5)
+    assert a.seed != b.seed and mns.Dropout(0.5).seed == a.seed and mns.Dropout(0.5, seed=9).seed == 9
+    a.calls += 7
+    b.load_state_dict(a.state_dict())
+    assert b.seed == a.seed and int(b.calls) == 7
+
+
+def test_rotary_frequencies_outlive_inference_mode(free):
+    """Copies made where no gradients are recorded serve a training pass later."""
+    with torch.inference_mode():
+        rot = mns.Rotary(8)
+        rot(X.clone())
+    q = X.clone().requires_grad_()
+    rot(q)
+    assert not rot.freqs.is_inference() and not any(f.is_inference() for f in rot._here.values())
 
 
 def test_lambda():

@@ -114,6 +114,11 @@ def test_rotary_in_place_in_one_projection(lib, dim, rot, inter, dtype):
     lib.muon_rotary(q, k, f, interleaved=inter, q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(both[:, :, 7], before[:, :, 7])
     assert torch.equal(q[..., rot:], before[:, :, :5, rot:])
+    one = before[0, :, None].clone()  # one token of 19 batch entries
+    q, k = one[:, :, :5], one[:, :, 5:7]
+    pos = torch.arange(19, device="cuda")[:, None]
+    lib.muon_rotary(q, k, f, positions=pos, interleaved=inter, q_out=q, k_out=k)
+    assert torch.equal(q[:, 0], want[0][0]) and torch.equal(k[:, 0], want[1][0])
     # three dimensions, values apart, an output with gaps
     t = before[0, :, :5].transpose(1, 2).contiguous().transpose(1, 2)
     out = torch.full((19, 5, dim + 3), 7.0, dtype=dtype, device="cuda")
@@ -325,6 +330,15 @@ def test_attention_scores(lib, kind, dim, dtype):
     ts[:2] = q, k
     run_case(lib, ts, True, scale=1.0, what=kind, rand=False)
     run_case(lib, ts, False, scale=0.5, what=kind, rand=False)
+
+
+@pytest.mark.parametrize("power", [-100, -40, 40, 60])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_magnitudes(lib, power, dtype):
+    """Values and gradients of any size: errors stay relative to the terms (the
+    products of both stay above 2^-126 and below 2^128)."""
+    q, k, v, lam, do = attention_inputs(1, 75, 75, 2, 1, 64, dtype)
+    run_case(lib, (q, k, v * 2.0 ** power, lam, do * 2.0 ** (20 if power < 0 else 0)))
 
 
 @pytest.mark.parametrize("lam", [0.0, 1.0, -3.0, 100.0])
