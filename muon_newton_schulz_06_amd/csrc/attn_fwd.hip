@@ -29,7 +29,8 @@
 // tokens, 28 heads of 64 on 4, bf16, causal: 700 to 720 µs (1000 TFLOP/s of the
 // four products) without the second sum and with the second map's result kept
 // alone, 790 with both; comparing every maximum: 800 and more.  One token of
-// 16384 keys, split over 512 workgroups: 11 µs, 3 TB/s, and 7.6 for the join.
+// 16384 keys, split over 512 workgroups: 11 µs, 3 TB/s, and 6 for the join (three of
+// a workgroup's four tiles on their way at once instead of one: 11.8).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -331,8 +332,8 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
 // from the logarithms of their sums, then both maps' columns, four a thread,
 // the splits dealt out to as many groups of threads as there are and the groups
 // added in order.
-template <typename T, int DP> __global__ __launch_bounds__(256) void attn_join(const AttnFwdLaunch L) {
-  constexpr int E = AT<T>::kBytes, COLS = DP, GROUPS = 256 / COLS;  // threads for 2 · 2·DP columns
+template <typename T, int DP, int THREADS> __global__ __launch_bounds__(THREADS) void attn_join(const AttnFwdLaunch L) {
+  constexpr int E = AT<T>::kBytes, COLS = DP, GROUPS = THREADS / COLS;  // threads for 2 · 2·DP columns
   __shared__ float weight[2][kMaxSplits], top[2], sums[2];
   __shared__ uint32_t most[2];  // the largest magnitude of a map's results
   __shared__ lf32x4 part[GROUPS][COLS];
@@ -372,7 +373,7 @@ template <typename T, int DP> __global__ __launch_bounds__(256) void attn_join(c
   const int col = tid % COLS, group = tid / COLS, map = col / (COLS / 2);
   const float* d = L.part + id * (4 * DP) + col * 4;
   lf32x4 res = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
   for (int s = group; s < L.splits; s += GROUPS) {
     const float w = weight[map][s];
     const lf32x4 v = *(const lf32x4*)(d + s * all * (4 * DP));
@@ -427,7 +428,10 @@ template <typename T, int DP, bool FEW> hipError_t run(const AttnFwdLaunch& L, h
 }
 template <typename T, int DP> hipError_t join(const AttnFwdLaunch& L, hipStream_t st) {
   const int64_t rows = L.s.nq * L.s.group * L.s.combos;
-  attn_join<T, DP><<<dim3((unsigned)rows), 256, 0, st>>>(L);
+  // a row's reads all in flight where there are many splits, and so few rows (one
+  // token, 128 splits: 7.6 µs by four waves a row, 6.0 by sixteen)
+  if (L.splits >= 32) attn_join<T, DP, 1024><<<dim3((unsigned)rows), 1024, 0, st>>>(L);
+  else attn_join<T, DP, 256><<<dim3((unsigned)rows), 256, 0, st>>>(L);
   return hipGetLastError();
 }
 
