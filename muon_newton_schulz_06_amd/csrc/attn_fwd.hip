@@ -22,15 +22,17 @@
 // is divided.  Where one key has most of a row, the rounding of its probability
 // then drops out; divided by the other sum, it would be an error of the whole
 // result, much larger than the gradients of such a row's scores,
-// P·(dA − δ), that the backward pass takes from it.
+// P·(dA − δ), that the backward pass takes from it.  (With few rows they are not
+// rounded but split in two, and the first sum serves for both.)
 //
 // Bound by the matrix unit and the exponentials beside it: a wave issues 24
 // products of 32×32×16 for 2048 probabilities, two waves per SIMD.  4 × 4096
 // tokens, 28 heads of 64 on 4, bf16, causal: 700 to 720 µs (1000 TFLOP/s of the
 // four products) without the second sum and with the second map's result kept
-// alone, 790 with both; comparing every maximum: 800 and more.  One token of
-// 16384 keys, split over 512 workgroups: 11 µs, 3 TB/s, and 6 for the join (three of
-// a workgroup's four tiles on their way at once instead of one: 11.8).
+// alone, 770 to 790 with both; comparing every maximum: 800 and more.  One token of
+// 16384 keys, split over 512 workgroups: 12.3 µs (2.7 TB/s; 11.2 with rounded
+// probabilities, an error of 2.2·10^-3 to 2.9·10^-3 instead of the output's own
+// 1.7·10^-3; three tiles on their way at once instead of one: no faster), and 6 for the join.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -60,6 +62,9 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
   constexpr int NC = DP / AT<T>::kStep;   // steps over a head's values
   constexpr int NV = 2 * DP / 32;         // 32-column groups of V
   constexpr int SP = AT<T>::kSteps32;     // steps over 32 keys
+  // With few rows the matrix unit waits for the loads anyway: a bf16 probability
+  // is two operands, its rounding and what that leaves (16 bits of it).
+  constexpr bool TWO = FEW && E == 2;
   __shared__ __attribute__((aligned(1024))) char lds[2 * F::kStage];
 
   const AttnShape& S = L.s;
@@ -165,7 +170,7 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
 #pragma unroll
       for (int r = 0; r < RS; ++r) s[r] = a_mma<T>(a, q[r][c], s[r]);
     }
-    lu32x4 p[RS][SP];
+    lu32x4 p[RS][SP], rest[TWO ? RS : 1][SP];
 #pragma unroll
     for (int r = 0; r < RS; ++r) {
       if (masked) {
@@ -207,7 +212,17 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
 #pragma unroll
       for (int t = 0; t < SP; ++t) {
         p[r][t] = a_operand<T>(e, t);
-        if constexpr (E == 2) lr[r] = a_operand_sum(p[r][t], lr[r]);
+        if constexpr (TWO) {
+          float d[16] = {};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t two = p[r][t][i / 2];
+            d[8 * t + i] = e[8 * t + i] - __uint_as_float(i % 2 ? two & 0xffff0000u : two << 16);
+          }
+          rest[r][t] = a_operand<T>(d, t);
+        } else if constexpr (E == 2) {
+          lr[r] = a_operand_sum(p[r][t], lr[r]);
+        }
       }
     }
 #pragma unroll
@@ -216,7 +231,10 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
       for (int n = 0; n < NV; ++n) {
         const lu32x4 a = cd.get(vt, t, n);
 #pragma unroll
-        for (int r = 0; r < RS; ++r) o[r][n] = a_mma<T>(a, p[r][t], o[r][n]);
+        for (int r = 0; r < RS; ++r) {
+          o[r][n] = a_mma<T>(a, p[r][t], o[r][n]);
+          if constexpr (TWO) o[r][n] = a_mma<T>(a, rest[r][t], o[r][n]);
+        }
       }
   };
 
@@ -242,7 +260,7 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
 #pragma unroll
   for (int r = 0; r < RS; ++r) {
     l[r] = a_half_sum(l[r]);
-    const float sum = E == 2 ? a_half_sum(lr[r]) : l[r];
+    const float sum = E == 2 && !TWO ? a_half_sum(lr[r]) : l[r];
     const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees no key: zeros
 #pragma unroll
     for (int n = 0; n < NV; ++n)
