@@ -123,6 +123,11 @@ def _strides(t):
     return _i64x3(b, n, h)
 
 
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape (the quickest way there)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _output(out, shape, dtype, dev, name):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev)
@@ -223,7 +228,7 @@ def _positions(r, positions, dev):
 
 def _turn(arr, i, t, t4, out, name):
     """Sets tensor i of a call: (its output, what arr points into)."""
-    o = _output(out, t.shape, t.dtype, t.device, name + "_out")
+    o = _like(t) if out is None else _output(out, t.shape, t.dtype, t.device, name + "_out")
     o4 = o if o.dim() == 4 else o.unsqueeze(0)
     arr[i] = MuonRotaryHeads(_ptr(t4), _ptr(o4), t4.shape[2], _strides(t4), _strides(o4))
     return o, t4
@@ -280,7 +285,7 @@ def muon_dropout(x, p: float, seed: int, offset=0, residual=None, out=None, stre
     with _on(dev, stream):
         x2, ldx = _input(x, "x")
         r2, ldr = _input(residual, "residual") if residual is not None else (None, 0)
-        y = _out(out, x.shape, x.dtype, dev, "out")
+        y = _like(x) if out is None else _out(out, x.shape, x.dtype, dev, "out")
         y2, ldy = _rows(y, "out")
         if y.numel():
             _check(L.muon_dropout(_ptr(x2), ldx, _ptr(r2), ldr, p, int(seed) & _U64, host, _ptr(tensor), _ptr(y2), ldy,
@@ -297,7 +302,7 @@ def muon_dropout_grad(dy, p: float, seed: int, offset=0, out=None, stream=None):
     host, tensor = _offset(offset, dev)
     with _on(dev, stream):
         d2, ldd = _input(dy, "dy")
-        y = _out(out, dy.shape, dy.dtype, dev, "out")
+        y = _like(dy) if out is None else _out(out, dy.shape, dy.dtype, dev, "out")
         y2, ldy = _rows(y, "out")
         if y.numel():
             _check(L.muon_dropout_grad(_ptr(d2), ldd, p, int(seed) & _U64, host, _ptr(tensor), _ptr(y2), ldy,
@@ -414,7 +419,7 @@ def muon_diff_attention_grad(dout, q, k, v, lam, out, saved, causal: bool = True
             if tuple(t.shape) != shape:
                 raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
         d4, o4 = _input_heads(dout, "dout"), _input_heads(out, "out")
-        grads = [torch.empty(t.shape, dtype=t.dtype, device=dev) if want else None
+        grads = [_like(t) if want else None
                  for t, want in ((q, want_dq), (k, want_dkv), (v, want_dkv))]
         dlam = torch.empty(f.heads, dtype=torch.float32, device=dev) if want_dlam else None
         none = _i64x3(0, 0, 0)
