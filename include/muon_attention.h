@@ -114,7 +114,8 @@ muon_status_t muon_dropout_grad(const void* dy, int64_t ld_dy, double p, uint64_
  *     the device) and sees itself alone.  Tokens before the first and from the
  *     last offset on give zeros.  Offsets outside [0, tokens] are cut to it, one
  *     below its predecessor is raised to it.
- *   1 ≤ dim ≤ 128; kv_heads divides heads; 0 < scale ≤ 1e30;
+ *   1 ≤ dim ≤ 128; kv_heads divides heads; 2^-60 ≤ scale ≤ 2^60 (and
+ *   |q·k| ≤ 1e30 for the gradients);
  *   batch · queries, batch · keys ≤ 2^24; queries · group < 2^30;
  *   batch · queries · heads ≤ 2^28; at most 2^23 workgroups (per batch entry and
  *   key/value head one for 32 to 128 rows of queries · group, or 128 keys).

@@ -514,7 +514,8 @@ AttnShape shape_of(const muon_diff_attention_t& f, const AttnLayout& l) {
 
 void attn_inputs(HeadArgs& a, const muon_diff_attention_t& f, const AttnTensors& t) {
   const size_t e = esize(f.dtype);
-  if (!(f.scale > 0 && f.scale <= 1e30f)) a.fail(MUON_ERR_INVALID_ARG, "scale must be > 0 and at most 1e30");
+  // the backward pass holds log-sums divided by scale·log2 e
+  if (!(f.scale >= 0x1p-60f && f.scale <= 0x1p60f)) a.fail(MUON_ERR_INVALID_ARG, "scale must be 2^-60 to 2^60");
   a.heads("q", f.q, t.q, e, false);
   a.heads("k", f.k, t.k, e, false);
   a.heads("v", f.v, t.v, e, false);

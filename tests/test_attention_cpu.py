@@ -111,7 +111,7 @@ CALLS = {
         (dict(dt=3), INVALID), (dict(batch=BIG, queries=2), UNSUPPORTED), (dict(batch=BIG, keys=2), UNSUPPORTED),
         (dict(heads=1 << 7, kv=1, queries=BIG), UNSUPPORTED), (dict(batch=1, heads=32, kv=32, queries=BIG), UNSUPPORTED),
         (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=math.inf), INVALID),
-        (dict(scale=math.nan), INVALID), (dict(scale=3e38), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID),
+        (dict(scale=math.nan), INVALID), (dict(scale=3e38), INVALID), (dict(scale=1e-20), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID),
         (dict(v=None), INVALID), (dict(lam=None), INVALID), (dict(out=None), INVALID), (dict(q=A + 1), INVALID),
         (dict(lam=D + 2), INVALID), (dict(seqs=-1), INVALID), (dict(seqs=2, offsets=Z), INVALID),
         (dict(seqs=2, offsets=Z, batch=1), INVALID), (dict(seqs=2, offsets=None, batch=1, keys=5), INVALID),

@@ -341,6 +341,16 @@ def test_attention_magnitudes(lib, power, dtype):
     run_case(lib, (q, k, v * 2.0 ** power, lam, do * 2.0 ** (20 if power < 0 else 0)))
 
 
+@pytest.mark.parametrize("power", [-60, 60])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_scales(lib, power, dtype):
+    """The smallest and largest scale, with scores of ordinary size from them."""
+    q, k, v, lam, do = attention_inputs(1, 75, 75, 2, 1, 64, dtype)
+    run_case(lib, (q * 2.0 ** -(power // 2), k * 2.0 ** -(power // 2), v, lam, do), scale=2.0 ** power)
+    if power < 0:  # flat maps: scores that all but vanish
+        run_case(lib, (q, k, v, lam, do), scale=2.0 ** power)
+
+
 @pytest.mark.parametrize("lam", [0.0, 1.0, -3.0, 100.0])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_attention_lambda(lib, lam, dtype):
