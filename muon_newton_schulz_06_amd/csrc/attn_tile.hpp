@@ -25,7 +25,6 @@ typedef short as16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) as16x4* a_lds_s4;
 typedef __attribute__((address_space(3))) const lu32x4* a_lds_u4;
 typedef __attribute__((address_space(3))) const uint32_t* a_lds_u1;
-typedef __attribute__((address_space(3))) lf32x4* a_lds_f4;
 
 template <typename T> struct AT {
   static constexpr int kBytes = 16 / LType<T>::kVec;
