@@ -300,7 +300,7 @@ void plan_splits(AttnLayout& l, bool bf16, int64_t nk) {
   const int64_t base = l.combos * l.rowBlocks, bn = attn_fwd_keys(bf16, l.dp);
   l.splits = 1;
   l.splitKeys = (int)((nk + bn - 1) / bn * bn);
-  if (base >= 256 || nk < 4 * bn) return;
+  if (base == 0 || base >= 256 || nk < 4 * bn) return;  // (0: no queries or no batch)
   const int64_t want = std::min<int64_t>(std::max<int64_t>(1, kMaxSplits / base), blocks_of(nk, 2 * bn));
   const int64_t keys = blocks_of(blocks_of(nk, want), bn) * bn;
   l.splits = (int)blocks_of(nk, keys);

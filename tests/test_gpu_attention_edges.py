@@ -1,0 +1,24 @@
+"""Attention calls at the edges of what the header allows."""
+import pytest
+import torch
+
+from test_gpu_attention import DTYPES, attention_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 72, 128])
+@pytest.mark.parametrize("batch,queries,keys", [(1, 0, 300), (2, 0, 4096), (0, 5, 300), (0, 5, 4096), (0, 0, 1000)])
+def test_no_queries_or_no_batch(lib, batch, queries, keys, dim, dtype):
+    """Against many keys too: no results, and gradients of zero for all of them."""
+    q, k, v, lam, do = (t.cuda() for t in attention_inputs(batch, queries, keys, 4, 2, dim, dtype))
+    sizes = (batch, queries, keys, 4, 2, dim, dtype)
+    assert lib.diff_attention_saved_size(*sizes) == 0
+    ws = torch.full((max(lib.diff_attention_workspace_size(*sizes, grad=True), 256),), 255, dtype=torch.uint8, device="cuda")
+    for causal in (True, False):
+        out, saved = lib.muon_diff_attention(q, k, v, lam, causal=causal, save=True)
+        assert out.shape == do.shape and saved.numel() == 0
+        for kw in (dict(), dict(workspace=ws)):
+            grads = lib.muon_diff_attention_grad(do, q, k, v, lam, out, saved, causal=causal, **kw)
+            assert [g.shape for g in grads] == [q.shape, k.shape, v.shape, lam.shape] and not any(g.any() for g in grads)
