@@ -113,7 +113,9 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   const int64_t rec0 = ((int64_t)batch * L.heads + hk * G) * S.nq + tok0;
   const uint32_t base = a_lds(lds);
   // The next tile to load: head g, tokens from t.  Past the last tile the loads
-  // deliver zeros.
+  // deliver zeros, and so they do for rows that see no key at all: their
+  // probabilities are 0, but 0 times an infinity or NaN of theirs is not.
+  const int seeing = S.causal ? max(1 - shift, 0) : 0;  // the first row that sees a key
   struct Place {
     int g, t;
   };
@@ -139,14 +141,15 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   locate();
   auto issue = [&](uint32_t buf) __attribute__((always_inline)) {
     const int left = filled < end ? nq - load.t : 0;
-    if (left >= 32) {
+    const int from = seeing - load.t;
+    if (left >= 32 && from <= 0) {
       ldq.issue(q, buf);
       ldq.issue(q + S.qs[2] * E, buf + RQ);
       ldd.issue(d, buf + 2 * RQ);
     } else {
-      ldq.issue(q, left, buf);
-      ldq.issue(q + S.qs[2] * E, left, buf + RQ);
-      ldd.issue(d, left, buf + 2 * RQ);
+      ldq.issue(q, from, left, buf);
+      ldq.issue(q + S.qs[2] * E, from, left, buf + RQ);
+      ldd.issue(d, from, left, buf + 2 * RQ);
     }
     // the records: bf16 recL by wave 0, recD by wave 1; fp32 rec by wave 0
     // (lanes past 31 deliver zeros behind the 32 records)

@@ -171,6 +171,16 @@ template <int RB, int ROWS, int NW> struct TileLoader {
       f_dma16(__builtin_amdgcn_readfirstlane(dst + (wave * N + p) * 1024),
               row0 + p * kRowsPer < left ? off[p] : kFfnNowhere, buf);
   }
+  // rows before `from` arrive as zeros too
+  __device__ __forceinline__ void issue(const char* base, int from, int left, uint32_t dst) const {
+    const fi32x4 buf = f_buffer((uint64_t)base);
+#pragma unroll
+    for (int p = 0; p < N; ++p) {
+      const int r = row0 + p * kRowsPer;
+      f_dma16(__builtin_amdgcn_readfirstlane(dst + (wave * N + p) * 1024), (r >= from) & (r < left) ? off[p] : kFfnNowhere,
+              buf);
+    }
+  }
 };
 
 // The tiles of one block that a workgroup runs: begin … end − 1.

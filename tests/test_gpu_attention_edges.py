@@ -22,3 +22,25 @@ def test_no_queries_or_no_batch(lib, batch, queries, keys, dim, dtype):
         for kw in (dict(), dict(workspace=ws)):
             grads = lib.muon_diff_attention_grad(do, q, k, v, lam, out, saved, causal=causal, **kw)
             assert [g.shape for g in grads] == [q.shape, k.shape, v.shape, lam.shape] and not any(g.any() for g in grads)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("queries,keys,heads,kv", [(40, 33, 4, 2), (300, 200, 3, 1), (100, 60, 7, 1), (5, 2, 4, 4), (70, 3, 6, 2),
+                                                   (333, 1, 2, 1), (520, 300, 2, 2)])
+def test_rows_that_see_no_key(lib, queries, keys, heads, kv, dim, dtype):
+    """More queries than keys, causal: the first rows see nothing.  Whatever is in
+    their q and dout reaches no gradient."""
+    blind = queries - keys
+    q, k, v, lam, do = (t.cuda() for t in attention_inputs(2, queries, keys, heads, kv, dim, dtype))
+    q[:, :blind], do[:, :blind] = 0, 0
+    ref, saved = lib.muon_diff_attention(q, k, v, lam, save=True)
+    refs = lib.muon_diff_attention_grad(do, q, k, v, lam, ref, saved)
+    assert not ref[:, :blind].any() and not refs[0][:, :blind].any() and all(torch.isfinite(g).all() for g in refs)
+    for bad_q, bad_do in ((float("nan"), float("nan")), (float("inf"), 1.0), (1.0, float("-inf")), (float("-inf"), float("nan"))):
+        q[:, :blind], do[:, :blind] = bad_q, bad_do
+        out, saved = lib.muon_diff_attention(q, k, v, lam, save=True)
+        grads = lib.muon_diff_attention_grad(do, q, k, v, lam, out, saved)
+        assert torch.equal(out, ref)
+        for name, a, b in zip(("dq", "dk", "dv", "dlam"), grads, refs):
+            assert torch.equal(a, b), (name, bad_q, bad_do)
