@@ -261,11 +261,13 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
   for (int r = 0; r < RS; ++r) {
     l[r] = a_half_sum(l[r]);
     const float sum = E == 2 && !TWO ? a_half_sum(lr[r]) : l[r];
-    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees no key: zeros
+    const bool some = !(sum == 0.f);
+    const float inv = 1.f / sum;
+    // a row that sees no key: zeros (its sums are 0 · v, which an infinity of v makes NaN)
 #pragma unroll
     for (int n = 0; n < NV; ++n)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[r][n][i] *= inv;
+      for (int i = 0; i < 16; ++i) o[r][n][i] = some ? o[r][n][i] * inv : 0.f;
   }
   if (L.splits > 1) {
 #pragma unroll

@@ -44,3 +44,19 @@ def test_rows_that_see_no_key(lib, queries, keys, heads, kv, dim, dtype):
         assert torch.equal(out, ref)
         for name, a, b in zip(("dq", "dk", "dv", "dlam"), grads, refs):
             assert torch.equal(a, b), (name, bad_q, bad_do)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("queries,keys,heads,kv", [(40, 33, 4, 2), (300, 200, 3, 1), (5, 2, 4, 4), (333, 1, 2, 1), (3000, 2990, 1, 1)])
+def test_results_of_rows_that_see_no_key(lib, queries, keys, heads, kv, dim, dtype):
+    """They are zeros whatever the values hold, by one pass and by splits of the keys."""
+    blind = queries - keys
+    q, k, v, lam, do = (t.cuda() for t in attention_inputs(2, queries, keys, heads, kv, dim, dtype))
+    ref = lib.muon_diff_attention(q, k, v, lam)
+    for bad in (float("nan"), float("inf")):
+        v[:, 0, :, 3] = bad
+        out, saved = lib.muon_diff_attention(q, k, v, lam, save=True)
+        assert not out[:, :blind].any() and torch.equal(lib.muon_diff_attention(q, k, v, lam)[:, :blind], out[:, :blind])
+        assert not torch.isfinite(out[:, blind:, :, 3]).any() and torch.equal(out[:, blind:, :, 4:], ref[:, blind:, :, 4:])
+        assert not lib.muon_diff_attention_grad(do, q, k, v, lam, out, saved)[0][:, :blind].any()
