@@ -170,8 +170,9 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
         return freqs / factor, 1.0
     if scaling != "yarn":
         raise ValueError(f'unknown scaling {scaling!r}; use None, "linear", "base" or "yarn"')
-    if original_length <= 0:
-        raise ValueError('scaling "yarn" needs original_length')
+    if not original_length > 0 or not base > 1 or not 0 < slow <= fast:
+        raise ValueError(f'scaling "yarn" needs original_length > 0, base > 1 and 0 < slow <= fast, got {original_length}, '
+                         f"{base}, {slow} and {fast}")
     # the (fractional) index whose frequency makes n turns over the original length
     def index(n):
         return dim * math.log(original_length / (n * 2 * math.pi)) / (2 * math.log(base))
