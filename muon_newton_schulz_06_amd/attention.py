@@ -337,7 +337,7 @@ def _attention(q, k, v, lam, causal, scale, offsets):
     lam = lam.contiguous()
     f = MuonDiffAttention(batch, queries, keys, qh // 2, kh // 2, dim, _ptr(q4), _ptr(k4), _ptr(v4), _ptr(lam),
                           _strides(q4), _strides(k4), _strides(v4), None, 0,
-                          dim ** -0.5 if scale is None else scale, int(bool(causal)), code)
+                          max(dim, 1) ** -0.5 if scale is None else scale, int(bool(causal)), code)
     if offsets is not None:
         _same(dev, torch.int32, offsets=offsets)
         if offsets.dim() != 1 or offsets.numel() < 2:
