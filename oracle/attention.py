@@ -177,3 +177,59 @@ def diff_attention_grad(dout, q, k, v, lam, causal=True, scale=None, offsets=Non
     for name in ("dq", "dk", "dv"):
         err[name] += (unit + 2 * e) * np.abs(got[name])
     return got, err
+
+
+# What the roundings of bf16 tensors leave in the mean: a rounding is off by a
+# uniform part of half a step, in the mean square by at most u²/3 of the value
+# (where it is a power of two, less elsewhere), and independent of the others, so
+# mean squares add.  The results' own rounding is not estimated: it is known.
+
+
+def bf16(x):
+    """Rounded to nearest, ties to even, by the upper 16 bits of fp32."""
+    b = np.ascontiguousarray(x, np.float32).view(np.uint32).astype(np.uint64)
+    b = (b + 0x7FFF + ((b >> 16) & 1)) >> 16 << 16
+    return b.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+def diff_attention_spread(dout, q, k, v, lam, causal=True, scale=None, offsets=None, few=False, u=2.0 ** -8):
+    """Mean squares of the errors of "out", "dq", "dk", "dv" before their own
+    rounding, element by element, where
+      – the forward pass takes its probabilities as operands of u, or u² with
+        `few`, and divides by the sum of what it takes: O = Σ P(1 + ε)v / Σ P(1 + ε)
+        is off by Σ P·ε·(v − O);
+      – δ = dout·O is formed from that O, kept in whole multiples of 2^-15 of its
+        row's largest value (off by less than one of them): by Σ P·ε·(dA − δ) and
+        Σ_d dout·(2^-15 max|O|);
+      – the backward pass rounds A = P_1 − λ·P_2 and dS = P·(dA − δ) to u."""
+    batch, queries, qh, dim = q.shape
+    heads, group = qh // 2, qh // k.shape[2]
+    scale = dim ** -0.5 if scale is None else scale
+    got = {"out": np.zeros((batch, queries, heads, 2 * dim)), "dq": np.zeros(q.shape), "dk": np.zeros(k.shape),
+           "dv": np.zeros(v.shape)}
+    w, wp = u * u / 3, (u * u if few else u) ** 2 / 3
+    for b, rows, cols in _problems(q, k, offsets):
+        for h in range(heads):
+            g, la, do, vv = h // group, lam[h], dout[b, rows, h], v[b, cols, h // group]
+            qs, ks = [q[b, rows, 2 * h + m] for m in (0, 1)], [k[b, cols, 2 * g + m] for m in (0, 1)]
+            maps, hidden = _head(*qs, *ks, vv, la, scale, causal)
+            dA, lone = do @ vv.T, (~hidden).sum(axis=-1, keepdims=True) <= 1
+            got["dv"][b, cols, g] += w * ((maps[0] - la * maps[1]) ** 2).T @ do ** 2
+            for m, (p, c) in enumerate(zip(maps, (1.0, la * la))):
+                o, delta, p2 = p @ vv, (p * dA).sum(axis=-1, keepdims=True), p * p
+                got["out"][b, rows, h] += c * wp * (p2 @ vv ** 2 - 2 * o * (p2 @ vv) + o ** 2 * p2.sum(axis=-1, keepdims=True))
+                step = 2.0 ** -15 * np.abs(o).max(axis=-1, keepdims=True, initial=0.0)
+                row = wp * (p2 * (dA - delta) ** 2).sum(axis=-1, keepdims=True) + step ** 2 * (do ** 2).sum(axis=-1, keepdims=True)
+                own = np.where(lone, 0.0, c * scale * scale * w * p2 * (dA - delta) ** 2)
+                row = np.where(lone, 0.0, c * scale * scale * row)
+                got["dq"][b, rows, 2 * h + m] = own @ ks[m] ** 2 + row * (p @ ks[m]) ** 2
+                got["dk"][b, cols, 2 * g + m] += (own + row * p2).T @ qs[m] ** 2
+    return got
+
+
+def spread_tolerance(ref, square):
+    """2-norm of the error of a bf16 result: its own rounding and the mean squares
+    of what came before.  A tenth more for the sample (thousands of errors of either
+    size), 2^-17 for the fp32 arithmetic."""
+    own = ((bf16(ref) - ref) ** 2).sum()
+    return 1.1 * np.sqrt(own + square.sum()) + 2.0 ** -17 * np.sqrt((ref ** 2).sum())
