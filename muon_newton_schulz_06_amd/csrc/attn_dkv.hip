@@ -216,6 +216,8 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
     }
   };
   lu32x4 ring[AHEAD];
+  // −L/c is finite, since an infinity would meet zeros in the product; a NaN stays
+  auto bounded = [](float x) __attribute__((always_inline)) { return x < -1e30f ? -1e30f : x; };
   const float unit = half ? 0.f : 1.f;
   // one statistics step: record values 0, 1, 2 (first) or 3, 4, 5 as three bf16, or fp32 value `at` times f
   auto stat = [&](lu32x4 r, auto first, float value, af32x16 c) __attribute__((always_inline)) {
@@ -256,10 +258,10 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
       if constexpr (j >= ALL) return;
       if constexpr (j < bS2) {
         if constexpr (j < NC) s1 = a_mma<T>(r, k[0][j], s1);
-        else s1 = stat(r, std::true_type{}, fmaxf(__uint_as_float(r[0]) * invc, -1e30f), s1);
+        else s1 = stat(r, std::true_type{}, bounded(__uint_as_float(r[0]) * invc), s1);
       } else if constexpr (j < bA) {
         if constexpr (j - bS2 < NC) s2 = a_mma<T>(r, k[1][j - bS2], s2);
-        else s2 = stat(r, std::false_type{}, fmaxf(__uint_as_float(r[1]) * invc, -1e30f), s2);
+        else s2 = stat(r, std::false_type{}, bounded(__uint_as_float(r[1]) * invc), s2);
       } else if constexpr (j < bV) {
         if constexpr (j - bA < 2 * NC) {
           a1 = a_mma<T>(r, v[j - bA], a1);

@@ -60,3 +60,25 @@ def test_results_of_rows_that_see_no_key(lib, queries, keys, heads, kv, dim, dty
         assert not out[:, :blind].any() and torch.equal(lib.muon_diff_attention(q, k, v, lam)[:, :blind], out[:, :blind])
         assert not torch.isfinite(out[:, blind:, :, 3]).any() and torch.equal(out[:, blind:, :, 4:], ref[:, blind:, :, 4:])
         assert not lib.muon_diff_attention_grad(do, q, k, v, lam, out, saved)[0][:, :blind].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("tokens", [20, 150])
+def test_bad_keys_show_in_the_gradients(lib, tokens, bad, dim, dtype):
+    """A key that makes a row's sum NaN leaves no finite gradient where that row
+    has a part, and changes nothing elsewhere."""
+    q, k, v, lam, do = (t.cuda() for t in attention_inputs(2, tokens, tokens, 4, 2, dim, dtype))
+    out, saved = lib.muon_diff_attention(q, k, v, lam, causal=False, save=True)
+    refs = lib.muon_diff_attention_grad(do, q, k, v, lam, out, saved, causal=False)
+    k[1, 7, 2] = bad  # first map of the second key head
+    out, saved = lib.muon_diff_attention(q, k, v, lam, causal=False, save=True)
+    dq, dk, dv, dlam = lib.muon_diff_attention_grad(do, q, k, v, lam, out, saved, causal=False)
+    assert not torch.isfinite(out[1, :, 2:]).any()
+    # (the second map's row sums stand apart from the first's: its gradients stay)
+    assert not torch.isfinite(dv[1, :, 1]).any()
+    assert not torch.isfinite(dk[1, :, 2]).any() and not torch.isfinite(dq[1, :, 4::2]).any()
+    for got, ref, heads in ((dq, refs[0], 4), (dk, refs[1], 2), (dv, refs[2], 1)):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1, :, :heads], ref[1, :, :heads])
+    assert torch.equal(dlam[:2], refs[3][:2])
