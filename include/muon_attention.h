@@ -108,7 +108,8 @@ muon_status_t muon_dropout_grad(const void* dy, int64_t ld_dy, double p, uint64_
  *   v: batch × keys × kv_heads × 2·dim;  out: batch × queries × heads × 2·dim;
  *   lambda: heads float32 values; strides {batch, token, head}.
  *   causal ≠ 0: query i sees the keys j ≤ i + keys − queries (the last query
- *     the last key).  A query that sees no key gives zeros, and gradients 0.
+ *     the last key).  A query that sees no key gives zeros, and gradients 0,
+ *     whatever it and its dout hold.
  *   sequences > 0: a packed batch (batch = 1, queries = keys = tokens): sequence
  *     i holds the tokens offsets[i] … offsets[i + 1] − 1 (sequences + 1 int32 on
  *     the device) and sees itself alone.  Tokens before the first and from the
@@ -118,10 +119,13 @@ muon_status_t muon_dropout_grad(const void* dy, int64_t ld_dy, double p, uint64_
  *   |q·k| ≤ 1e30 for the gradients);
  *   batch · queries, batch · keys ≤ 2^24; queries · group < 2^30;
  *   batch · queries · heads ≤ 2^28; at most 2^23 workgroups (per batch entry and
- *   key/value head one for 32 to 128 rows of queries · group, or 128 keys).
+ *   key/value head one for 32 to 128 rows of queries · group, or 128 keys, and two
+ *   and one per sequence more of a packed batch).
  * Keys behind the end of a sequence are never read.  Keys of the same sequence
  * that only the causal rule hides enter with probability 0: an infinite or NaN
- * value of v there reaches the row as 0 · v does.
+ * value of v there may reach the row as 0 · v does.  So it is with the gradients:
+ * of hidden keys 0 · k may reach dq, and of rows that see other keys, but not this
+ * one, 0 · q may reach dk and 0 · dout dv.
  * Tensors whose heads are not whole 16-byte chunks at 16-byte aligned addresses
  * (or with tokens 2^24 or more elements apart) are copied to the workspace. */
 typedef struct muon_diff_attention {

@@ -565,7 +565,8 @@ class DiffAttention(torch.nn.Module):
 
     forward(q, k, v, offsets=None): (batch, tokens, 2·heads, dim), (batch, tokens,
     2·kv_heads, dim), (batch, tokens, kv_heads, 2·dim) to (batch, tokens, heads,
-    2·dim); a packed batch without the batch dimension and with offsets."""
+    2·dim); a packed batch without the batch dimension and with offsets.  The norm
+    takes up to 2^24 rows: batch · tokens · heads."""
 
     def __init__(self, heads: int, dim: int, kv_heads: int | None = None, lambda_init: float = 0.8,
                  causal: bool = True, eps: float = 1e-5, device=None, dtype=None):

@@ -109,9 +109,6 @@ int attn_fwd_keys(bool bf16, int dp);
 hipError_t launch_attn_fwd(bool bf16, int dp, bool few, const AttnFwdLaunch& L, hipStream_t st);
 hipError_t launch_attn_join(bool bf16, int dp, const AttnFwdLaunch& L, hipStream_t st);
 
-// What the backward products need of a row: {L1, L2, δ1, δ2}, and for bf16 the
-// same as operands of a product (see attn_dkv), two 16-byte records per row.
-// All are [batch][head][token].
 // How the blocks (of rows or keys) of all combos are dealt out: a workgroup per
 // block (streams = 0), or equal stretches of the tiles of all blocks, at least
 // `least` tiles each.
@@ -129,8 +126,10 @@ struct AttnGradLaunch {
   const void* out;  // any alignment; read for fp32 only
   int64_t os[3];
   int32_t outVec;  // out is whole aligned chunks too
+  // What the products need of a row, [batch][head][token]: {L1, L2, δ1, δ2}, and
+  // for bf16 the same as operands of a product (see attn_dkv), two 16-byte records.
   lf4* rec;
-  lu4 *recL, *recD;  // bf16 only
+  lu4 *recL, *recD;
   float* rowLam;     // per row δ2 as the products give it, [batch][head][token]
   void *dq, *dk, *dv;
   int64_t dqs[3], dks[3], dvs[3];

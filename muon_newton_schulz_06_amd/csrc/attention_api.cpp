@@ -284,7 +284,7 @@ void dense(int64_t s[3], const Heads& h, int64_t pitch) {
 
 struct AttnLayout {
   size_t stat, unit, kept, saved;  // in `saved`
-  size_t list[2], q, k, v, part, partStat, total;
+  size_t list, q, k, v, part, partStat, total;
   int64_t rows;            // of a combo
   int64_t combos, pitch;
   int dp;
@@ -332,7 +332,7 @@ AttnLayout attn_layout(const muon_diff_attention_t& f) {
   l.rowBlocks = blocks_of(l.rows, per);
   if (f.sequences > 0) {
     l.rowBlocks = l.rows / per + f.sequences + 2;
-    l.list[0] = take(256 + (size_t)l.rowBlocks * sizeof(AttnBlock));
+    l.list = take(256 + (size_t)l.rowBlocks * sizeof(AttnBlock));
   }
   l.q = take(direct(f.q, t.q, e) ? 0 : copy_bytes(t.q, e));
   l.k = take(direct(f.k, t.k, e) ? 0 : copy_bytes(t.k, e));
@@ -614,7 +614,7 @@ muon_status_t muon_diff_attention(const muon_diff_attention_t* f, void* out, con
     const bool bf16 = call.bf16();
     if (f->sequences > 0) {
       AttnPrepLaunch P = prep_of(*f);
-      L.list = call.list(P, l.list[0], (int32_t)f->queries, L.s.group, attn_fwd_rows(bf16, l.dp, l.few));
+      L.list = call.list(P, l.list, (int32_t)f->queries, L.s.group, attn_fwd_rows(bf16, l.dp, l.few));
       s = launched("blocks of the batch", launch_attn_prep(P, st), st);
       if (s != MUON_OK) return s;
     }

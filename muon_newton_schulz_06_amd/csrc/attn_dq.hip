@@ -17,9 +17,10 @@
 // some 130 operations and 32 exponentials, two waves per SIMD (64-wide bf16).
 // 4 × 4096 tokens, 28 heads of 64 on 4: 800 µs, 900 TFLOP/s.  Where there are
 // fewer blocks than twice the CUs' places, equal stretches of tiles as in
-// attn_dkv (333 tokens, fp32: 78 µs by blocks, 28 + 10 in stretches); the blocks
-// of a packed batch stay whole (232 µs, in stretches 349).  dS between the
-// products instead of all at once: 793 µs, the same.
+// attn_dkv (333 tokens, fp32: 78 µs by blocks, 28 + 10 in stretches).  A packed
+// batch of more blocks keeps them whole, unlike there (8192 tokens in 11
+// documents: 232 µs, in stretches 349).  dS between the products instead of all
+// at once: 793 µs, the same.
 #include <hip/hip_runtime.h>
 
 #include "attention.hpp"
