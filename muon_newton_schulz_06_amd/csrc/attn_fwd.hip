@@ -66,6 +66,7 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
   // is two operands, its rounding and what that leaves (16 bits of it).
   constexpr bool TWO = FEW && E == 2;
   __shared__ __attribute__((aligned(1024))) char lds[2 * F::kStage];
+  __shared__ int odd[F::kWaves];
 
   const AttnShape& S = L.s;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -139,9 +140,9 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
   const uint32_t base = a_lds(lds);
   auto issue = [&](int key, uint32_t buf) __attribute__((always_inline)) {
     const char* k = k1 + (int64_t)key * S.ks[1] * E;
-    ldk.issue(k, nk - key, buf);
-    ldk.issue(k + S.ks[2] * E, nk - key, buf + BN * F::kK);
-    ldv.issue(v0 + (int64_t)key * S.vs[1] * E, nk - key, buf + 2 * BN * F::kK);
+    ldk.issue(k, most - key, buf);
+    ldk.issue(k + S.ks[2] * E, most - key, buf + BN * F::kK);
+    ldv.issue(v0 + (int64_t)key * S.vs[1] * E, most - key, buf + 2 * BN * F::kK);
   };
   const RowReader<F::kK> rd(lane, map * (BN * F::kK));  // in the map's own keys
   const ColReader<T, F::kV> cd(lane);
@@ -173,6 +174,7 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
     lu32x4 p[RS][SP], rest[TWO ? RS : 1][SP];
 #pragma unroll
     for (int r = 0; r < RS; ++r) {
+      __builtin_amdgcn_sched_barrier(0);  // (the rows' exponentials in turn: 2% of a packed batch's time)
       if (masked) {
         const int n = lim[r] - key - 4 * half;
 #pragma unroll
@@ -238,19 +240,77 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
       }
   };
 
+  // A tile of values of which some rows see only a part: an infinity or NaN is
+  // added to the sums of the rows that see its key, and leaves the tile, where a
+  // probability of 0 times it would reach the others.  Without one the look at the
+  // tile is all (a block has one or two such tiles: 4 × 4096 tokens 755 µs without
+  // the look, 751 to 773 with it; packed 218 and 221).
+  auto part = [&](uint32_t vt, int key) __attribute__((always_inline)) {
+    typedef __attribute__((address_space(3))) lu32x4* Chunk;
+    constexpr int kPer = BN * F::kV / 16 / F::kThreads;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) top = a_top<T>(*(Chunk)(uintptr_t)(vt + (tid + i * F::kThreads) * 16), top);
+    const bool any = __any(a_odd<T>(top));
+    if (lane == 0) odd[wave] = any;
+    a_meet();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < F::kWaves; ++w) all |= odd[w];
+    if (__builtin_expect(!__builtin_amdgcn_readfirstlane(all), 1)) return;
+    // as products that overflow, so that they take the sums' own place: of +-2^100
+    // where an infinity of that sign (or a NaN: both) stands, and of 2^100 where seen
+#pragma clang loop unroll(disable)
+    for (int t = 0; t < BN / AT<T>::kStep; ++t) {
+      lu32x4 seen[RS];
+#pragma unroll
+      for (int r = 0; r < RS; ++r) seen[r] = a_below<T>(lim[r] - key - AT<T>::kStep * t - 4 * half);
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const lu32x4 v = cd.get(vt, t, n);
+#pragma unroll
+        for (int sign = 0; sign < 2; ++sign) {
+          const lu32x4 a = a_odd_of<T>(v, sign);
+#pragma unroll
+          for (int r = 0; r < RS; ++r) o[r][n] = a_mma<T>(a, seen[r], o[r][n]);
+        }
+      }
+    }
+    a_meet();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const Chunk c = (Chunk)(uintptr_t)(vt + (tid + i * F::kThreads) * 16);
+      *c = a_finite<T>(*c);
+    }
+    a_meet();
+  };
+
   if (kBegin < kEnd) issue(kBegin, base);
-  // the two buffers by turns, their addresses constants
-  for (int key = kBegin; key < kEnd; key += 2 * BN) {
+  // The two buffers by turns, their addresses constants: pairs of tiles that all rows
+  // see whole, then the others.
+  int key = kBegin;
+  for (const int whole = min(least, kEnd); key + 2 * BN <= whole; key += 2 * BN) {
     a_for<0, 2>([&](auto bc) __attribute__((always_inline)) {
       constexpr int b = decltype(bc)::value;
+      const uint32_t buf = base + b * F::kStage;
+      a_landed();  // this tile; the other buffer is free
+      if (b == 0 || key + 2 * BN < kEnd) issue(key + (b + 1) * BN, base + (1 - b) * F::kStage);
+#pragma unroll
+      for (int j = 0; j < BN; j += 32) step(buf + j * F::kK, buf + 2 * BN * F::kK + j * F::kV, key + b * BN + j, false);
+    });
+  }
+  for (; key < kEnd; key += 2 * BN) {
+    a_for<0, 2>([&](auto bc) __attribute__((always_inline)) {
+      constexpr int b = decltype(bc)::value;
+      const uint32_t buf = base + b * F::kStage;
       const int k0 = key + b * BN;
       if (k0 >= kEnd) return;
-      a_landed();  // this tile; the other buffer is free
+      a_landed();
       if (k0 + BN < kEnd) issue(k0 + BN, base + (1 - b) * F::kStage);
+      if (least < most && k0 + BN > least) part(buf + 2 * BN * F::kK, k0);
 #pragma unroll
       for (int j = 0; j < BN; j += 32) {
         if (k0 + j >= kEnd) break;
-        const uint32_t buf = base + b * F::kStage;
         step(buf + j * F::kK, buf + 2 * BN * F::kK + j * F::kV, k0 + j, k0 + j + 32 > least);
       }
     });
@@ -261,13 +321,11 @@ __global__ __launch_bounds__((Fwd<T, DP, FEW>::kThreads), 2) void attn_fwd(const
   for (int r = 0; r < RS; ++r) {
     l[r] = a_half_sum(l[r]);
     const float sum = E == 2 && !TWO ? a_half_sum(lr[r]) : l[r];
-    const bool some = !(sum == 0.f);
-    const float inv = 1.f / sum;
-    // a row that sees no key: zeros (its sums are 0 · v, which an infinity of v makes NaN)
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;  // a row that sees no key: zeros
 #pragma unroll
     for (int n = 0; n < NV; ++n)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[r][n][i] = some ? o[r][n][i] * inv : 0.f;
+      for (int i = 0; i < 16; ++i) o[r][n][i] *= inv;
   }
   if (L.splits > 1) {
 #pragma unroll

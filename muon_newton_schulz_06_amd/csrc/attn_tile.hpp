@@ -67,6 +67,70 @@ __device__ __forceinline__ float a_operand_sum(const lu32x4& op, float sum) {
   return sum;
 }
 
+// Infinities and NaN in tiles.  0 times one of them is NaN, so where a
+// probability of 0 stands for "not seen" they have to stay out of the product.
+// The running largest magnitude of chunks (bf16: in either half of the word), and
+// whether it is one of them.
+template <typename T> __device__ __forceinline__ uint32_t a_top(lu32x4 v, uint32_t top) {
+  typedef uint16_t Two __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = v[i] & (AT<T>::kBytes == 2 ? 0x7fff7fffu : 0x7fffffffu);
+    if constexpr (AT<T>::kBytes == 2)
+      top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(Two, m), __builtin_bit_cast(Two, top)));
+    else
+      top = max(top, m);
+  }
+  return top;
+}
+template <typename T> __device__ __forceinline__ bool a_odd(uint32_t top) {
+  return top >= 0x7f800000u || (AT<T>::kBytes == 2 && (top & 0xffffu) >= 0x7f80u);
+}
+// A chunk with zeros in their place.
+template <typename T> __device__ __forceinline__ lu32x4 a_finite(lu32x4 v) {
+  lu32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t hi = (v[i] & 0x7f800000u) == 0x7f800000u ? 0u : AT<T>::kBytes == 2 ? 0xffff0000u : 0xffffffffu;
+    r[i] = v[i] & (AT<T>::kBytes == 2 ? hi | ((v[i] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) : hi);
+  }
+  return r;
+}
+// Operands whose products overflow: ±2^100 where a chunk has an infinity of the
+// sign or a NaN; 2^100 at the first n indexes of a lane's part of a step (counted
+// over both halves: 4·half is taken off n by the caller).
+template <typename T> __device__ __forceinline__ lu32x4 a_odd_of(lu32x4 v, int negative) {
+  constexpr bool two = AT<T>::kBytes == 2;
+  lu32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = 0;
+#pragma unroll
+    for (int h = 0; h < (two ? 2 : 1); ++h) {
+      const uint32_t x = two && h == 0 ? v[i] << 16 : two ? v[i] & 0xffff0000u : v[i], m = x & 0x7fffffffu;
+      const bool odd = m > 0x7f800000u || x == (negative ? 0xff800000u : 0x7f800000u);
+      const uint32_t big = odd ? negative ? 0xf1800000u : 0x71800000u : 0u;
+      r[i] |= two && h == 0 ? big >> 16 : big;
+    }
+  }
+  return r;
+}
+template <typename T> __device__ __forceinline__ lu32x4 a_below(int n) {
+  lu32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (AT<T>::kBytes == 2) {
+      const int first = 8 * (i >> 1) + 2 * (i & 1);
+      r[i] = (first < n ? 0x7180u : 0u) | (first + 1 < n ? 0x71800000u : 0u);
+    } else {
+      r[i] = i < n ? 0x71800000u : 0u;
+    }
+  }
+  return r;
+}
+// Every wave is here, and its LDS accesses are done (loads into LDS may be on their way).
+__device__ __forceinline__ void a_meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // Step s of a result as an operand.
 template <typename T> __device__ __forceinline__ lu32x4 a_operand(const float (&p)[16], int s) {
   lu32x4 r;

@@ -82,3 +82,58 @@ def test_bad_keys_show_in_the_gradients(lib, tokens, bad, dim, dtype):
     for got, ref, heads in ((dq, refs[0], 4), (dk, refs[1], 2), (dv, refs[2], 1)):
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1, :, :heads], ref[1, :, :heads])
     assert torch.equal(dlam[:2], refs[3][:2])
+
+
+# Tokens, and one of them that is bad: in the first, a middle and the last row of
+# tiles and blocks, with groups that put several heads' rows into one tile.
+HIDDEN = [(40, 20, 4, 2), (40, 0, 2, 2), (200, 199, 3, 1), (333, 150, 7, 1), (520, 300, 2, 2), (130, 31, 4, 4), (20, 9, 2, 1)]
+BAD = [float("nan"), float("inf"), float("-inf")]
+
+
+def clean(lib, tokens, heads, kv, dim, dtype, packed):
+    """(tensors, what calls take beside them, results and gradients)"""
+    ts = [t.cuda() for t in attention_inputs(1 if packed else 2, tokens, tokens, heads, kv, dim, dtype)]
+    kw = {}
+    if packed:  # the bad token's sequence begins at 0
+        ts = [t[0] if t.dim() == 4 else t for t in ts]
+        kw = dict(offsets=torch.tensor([0, tokens], dtype=torch.int32, device="cuda"))
+    return ts, kw, passes(lib, ts, kw)
+
+
+def passes(lib, ts, kw):
+    q, k, v, lam, do = ts
+    out, saved = lib.muon_diff_attention(q, k, v, lam, save=True, **kw)
+    assert torch.equal(out.nan_to_num(7.0), lib.muon_diff_attention(q, k, v, lam, **kw).nan_to_num(7.0))
+    return out, *lib.muon_diff_attention_grad(do, q, k, v, lam, out, saved, **kw)
+
+
+def same_but(got, ref, hit, what):
+    """Bits outside `hit` (True where the bad value has a part)."""
+    assert torch.equal(got[~hit], ref[~hit]), what
+
+
+def all_bad(got, hit, what):
+    assert not torch.isfinite(got[hit]).any(), what
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("tokens,at,heads,kv", HIDDEN)
+def test_hidden_values(lib, tokens, at, heads, kv, packed, dim, dtype):
+    """An infinity or NaN in a value of token `at` reaches the same value of the
+    results from that token on, and nothing else of them."""
+    ts, kw, ref = clean(lib, tokens, heads, kv, dim, dtype, packed)
+    g = heads // kv
+    for bad in BAD:
+        v = ts[2].clone()
+        v[..., at, kv - 1, 5] = bad
+        got = passes(lib, [*ts[:2], v, *ts[3:]], kw)
+        hit = torch.zeros_like(ref[0], dtype=torch.bool)
+        hit[..., at:, heads - g:, 5] = True
+        same_but(got[0], ref[0], hit, ("out", bad))
+        all_bad(got[0], hit, ("out", bad))
+        hit = torch.zeros_like(ref[1], dtype=torch.bool)
+        hit[..., at:, 2 * (heads - g):, :] = True
+        same_but(got[1], ref[1], hit, ("dq", bad))
+        assert torch.equal(got[3], ref[3])  # the values have no part in their gradient
