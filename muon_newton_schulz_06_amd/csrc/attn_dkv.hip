@@ -113,9 +113,7 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   const int64_t rec0 = ((int64_t)batch * L.heads + hk * G) * S.nq + tok0;
   const uint32_t base = a_lds(lds);
   // The next tile to load: head g, tokens from t.  Past the last tile the loads
-  // deliver zeros, and so they do for rows that see no key at all: their
-  // probabilities are 0, but 0 times an infinity or NaN of theirs is not.
-  const int seeing = S.causal ? max(1 - shift, 0) : 0;  // the first row that sees a key
+  // deliver zeros.
   struct Place {
     int g, t;
   };
@@ -141,15 +139,14 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   locate();
   auto issue = [&](uint32_t buf) __attribute__((always_inline)) {
     const int left = filled < end ? nq - load.t : 0;
-    const int from = seeing - load.t;
-    if (left >= 32 && from <= 0) {
+    if (left >= 32) {
       ldq.issue(q, buf);
       ldq.issue(q + S.qs[2] * E, buf + RQ);
       ldd.issue(d, buf + 2 * RQ);
     } else {
-      ldq.issue(q, from, left, buf);
-      ldq.issue(q + S.qs[2] * E, from, left, buf + RQ);
-      ldd.issue(d, from, left, buf + 2 * RQ);
+      ldq.issue(q, left, buf);
+      ldq.issue(q + S.qs[2] * E, left, buf + RQ);
+      ldd.issue(d, left, buf + 2 * RQ);
     }
     // the records: bf16 recL by wave 0, recD by wave 1; fp32 rec by wave 0
     // (lanes past 31 deliver zeros behind the 32 records)
@@ -215,6 +212,22 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
       return cq.get(buf + m * RQ, u, n);
     }
   };
+  // Rows with an infinity or NaN: for the keys that a row does not see its
+  // probabilities and dS are 0, but 0 times these is not.  So a row of Q leaves the
+  // tile where its log-sum is not finite (then dS is NaN, or P is 0, by that), and
+  // the odd values leave a row of dO (dS is NaN by δ; dV follows behind the tiles).
+  // Every wave does so for itself, all alike, before its products over the rows.
+  bool odd = false;
+  auto clean = [&](uint32_t buf, uint32_t bad) __attribute__((always_inline)) {
+    odd = true;
+#pragma clang loop unroll(disable)
+    for (int c = 0; c < 2 * NC; ++c) {
+      if (c < NC && (bad & 1)) rq.put(buf, c, lu32x4{0, 0, 0, 0});
+      if (c < NC && (bad & 2)) rq.put(buf + RQ, c, lu32x4{0, 0, 0, 0});
+      if (bad) rd.put(buf + 2 * RQ, c, a_finite<T>(rd.get(buf + 2 * RQ, c)));
+    }
+  };
+  static_assert(bV - AHEAD > NC, "rows are clean before they are read as columns");
   lu32x4 ring[AHEAD];
   // −L/c is finite, since an infinity would meet zeros in the product; a NaN stays
   auto bounded = [](float x) __attribute__((always_inline)) { return x < -1e30f ? -1e30f : x; };
@@ -259,6 +272,12 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
       if constexpr (j < bS2) {
         if constexpr (j < NC) s1 = a_mma<T>(r, k[0][j], s1);
         else s1 = stat(r, std::true_type{}, bounded(__uint_as_float(r[0]) * invc), s1);
+        if constexpr (j == NC) {
+          uint32_t bad = r[3];
+          if constexpr (E == 4)
+            bad = a_bad_row(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]), __uint_as_float(r[3]));
+          if (__builtin_expect(__any(bad != 0), 0)) clean(base + decltype(stage)::value * F::kStage, bad);
+        }
       } else if constexpr (j < bA) {
         if constexpr (j - bS2 < NC) s2 = a_mma<T>(r, k[1][j - bS2], s2);
         else s2 = stat(r, std::false_type{}, bounded(__uint_as_float(r[1]) * invc), s2);
@@ -359,6 +378,32 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
   }
   // no load may still be on its way into LDS when the workgroup ends
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  // the odd values of dO, for the keys that their rows see
+  if (kV && odd) {
+    for (int i = begin; i < end; ++i) {
+      const int g = i / perHead, t0 = first + 32 * (i % perHead), t1 = t0 + (lane & 31);
+      uint32_t bad = 0;
+      if (t1 < nq) {
+        const lf4 r = L.rec[rec0 + (int64_t)g * S.nq + t1];
+        bad = a_bad_row(r.v[0], r.v[1], r.v[2], r.v[3]);
+      }
+      for (uint32_t rows = (uint32_t)__ballot(bad != 0); rows; rows &= rows - 1) {
+        const int t = t0 + __builtin_ctz(rows);
+        const char* o = d0 + (t * L.gs[1] + g * L.gs[2]) * E;
+#pragma unroll
+        for (int n = 0; n < 2 * ND; ++n) {
+          const int c = n * 32 + (lane & 31);
+          const float x = c < 2 * S.dim ? LType<T>::get(o, c) : 0.f, nan = x - x;  // (0 where x is finite)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int kk = key0 + 8 * (e >> 2) + 4 * half + (e & 3);
+            dv[n][e] += !S.causal || kk < t + shift ? nan : 0.f;
+          }
+        }
+      }
+    }
+  }
 
   // registers run over keys here: lane l has column l % 32 of every sum
 #pragma unroll

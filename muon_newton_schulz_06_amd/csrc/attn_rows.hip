@@ -61,9 +61,12 @@ __global__ __launch_bounds__(kPrep) void attn_rows(const AttnGradLaunch L, const
     const char* o2 = (const char*)S.kept + at2 * S.pitch * E;
     const int width = 2 * S.dim;
     float s1 = 0.f, s2 = 0.f;
+    uint32_t top = 0;
     for (int c = lane * V; c < width; c += 16 * V) {
       float x[V], y[V], z[V];
-      l_widen<T>(*(const lu32x4*)(d + c * E), x);  // zeros past the width, as in the kept rows
+      const lu32x4 dx = *(const lu32x4*)(d + c * E);
+      top = a_top<T>(dx, top);
+      l_widen<T>(dx, x);  // zeros past the width, as in the kept rows
       if constexpr (E == 2) {
         widen_whole(*(const lu32x4*)(o1 + c * E), y);
         widen_whole(*(const lu32x4*)(o2 + c * E), z);
@@ -77,6 +80,7 @@ __global__ __launch_bounds__(kPrep) void attn_rows(const AttnGradLaunch L, const
         s2 += x[i] * z[i];
       }
     }
+    if (a_odd<T>(top)) s1 = s2 = __builtin_nanf("");  // of an infinity too: attn_dkv takes it out of dO
 #pragma unroll
     for (int w = 8; w > 0; w >>= 1) {
       s1 += __shfl_xor(s1, w, 64);
@@ -90,6 +94,7 @@ __global__ __launch_bounds__(kPrep) void attn_rows(const AttnGradLaunch L, const
       s1 += S.lam[h] * s2;
     }
     const float l1 = S.stat[(combo * 2) * all + row], l2 = S.stat[(combo * 2 + 1) * all + row];
+    const uint32_t bad = a_bad_row(l1, l2, s1, s2);
     if (l2 == -kNegInf) s1 = s2 = 0.f;  // a row that sees no key, whatever its dO holds
     const int64_t at = (b * L.heads + h) * S.nq + t;
     L.rec[at] = lf4{{l1, l2, s1, s2}};
@@ -98,7 +103,8 @@ __global__ __launch_bounds__(kPrep) void attn_rows(const AttnGradLaunch L, const
       uint32_t a[3], e[3];
       split3(fmaxf(fminf(-l1 / S.c, 1e30f), -1e30f), a);
       split3(fmaxf(fminf(-l2 / S.c, 1e30f), -1e30f), e);
-      L.recL[at] = lu4{{a[0] | a[1] << 16, a[2] | e[0] << 16, e[1] | e[2] << 16, 0u}};
+      // (as values of the product the marks are as good as zeros, and meet zeros)
+      L.recL[at] = lu4{{a[0] | a[1] << 16, a[2] | e[0] << 16, e[1] | e[2] << 16, bad}};
       split3(-s1, a);
       split3(-s2, e);
       L.recD[at] = lu4{{a[0] | a[1] << 16, a[2] | e[0] << 16, e[1] | e[2] << 16, 0u}};

@@ -128,6 +128,13 @@ template <typename T> __device__ __forceinline__ lu32x4 a_below(int n) {
   }
   return r;
 }
+// What is not finite of a row's log-sums and δ: bits 0 and 1 the maps' log-sums (a
+// row whose q is odd has neither finite), bit 2 anything.
+__device__ __forceinline__ uint32_t a_bad_row(float l1, float l2, float d1, float d2) {
+  auto odd = [](float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; };
+  const uint32_t l = (odd(l1) ? 1u : 0u) | (odd(l2) ? 2u : 0u);
+  return l | (l || odd(d1) || odd(d2) ? 4u : 0u);
+}
 // Every wave is here, and its LDS accesses are done (loads into LDS may be on their way).
 __device__ __forceinline__ void a_meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -234,16 +241,6 @@ template <int RB, int ROWS, int NW> struct TileLoader {
     for (int p = 0; p < N; ++p)
       f_dma16(__builtin_amdgcn_readfirstlane(dst + (wave * N + p) * 1024),
               row0 + p * kRowsPer < left ? off[p] : kFfnNowhere, buf);
-  }
-  // rows before `from` arrive as zeros too
-  __device__ __forceinline__ void issue(const char* base, int from, int left, uint32_t dst) const {
-    const fi32x4 buf = f_buffer((uint64_t)base);
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-      const int r = row0 + p * kRowsPer;
-      f_dma16(__builtin_amdgcn_readfirstlane(dst + (wave * N + p) * 1024), (r >= from) & (r < left) ? off[p] : kFfnNowhere,
-              buf);
-    }
   }
 };
 

@@ -137,3 +137,44 @@ def test_hidden_values(lib, tokens, at, heads, kv, packed, dim, dtype):
         hit[..., at:, 2 * (heads - g):, :] = True
         same_but(got[1], ref[1], hit, ("dq", bad))
         assert torch.equal(got[3], ref[3])  # the values have no part in their gradient
+
+
+def bad_rows(lib, tokens, at, heads, kv, dim, dtype, packed, which):
+    """A bad value of token `at` in a query or the incoming gradient reaches the
+    gradients of that row and of the keys that it sees, and nothing else."""
+    ts, kw, ref = clean(lib, tokens, heads, kv, dim, dtype, packed)
+    g, h = heads // kv, heads - 1
+    for bad in BAD:
+        new = [t.clone() for t in ts]
+        if which == "q":
+            new[0][..., at, 2 * h:2 * h + 2, :] = bad
+        else:
+            new[4][..., at, h, 3] = bad
+        out, dq, dk, dv, dlam = passes(lib, new, kw)
+        hit = [torch.zeros_like(t, dtype=torch.bool) for t in ref]
+        hit[0][..., at, h, :] = which == "q"
+        hit[1][..., at, 2 * h:2 * h + 2, :] = True
+        hit[2][..., :at + 1, 2 * (kv - 1):, :] = True
+        hit[3][..., :at + 1, kv - 1, :] = True
+        hit[4][h] = True
+        for name, a, b, m in zip(("out", "dq", "dk", "dv", "dlam"), (out, dq, dk, dv, dlam), ref, hit):
+            same_but(a, b, m, (name, bad))
+        # (the row that sees one key has no gradient of its scores)
+        if at:
+            all_bad(dq, hit[1], ("dq", bad))
+            all_bad(dk, hit[2], ("dk", bad))
+        if which == "q":
+            all_bad(dv, hit[3], ("dv", bad))
+        else:  # the same value of the values alone
+            all_bad(dv[..., :at + 1, kv - 1, 3], ..., ("dv", bad))
+            hit[3][..., [i for i in range(2 * dim) if i != 3]] = False
+            same_but(dv, ref[3], hit[3], ("dv", bad))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("which", ["q", "dout"])
+@pytest.mark.parametrize("tokens,at,heads,kv", HIDDEN)
+def test_hidden_rows(lib, tokens, at, heads, kv, which, packed, dim, dtype):
+    bad_rows(lib, tokens, at, heads, kv, dim, dtype, packed, which)
