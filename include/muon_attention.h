@@ -122,9 +122,9 @@ muon_status_t muon_dropout_grad(const void* dy, int64_t ld_dy, double p, uint64_
  *   key/value head one for 32 to 128 rows of queries · group, or 128 keys, and two
  *   and one per sequence more of a packed batch).
  * Keys behind the end of a sequence are never read.  Infinities and NaN of keys
- * and values that the causal rule hides from a row do not reach its result, and
- * those of a row's q and dout not the gradients of keys that it does not see.  (Of
- * hidden keys 0 · k may reach dq.)
+ * and values that the causal rule hides from a row reach neither its result nor its
+ * gradient, and those of a row's q and dout not the gradients of keys that it does
+ * not see.
  * Tensors whose heads are not whole 16-byte chunks at 16-byte aligned addresses
  * (or with tokens 2^24 or more elements apart) are copied to the workspace. */
 typedef struct muon_diff_attention {

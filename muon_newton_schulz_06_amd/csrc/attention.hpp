@@ -130,6 +130,7 @@ struct AttnGradLaunch {
   // for bf16 the same as operands of a product (see attn_dkv), two 16-byte records.
   lf4* rec;
   lu4 *recL, *recD;
+  uint8_t* oddKeys;  // [combo][key]: whether a key holds an infinity or NaN; null: of no matter
   float* rowLam;     // per row δ2 as the products give it, [batch][head][token]
   void *dq, *dk, *dv;
   int64_t dqs[3], dks[3], dvs[3];

@@ -357,7 +357,7 @@ struct RunsPlan {
 };
 
 struct AttnGradLayout {
-  size_t q, k, v, dout, rec, recL, recD, rowLam, part, rowPart, total;
+  size_t q, k, v, dout, rec, recL, recD, rowLam, oddKeys, part, rowPart, total;
   RunsPlan keys, rows;
 };
 
@@ -404,6 +404,7 @@ AttnGradLayout attn_grad_layout(const muon_diff_attention_t& f, const AttnLayout
   g.recL = take(bf16 ? rows * 16 : 0);
   g.recD = take(bf16 ? rows * 16 : 0);
   g.rowLam = take(rows * 4);
+  g.oddKeys = take((size_t)(l.combos * f.keys));  // (causal or not: the size queries do not ask)
   g.part = take((size_t)g.keys.streams * 2 * kDkvKeys * 4 * l.dp * 4);
   g.rowPart = take((size_t)g.rows.streams * 2 * kDqRows * (2 * l.dp + 4) * 4);
   g.total = at;
@@ -712,6 +713,7 @@ muon_status_t muon_diff_attention_grad(const muon_diff_attention_t* f, const voi
     L.recL = (lu4*)(ws + w.recL);
     L.recD = (lu4*)(ws + w.recD);
     L.rowLam = (float*)(ws + w.rowLam);
+    if (wantQ && f->causal) L.oddKeys = (uint8_t*)(ws + w.oddKeys);
     L.dq = grads->dq;
     L.dqVec = output_strides(L.dqs, grads->dq, gq, e);
     L.dk = grads->dk;

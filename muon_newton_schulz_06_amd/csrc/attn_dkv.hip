@@ -213,21 +213,29 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
     }
   };
   // Rows with an infinity or NaN: for the keys that a row does not see its
-  // probabilities and dS are 0, but 0 times these is not.  So a row of Q leaves the
-  // tile where its log-sum is not finite (then dS is NaN, or P is 0, by that), and
-  // the odd values leave a row of dO (dS is NaN by δ; dV follows behind the tiles).
-  // Every wave does so for itself, all alike, before its products over the rows.
+  // probabilities and dS are 0, but 0 times these is not.  So the odd values leave a
+  // row of dO (dS is NaN by δ; dV follows behind the tiles), and a row of Q leaves the
+  // tile where its log-sum is not finite (P is NaN, ∞ or 0 by that), once every wave has
+  // its scores.  All waves do so alike, before their products over the rows.
   bool odd = false;
+  constexpr int kLook = kK ? bA - 1 : NC;  // a product that reads the records
+  static_assert((kV ? bV : bK1) - AHEAD > kLook, "rows are clean before they are read as columns");
   auto clean = [&](uint32_t buf, uint32_t bad) __attribute__((always_inline)) {
     odd = true;
+    if constexpr (kK) a_meet();
 #pragma clang loop unroll(disable)
     for (int c = 0; c < 2 * NC; ++c) {
-      if (c < NC && (bad & 1)) rq.put(buf, c, lu32x4{0, 0, 0, 0});
-      if (c < NC && (bad & 2)) rq.put(buf + RQ, c, lu32x4{0, 0, 0, 0});
-      if (bad) rd.put(buf + 2 * RQ, c, a_finite<T>(rd.get(buf + 2 * RQ, c)));
+      if (kK && c < NC && (bad & 1)) rq.put(buf, c, lu32x4{0, 0, 0, 0});
+      if (kK && c < NC && (bad & 2)) rq.put(buf + RQ, c, lu32x4{0, 0, 0, 0});
+      if (kV && bad) rd.put(buf + 2 * RQ, c, a_finite<T>(rd.get(buf + 2 * RQ, c)));
     }
   };
-  static_assert(bV - AHEAD > NC, "rows are clean before they are read as columns");
+  auto look = [&](uint32_t buf, lu32x4 rec) __attribute__((always_inline)) {
+    uint32_t bad = rec[3];
+    if constexpr (E == 4)
+      bad = a_bad_row(__uint_as_float(rec[0]), __uint_as_float(rec[1]), __uint_as_float(rec[2]), __uint_as_float(rec[3]));
+    if (__builtin_expect(__any(bad), 0)) clean(buf, bad);
+  };
   lu32x4 ring[AHEAD];
   // −L/c is finite, since an infinity would meet zeros in the product; a NaN stays
   auto bounded = [](float x) __attribute__((always_inline)) { return x < -1e30f ? -1e30f : x; };
@@ -272,15 +280,11 @@ __global__ __launch_bounds__(256, 1) void attn_dkv(const AttnGradLaunch L) {
       if constexpr (j < bS2) {
         if constexpr (j < NC) s1 = a_mma<T>(r, k[0][j], s1);
         else s1 = stat(r, std::true_type{}, bounded(__uint_as_float(r[0]) * invc), s1);
-        if constexpr (j == NC) {
-          uint32_t bad = r[3];
-          if constexpr (E == 4)
-            bad = a_bad_row(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]), __uint_as_float(r[3]));
-          if (__builtin_expect(__any(bad != 0), 0)) clean(base + decltype(stage)::value * F::kStage, bad);
-        }
+        if constexpr (j == kLook) look(base + decltype(stage)::value * F::kStage, r);
       } else if constexpr (j < bA) {
         if constexpr (j - bS2 < NC) s2 = a_mma<T>(r, k[1][j - bS2], s2);
         else s2 = stat(r, std::false_type{}, bounded(__uint_as_float(r[1]) * invc), s2);
+        if constexpr (j == kLook) look(base + decltype(stage)::value * F::kStage, r);
       } else if constexpr (j < bV) {
         if constexpr (j - bA < 2 * NC) {
           a1 = a_mma<T>(r, v[j - bA], a1);

@@ -119,9 +119,9 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
   const uint32_t base = a_lds(lds);
   auto issue = [&](int key, uint32_t buf) __attribute__((always_inline)) {
     const char* k = k1 + (int64_t)key * S.ks[1] * E;
-    ldk.issue(k, nk - key, buf);
-    ldk.issue(k + S.ks[2] * E, nk - key, buf + BN * F::kK);
-    ldv.issue(v0 + (int64_t)key * S.vs[1] * E, nk - key, buf + 2 * BN * F::kK);
+    ldk.issue(k, kSee - key, buf);
+    ldk.issue(k + S.ks[2] * E, kSee - key, buf + BN * F::kK);
+    ldv.issue(v0 + (int64_t)key * S.vs[1] * E, kSee - key, buf + 2 * BN * F::kK);
   };
   const RowReader<F::kK> rk(lane);
   const RowReader<F::kV> rv(lane);
@@ -199,11 +199,44 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
     });
   };
 
+  // Infinities and NaN of keys: of one that a row does not see dS is 0, but 0 times
+  // them is not.  Where there are any among the keys that only some of the rows see,
+  // this goes through those tiles: rows that see such a key become NaN (as their
+  // log-sums are, but for scores of −∞), and its values leave the tile.
+  uint32_t flag = 0;
+  if (const int from = max(least, kBegin); from < kEnd && S.causal) {
+    const uint8_t* o = L.oddKeys + (int64_t)P.combo * S.nk + tok0;
+    if (from + lane < kEnd) flag = o[from + lane];
+    for (int j = from + 64; j < kEnd; j += 64)
+      if (j + lane < kEnd) flag |= o[j + lane];
+  }
+  auto clean = [&](uint32_t buf, int key) __attribute__((always_inline)) {
+    static_assert(BN == 32, "a lane per key and map");
+    typedef __attribute__((address_space(3))) lu32x4* Chunk;
+    uint32_t top = 0;
+#pragma clang loop unroll(disable)
+    for (int c = 0; c < F::kK / 16; ++c) top = a_top<T>(*(Chunk)(uintptr_t)(buf + lane * F::kK + c * 16), top);
+    const uint64_t bad = __ballot(a_odd<T>(top));
+    const int n = lim - key;
+    const uint32_t seen = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1;
+    if ((uint32_t)bad & seen) l1 = __builtin_nanf("");
+    if ((uint32_t)(bad >> 32) & seen) l2 = __builtin_nanf("");
+    a_meet();
+#pragma clang loop unroll(disable)
+    for (int i = tid; i < 2 * BN * F::kK / 16; i += F::kThreads) {
+      const Chunk c = (Chunk)(uintptr_t)(buf + i * 16);
+      *c = a_finite<T>(*c);
+    }
+    a_meet();
+  };
+
   __syncthreads();  // every wave has left the LDS of the piece before
   if (kBegin < kEnd) {
     issue(kBegin, base);
     a_landed();
+    const bool look = kBegin + BN > least && __any(flag);
     if (kBegin + BN < kEnd) issue(kBegin + BN, base + F::kStage);
+    if (__builtin_expect(look, 0)) clean(base, kBegin);
     a_for<0, AHEAD>([&](auto jc) __attribute__((always_inline)) {
       ring[decltype(jc)::value] = read(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{}, jc);
     });
@@ -219,7 +252,9 @@ __global__ __launch_bounds__(256, (Dq<T, DP>::kWavesPerSimd)) void attn_dq(const
         step(bc, sc, k0 + 32 * s, k0 + 32 * s + 32 > least, [&]() __attribute__((always_inline)) {
           if constexpr (s == STEPS - 1) {
             a_landed();  // the next tile is there, this one has been read by every wave
+            const bool look = k0 + BN < kEnd && k0 + 2 * BN > least && __any(flag);
             if (k0 + 2 * BN < kEnd) issue(k0 + 2 * BN, base + b * F::kStage);
+            if (__builtin_expect(look, 0)) clean(base + (1 - b) * F::kStage, k0 + BN);
           }
         });
       });

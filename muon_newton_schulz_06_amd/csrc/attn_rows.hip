@@ -38,15 +38,34 @@ __device__ __forceinline__ void widen_whole(const lu32x4& v, float (&f)[8]) {
   }
 }
 
+// Which keys hold an infinity or NaN, for attn_dq: 16 lanes the two maps of a key.
+template <typename T> __device__ __forceinline__ void odd_keys(const AttnGradLaunch& L, int block, int blocks) {
+  constexpr int V = LType<T>::kVec, E = AT<T>::kBytes;
+  const AttnShape& S = L.s;
+  const int lane = threadIdx.x & 15, chunks = (S.dim + V - 1) / V;
+  const int64_t keys = (int64_t)S.combos * S.nk;
+  for (int64_t id = (int64_t)block * (kPrep / 16) + (threadIdx.x >> 4); id < keys; id += (int64_t)blocks * (kPrep / 16)) {
+    const int64_t bt = id / S.kv, hk = id - bt * S.kv, b = bt / S.nk, t = bt - b * S.nk;
+    const char* k = (const char*)S.k + (b * S.ks[0] + t * S.ks[1] + 2 * hk * S.ks[2]) * E;
+    uint32_t top = 0;
+    for (int i = lane; i < 2 * chunks; i += 16)
+      top = a_top<T>(*(const lu32x4*)(k + (i < chunks ? 0 : S.ks[2] * E) + (i < chunks ? i : i - chunks) * 16), top);
+    const uint64_t odd = __ballot(a_odd<T>(top)) >> (threadIdx.x & 48);
+    if (lane == 0) L.oddKeys[(b * S.kv + hk) * S.nk + t] = (odd & 0xffff) != 0;
+  }
+}
+
 // The first workgroups make the lists of the products that follow, which take as
 // long (7 µs: scans and searches by one workgroup) as the sums of few rows.
 template <typename T, bool VEC>
-__global__ __launch_bounds__(kPrep) void attn_rows(const AttnGradLaunch L, const AttnPrepLaunch P) {
+__global__ __launch_bounds__(kPrep, 8)  // two workgroups a CU
+void attn_rows(const AttnGradLaunch L, const AttnPrepLaunch P, int blocks) {
   if ((int)blockIdx.x < P.lists) return attn_lists(P, blockIdx.x);
+  if ((int)blockIdx.x >= P.lists + blocks) return odd_keys<T>(L, blockIdx.x - P.lists - blocks, gridDim.x - P.lists - blocks);
   constexpr int V = LType<T>::kVec, E = AT<T>::kBytes;
   const AttnShape& S = L.s;
   const int64_t rows = (int64_t)L.batch * S.nq * L.heads;
-  const int64_t each = (int64_t)(gridDim.x - P.lists) * (kPrep / 16);
+  const int64_t each = (int64_t)blocks * (kPrep / 16);
   for (int64_t id = (int64_t)(blockIdx.x - P.lists) * (kPrep / 16) + (threadIdx.x >> 4); id < rows; id += each) {
     const int lane = threadIdx.x & 15;
     const int64_t bt = id / L.heads;
@@ -103,6 +122,14 @@ __global__ __launch_bounds__(kPrep) void attn_rows(const AttnGradLaunch L, const
       uint32_t a[3], e[3];
       split3(fmaxf(fminf(-l1 / S.c, 1e30f), -1e30f), a);
       split3(fmaxf(fminf(-l2 / S.c, 1e30f), -1e30f), e);
+      if (__builtin_expect(bad, 0)) {
+        // a NaN is three finite values whose sum is infinite; and a map without a finite
+        // log-sum has P = 0, ∞ or NaN whatever δ, whose NaN would meet zeros too
+        if (l1 != l1) a[0] = a[1] = a[2] = 0x7f7fu;
+        if (l2 != l2) e[0] = e[1] = e[2] = 0x7f7fu;
+        if (bad & 1) s1 = 0.f;
+        if (bad & 2) s2 = 0.f;
+      }
       // (as values of the product the marks are as good as zeros, and meet zeros)
       L.recL[at] = lu4{{a[0] | a[1] << 16, a[2] | e[0] << 16, e[1] | e[2] << 16, bad}};
       split3(-s1, a);
@@ -140,11 +167,12 @@ __global__ __launch_bounds__(kLamThreads) void attn_dlam(const AttnGradLaunch L)
 }  // namespace
 
 hipError_t launch_attn_rows(bool bf16, const AttnGradLaunch& L, const AttnPrepLaunch& P, hipStream_t st) {
-  const int64_t rows = (int64_t)L.batch * L.s.nq * L.heads, per = kPrep / 16;
-  const dim3 grid((unsigned)(P.lists + std::min<int64_t>((rows + per - 1) / per, 1 << 20)));
-  if (bf16) attn_rows<Bf16, true><<<grid, kPrep, 0, st>>>(L, P);
-  else if (L.outVec) attn_rows<float, true><<<grid, kPrep, 0, st>>>(L, P);
-  else attn_rows<float, false><<<grid, kPrep, 0, st>>>(L, P);
+  auto blocks = [](int64_t n) { return (int)std::min<int64_t>((n + kPrep / 16 - 1) / (kPrep / 16), 1 << 20); };
+  const int rows = blocks((int64_t)L.batch * L.s.nq * L.heads);
+  const dim3 grid((unsigned)(P.lists + rows + (L.oddKeys ? blocks((int64_t)L.s.combos * L.s.nk) : 0)));
+  if (bf16) attn_rows<Bf16, true><<<grid, kPrep, 0, st>>>(L, P, rows);
+  else if (L.outVec) attn_rows<float, true><<<grid, kPrep, 0, st>>>(L, P, rows);
+  else attn_rows<float, false><<<grid, kPrep, 0, st>>>(L, P, rows);
   return hipGetLastError();
 }
 

@@ -128,8 +128,8 @@ template <typename T> __device__ __forceinline__ lu32x4 a_below(int n) {
   }
   return r;
 }
-// What is not finite of a row's log-sums and δ: bits 0 and 1 the maps' log-sums (a
-// row whose q is odd has neither finite), bit 2 anything.
+// What is not finite of a row's log-sums and δ: bits 0 and 1 the maps' log-sums (that
+// of an odd q is not), bit 2 anything.
 __device__ __forceinline__ uint32_t a_bad_row(float l1, float l2, float d1, float d2) {
   auto odd = [](float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; };
   const uint32_t l = (odd(l1) ? 1u : 0u) | (odd(l2) ? 2u : 0u);

@@ -178,3 +178,29 @@ def bad_rows(lib, tokens, at, heads, kv, dim, dtype, packed, which):
 @pytest.mark.parametrize("tokens,at,heads,kv", HIDDEN)
 def test_hidden_rows(lib, tokens, at, heads, kv, which, packed, dim, dtype):
     bad_rows(lib, tokens, at, heads, kv, dim, dtype, packed, which)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("tokens,at,heads,kv", HIDDEN)
+def test_hidden_keys(lib, tokens, at, heads, kv, packed, dim, dtype):
+    """A key without finite values reaches no row before it."""
+    ts, kw, ref = clean(lib, tokens, heads, kv, dim, dtype, packed)
+    g = heads // kv
+    for bad in BAD:
+        k = ts[1].clone()
+        k[..., at, 2 * (kv - 1), :] = bad  # the first map's
+        out, dq, dk, dv, dlam = passes(lib, [ts[0], k, *ts[2:]], kw)
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[..., at:, heads - g:, :] = True
+        same_but(out, ref[0], hit, ("out", bad))
+        all_bad(out, hit, ("out", bad))
+        hit = torch.zeros_like(dq, dtype=torch.bool)
+        hit[..., at:, 2 * (heads - g)::2, :] = True
+        same_but(dq, ref[1], hit, ("dq", bad))
+        if at:
+            all_bad(dq, hit, ("dq", bad))
+        assert torch.equal(dk[..., :2 * (kv - 1), :], ref[2][..., :2 * (kv - 1), :])
+        assert torch.equal(dk[..., 2 * kv - 1, :], ref[2][..., 2 * kv - 1, :])  # the second map's
+        assert torch.equal(dlam, ref[4])
