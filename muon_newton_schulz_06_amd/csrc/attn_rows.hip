@@ -82,16 +82,21 @@ void attn_rows(const AttnGradLaunch L, const AttnPrepLaunch P, int blocks) {
     float s1 = 0.f, s2 = 0.f;
     uint32_t top = 0;
     for (int c = lane * V; c < width; c += 16 * V) {
+      // zeros past the width, as in the kept rows
+      const lu32x4 cx = *(const lu32x4*)(d + c * E), cz = *(const lu32x4*)(o2 + c * E);
+      lu32x4 cy;
+      if constexpr (E == 2) cy = *(const lu32x4*)(o1 + c * E);
+      else cy = l_load<T, VEC>(o1, c, width);
+      __builtin_amdgcn_sched_barrier(0);  // all three on their way
+      top = a_top<T>(cx, top);
       float x[V], y[V], z[V];
-      const lu32x4 dx = *(const lu32x4*)(d + c * E);
-      top = a_top<T>(dx, top);
-      l_widen<T>(dx, x);  // zeros past the width, as in the kept rows
+      l_widen<T>(cx, x);
       if constexpr (E == 2) {
-        widen_whole(*(const lu32x4*)(o1 + c * E), y);
-        widen_whole(*(const lu32x4*)(o2 + c * E), z);
+        widen_whole(cy, y);
+        widen_whole(cz, z);
       } else {
-        l_widen<T>(l_load<T, VEC>(o1, c, width), y);
-        l_widen<T>(*(const lu32x4*)(o2 + c * E), z);
+        l_widen<T>(cy, y);
+        l_widen<T>(cz, z);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {

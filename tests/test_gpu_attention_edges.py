@@ -204,3 +204,50 @@ def test_hidden_keys(lib, tokens, at, heads, kv, packed, dim, dtype):
         assert torch.equal(dk[..., :2 * (kv - 1), :], ref[2][..., :2 * (kv - 1), :])
         assert torch.equal(dk[..., 2 * kv - 1, :], ref[2][..., 2 * kv - 1, :])  # the second map's
         assert torch.equal(dlam, ref[4])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 40])
+@pytest.mark.parametrize("queries,keys,heads,kv", [(8, 4096, 4, 2), (5, 700, 6, 2), (40, 5000, 3, 1), (3, 1, 2, 2), (300, 5000, 2, 1)])
+def test_hidden_among_many_keys(lib, queries, keys, heads, kv, dim, dtype):
+    """The last rows of a long context, its keys split: a bad key or value that only
+    some of them see, and one that all see."""
+    ts = [t.cuda() for t in attention_inputs(2, queries, keys, heads, kv, dim, dtype)]
+    ref = passes(lib, ts, {})
+    g = heads // kv
+    for at in {max(keys - 1 - queries // 3, 0), keys - 1, max(keys - queries, 0), keys // 2}:
+        first = max(at - (keys - queries), 0)  # the first row that sees it
+        for bad in BAD:
+            for which, head, part in ((1, 2 * (kv - 1), slice(None)), (2, kv - 1, 5)):
+                new = [t.clone() for t in ts]
+                new[which][:, at, head, part] = bad
+                out, dq, dk, dv, dlam = passes(lib, new, {})
+                hit = torch.zeros_like(out, dtype=torch.bool)
+                hit[:, first:, heads - g:, part] = True
+                same_but(out, ref[0], hit, ("out", at, bad))
+                all_bad(out, hit, ("out", at, bad))
+                hit = torch.zeros_like(dq, dtype=torch.bool)
+                hit[:, first:, 2 * (heads - g):: 2 if which == 1 else 1] = True
+                same_but(dq, ref[1], hit, ("dq", at, bad))
+                if which == 2:
+                    assert torch.equal(dv, ref[3])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_bad_sequences_stay_alone(lib, causal, dim, dtype):
+    """Nothing of a packed batch's sequence reaches its neighbours."""
+    tokens, at = 300, (97, 161)
+    q, k, v, lam, do = (t.cuda() if t.dim() == 1 else t[0].cuda() for t in attention_inputs(1, tokens, tokens, 3, 1, dim, dtype))
+    off = torch.tensor([0, *at, tokens], dtype=torch.int32, device="cuda")
+    kw = dict(offsets=off, causal=causal)
+    ref = passes(lib, [q, k, v, lam, do], kw)
+    for bad in BAD:
+        new = [t.clone() for t in (q, k, v, lam, do)]
+        for i in (0, 1, 2, 4):
+            new[i][at[0]:at[1]] = bad
+        got = passes(lib, new, kw)
+        for name, a, b in zip(("out", "dq", "dk", "dv"), got, ref):
+            assert torch.equal(a[:at[0]], b[:at[0]]) and torch.equal(a[at[1]:], b[at[1]:]), (name, bad)
+            assert name == "dq" or not torch.isfinite(a[at[0] + 1:at[1]]).any(), (name, bad)
